@@ -63,7 +63,7 @@ typedef enum {
     WKV_ERR_ALIAS = -5,      /* an output overlaps an input or another output */
     WKV_ERR_CUDA = -6,       /* CUDA launch error; see wkv_last_cuda_error() */
     WKV_ERR_TIMEOUT = -7,    /* a cross-block wait on the GPU gave up (from wkv_workspace_status) */
-    WKV_ERR_WORKSPACE = -8,  /* wkv_backward: workspace NULL or smaller than wkv_backward_workspace_bytes() */
+    WKV_ERR_WORKSPACE = -8,  /* a backward call: workspace NULL or smaller than its _workspace_bytes() */
     WKV_ERR_SCRATCH = -9     /* wkv_forward_noalloc: problem needs more than its built-in scratch */
 } wkv_status;
 
@@ -484,6 +484,93 @@ int wkv5_forward(int64_t B, int64_t T, int64_t C, int64_t H, int dtype,
 int wkv_token_shift(int64_t B, int64_t T, int64_t C, int dtype, int nmix,
                     const void* x, const float* mu, const void* x_prev,
                     void* out, void* x_last, cudaStream_t stream);
+
+/*
+ * The gated delta rule: matrix-valued states whose update corrects what the
+ * state already holds for the token's key.  Heads of N channels (32, 64 or
+ * 128), H value heads; Hk key heads, H a multiple of Hk, value head h taking
+ * r and k of key head h / (H / Hk).  Per value head, with decay rate w_t >= 0
+ * and learning rate beta_t of the head's token:
+ *
+ *   e_t = v_t - e^{-w_t} S_{t-1}^T k_t
+ *   S_t = e^{-w_t} S_{t-1} + beta_t k_t e_t^T
+ *   y_t = S_t^T r_t                      (the state after the token's update)
+ *
+ * Layouts: r, k (B,T,Hk*N) and v, y (B,T,H*N) in dtype; w, beta (B,T,H)
+ * float32; states (B,H,N,N) float32, S[b][h][key channel][value channel].
+ * A decay rate of +infinity forgets the state before the token (a document
+ * border); beta = 0 with w = 0 leaves the state as it is (padding).  Keys
+ * are taken as they are: with beta |k|^2 above 2 the recurrence grows.
+ * All arithmetic is float32, the outputs rounded once to dtype; the order of
+ * every sum is fixed, so equal calls give equal bits.
+ *
+ * wkv_delta_forward -- a chunk of T tokens.  state_in NULL: zeros; state_out
+ * NULL: not wanted; it may equal state_in and must overlap nothing else.
+ * Feeding it back chains chunks exactly like one pass.  T == 0: state_out =
+ * state_in.  16-byte aligned r, k, v are read in 16-byte pieces.  Errors as
+ * wkv5_forward.  Asynchronous on `stream`; no workspace.
+ */
+int wkv_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int dtype,
+                      const float* w, const float* beta, const void* r, const void* k, const void* v,
+                      const float* state_in, void* y, float* state_out, cudaStream_t stream);
+
+/*
+ * wkv_delta_step -- one token for L layers of B sequences: w, beta (L,B,H),
+ * r, k (L,B,Hk*N), v, y (L,B,H*N), state (L,B,H,N,N) updated in place.  y
+ * and state must not overlap anything else.
+ */
+int wkv_delta_step(int64_t L, int64_t B, int64_t Hk, int64_t H, int64_t N, int dtype,
+                   const float* w, const float* beta, const void* r, const void* k, const void* v,
+                   float* state, void* y, cudaStream_t stream);
+
+/*
+ * wkv_delta_backward -- gradients of wkv_delta_forward given dy (B,T,H*N) in
+ * dtype and dstate_out (B,H,N,N) float32, dL/d(returned state), or NULL:
+ * dr, dk (B,T,Hk*N) and dv (B,T,H*N) in dtype, dr and dk summed over the
+ * value heads that share a key head; dw, dbeta (B,T,H) float32; dstate_in
+ * (B,H,N,N) float32 or NULL.  dw is 0 where e^{-w} is 0.  No output may
+ * overlap an input, another output or the workspace.  The workspace (256-byte
+ * aligned, no initialisation, wkv_delta_backward_workspace_bytes() bytes)
+ * holds nothing between calls.  T == 0: dstate_in = dstate_out (zeros if
+ * NULL), nothing else is written.  WKV_ERR_WORKSPACE: NULL or too small.
+ */
+size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t N);
+int wkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int dtype,
+                       const float* w, const float* beta, const void* r, const void* k, const void* v,
+                       const float* state_in, const void* dy, const float* dstate_out,
+                       void* dr, void* dk, void* dv, float* dw, float* dbeta, float* dstate_in,
+                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Activation of wkv_group_norm. */
+typedef enum { WKV_ACT_NONE = 0, WKV_ACT_SILU = 1, WKV_ACT_SIGMOID = 2 } wkv_act;
+
+/*
+ * wkv_group_norm -- group norm with an activation, channels last: the norm of
+ * the matrix-state operators' heads and the gate that follows it.  x, y
+ * (rows, C) in dtype, rows = tokens; every row's channels in G groups of
+ * C / G, each normalised by its own mean and (biased) variance:
+ *   hat = (x - mean) / sqrt(var + eps),  z = weight * hat + bias,
+ *   y = act(z), or z * act(gate) where gate (rows, C) in dtype is given.
+ * weight, bias (C,) float32 or NULL (ones, zeros); eps > 0 (WKV_ERR_SHAPE
+ * otherwise, as for G that does not divide C and an unknown act).  y must not
+ * overlap an input.  float32 arithmetic, rounded once.
+ */
+int wkv_group_norm(int64_t rows, int64_t C, int64_t G, int dtype, int act, float eps,
+                   const void* x, const float* weight, const float* bias, const void* gate,
+                   void* y, cudaStream_t stream);
+
+/*
+ * wkv_group_norm_backward -- gradients of wkv_group_norm given dy (rows, C):
+ * dx (and dgate, exactly when gate is given) in dtype, dweight and dbias (C,)
+ * float32 sums over the rows in a fixed order, each NULL if not wanted.  The
+ * workspace (256-byte aligned, uninitialised, _workspace_bytes()) is needed
+ * for dweight or dbias only.  No output may overlap anything else.
+ */
+size_t wkv_group_norm_backward_workspace_bytes(int64_t rows, int64_t C, int64_t G, int dtype);
+int wkv_group_norm_backward(int64_t rows, int64_t C, int64_t G, int dtype, int act, float eps,
+                            const void* x, const float* weight, const float* bias, const void* gate,
+                            const void* dy, void* dx, float* dweight, float* dbias, void* dgate,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -14,6 +14,7 @@ Two layers:
   ``data_ptr()`` values and the current stream, and raise ``WkvError`` on a
   non-zero status.
 """
+import contextlib
 import ctypes
 import functools
 import os
@@ -33,7 +34,9 @@ STATUS = {
 EXPORTS = ("wkv_forward", "wkv_forward_ex", "wkv_forward_workspace_bytes", "wkv_workspace_init", "wkv_workspace_status",
            "wkv_step", "wkv_forward_noalloc", "wkv_forward_noalloc_scratch_bytes", "wkv_forward_noalloc_status",
            "wkv_backward", "wkv_state", "wkv_state_combine", "wkv5_forward",
-           "wkv_backward_workspace_bytes", "wkv_token_shift", "wkv_strerror", "wkv_last_cuda_error",
+           "wkv_backward_workspace_bytes", "wkv_token_shift", "wkv_delta_forward", "wkv_delta_step",
+           "wkv_delta_backward", "wkv_delta_backward_workspace_bytes", "wkv_group_norm", "wkv_group_norm_backward",
+           "wkv_group_norm_backward_workspace_bytes", "wkv_strerror", "wkv_last_cuda_error",
            "wkv_abi_version")
 
 _lib = None
@@ -94,6 +97,20 @@ def lib():
         L.wkv_backward.restype = i32
         L.wkv_backward_workspace_bytes.argtypes = [i64, i64, i64, i32]
         L.wkv_backward_workspace_bytes.restype = sz
+        L.wkv_delta_forward.argtypes = [i64] * 5 + [i32] + [vp] * 9
+        L.wkv_delta_forward.restype = i32
+        L.wkv_delta_step.argtypes = [i64] * 5 + [i32] + [vp] * 8
+        L.wkv_delta_step.restype = i32
+        L.wkv_delta_backward.argtypes = [i64] * 5 + [i32] + [vp] * 15 + [sz, vp]
+        L.wkv_delta_backward.restype = i32
+        L.wkv_delta_backward_workspace_bytes.argtypes = [i64] * 4
+        L.wkv_delta_backward_workspace_bytes.restype = sz
+        L.wkv_group_norm.argtypes = [i64] * 3 + [i32, i32, ctypes.c_float] + [vp] * 6
+        L.wkv_group_norm.restype = i32
+        L.wkv_group_norm_backward.argtypes = [i64] * 3 + [i32, i32, ctypes.c_float] + [vp] * 10 + [sz, vp]
+        L.wkv_group_norm_backward.restype = i32
+        L.wkv_group_norm_backward_workspace_bytes.argtypes = [i64] * 3 + [i32]
+        L.wkv_group_norm_backward_workspace_bytes.restype = sz
         L.wkv_strerror.argtypes = [i32]
         L.wkv_strerror.restype = ctypes.c_char_p
         L.wkv_last_cuda_error.argtypes = []
@@ -487,3 +504,206 @@ def wkv_step(w, u, k, v, state, r=None, *, y=None, stream=None):
     _check(lib().wkv_step(Lr, B, C, code, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(r), _ptr(state), _ptr(y),
                           _stream_ptr(stream, dev)), "wkv_step")
     return y
+
+
+def _on_device(dev):
+    """Context in which `dev` is the current device (the library launches on
+    the current one)."""
+    torch = _torch()
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _delta_sizes(k, v, H, where):
+    """(lead sizes, Hk, N) of k (., ., Hk * N) and v (., ., H * N)."""
+    if k.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"{where}: k and v must have three dimensions")
+    if H <= 0 or v.shape[2] % H != 0 or v.shape[2] == 0:
+        raise ValueError(f"{where}: v's {v.shape[2]} channels are not {H} heads")
+    N = v.shape[2] // H
+    if k.shape[2] % N != 0 or k.shape[2] == 0 or H % (k.shape[2] // N) != 0:
+        raise ValueError(f"{where}: k's {k.shape[2]} channels are not heads of {N} that {H} value heads share evenly")
+    if k.device.type != "cuda":
+        raise ValueError(f"{where} runs on CUDA tensors only")
+    return v.shape[0], v.shape[1], k.shape[2] // N, N
+
+
+def wkv_delta_forward(w, beta, r, k, v, H, state_in=None, *, y=None, state_out=None, want_state=True, stream=None):
+    """Gated delta rule over one chunk.  r, k: (B, T, Hk * N), v: (B, T, H * N)
+    float32 or bfloat16 CUDA tensors, N in {32, 64, 128} and H a multiple of
+    Hk (value head h takes key head h // (H // Hk)); w (decay rates, inf
+    forgets the state), beta: (B, T, H) float32; state_in: (B, H, N, N)
+    float32 or None (zeros).  Per head
+        e_t = v_t - exp(-w_t) S^T k_t,  S <- exp(-w_t) S + beta_t k_t e_t^T,  y_t = S^T r_t.
+    Returns (y, state_out); state_out may be state_in."""
+    torch = _torch()
+    B, T, Hk, N = _delta_sizes(k, v, H, "wkv_delta_forward")
+    dev, code = k.device, _dtype_code(k)
+    for t, name in ((r, "r"), (k, "k")):
+        _need(t, name, (B, T, Hk * N), k.dtype, dev)
+    _need(v, "v", (B, T, H * N), k.dtype, dev)
+    for t, name in ((w, "w"), (beta, "beta")):
+        _need(t, name, (B, T, H), torch.float32, dev)
+    _need(state_in, "state_in", (B, H, N, N), torch.float32, dev)
+    if y is None:
+        y = torch.empty((B, T, H * N), dtype=k.dtype, device=dev)
+    _need(y, "y", (B, T, H * N), k.dtype, dev)
+    if state_out is None and want_state:
+        state_out = torch.empty((B, H, N, N), dtype=torch.float32, device=dev)
+    _need(state_out, "state_out", (B, H, N, N), torch.float32, dev)
+    with _on_device(dev):
+        _check(lib().wkv_delta_forward(B, T, Hk, H, N, code, _ptr(w), _ptr(beta), _ptr(r), _ptr(k), _ptr(v),
+                                       _ptr(state_in), _ptr(y), _ptr(state_out), _stream_ptr(stream, dev)),
+               "wkv_delta_forward")
+    return y, state_out
+
+
+def wkv_delta_step(w, beta, r, k, v, state, *, y=None, stream=None):
+    """Gated delta rule, one token for L layers of B sequences: r, k
+    (L, B, Hk * N), v (L, B, H * N), w, beta (L, B, H) float32, state
+    (L, B, H, N, N) float32 updated in place.  Returns y (L, B, H * N)."""
+    torch = _torch()
+    if state.dim() != 5:
+        raise ValueError("state must be (L, B, H, N, N)")
+    H = state.shape[2]
+    Lr, B, Hk, N = _delta_sizes(k, v, H, "wkv_delta_step")
+    dev, code = k.device, _dtype_code(k)
+    for t, name in ((r, "r"), (k, "k")):
+        _need(t, name, (Lr, B, Hk * N), k.dtype, dev)
+    _need(v, "v", (Lr, B, H * N), k.dtype, dev)
+    for t, name in ((w, "w"), (beta, "beta")):
+        _need(t, name, (Lr, B, H), torch.float32, dev)
+    _need(state, "state", (Lr, B, H, N, N), torch.float32, dev)
+    if y is None:
+        y = torch.empty((Lr, B, H * N), dtype=k.dtype, device=dev)
+    _need(y, "y", (Lr, B, H * N), k.dtype, dev)
+    with _on_device(dev):
+        _check(lib().wkv_delta_step(Lr, B, Hk, H, N, code, _ptr(w), _ptr(beta), _ptr(r), _ptr(k), _ptr(v), _ptr(state),
+                                    _ptr(y), _stream_ptr(stream, dev)), "wkv_delta_step")
+    return y
+
+
+def _scratch(nbytes, workspace, dev, stream):
+    """(pointer, bytes, owner) of `nbytes` of scratch that needs no clearing:
+    the caller's Workspace, or memory of the current stream's pool that goes
+    back to it when the call's kernels are queued."""
+    if nbytes == 0:
+        return None, 0, None
+    if workspace is not None:
+        return (*workspace.get(nbytes, stream), None)
+    torch = _torch()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return buf.data_ptr(), nbytes, buf
+
+
+def wkv_delta_backward(w, beta, r, k, v, H, state_in=None, *, dy, dstate_out=None, dr=None, dk=None, dv=None, dw=None,
+                       dbeta=None, dstate_in=None, want_dstate_in=True, workspace: Workspace = None, stream=None):
+    """Gradients of wkv_delta_forward.  dy: (B, T, H * N) like v; dstate_out:
+    (B, H, N, N) float32, the gradient of the returned state, or None.
+    Returns (dr, dk, dv, dw, dbeta, dstate_in); dr and dk are summed over the
+    value heads that share a key head, dw and dbeta are (B, T, H) float32."""
+    torch = _torch()
+    B, T, Hk, N = _delta_sizes(k, v, H, "wkv_delta_backward")
+    dev, code = k.device, _dtype_code(k)
+    empty = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+    f32 = torch.float32
+    dr = empty((B, T, Hk * N), k.dtype) if dr is None else dr
+    dk = empty((B, T, Hk * N), k.dtype) if dk is None else dk
+    dv = empty((B, T, H * N), k.dtype) if dv is None else dv
+    dw = empty((B, T, H), f32) if dw is None else dw
+    dbeta = empty((B, T, H), f32) if dbeta is None else dbeta
+    if dstate_in is None and want_dstate_in:
+        dstate_in = empty((B, H, N, N), f32)
+    for t, name in ((r, "r"), (k, "k"), (dr, "dr"), (dk, "dk")):
+        _need(t, name, (B, T, Hk * N), k.dtype, dev)
+    for t, name in ((v, "v"), (dy, "dy"), (dv, "dv")):
+        _need(t, name, (B, T, H * N), k.dtype, dev)
+    for t, name in ((w, "w"), (beta, "beta"), (dw, "dw"), (dbeta, "dbeta")):
+        _need(t, name, (B, T, H), f32, dev)
+    for t, name in ((state_in, "state_in"), (dstate_out, "dstate_out"), (dstate_in, "dstate_in")):
+        _need(t, name, (B, H, N, N), f32, dev)
+    with _on_device(dev):
+        nbytes = int(lib().wkv_delta_backward_workspace_bytes(B, T, H, N))
+        ws_ptr, ws_bytes, owner = _scratch(nbytes, workspace, dev, stream)
+        _check(lib().wkv_delta_backward(B, T, Hk, H, N, code, _ptr(w), _ptr(beta), _ptr(r), _ptr(k), _ptr(v),
+                                        _ptr(state_in), _ptr(dy), _ptr(dstate_out), _ptr(dr), _ptr(dk), _ptr(dv),
+                                        _ptr(dw), _ptr(dbeta), _ptr(dstate_in), ws_ptr, ws_bytes,
+                                        _stream_ptr(stream, dev)), "wkv_delta_backward")
+    return dr, dk, dv, dw, dbeta, dstate_in
+
+
+_ACTS = {"none": 0, "silu": 1, "sigmoid": 2}
+
+
+def _norm_args(x, G, weight, bias, gate, act, where):
+    torch = _torch()
+    if x.dim() < 1 or G <= 0 or x.shape[-1] % G != 0:
+        raise ValueError(f"{where}: x's channels are not {G} groups")
+    if act not in _ACTS:
+        raise ValueError(f"{where}: act must be one of {sorted(_ACTS)}")
+    if x.device.type != "cuda":
+        raise ValueError(f"{where} runs on CUDA tensors only")
+    C = x.shape[-1]
+    _need(x, "x", x.shape, x.dtype, x.device)
+    _need(gate, "gate", x.shape, x.dtype, x.device)
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        _need(t, name, (C,), torch.float32, x.device)
+    rows = 1
+    for n in x.shape[:-1]:
+        rows *= n
+    return rows, C, x.device, _dtype_code(x)
+
+
+def wkv_group_norm(x, G, weight=None, bias=None, gate=None, *, act="none", eps=1e-5, y=None, stream=None):
+    """Group norm with an activation, channels last: x (..., C) float32 or
+    bfloat16, each token's channels in G groups normalised by their own mean
+    and variance, z = weight * hat + bias (weight, bias (C,) float32 or None);
+    y = act(z), or z * act(gate) with a gate like x.  act: "none", "silu" or
+    "sigmoid".  Returns y."""
+    rows, C, dev, code = _norm_args(x, G, weight, bias, gate, act, "wkv_group_norm")
+    if y is None:
+        y = _torch().empty(x.shape, dtype=x.dtype, device=dev)
+    _need(y, "y", x.shape, x.dtype, dev)
+    with _on_device(dev):
+        _check(lib().wkv_group_norm(rows, C, G, code, _ACTS[act], eps, _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate),
+                                    _ptr(y), _stream_ptr(stream, dev)), "wkv_group_norm")
+    return y
+
+
+def wkv_group_norm_backward(x, G, weight=None, bias=None, gate=None, *, dy, act="none", eps=1e-5, dx=None, dweight=None,
+                            dbias=None, dgate=None, workspace: Workspace = None, stream=None):
+    """Gradients of wkv_group_norm: (dx, dweight, dbias, dgate), dweight and
+    dbias (C,) float32 sums over the tokens; the gradient of an argument that
+    is None is None."""
+    torch = _torch()
+    rows, C, dev, code = _norm_args(x, G, weight, bias, gate, act, "wkv_group_norm_backward")
+    _need(dy, "dy", x.shape, x.dtype, dev)
+    for t, g, name in ((weight, dweight, "dweight"), (bias, dbias, "dbias"), (gate, dgate, "dgate")):
+        if t is None and g is not None:
+            raise ValueError(f"{name}: there is no {name[1:]}")
+    if dx is None:
+        dx = torch.empty_like(x)
+    if gate is not None and dgate is None:
+        dgate = torch.empty_like(x)
+    if weight is not None and dweight is None:
+        dweight = torch.empty((C,), dtype=torch.float32, device=dev)
+    if bias is not None and dbias is None:
+        dbias = torch.empty((C,), dtype=torch.float32, device=dev)
+    _need(dx, "dx", x.shape, x.dtype, dev)
+    _need(dgate, "dgate", x.shape, x.dtype, dev)
+    for t, name in ((dweight, "dweight"), (dbias, "dbias")):
+        _need(t, name, (C,), torch.float32, dev)
+    with _on_device(dev):
+        nbytes = 0
+        if weight is not None or bias is not None:
+            nbytes = int(lib().wkv_group_norm_backward_workspace_bytes(rows, C, G, code))
+        ws_ptr, ws_bytes, owner = _scratch(nbytes, workspace, dev, stream)
+        _check(lib().wkv_group_norm_backward(rows, C, G, code, _ACTS[act], eps, _ptr(x), _ptr(weight), _ptr(bias),
+                                             _ptr(gate), _ptr(dy), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(dgate),
+                                             ws_ptr, ws_bytes, _stream_ptr(stream, dev)), "wkv_group_norm_backward")
+    return dx, dweight, dbias, dgate

@@ -7,12 +7,13 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libwkv.so")
-SOURCES = [os.path.join(CSRC, "wkv_api.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("wkv_api.cu", "wkv_delta.cu", "wkv_norm.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + \
     [os.path.join(ROOT, "include", "wkv.h")]
 
@@ -24,9 +25,9 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA 12.9 toolkit is required to build libwkv.so")
 
 
-def build_command(out: str, extra=()):
+def compile_command(src: str, out: str, extra=()):
     return [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-std=c++17", "-lineinfo",
-            "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-warn-spills", *extra, "-o", out, *SOURCES]
+            "-Xcompiler", "-fPIC", "-Xptxas", "-warn-spills", *extra, "-c", "-o", out, src]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -36,8 +37,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if all(os.path.getmtime(p) <= t for p in DEPENDS):
             return LIB
     tmp = LIB + ".tmp"
-    cmd = build_command(tmp, ("-Xptxas", "-v") if verbose else ())
-    subprocess.run(cmd, check=True)
+    extra = ("-Xptxas", "-v") if verbose else ()
+    with tempfile.TemporaryDirectory() as work:
+        objs = [os.path.join(work, os.path.basename(src) + ".o") for src in SOURCES]
+        jobs = [subprocess.Popen(compile_command(src, obj, extra)) for src, obj in zip(SOURCES, objs)]
+        for src, job in zip(SOURCES, jobs):
+            if job.wait() != 0:
+                raise subprocess.CalledProcessError(job.returncode, compile_command(src, "-"))
+        subprocess.run([nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
     return LIB
 

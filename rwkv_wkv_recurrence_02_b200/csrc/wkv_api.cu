@@ -13,6 +13,7 @@
 #include <mutex>
 
 #include "../../include/wkv.h"
+#include "wkv_host.cuh"
 #include "wkv_chunk.cuh"
 #include "wkv_lane.cuh"
 #include "wkv_part.cuh"
@@ -27,10 +28,8 @@
 
 namespace {
 
-thread_local char g_last_cuda_error[256] = "";
+using namespace wkv::host;
 
-constexpr int64_t kMaxElems = int64_t(1) << 62;
-constexpr int kMaxDevices = 64;
 int g_sm_count[kMaxDevices] = {0};
 
 // Register-load look-back kernel: W compute warps per CTA, LS tokens per warp
@@ -108,34 +107,6 @@ uint64_t wait_limit_ns() {
     }();
     return v;
 }
-
-int record_cuda(cudaError_t e) {
-    if (e == cudaSuccess) return WKV_OK;
-    std::snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "%s: %s", cudaGetErrorName(e),
-                  cudaGetErrorString(e));
-    return WKV_ERR_CUDA;
-}
-
-int check_launch() { return record_cuda(cudaPeekAtLastError()); }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// [p, p+bytes) intersects [q, q+qbytes)?
-bool overlaps(const void* p, size_t bytes, const void* q, size_t qbytes) {
-    if (p == nullptr || q == nullptr || bytes == 0 || qbytes == 0) return false;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return a < b + qbytes && b < a + bytes;
-}
-
-bool mul_ok(int64_t a, int64_t b, int64_t c, int64_t* out) {
-    if (a < 0 || b < 0 || c < 0) return false;
-    __int128 p = static_cast<__int128>(a) * b * c;
-    if (p >= kMaxElems) return false;
-    *out = static_cast<int64_t>(p);
-    return true;
-}
-
-size_t elem_bytes(int dtype) { return dtype == WKV_BF16 ? 2 : 4; }
 
 struct ChunkGeom {
     int64_t nCB, nLB, nchunks, units;

@@ -1,0 +1,250 @@
+// wkv_delta.cu -- host side of the gated delta rule's entry points
+// (wkv_delta_forward, wkv_delta_step, wkv_delta_backward): argument checks,
+// the workspace's layout and the launches.
+#include "wkv_delta.cuh"
+#include "wkv_host.cuh"
+
+namespace {
+
+using namespace wkv::host;
+namespace d = wkv::delta;
+
+// A walk's shape for each head size: RG lanes along the reduction axis, CC
+// lines a lane, NW warps a CTA, TB tokens a block.
+template <int N>
+struct Cfg;
+template <>
+struct Cfg<32> {
+    static constexpr int RG = 4, CC = 2, NW = 2, TB = 16;
+};
+template <>
+struct Cfg<64> {
+    static constexpr int RG = 4, CC = 2, NW = 4, TB = 16;
+};
+template <>
+struct Cfg<128> {
+    static constexpr int RG = 8, CC = 4, NW = 4, TB = 8;
+};
+
+template <typename IO, int N, bool WANT_Y>
+int launch_forward(const d::Args& a, cudaStream_t st) {
+    using C = Cfg<N>;
+    using G = d::ForwardShape<IO, N, C::RG, C::CC, C::NW, C::TB, WANT_Y>;
+    auto kern = d::delta_forward_kernel<IO, N, C::RG, C::CC, C::NW, C::TB, WANT_Y>;
+    static bool ready[kMaxDevices] = {false};
+    const int rc = allow_smem(kern, G::SMEM, ready);
+    return rc != WKV_OK ? rc : launch(kern, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, st, a);
+}
+
+template <typename IO, int N>
+int launch_reverse(const d::Args& a, cudaStream_t st) {
+    using C = Cfg<N>;
+    using G = d::ReverseShape<IO, N, C::RG, C::CC, C::NW, C::TB>;
+    auto kern = d::delta_reverse_kernel<IO, N, C::RG, C::CC, C::NW, C::TB>;
+    static bool ready[kMaxDevices] = {false};
+    const int rc = allow_smem(kern, G::SMEM, ready);
+    return rc != WKV_OK ? rc : launch(kern, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, st, a);
+}
+
+template <typename IO, int N>
+int launch_rows(const d::Args& a, bool grad, cudaStream_t st) {
+    using C = Cfg<N>;
+    using G = d::RowShape<IO, N, C::RG, C::CC, C::NW, C::TB>;
+    if (!grad) {
+        auto kern = d::delta_state_rows_kernel<IO, N, C::RG, C::CC, C::NW, C::TB>;
+        static bool ready[kMaxDevices] = {false};
+        const int rc = allow_smem(kern, G::SMEM, ready);
+        return rc != WKV_OK ? rc : launch(kern, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, st, a);
+    }
+    auto kern = d::delta_grad_rows_kernel<IO, N, C::RG, C::CC, C::NW, C::TB>;
+    static bool ready[kMaxDevices] = {false};
+    const int rc = allow_smem(kern, G::SMEM, ready);
+    return rc != WKV_OK ? rc : launch(kern, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, st, a);
+}
+
+template <int N>
+constexpr int slots() {
+    return N / d::Tile<N, Cfg<N>::RG, Cfg<N>::CC>::CW;
+}
+
+struct Layout {
+    size_t e, du, dr, dk, dk2, check, phi, term, bytes;
+};
+
+Layout layout(int64_t B, int64_t T, int64_t H, int64_t N) {
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    const size_t val = up(size_t(B) * T * H * N * 4), heads = size_t(B) * H;
+    const size_t chunks = size_t((T + d::kCheck - 1) / d::kCheck) + 1;
+    const size_t slot = N == 32 ? slots<32>() : N == 64 ? slots<64>() : slots<128>();
+    Layout l{};
+    l.e = 0;
+    l.du = l.e + val;
+    l.dr = l.du + val;
+    l.dk = l.dr + val;
+    l.dk2 = l.dk + val;
+    l.check = l.dk2 + val;
+    l.phi = l.check + up(heads * chunks * N * N * 4);
+    l.term = l.phi + up(heads * chunks * slot * 4);
+    l.bytes = l.term + up(heads * T * 4);
+    return l;
+}
+
+template <typename IO, int N>
+int run_backward(d::Args& a, void* dr, void* dk, float* dw, float* dbeta, float* term, cudaStream_t st) {
+    int rc = launch_forward<IO, N, false>(a, st);
+    if (rc == WKV_OK) rc = launch_reverse<IO, N>(a, st);
+    if (rc == WKV_OK) rc = launch_rows<IO, N>(a, false, st);
+    if (rc == WKV_OK) rc = launch_rows<IO, N>(a, true, st);
+    if (rc == WKV_OK)
+        rc = launch(d::delta_tokens_kernel<IO, N>, (a.B * a.T * a.Hk + 7) / 8, 256, 0, st, a, static_cast<IO*>(dr),
+                    static_cast<IO*>(dk), dbeta, term);
+    if (rc == WKV_OK) {
+        const int64_t n = a.B * ((a.T + d::kCheck - 1) / d::kCheck) * a.H;
+        rc = launch(d::delta_dw_kernel<slots<N>()>, (n + 127) / 128, 128, 0, st, a, term, dw);
+    }
+    return rc;
+}
+
+template <typename IO, int N>
+int run_step(int64_t heads, int64_t Hk, int64_t H, const float* w, const float* beta, const void* r, const void* k,
+             const void* v, float* state, void* y, cudaStream_t st) {
+    constexpr int CL = N == 128 ? 4 : 8, NW = 4, PARTS = N / (CL * 4);
+    return launch(d::delta_step_kernel<IO, N, CL, NW>, (heads * PARTS + NW - 1) / NW, NW * 32, 0, st, heads, Hk, H, w,
+                  beta, static_cast<const IO*>(r), static_cast<const IO*>(k), static_cast<const IO*>(v), state,
+                  static_cast<IO*>(y), aligned(state, 16));
+}
+
+// sizes: the counts of keys, values, per-head scalars and states, or an error
+struct Sizes {
+    int64_t keys, values, scalars, states;
+};
+int sizes(int64_t lead0, int64_t lead1, int64_t nstates, int64_t Hk, int64_t H, int64_t N, Sizes* s) {
+    if (lead0 < 0 || lead1 < 0 || nstates < 0 || (N != 32 && N != 64 && N != 128) || Hk <= 0 || H <= 0 || H % Hk != 0)
+        return WKV_ERR_SHAPE;
+    int64_t tokens = 0, hn = 0;
+    if (!mul_ok(lead0, lead1, 1, &tokens) || !mul_ok(H, N, 1, &hn)) return WKV_ERR_SHAPE;
+    if (!mul_ok(tokens, hn, 8, &s->values) || !mul_ok(nstates, hn, N * 8, &s->states)) return WKV_ERR_SHAPE;
+    s->values /= 8;
+    s->states /= 8;
+    s->keys = tokens * Hk * N;
+    s->scalars = tokens * H;
+    return WKV_OK;
+}
+
+// f(type tag, head size) for the call's type and head size
+template <typename F>
+int with_type(int dtype, int64_t N, F f) {
+    auto pick = [&](auto tag) {
+        if (N == 32) return f(tag, std::integral_constant<int, 32>{});
+        if (N == 64) return f(tag, std::integral_constant<int, 64>{});
+        return f(tag, std::integral_constant<int, 128>{});
+    };
+    return dtype == WKV_F32 ? pick(float{}) : pick(__nv_bfloat16{});
+}
+
+// the state passed through when there is no token
+int pass_state(const float* in, float* out, size_t bytes, cudaStream_t st) {
+    if (out == nullptr || out == in || bytes == 0) return WKV_OK;
+    if (!aligned(out, 4) || !aligned(in, 4)) return WKV_ERR_ALIGN;
+    if (overlaps(in, bytes, out, bytes)) return WKV_ERR_ALIAS;
+    if (in) return record_cuda(cudaMemcpyAsync(out, in, bytes, cudaMemcpyDeviceToDevice, st));
+    return record_cuda(cudaMemsetAsync(out, 0, bytes, st));
+}
+
+}  // namespace
+
+extern "C" {
+
+int wkv_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int dtype, const float* w,
+                      const float* beta, const void* r, const void* k, const void* v, const float* state_in, void* y,
+                      float* state_out, cudaStream_t stream) {
+    if (dtype != WKV_F32 && dtype != WKV_BF16) return WKV_ERR_DTYPE;
+    Sizes n{};
+    int rc = sizes(B, T, B, Hk, H, N, &n);
+    if (rc != WKV_OK) return rc;
+    if (B == 0) return WKV_OK;
+    const size_t eb = elem_bytes(dtype), sb = size_t(n.states) * 4;
+    if (T == 0) return pass_state(state_in, state_out, sb, stream);
+    if (!w || !beta || !r || !k || !v || !y) return WKV_ERR_NULLPTR;
+    const Span ins[] = {{w, size_t(n.scalars) * 4, 4}, {beta, size_t(n.scalars) * 4, 4}, {r, size_t(n.keys) * eb, eb},
+                        {k, size_t(n.keys) * eb, eb}, {v, size_t(n.values) * eb, eb},
+                        {state_in == state_out ? nullptr : state_in, sb, 4}};
+    const Span outs[] = {{y, size_t(n.values) * eb, eb}, {state_out, sb, 4}};
+    rc = check_spans(ins, outs);
+    if (rc != WKV_OK) return rc;
+    d::Args a{};
+    a.B = B, a.T = T, a.Hk = Hk, a.H = H;
+    a.w = w, a.beta = beta, a.r = r, a.k = k, a.v = v, a.s_in = state_in, a.y = y, a.s_out = state_out;
+    a.vec = aligned(r, 16) && aligned(k, 16) && aligned(v, 16);
+    rc = with_type(dtype, N, [&](auto tag, auto size) {
+        return launch_forward<decltype(tag), decltype(size)::value, true>(a, stream);
+    });
+    return rc != WKV_OK ? rc : check_launch();
+}
+
+int wkv_delta_step(int64_t L, int64_t B, int64_t Hk, int64_t H, int64_t N, int dtype, const float* w,
+                   const float* beta, const void* r, const void* k, const void* v, float* state, void* y,
+                   cudaStream_t stream) {
+    if (dtype != WKV_F32 && dtype != WKV_BF16) return WKV_ERR_DTYPE;
+    Sizes n{};
+    int rc = sizes(L, B, L >= 0 && B >= 0 && L < (int64_t(1) << 31) && B < (int64_t(1) << 31) ? L * B : -1, Hk, H, N, &n);
+    if (rc != WKV_OK) return rc;
+    if (L == 0 || B == 0) return WKV_OK;
+    if (!w || !beta || !r || !k || !v || !state || !y) return WKV_ERR_NULLPTR;
+    const size_t eb = elem_bytes(dtype);
+    const Span ins[] = {{w, size_t(n.scalars) * 4, 4}, {beta, size_t(n.scalars) * 4, 4}, {r, size_t(n.keys) * eb, eb},
+                        {k, size_t(n.keys) * eb, eb}, {v, size_t(n.values) * eb, eb}};
+    const Span outs[] = {{y, size_t(n.values) * eb, eb}, {state, size_t(n.states) * 4, 4}};
+    rc = check_spans(ins, outs);
+    if (rc != WKV_OK) return rc;
+    rc = with_type(dtype, N, [&](auto tag, auto size) {
+        return run_step<decltype(tag), decltype(size)::value>(L * B * H, Hk, H, w, beta, r, k, v, state, y, stream);
+    });
+    return rc != WKV_OK ? rc : check_launch();
+}
+
+size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t N) {
+    Sizes n{};
+    if (sizes(B, T, B, 1, H, N, &n) != WKV_OK || B == 0 || T == 0) return 0;
+    return layout(B, T, H, N).bytes;
+}
+
+int wkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int dtype, const float* w,
+                       const float* beta, const void* r, const void* k, const void* v, const float* state_in,
+                       const void* dy, const float* dstate_out, void* dr, void* dk, void* dv, float* dw, float* dbeta,
+                       float* dstate_in, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (dtype != WKV_F32 && dtype != WKV_BF16) return WKV_ERR_DTYPE;
+    Sizes n{};
+    int rc = sizes(B, T, B, Hk, H, N, &n);
+    if (rc != WKV_OK) return rc;
+    if (B == 0) return WKV_OK;
+    const size_t eb = elem_bytes(dtype), sb = size_t(n.states) * 4;
+    if (T == 0) {
+        if (dstate_in == dstate_out && dstate_in != nullptr) return WKV_ERR_ALIAS;
+        return pass_state(dstate_out, dstate_in, sb, stream);
+    }
+    if (!w || !beta || !r || !k || !v || !dy || !dr || !dk || !dv || !dw || !dbeta) return WKV_ERR_NULLPTR;
+    const Layout l = layout(B, T, H, N);
+    if (workspace == nullptr || workspace_bytes < l.bytes) return WKV_ERR_WORKSPACE;
+    const size_t kb = size_t(n.keys) * eb, vb = size_t(n.values) * eb, pb = size_t(n.scalars) * 4;
+    const Span ins[] = {{w, pb, 4}, {beta, pb, 4}, {r, kb, eb}, {k, kb, eb}, {v, vb, eb}, {state_in, sb, 4},
+                        {dy, vb, eb}, {dstate_out, sb, 4}};
+    const Span outs[] = {{dr, kb, eb}, {dk, kb, eb}, {dv, vb, eb}, {dw, pb, 4}, {dbeta, pb, 4}, {dstate_in, sb, 4},
+                         {workspace, l.bytes, 256}};
+    rc = check_spans(ins, outs);
+    if (rc != WKV_OK) return rc;
+    char* ws = static_cast<char*>(workspace);
+    auto f = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+    d::Args a{};
+    a.B = B, a.T = T, a.Hk = Hk, a.H = H;
+    a.w = w, a.beta = beta, a.r = r, a.k = k, a.v = v, a.dy = dy, a.s_in = state_in, a.ds_out = dstate_out;
+    a.dv = dv, a.ds_in = dstate_in;
+    a.e = f(l.e), a.du = f(l.du), a.dr = f(l.dr), a.dk = f(l.dk), a.dk2 = f(l.dk2), a.check = f(l.check), a.phi = f(l.phi);
+    a.vec = aligned(r, 16) && aligned(k, 16) && aligned(v, 16) && aligned(dy, 16);
+    rc = with_type(dtype, N, [&](auto tag, auto size) {
+        return run_backward<decltype(tag), decltype(size)::value>(a, dr, dk, dw, dbeta, f(l.term), stream);
+    });
+    return rc != WKV_OK ? rc : check_launch();
+}
+
+}  // extern "C"

@@ -1,0 +1,440 @@
+// wkv_norm.cuh -- group norm with an activation, channels last, forward and
+// reverse: every token's channels in G groups (the heads of the matrix-state
+// operators), each normalised by its own mean and variance.
+//
+//   hat = (x - mean) / sqrt(var + eps),  z = weight * hat + bias
+//   y = act(z) without a gate, z * act(gate) with one
+//
+// A lane holds V vectors of PER channels of one group, LPG lanes a group (a
+// power of two, the lanes behind the group's last channel idle), and keeps
+// its channels over `span` tokens, so weight and bias stay in registers and
+// the reverse mode sums dweight and dbias there.  Mean and variance are two
+// passes over registers: x is read once.  Bound by memory: the rows of
+// kUnroll tokens are in flight at once.
+#pragma once
+
+#include "wkv_common.cuh"
+
+namespace wkv {
+namespace norm {
+
+enum Act { kNone = 0, kSilu = 1, kSigmoid = 2 };
+
+struct Args {
+    int64_t rows, C;
+    int group, lpg, lpg_log2;   // channels of a group, lanes of a group
+    int64_t slots;              // lanes of a row, in whole warps
+    int span;                   // rows a lane takes
+    int act;
+    float eps, inv_group;
+    const void* x;
+    const void* gate;
+    const float* weight;
+    const float* bias;
+    const void* dy;
+    void* y;
+    void* dx;
+    void* dgate;
+    float* part;                // (chunks, 2, C) partial dweight, dbias or NULL
+};
+
+template <typename IO, int PER>
+struct Pack {
+    static_assert(PER * sizeof(IO) <= 16, "one access");
+    static constexpr int WORDS = PER * int(sizeof(IO)) / 4 > 0 ? PER * int(sizeof(IO)) / 4 : 1;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const IO* p) {
+        if constexpr (PER * sizeof(IO) == 16) {
+            const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else if constexpr (PER * sizeof(IO) == 8) {
+            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
+            w[0] = v.x, w[1] = v.y;
+        } else if constexpr (PER * sizeof(IO) == 4) {
+            w[0] = __ldcs(reinterpret_cast<const unsigned int*>(p));
+        } else {
+            w[0] = __ldcs(reinterpret_cast<const unsigned short*>(p));
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(IO) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+    __device__ __forceinline__ void put(int i, float v) {
+        if constexpr (sizeof(IO) == 4) {
+            w[i] = __float_as_uint(v);
+        } else {
+            const uint32_t b = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            if (i % 2) w[i / 2] |= b << 16;   // after the even one
+            else w[i / 2] = b;
+        }
+    }
+    __device__ __forceinline__ void store(IO* p) const {
+        if constexpr (PER * sizeof(IO) == 16) __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+        else if constexpr (PER * sizeof(IO) == 8) __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
+        else if constexpr (PER * sizeof(IO) == 4) __stcs(reinterpret_cast<unsigned int*>(p), w[0]);
+        else *reinterpret_cast<unsigned short*>(p) = static_cast<unsigned short>(w[0]);
+    }
+};
+
+// 1 / (1 + e^-x): ex2 and rcp are within 2 ulp, the argument's rounding adds
+// |x| 2^-24 (the outputs' float32 bound is 2e-5)
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-x * kLog2e)); }
+__device__ __forceinline__ float act(int kind, float x) {
+    if (kind == kNone) return x;
+    const float s = sigmoid(x);
+    return kind == kSilu ? x * s : s;
+}
+// the activation and its slope
+__device__ __forceinline__ float act_slope(int kind, float x, float* slope) {
+    if (kind == kNone) {
+        *slope = 1.f;
+        return x;
+    }
+    const float s = sigmoid(x);
+    if (kind == kSilu) {
+        *slope = s * fmaf(x, 1.f - s, 1.f);
+        return x * s;
+    }
+    *slope = s * (1.f - s);
+    return s;
+}
+
+__device__ __forceinline__ float group_sum(float x, int lpg) {
+    for (int o = lpg / 2; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// a lane's place: its group's first channel, the offsets of its vectors
+template <int PER, int V>
+struct Place {
+    int64_t slot, chunk, c0;   // c0: the lane's first channel
+    int n;                     // vectors of it that exist
+    __device__ __forceinline__ Place(const Args& a) {
+        const int64_t id = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+        slot = id % a.slots;
+        chunk = id / a.slots;
+        const int l = int(slot) & (a.lpg - 1);
+        const int64_t grp = slot >> a.lpg_log2;
+        c0 = grp * a.group + int64_t(l) * PER;
+        const int vecs = a.group / PER;
+        n = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (l + v * a.lpg < vecs) n = v + 1;
+        if (grp * a.group >= a.C) n = 0;
+    }
+};
+
+template <typename IO, int PER, int V, int U, bool GATE>
+__global__ void __launch_bounds__(256) forward_kernel(const Args a) {
+    pdl_begin();
+    const Place<PER, V> at(a);
+    const int64_t r0 = at.chunk * a.span;
+    if (r0 >= a.rows) return;   // whole warps: slots is a multiple of 32
+    const int64_t r1 = r0 + a.span < a.rows ? r0 + a.span : a.rows;
+    const int step = a.lpg * PER;
+    float wt[V][PER], bs[V][PER];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int64_t c = at.c0 + v * step + i;
+            wt[v][i] = a.weight != nullptr && v < at.n ? __ldg(a.weight + c) : 1.f;
+            bs[v][i] = a.bias != nullptr && v < at.n ? __ldg(a.bias + c) : 0.f;
+        }
+    for (int64_t r = r0; r < r1; r += U) {
+        Pack<IO, PER> x[U][V], gt[U][V];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                x[u][v].clear();
+                if (r + u < r1 && v < at.n) {
+                    const int64_t off = (r + u) * a.C + at.c0 + v * step;
+                    x[u][v].load(static_cast<const IO*>(a.x) + off);
+                    if constexpr (GATE) gt[u][v].load(static_cast<const IO*>(a.gate) + off);
+                }
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (r + u >= r1) break;
+            float s = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int i = 0; i < PER; ++i) s += x[u][v].get(i);
+            const float mean = group_sum(s, a.lpg) * a.inv_group;
+            s = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (v < at.n)
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const float d = x[u][v].get(i) - mean;
+                        s = fmaf(d, d, s);
+                    }
+            const float inv = rsqrtf(fmaf(group_sum(s, a.lpg), a.inv_group, a.eps));
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (v < at.n) {
+                    Pack<IO, PER> o;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const float z = fmaf((x[u][v].get(i) - mean) * inv, wt[v][i], bs[v][i]);
+                        o.put(i, GATE ? z * act(a.act, gt[u][v].get(i)) : act(a.act, z));
+                    }
+                    o.store(static_cast<IO*>(a.y) + (r + u) * a.C + at.c0 + v * step);
+                }
+        }
+    }
+}
+
+// dz = dy act'(z) without a gate, dy act(gate) with one (dgate = dy z act'(gate));
+// dweight = sum dz hat, dbias = sum dz over the tokens;
+// dx = (h - mean(h) - hat mean(h hat)) / sqrt(var + eps), h = weight dz.
+template <typename IO, int PER, int V, int U, bool GATE>
+__global__ void __launch_bounds__(256) backward_kernel(const Args a) {
+    pdl_begin();
+    const Place<PER, V> at(a);
+    const int64_t r0 = at.chunk * a.span;
+    if (r0 >= a.rows) return;
+    const int64_t r1 = r0 + a.span < a.rows ? r0 + a.span : a.rows;
+    const int step = a.lpg * PER;
+    float wt[V][PER], bs[V][PER], dw[V][PER], db[V][PER];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int64_t c = at.c0 + v * step + i;
+            wt[v][i] = a.weight != nullptr && v < at.n ? __ldg(a.weight + c) : 1.f;
+            bs[v][i] = a.bias != nullptr && v < at.n ? __ldg(a.bias + c) : 0.f;
+            dw[v][i] = db[v][i] = 0.f;
+        }
+    for (int64_t r = r0; r < r1; r += U) {
+        Pack<IO, PER> x[U][V], gt[U][V], dy[U][V];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                x[u][v].clear();
+                dy[u][v].clear();
+                if (r + u < r1 && v < at.n) {
+                    const int64_t off = (r + u) * a.C + at.c0 + v * step;
+                    x[u][v].load(static_cast<const IO*>(a.x) + off);
+                    dy[u][v].load(static_cast<const IO*>(a.dy) + off);
+                    if constexpr (GATE) gt[u][v].load(static_cast<const IO*>(a.gate) + off);
+                }
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (r + u >= r1) break;
+            float s = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int i = 0; i < PER; ++i) s += x[u][v].get(i);
+            const float mean = group_sum(s, a.lpg) * a.inv_group;
+            s = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (v < at.n)
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const float d = x[u][v].get(i) - mean;
+                        s = fmaf(d, d, s);
+                    }
+            const float inv = rsqrtf(fmaf(group_sum(s, a.lpg), a.inv_group, a.eps));
+            float h1 = 0.f, h2 = 0.f;
+            float h[V][PER];
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (v < at.n) {
+                    Pack<IO, PER> o;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const float hat = (x[u][v].get(i) - mean) * inv;
+                        const float z = fmaf(hat, wt[v][i], bs[v][i]);
+                        const float g = dy[u][v].get(i);
+                        float slope, dz;
+                        if constexpr (GATE) {
+                            dz = g * act_slope(a.act, gt[u][v].get(i), &slope);
+                            o.put(i, g * z * slope);
+                        } else {
+                            act_slope(a.act, z, &slope);
+                            dz = g * slope;
+                        }
+                        dw[v][i] = fmaf(dz, hat, dw[v][i]);
+                        db[v][i] += dz;
+                        h[v][i] = wt[v][i] * dz;
+                        h1 += h[v][i];
+                        h2 = fmaf(h[v][i], hat, h2);
+                    }
+                    if constexpr (GATE) o.store(static_cast<IO*>(a.dgate) + (r + u) * a.C + at.c0 + v * step);
+                }
+            h1 = group_sum(h1, a.lpg) * a.inv_group;
+            h2 = group_sum(h2, a.lpg) * a.inv_group;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (v < at.n) {
+                    Pack<IO, PER> o;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const float hat = (x[u][v].get(i) - mean) * inv;
+                        o.put(i, inv * (h[v][i] - h1 - hat * h2));
+                    }
+                    o.store(static_cast<IO*>(a.dx) + (r + u) * a.C + at.c0 + v * step);
+                }
+        }
+    }
+    if (a.part != nullptr) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (v < at.n)
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int64_t c = at.c0 + v * step + i;
+                    a.part[(at.chunk * 2) * a.C + c] = dw[v][i];
+                    a.part[(at.chunk * 2 + 1) * a.C + c] = db[v][i];
+                }
+    }
+}
+
+// Groups too large for registers: one CTA per (token, group), the group read
+// again from the caches for each pass.
+__device__ __forceinline__ float block_sum(float x, float* sm) {
+    for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) sm[threadIdx.x / 32] = x;
+    __syncthreads();
+    x = 0.f;
+    for (int i = 0; i < int(blockDim.x) / 32; ++i) x += sm[i];
+    return x;
+}
+
+template <typename IO>
+__device__ __forceinline__ float at1(const void* p, int64_t i) {
+    if constexpr (sizeof(IO) == 4) return static_cast<const float*>(p)[i];
+    else return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+template <typename IO>
+__device__ __forceinline__ void put1(void* p, int64_t i, float v) {
+    if constexpr (sizeof(IO) == 4) static_cast<float*>(p)[i] = v;
+    else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+template <typename IO, bool BWD>
+__global__ void __launch_bounds__(256) large_kernel(const Args a, int64_t groups) {
+    __shared__ float sm[8];
+    pdl_begin();
+    for (int64_t id = blockIdx.x; id < a.rows * groups; id += gridDim.x) {
+        const int64_t r = id / groups, base = (id % groups) * a.group;
+        const int64_t off = r * a.C + base;
+        float s = 0.f;
+        for (int i = threadIdx.x; i < a.group; i += blockDim.x) s += at1<IO>(a.x, off + i);
+        const float mean = block_sum(s, sm) * a.inv_group;
+        s = 0.f;
+        for (int i = threadIdx.x; i < a.group; i += blockDim.x) {
+            const float d = at1<IO>(a.x, off + i) - mean;
+            s = fmaf(d, d, s);
+        }
+        const float inv = rsqrtf(fmaf(block_sum(s, sm), a.inv_group, a.eps));
+        float h1 = 0.f, h2 = 0.f;
+        for (int pass = 0; pass < (BWD ? 2 : 1); ++pass) {
+            for (int i = threadIdx.x; i < a.group; i += blockDim.x) {
+                const float wt = a.weight ? a.weight[base + i] : 1.f, bs = a.bias ? a.bias[base + i] : 0.f;
+                const float hat = (at1<IO>(a.x, off + i) - mean) * inv, z = fmaf(hat, wt, bs);
+                if constexpr (!BWD) {
+                    put1<IO>(a.y, off + i, a.gate ? z * act(a.act, at1<IO>(a.gate, off + i)) : act(a.act, z));
+                } else {
+                    const float g = at1<IO>(a.dy, off + i);
+                    float slope, dz;
+                    if (a.gate) {
+                        dz = g * act_slope(a.act, at1<IO>(a.gate, off + i), &slope);
+                        if (pass == 0) put1<IO>(a.dgate, off + i, g * z * slope);
+                    } else {
+                        act_slope(a.act, z, &slope);
+                        dz = g * slope;
+                    }
+                    const float h = wt * dz;
+                    if (pass == 0) {
+                        h1 += h;
+                        h2 = fmaf(h, hat, h2);
+                    } else {
+                        put1<IO>(a.dx, off + i, inv * (h - h1 - hat * h2));
+                    }
+                }
+            }
+            if (BWD && pass == 0) {
+                h1 = block_sum(h1, sm) * a.inv_group;
+                h2 = block_sum(h2, sm) * a.inv_group;
+            }
+        }
+        if constexpr (BWD) {
+            // per (token, group) statistics for the parameters' sums
+            if (threadIdx.x == 0 && a.part != nullptr) a.part[2 * id] = mean, a.part[2 * id + 1] = inv;
+        }
+    }
+}
+
+// dweight, dbias of large groups: each thread one channel over a chunk of
+// tokens, with the statistics that large_kernel left.
+template <typename IO>
+__global__ void __launch_bounds__(128) large_params_kernel(const Args a, int64_t groups, const float* __restrict__ stats,
+                                                           float* __restrict__ part, int64_t per) {
+    const int64_t c = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+    pdl_begin();
+    if (c >= a.C) return;
+    const float wt = a.weight ? a.weight[c] : 1.f, bs = a.bias ? a.bias[c] : 0.f;
+    const int64_t r0 = blockIdx.y * per, r1 = r0 + per < a.rows ? r0 + per : a.rows, grp = c / a.group;
+    float dw = 0.f, db = 0.f;
+    for (int64_t r = r0; r < r1; ++r) {
+        const float2 st = reinterpret_cast<const float2*>(stats)[r * groups + grp];
+        const float hat = (at1<IO>(a.x, r * a.C + c) - st.x) * st.y;
+        float slope, dz = at1<IO>(a.dy, r * a.C + c);
+        if (a.gate) {
+            dz *= act(a.act, at1<IO>(a.gate, r * a.C + c));
+        } else {
+            act_slope(a.act, fmaf(hat, wt, bs), &slope);
+            dz *= slope;
+        }
+        dw = fmaf(dz, hat, dw);
+        db += dz;
+    }
+    part[(int64_t(blockIdx.y) * 2) * a.C + c] = dw;
+    part[(int64_t(blockIdx.y) * 2 + 1) * a.C + c] = db;
+}
+
+// the chunks' partial sums, in a fixed order: 32 channels x 8 lanes of chunks
+__global__ void __launch_bounds__(256) params_kernel(int64_t C, int64_t chunks, const float* __restrict__ part,
+                                                     float* __restrict__ dweight, float* __restrict__ dbias) {
+    __shared__ float sm[2][8][33];
+    const int cx = threadIdx.x % 32, k = threadIdx.x / 32;
+    const int64_t c = int64_t(blockIdx.x) * 32 + cx;
+    pdl_begin();
+    float dw = 0.f, db = 0.f;
+    if (c < C) {
+#pragma unroll 4
+        for (int64_t i = k; i < chunks; i += 8) {
+            dw += part[2 * i * C + c];
+            db += part[(2 * i + 1) * C + c];
+        }
+    }
+    sm[0][k][cx] = dw;
+    sm[1][k][cx] = db;
+    __syncthreads();
+    if (k < 2 && c < C) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += sm[k][i][cx];
+        float* out = k == 0 ? dweight : dbias;
+        if (out != nullptr) out[c] = s;
+    }
+}
+
+}  // namespace norm
+}  // namespace wkv
