@@ -1,7 +1,7 @@
 // wkv_delta.cu -- host side of the gated delta rule's entry points
 // (wkv_delta_forward, wkv_delta_step, wkv_delta_backward): argument checks,
 // the workspace's layout and the launches.
-#include "wkv_delta.cuh"
+#include "wkv_delta_mma.cuh"
 #include "wkv_host.cuh"
 
 namespace {
@@ -26,14 +26,18 @@ struct Cfg<128> {
     static constexpr int RG = 8, CC = 4, NW = 4, TB = 8;
 };
 
-template <typename IO, int N, bool WANT_Y>
-int launch_forward(const d::Args& a, cudaStream_t st) {
-    using C = Cfg<N>;
-    using G = d::ForwardShape<IO, N, C::RG, C::CC, C::NW, C::TB, WANT_Y>;
-    auto kern = d::delta_forward_kernel<IO, N, C::RG, C::CC, C::NW, C::TB, WANT_Y>;
+template <typename IO, int N, int NW, bool WANT_Y>
+int launch_forward_nw(const d::Args& a, cudaStream_t st) {
+    using G = d::MmaForward<IO, N, NW, WANT_Y>;
+    auto kern = d::delta_forward_mma_kernel<IO, N, NW, WANT_Y>;
     static bool ready[kMaxDevices] = {false};
     const int rc = allow_smem(kern, G::SMEM, ready);
     return rc != WKV_OK ? rc : launch(kern, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, st, a);
+}
+
+template <typename IO, int N, bool WANT_Y>
+int launch_forward(const d::Args& a, cudaStream_t st) {
+    return launch_forward_nw<IO, N, N == 32 ? 2 : 4, WANT_Y>(a, st);
 }
 
 template <typename IO, int N>
@@ -175,7 +179,7 @@ int wkv_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, in
     d::Args a{};
     a.B = B, a.T = T, a.Hk = Hk, a.H = H;
     a.w = w, a.beta = beta, a.r = r, a.k = k, a.v = v, a.s_in = state_in, a.y = y, a.s_out = state_out;
-    a.vec = aligned(r, 16) && aligned(k, 16) && aligned(v, 16);
+    a.vec = aligned(r, 16) && aligned(k, 16) && aligned(v, 16) && aligned(y, 16);
     rc = with_type(dtype, N, [&](auto tag, auto size) {
         return launch_forward<decltype(tag), decltype(size)::value, true>(a, stream);
     });
