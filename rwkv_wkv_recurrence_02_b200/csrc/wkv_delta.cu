@@ -1,30 +1,13 @@
 // wkv_delta.cu -- host side of the gated delta rule's entry points
 // (wkv_delta_forward, wkv_delta_step, wkv_delta_backward): argument checks,
 // the workspace's layout and the launches.
-#include "wkv_delta_mma.cuh"
+#include "wkv_delta_mma_bwd.cuh"
 #include "wkv_host.cuh"
 
 namespace {
 
 using namespace wkv::host;
 namespace d = wkv::delta;
-
-// A walk's shape for each head size: RG lanes along the reduction axis, CC
-// lines a lane, NW warps a CTA, TB tokens a block.
-template <int N>
-struct Cfg;
-template <>
-struct Cfg<32> {
-    static constexpr int RG = 4, CC = 2, NW = 2, TB = 16;
-};
-template <>
-struct Cfg<64> {
-    static constexpr int RG = 4, CC = 2, NW = 4, TB = 16;
-};
-template <>
-struct Cfg<128> {
-    static constexpr int RG = 8, CC = 4, NW = 4, TB = 8;
-};
 
 template <typename IO, int N, int NW, bool WANT_Y>
 int launch_forward_nw(const d::Args& a, cudaStream_t st) {
@@ -42,25 +25,19 @@ int launch_forward(const d::Args& a, cudaStream_t st) {
 
 template <typename IO, int N>
 int launch_reverse(const d::Args& a, cudaStream_t st) {
-    using C = Cfg<N>;
-    using G = d::ReverseShape<IO, N, C::RG, C::CC, C::NW, C::TB>;
-    auto kern = d::delta_reverse_kernel<IO, N, C::RG, C::CC, C::NW, C::TB>;
+    constexpr int NW = N == 32 ? 2 : 4;
+    using G = d::MmaReverse<IO, N, NW>;
+    auto kern = d::delta_reverse_mma_kernel<IO, N, NW>;
     static bool ready[kMaxDevices] = {false};
     const int rc = allow_smem(kern, G::SMEM, ready);
     return rc != WKV_OK ? rc : launch(kern, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, st, a);
 }
 
-template <typename IO, int N>
-int launch_rows(const d::Args& a, bool grad, cudaStream_t st) {
-    using C = Cfg<N>;
-    using G = d::RowShape<IO, N, C::RG, C::CC, C::NW, C::TB>;
-    if (!grad) {
-        auto kern = d::delta_state_rows_kernel<IO, N, C::RG, C::CC, C::NW, C::TB>;
-        static bool ready[kMaxDevices] = {false};
-        const int rc = allow_smem(kern, G::SMEM, ready);
-        return rc != WKV_OK ? rc : launch(kern, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, st, a);
-    }
-    auto kern = d::delta_grad_rows_kernel<IO, N, C::RG, C::CC, C::NW, C::TB>;
+template <typename IO, int N, bool GRAD>
+int launch_rows(const d::Args& a, cudaStream_t st) {
+    constexpr int NW = N == 32 ? 2 : 4;
+    using G = d::MmaRows<IO, N, NW, GRAD>;
+    auto kern = d::delta_rows_mma_kernel<IO, N, NW, GRAD>;
     static bool ready[kMaxDevices] = {false};
     const int rc = allow_smem(kern, G::SMEM, ready);
     return rc != WKV_OK ? rc : launch(kern, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, st, a);
@@ -68,7 +45,7 @@ int launch_rows(const d::Args& a, bool grad, cudaStream_t st) {
 
 template <int N>
 constexpr int slots() {
-    return N / d::Tile<N, Cfg<N>::RG, Cfg<N>::CC>::CW;
+    return N / 16;
 }
 
 struct Layout {
@@ -97,8 +74,8 @@ template <typename IO, int N>
 int run_backward(d::Args& a, void* dr, void* dk, float* dw, float* dbeta, float* term, cudaStream_t st) {
     int rc = launch_forward<IO, N, false>(a, st);
     if (rc == WKV_OK) rc = launch_reverse<IO, N>(a, st);
-    if (rc == WKV_OK) rc = launch_rows<IO, N>(a, false, st);
-    if (rc == WKV_OK) rc = launch_rows<IO, N>(a, true, st);
+    if (rc == WKV_OK) rc = launch_rows<IO, N, false>(a, st);
+    if (rc == WKV_OK) rc = launch_rows<IO, N, true>(a, st);
     if (rc == WKV_OK)
         rc = launch(d::delta_tokens_kernel<IO, N>, (a.B * a.T * a.Hk + 7) / 8, 256, 0, st, a, static_cast<IO*>(dr),
                     static_cast<IO*>(dk), dbeta, term);
@@ -244,7 +221,7 @@ int wkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, i
     a.w = w, a.beta = beta, a.r = r, a.k = k, a.v = v, a.dy = dy, a.s_in = state_in, a.ds_out = dstate_out;
     a.dv = dv, a.ds_in = dstate_in;
     a.e = f(l.e), a.du = f(l.du), a.dr = f(l.dr), a.dk = f(l.dk), a.dk2 = f(l.dk2), a.check = f(l.check), a.phi = f(l.phi);
-    a.vec = aligned(r, 16) && aligned(k, 16) && aligned(v, 16) && aligned(dy, 16);
+    a.vec = aligned(r, 16) && aligned(k, 16) && aligned(v, 16) && aligned(dy, 16) && aligned(dv, 16);
     rc = with_type(dtype, N, [&](auto tag, auto size) {
         return run_backward<decltype(tag), decltype(size)::value>(a, dr, dk, dw, dbeta, f(l.term), stream);
     });

@@ -129,9 +129,9 @@ __device__ __forceinline__ void split_rows(__nv_bfloat16* dst, int piece, const 
     }
 }
 
-// (16 tokens x N) (N x 16 tokens)^T of two staged arrays of KP pieces each:
-// C[t][s] = x_t . y_s
-template <int N, int KP>
+// (16 tokens x N) (N x 16 tokens)^T of two staged arrays of KX and KY pieces,
+// the products of the first ORD orders: C[t][s] = x_t . y_s
+template <int N, int KX, int KY, int ORD>
 __device__ __forceinline__ void gram(float (&c)[2][4], const __nv_bfloat16* x, const __nv_bfloat16* y, int piece, int lane) {
     constexpr int LD = N + 8;
 #pragma unroll
@@ -143,19 +143,19 @@ __device__ __forceinline__ void gram(float (&c)[2][4], const __nv_bfloat16* x, c
     const int rb = (lane & 7) + (lane >> 4) * 8, cb = ((lane >> 3) & 1) * 8;
 #pragma unroll
     for (int kk = 0; kk < N / 16; ++kk) {
-        uint32_t a[KP][4], b[KP][4];
+        uint32_t a[KX][4], b[KY][4];
 #pragma unroll
-        for (int p = 0; p < KP; ++p) {
-            ldsm4(a[p], smem_u32(x + p * piece + ra * LD + kk * 16 + ca));
-            ldsm4(b[p], smem_u32(y + p * piece + rb * LD + kk * 16 + cb));
-        }
+        for (int p = 0; p < KX; ++p) ldsm4(a[p], smem_u32(x + p * piece + ra * LD + kk * 16 + ca));
 #pragma unroll
-        for (int o = KP - 1; o >= 0; --o)
+        for (int p = 0; p < KY; ++p) ldsm4(b[p], smem_u32(y + p * piece + rb * LD + kk * 16 + cb));
 #pragma unroll
-            for (int p = 0; p <= o; ++p) {
-                mma(c[0], a[p], b[o - p][0], b[o - p][1]);
-                mma(c[1], a[p], b[o - p][2], b[o - p][3]);
-            }
+        for (int o = ORD - 1; o >= 0; --o)
+#pragma unroll
+            for (int p = 0; p < KX && p <= o; ++p)
+                if (o - p < KY) {
+                    mma(c[0], a[p], b[o - p][0], b[o - p][1]);
+                    mma(c[1], a[p], b[o - p][2], b[o - p][3]);
+                }
     }
 }
 
@@ -176,6 +176,140 @@ __device__ __forceinline__ void invert_column(const float* A, int lane, float (&
         }
         x[i] = acc[0] + acc[1];
     }
+}
+
+// Decays of a chunk (one warp; lane % 16 is a token): gam[t][s] = product of
+// the decays of tokens s + 1 .. t (0 above the diagonal; row pitch 17), the
+// products up to a token and after it.
+struct ChunkDecay {
+    float upto, after;
+};
+__device__ __forceinline__ ChunkDecay chunk_decay(const float* w, float* gam, int lane) {
+    const int tl = lane % 16;
+    const float al = expf(-w[tl]);
+    ChunkDecay d{0.f, 0.f};
+    float run = 1.f;
+#pragma unroll
+    for (int t = 0; t < kChunk; ++t) {
+        const float at = __shfl_sync(0xffffffffu, al, t);
+        d.after = t == tl ? 1.f : d.after * at;
+        run *= at;
+        if (t == tl) d.upto = run;
+        if (lane < 16) gam[t * 17 + tl] = d.after;
+    }
+    return d;
+}
+
+// (v0, v1) of row t, columns s, s + 1 into the pieces of a 16 x 16 matrix
+template <int NP>
+__device__ __forceinline__ void put_pieces(__nv_bfloat16* m, int t, int s, float v0, float v1) {
+    uint32_t p[NP];
+    split2<NP>(v0, v1, p);
+#pragma unroll
+    for (int q = 0; q < NP; ++q) *reinterpret_cast<uint32_t*>(m + q * kChunk * kMatLd + t * kMatLd + s) = p[q];
+}
+
+// The inverse of I + A (A in shared memory) as three pieces.
+__device__ __forceinline__ void put_inverse(__nv_bfloat16* m, const float* A, int lane) {
+    float x[kChunk];
+    invert_column(A, lane, x);
+#pragma unroll
+    for (int i = 0; i < kChunk / 2; ++i) {
+        const float v = lane < 16 ? x[i] : x[i + 8];
+        const int t = lane < 16 ? i : i + 8;
+        uint32_t p[3];
+        split2<3>(v, 0.f, p);
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+            m[q * kChunk * kMatLd + t * kMatLd + lane % 16] = __ushort_as_bfloat16(static_cast<unsigned short>(p[q]));
+    }
+}
+
+// A 16-token x 16-line tile of staged rows, transposed, in the accumulator
+// layout: x[n][i] is line lane / 4 + 8 (i / 2), token 8 n + 2 (lane % 4) + i % 2.
+template <typename IO>
+__device__ __forceinline__ void load_lines(float (&x)[2][4], const IO* rows, int ld, int lane) {
+    if constexpr (sizeof(IO) == 2) {
+        uint32_t f[4];
+        const int m = lane >> 3;
+        ldsm4t(f, smem_u32(rows + ((lane & 7) + (m >> 1) * 8) * ld + (m & 1) * 8));
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[n][i] = __uint_as_float((i & 1) ? f[2 * n + (i >> 1)] & 0xffff0000u : f[2 * n + (i >> 1)] << 16);
+    } else {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[n][i] = to_f32(rows[(8 * n + 2 * (lane % 4) + (i & 1)) * ld + lane / 4 + (i >> 1) * 8]);
+    }
+}
+
+// Such a tile to rows of global memory (row t at out + t * stride), rows
+// below nt.  bfloat16 goes through `rows`, a staged tile that only this warp
+// uses, to 16-byte stores.
+template <typename OUT, typename IO>
+__device__ __forceinline__ void store_lines(OUT* out, int64_t stride, int nt, const float (&x)[2][4], IO* rows, int ld,
+                                            bool vec, int lane) {
+    if constexpr (sizeof(OUT) == 2) {
+        uint32_t f[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int hrow = 0; hrow < 2; ++hrow) {
+                const __nv_bfloat162 v2 = __floats2bfloat162_rn(x[n][2 * hrow], x[n][2 * hrow + 1]);
+                f[2 * n + hrow] = *reinterpret_cast<const uint32_t*>(&v2);
+            }
+        const int m = lane >> 3;
+        stsm4t(smem_u32(rows + ((lane & 7) + (m >> 1) * 8) * ld + (m & 1) * 8), f);
+        __syncwarp();
+        const int t = lane / 2, col = (lane % 2) * 8;
+        const uint4 v4 = *reinterpret_cast<const uint4*>(rows + t * ld + col);
+        if (t < nt) {
+            OUT* o = out + t * stride + col;
+            if (vec) {
+                *reinterpret_cast<uint4*>(o) = v4;
+            } else {
+                const uint32_t wd[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    reinterpret_cast<unsigned short*>(o)[i] = static_cast<unsigned short>(wd[i / 2] >> (16 * (i & 1)));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = 8 * n + 2 * (lane % 4) + (i & 1);
+                if (t < nt) out[t * stride + lane / 4 + (i >> 1) * 8] = x[n][i];
+            }
+    }
+}
+
+// x times a factor for each token
+__device__ __forceinline__ void scale_tokens(float (&x)[2][4], const float* f, int lane) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const float2 v = pair_at(f, n, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[n][i] *= (i & 1) ? v.y : v.x;
+    }
+}
+
+template <int NP>
+__device__ __forceinline__ void sum_orders(float (&x)[2][4], const float (&o)[NP][2][4]) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float s = o[NP - 1][n][i];
+#pragma unroll
+            for (int p = NP - 2; p >= 0; --p) s += o[p][n][i];
+            x[n][i] = s;
+        }
 }
 
 template <typename IO, int N, int NW, bool WANT_Y>
@@ -270,24 +404,15 @@ __global__ void __launch_bounds__(32 * NW) delta_forward_mma_kernel(const Args a
     // A, its inverse and P of one chunk (one warp)
     auto prepare = [&](int c, const __nv_bfloat16* kb, const __nv_bfloat16* rb, const float* ws) {
         const int tl = lane % 16;
-        const float al = expf(-ws[c * kChunk + tl]), be = ws[BLK + c * kChunk + tl];
-        float prod = 0.f, run = 1.f, gt = 0.f;
-#pragma unroll
-        for (int t = 0; t < kChunk; ++t) {
-            const float at = __shfl_sync(0xffffffffu, al, t);
-            prod = t == tl ? 1.f : prod * at;
-            run *= at;
-            if (t == tl) gt = run;
-            if (lane < 16) gam[t * 17 + tl] = prod;
-        }
+        const ChunkDecay d = chunk_decay(ws + c * kChunk, gam, lane);
         if (lane < 16) {
-            sc[c * kChunk + tl] = gt;
-            sc[BLK + c * kChunk + tl] = prod * be;
+            sc[c * kChunk + tl] = d.upto;
+            sc[BLK + c * kChunk + tl] = d.after * ws[BLK + c * kChunk + tl];
         }
         __syncwarp();
         float kk[2][4], rk[2][4];
-        gram<N, KP>(kk, kb + c * kChunk * LD, kb + c * kChunk * LD, G::PIECE, lane);
-        if constexpr (WANT_Y) gram<N, KP>(rk, rb + c * kChunk * LD, kb + c * kChunk * LD, G::PIECE, lane);
+        gram<N, KP, KP, KP>(kk, kb + c * kChunk * LD, kb + c * kChunk * LD, G::PIECE, lane);
+        if constexpr (WANT_Y) gram<N, KP, KP, KP>(rk, rb + c * kChunk * LD, kb + c * kChunk * LD, G::PIECE, lane);
         __nv_bfloat16* tm = mats + c * (3 + (WANT_Y ? PP : 0)) * G::MAT;
         __nv_bfloat16* pm = tm + 3 * G::MAT;
 #pragma unroll
@@ -300,27 +425,11 @@ __global__ void __launch_bounds__(32 * NW) delta_forward_mma_kernel(const Args a
                 const float g0 = gam[t * 17 + s] * bs.x, g1 = gam[t * 17 + s + 1] * bs.y;
                 amat[t * 20 + s] = s < t ? g0 * kk[n][2 * hrow] : 0.f;
                 amat[t * 20 + s + 1] = s + 1 < t ? g1 * kk[n][2 * hrow + 1] : 0.f;
-                if constexpr (WANT_Y) {
-                    uint32_t p[PP];
-                    split2<PP>(g0 * rk[n][2 * hrow], g1 * rk[n][2 * hrow + 1], p);
-#pragma unroll
-                    for (int q = 0; q < PP; ++q) *reinterpret_cast<uint32_t*>(pm + q * G::MAT + t * kMatLd + s) = p[q];
-                }
+                if constexpr (WANT_Y) put_pieces<PP>(pm, t, s, g0 * rk[n][2 * hrow], g1 * rk[n][2 * hrow + 1]);
             }
         }
         __syncwarp();
-        float x[kChunk];
-        invert_column(amat, lane, x);
-#pragma unroll
-        for (int i = 0; i < kChunk / 2; ++i) {
-            const float v = lane < 16 ? x[i] : x[i + 8];
-            const int t = lane < 16 ? i : i + 8;
-            uint32_t p[3];
-            split2<3>(v, 0.f, p);
-#pragma unroll
-            for (int q = 0; q < 3; ++q)
-                tm[q * G::MAT + t * kMatLd + tl] = __ushort_as_bfloat16(static_cast<unsigned short>(p[q]));
-        }
+        put_inverse(tm, amat, lane);
         __syncwarp();
     };
 
@@ -383,22 +492,7 @@ __global__ void __launch_bounds__(32 * NW) delta_forward_mma_kernel(const Args a
             float2 gg[2];
 #pragma unroll
             for (int n = 0; n < 2; ++n) gg[n] = pair_at(sc + c * kChunk, n, lane);
-            if constexpr (KP == 1) {
-                uint32_t f[4];
-                const int m = lane >> 3;
-                ldsm4t(f, smem_u32(vb + (c * kChunk + (lane & 7) + (m >> 1) * 8) * G::LDV + j0 + (m & 1) * 8));
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[n][i] = __uint_as_float((i & 1) ? f[2 * n + (i >> 1)] & 0xffff0000u : f[2 * n + (i >> 1)] << 16);
-            } else {
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[n][i] = to_f32(vb[(c * kChunk + 8 * n + 2 * (lane % 4) + (i & 1)) * G::LDV + j0 + lane / 4 + (i >> 1) * 8]);
-            }
+            load_lines(x, vb + c * kChunk * G::LDV + j0, G::LDV, lane);
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -421,10 +515,7 @@ __global__ void __launch_bounds__(32 * NW) delta_forward_mma_kernel(const Args a
                         mma(ea[i + p][1], xp[i], f[2], f[3]);
                     }
                 }
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) e[n][i] = ea[0][n][i] + (ea[1][n][i] + ea[2][n][i]);
+                sum_orders<3>(e, ea);
             }
             // S <- g_15 S + (G beta E)^T K
             {
@@ -458,13 +549,7 @@ __global__ void __launch_bounds__(32 * NW) delta_forward_mma_kernel(const Args a
                 }
             }
             if constexpr (!WANT_Y) {
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = c * kChunk + 8 * n + 2 * (lane % 4) + (i & 1);
-                        if (t < nt) a.e[vbase + (t0 + t) * vs + j0 + lane / 4 + (i >> 1) * 8] = e[n][i];
-                    }
+                store_lines(a.e + vbase + (t0 + c * kChunk) * vs + j0, vs, nt - c * kChunk, e, vb, 0, false, lane);
             } else {
                 // Y = g R S + P E
                 uint32_t ep[PP][4];
@@ -481,51 +566,16 @@ __global__ void __launch_bounds__(32 * NW) delta_forward_mma_kernel(const Args a
                         mma(ya[i + p][1], ep[i], f[2], f[3]);
                     }
                 }
-                float y[2][4];
+                float y[2][4], q[2][4];
+                sum_orders<PP>(q, qa);
+                sum_orders<PP>(y, ya);
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float q = qa[PP - 1][n][i], s = ya[PP - 1][n][i];
-#pragma unroll
-                        for (int p = PP - 2; p >= 0; --p) q += qa[p][n][i], s += ya[p][n][i];
-                        y[n][i] = fmaf((i & 1) ? gg[n].y : gg[n].x, q, s);
-                    }
-                if constexpr (KP == 1) {
-                    // through the V tile's columns, which only this warp reads
-                    uint32_t f[4];
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int hrow = 0; hrow < 2; ++hrow) {
-                            const __nv_bfloat162 v2 = __floats2bfloat162_rn(y[n][2 * hrow], y[n][2 * hrow + 1]);
-                            f[2 * n + hrow] = *reinterpret_cast<const uint32_t*>(&v2);
-                        }
-                    const int m = lane >> 3;
-                    stsm4t(smem_u32(vb + (c * kChunk + (lane & 7) + (m >> 1) * 8) * G::LDV + j0 + (m & 1) * 8), f);
-                    __syncwarp();
-                    const int t = c * kChunk + lane / 2, col = j0 + (lane % 2) * 8;
-                    const uint4 v4 = *reinterpret_cast<const uint4*>(vb + t * G::LDV + col);
-                    if (t < nt) {
-                        IO* yp = static_cast<IO*>(a.y) + vbase + (t0 + t) * vs + col;
-                        if (a.vec) {
-                            *reinterpret_cast<uint4*>(yp) = v4;
-                        } else {
-                            const uint32_t wd[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                reinterpret_cast<unsigned short*>(yp)[i] = static_cast<unsigned short>(wd[i / 2] >> (16 * (i & 1)));
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int t = c * kChunk + 8 * n + 2 * (lane % 4) + (i & 1);
-                            if (t < nt) put(static_cast<IO*>(a.y) + vbase + (t0 + t) * vs + j0 + lane / 4 + (i >> 1) * 8, y[n][i]);
-                        }
-                }
+                    for (int i = 0; i < 4; ++i) y[n][i] = fmaf((i & 1) ? gg[n].y : gg[n].x, q[n][i], y[n][i]);
+                // through the V tile's columns, which only this warp reads
+                store_lines(static_cast<IO*>(a.y) + vbase + (t0 + c * kChunk) * vs + j0, vs, nt - c * kChunk, y,
+                            vb + c * kChunk * G::LDV + j0, G::LDV, a.vec, lane);
             }
         }
     }
