@@ -534,7 +534,7 @@ int wkv_delta_step(int64_t L, int64_t B, int64_t Hk, int64_t H, int64_t N, int d
  * holds nothing between calls.  T == 0: dstate_in = dstate_out (zeros if
  * NULL), nothing else is written.  WKV_ERR_WORKSPACE: NULL or too small.
  */
-size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t N);
+size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N);
 int wkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int dtype,
                        const float* w, const float* beta, const void* r, const void* k, const void* v,
                        const float* state_in, const void* dy, const float* dstate_out,

@@ -103,7 +103,7 @@ def lib():
         L.wkv_delta_step.restype = i32
         L.wkv_delta_backward.argtypes = [i64] * 5 + [i32] + [vp] * 15 + [sz, vp]
         L.wkv_delta_backward.restype = i32
-        L.wkv_delta_backward_workspace_bytes.argtypes = [i64] * 4
+        L.wkv_delta_backward_workspace_bytes.argtypes = [i64] * 5
         L.wkv_delta_backward_workspace_bytes.restype = sz
         L.wkv_group_norm.argtypes = [i64] * 3 + [i32, i32, ctypes.c_float] + [vp] * 6
         L.wkv_group_norm.restype = i32
@@ -628,7 +628,7 @@ def wkv_delta_backward(w, beta, r, k, v, H, state_in=None, *, dy, dstate_out=Non
     for t, name in ((state_in, "state_in"), (dstate_out, "dstate_out"), (dstate_in, "dstate_in")):
         _need(t, name, (B, H, N, N), f32, dev)
     with _on_device(dev):
-        nbytes = int(lib().wkv_delta_backward_workspace_bytes(B, T, H, N))
+        nbytes = int(lib().wkv_delta_backward_workspace_bytes(B, T, Hk, H, N))
         ws_ptr, ws_bytes, owner = _scratch(nbytes, workspace, dev, stream)
         _check(lib().wkv_delta_backward(B, T, Hk, H, N, code, _ptr(w), _ptr(beta), _ptr(r), _ptr(k), _ptr(v),
                                         _ptr(state_in), _ptr(dy), _ptr(dstate_out), _ptr(dr), _ptr(dk), _ptr(dv),

@@ -11,7 +11,7 @@ namespace d = wkv::delta;
 
 template <typename IO, int N, int NW, bool WANT_Y>
 int launch_forward_nw(const d::Args& a, cudaStream_t st) {
-    using G = d::MmaForward<IO, N, NW, WANT_Y>;
+    using G = d::ForwardShape<IO, N, NW, WANT_Y>;
     auto kern = d::delta_forward_mma_kernel<IO, N, NW, WANT_Y>;
     static bool ready[kMaxDevices] = {false};
     const int rc = allow_smem(kern, G::SMEM, ready);
@@ -26,7 +26,7 @@ int launch_forward(const d::Args& a, cudaStream_t st) {
 template <typename IO, int N>
 int launch_reverse(const d::Args& a, cudaStream_t st) {
     constexpr int NW = N == 32 ? 2 : 4;
-    using G = d::MmaReverse<IO, N, NW>;
+    using G = d::ReverseShape<IO, N, NW>;
     auto kern = d::delta_reverse_mma_kernel<IO, N, NW>;
     static bool ready[kMaxDevices] = {false};
     const int rc = allow_smem(kern, G::SMEM, ready);
@@ -43,45 +43,39 @@ int launch_rows(const d::Args& a, cudaStream_t st) {
     return rc != WKV_OK ? rc : launch(kern, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, st, a);
 }
 
-template <int N>
-constexpr int slots() {
-    return N / 16;
-}
-
 struct Layout {
-    size_t e, du, dr, dk, dk2, check, phi, term, bytes;
+    size_t e, du, drh, dkh, check, phi, pr, pv, bytes;
 };
 
-Layout layout(int64_t B, int64_t T, int64_t H, int64_t N) {
+// share: value heads to a key head
+Layout layout(int64_t B, int64_t T, int64_t H, int64_t N, bool share) {
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     const size_t val = up(size_t(B) * T * H * N * 4), heads = size_t(B) * H;
-    const size_t chunks = size_t((T + d::kCheck - 1) / d::kCheck) + 1;
-    const size_t slot = N == 32 ? slots<32>() : N == 64 ? slots<64>() : slots<128>();
+    const size_t chunks = size_t((T + d::kCheck - 1) / d::kCheck) + 1, slots = size_t(N) / 16;
     Layout l{};
     l.e = 0;
     l.du = l.e + val;
-    l.dr = l.du + val;
-    l.dk = l.dr + val;
-    l.dk2 = l.dk + val;
-    l.check = l.dk2 + val;
+    l.dkh = l.du + val;
+    l.drh = l.dkh + val;
+    l.check = l.drh + (share ? val : 0);
     l.phi = l.check + up(heads * chunks * N * N * 4);
-    l.term = l.phi + up(heads * chunks * slot * 4);
-    l.bytes = l.term + up(heads * T * 4);
+    l.pr = l.phi + up(heads * chunks * slots * 4);
+    l.pv = l.pr + up(heads * T * slots * 4);
+    l.bytes = l.pv + up(heads * T * slots * 4);
     return l;
 }
 
 template <typename IO, int N>
-int run_backward(d::Args& a, void* dr, void* dk, float* dw, float* dbeta, float* term, cudaStream_t st) {
+int run_backward(const d::Args& a, cudaStream_t st) {
     int rc = launch_forward<IO, N, false>(a, st);
     if (rc == WKV_OK) rc = launch_reverse<IO, N>(a, st);
     if (rc == WKV_OK) rc = launch_rows<IO, N, false>(a, st);
     if (rc == WKV_OK) rc = launch_rows<IO, N, true>(a, st);
-    if (rc == WKV_OK)
-        rc = launch(d::delta_tokens_kernel<IO, N>, (a.B * a.T * a.Hk + 7) / 8, 256, 0, st, a, static_cast<IO*>(dr),
-                    static_cast<IO*>(dk), dbeta, term);
+    if (rc == WKV_OK && a.H != a.Hk)
+        rc = launch(d::delta_share_kernel<IO, N>, (a.B * a.T * a.Hk * (N / 4) + 255) / 256, 256, 0, st, a);
     if (rc == WKV_OK) {
         const int64_t n = a.B * ((a.T + d::kCheck - 1) / d::kCheck) * a.H;
-        rc = launch(d::delta_dw_kernel<slots<N>()>, (n + 127) / 128, 128, 0, st, a, term, dw);
+        rc = launch(d::delta_dw_kernel<N / 16>, (n + 63) / 64, 64, 0, st, a);
     }
     return rc;
 }
@@ -184,10 +178,10 @@ int wkv_delta_step(int64_t L, int64_t B, int64_t Hk, int64_t H, int64_t N, int d
     return rc != WKV_OK ? rc : check_launch();
 }
 
-size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t N) {
+size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N) {
     Sizes n{};
-    if (sizes(B, T, B, 1, H, N, &n) != WKV_OK || B == 0 || T == 0) return 0;
-    return layout(B, T, H, N).bytes;
+    if (sizes(B, T, B, Hk, H, N, &n) != WKV_OK || B == 0 || T == 0) return 0;
+    return layout(B, T, H, N, H != Hk).bytes;
 }
 
 int wkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int dtype, const float* w,
@@ -205,7 +199,7 @@ int wkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, i
         return pass_state(dstate_out, dstate_in, sb, stream);
     }
     if (!w || !beta || !r || !k || !v || !dy || !dr || !dk || !dv || !dw || !dbeta) return WKV_ERR_NULLPTR;
-    const Layout l = layout(B, T, H, N);
+    const Layout l = layout(B, T, H, N, H != Hk);
     if (workspace == nullptr || workspace_bytes < l.bytes) return WKV_ERR_WORKSPACE;
     const size_t kb = size_t(n.keys) * eb, vb = size_t(n.values) * eb, pb = size_t(n.scalars) * 4;
     const Span ins[] = {{w, pb, 4}, {beta, pb, 4}, {r, kb, eb}, {k, kb, eb}, {v, vb, eb}, {state_in, sb, 4},
@@ -220,10 +214,13 @@ int wkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, i
     a.B = B, a.T = T, a.Hk = Hk, a.H = H;
     a.w = w, a.beta = beta, a.r = r, a.k = k, a.v = v, a.dy = dy, a.s_in = state_in, a.ds_out = dstate_out;
     a.dv = dv, a.ds_in = dstate_in;
-    a.e = f(l.e), a.du = f(l.du), a.dr = f(l.dr), a.dk = f(l.dk), a.dk2 = f(l.dk2), a.check = f(l.check), a.phi = f(l.phi);
-    a.vec = aligned(r, 16) && aligned(k, 16) && aligned(v, 16) && aligned(dy, 16) && aligned(dv, 16);
+    a.dr = dr, a.dk = dk, a.dw = dw, a.dbeta = dbeta;
+    a.e = f(l.e), a.du = f(l.du), a.drh = f(l.drh), a.dkh = f(l.dkh), a.check = f(l.check), a.phi = f(l.phi);
+    a.pr = f(l.pr), a.pv = f(l.pv);
+    a.vec = aligned(r, 16) && aligned(k, 16) && aligned(v, 16) && aligned(dy, 16) && aligned(dv, 16) &&
+            aligned(dr, 16) && aligned(dk, 16);
     rc = with_type(dtype, N, [&](auto tag, auto size) {
-        return run_backward<decltype(tag), decltype(size)::value>(a, dr, dk, dw, dbeta, f(l.term), stream);
+        return run_backward<decltype(tag), decltype(size)::value>(a, stream);
     });
     return rc != WKV_OK ? rc : check_launch();
 }

@@ -14,7 +14,7 @@
 //   <Dn_{t-1}, S_{t-1}> = <Dn_t, S_t> + r_t . dr_t - dv_t . v_t.
 //
 // wkv_delta_mma.cuh has the forward walk, wkv_delta_mma_bwd.cuh the reverse
-// mode's; here are the single-token step and what ends the reverse mode.
+// mode; here is the single-token step.
 #pragma once
 
 #include "wkv_common.cuh"
@@ -48,91 +48,22 @@ struct Args {
     const float* ds_out;
     void* dv;
     float* ds_in;
-    // reverse mode's workspace
+    // reverse mode's outputs
+    void* dr;            // (B, T, Hk, N)
+    void* dk;
+    float* dw;           // (B, T, H)
+    float* dbeta;
+    // its workspace
     float* e;            // (B, T, H, N)
     float* du;
-    float* dr;           // (B, T, H, N), per value head
-    float* dk;           // the state's part
-    float* dk2;          // the gradient state's part
+    float* drh;          // (B, T, H, N): dr of each value head, where heads share keys
+    float* dkh;          // dk: the state's part, then of each value head
     float* check;        // (B, H, n + 1, N, N), n = ceil(T / kCheck)
-    float* phi;          // (B, H, n + 1, slots)
+    float* phi;          // (B, H, n + 1, slots), slots = N / 16
+    float* pr;           // (slots, B, T, H): parts of r . dr
+    float* pv;           // and of dv . v
     bool vec;            // 16-byte loads of every tensor in the I/O type
 };
-
-// ---------------------------------------------------------------------------
-// Per token: dr and dk of a key head (the sums over the value heads that share
-// it), dbeta, and the token's term of dw's sum.  One warp per (sequence,
-// token, key head).
-// ---------------------------------------------------------------------------
-template <typename IO, int N>
-__global__ void __launch_bounds__(256) delta_tokens_kernel(const Args a, IO* __restrict__ dr, IO* __restrict__ dk,
-                                                           float* __restrict__ dbeta, float* __restrict__ term) {
-    constexpr int E = N / 32;
-    const int lane = threadIdx.x % 32;
-    const int64_t id = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) / 32;
-    pdl_begin();
-    if (id >= a.B * a.T * a.Hk) return;
-    const int64_t bt = id / a.Hk, hk = id % a.Hk;
-    const int share = int(a.H / a.Hk);
-    float rr[E], sr[E], sk[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        rr[i] = to_f32(static_cast<const IO*>(a.r)[id * N + i * 32 + lane]);
-        sr[i] = sk[i] = 0.f;
-    }
-    for (int s = 0; s < share; ++s) {
-        const int64_t hh = bt * a.H + hk * share + s;
-        float x1 = 0.f, x2 = 0.f, x3 = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int64_t at = hh * N + i * 32 + lane;
-            const float gr = a.dr[at], du = a.du[at];
-            sr[i] += gr;
-            sk[i] += a.dk[at] + a.dk2[at];
-            x1 = fmaf(rr[i], gr, x1);
-            x2 = fmaf(du, to_f32(static_cast<const IO*>(a.v)[at]), x2);
-            x3 = fmaf(du, a.e[at], x3);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) {
-            x1 += __shfl_xor_sync(0xffffffffu, x1, o);
-            x2 += __shfl_xor_sync(0xffffffffu, x2, o);
-            x3 += __shfl_xor_sync(0xffffffffu, x3, o);
-        }
-        if (lane == 0) {
-            dbeta[hh] = x3;
-            term[hh] = x1 - a.beta[hh] * x2;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        put(dr + id * N + i * 32 + lane, sr[i]);
-        put(dk + id * N + i * 32 + lane, sk[i]);
-    }
-}
-
-// dw of a chunk: the sum <Dn, S> from the chunk's end backwards; its first
-// token's is the border's own.  One thread per (sequence, chunk, head).
-template <int SLOTS>
-__global__ void __launch_bounds__(128) delta_dw_kernel(const Args a, const float* __restrict__ term, float* __restrict__ dw) {
-    const int64_t nchunk = (a.T + kCheck - 1) / kCheck;
-    const int64_t id = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-    pdl_begin();
-    if (id >= a.B * nchunk * a.H) return;
-    const int64_t h = id % a.H, c = id / a.H % nchunk, b = id / a.H / nchunk;
-    const float* phi = a.phi + ((b * a.H + h) * (nchunk + 1) + c) * SLOTS;
-    float first = 0.f, x = 0.f;
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s) first += phi[s], x += phi[SLOTS + s];
-    const int64_t t0 = c * kCheck, t1 = t0 + kCheck < a.T ? t0 + kCheck : a.T;
-    for (int64_t t = t1 - 1; t > t0; --t) {
-        const int64_t at = (b * a.T + t) * a.H + h;
-        x += term[at];
-        // a state that nothing is left of has no gradient, whatever the sum's rounding left
-        dw[at] = expf(-a.w[at]) == 0.f ? 0.f : -x;
-    }
-    dw[(b * a.T + t0) * a.H + h] = -first;
-}
 
 // ---------------------------------------------------------------------------
 // One token for L layers (B sequences, H heads each): the state is read once,

@@ -49,11 +49,34 @@ __device__ __forceinline__ void stsm4t(uint32_t addr, const uint32_t (&r)[4]) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
                  :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
+// c += A B, or c = A B
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// a 16-wide B operand (two tiles)
+__device__ __forceinline__ void mma2(float (&c)[2][4], const uint32_t (&a)[4], const uint32_t (&f)[4], bool first) {
+    if (first) {
+        mma_first(c[0], a, f[0], f[1]);
+        mma_first(c[1], a, f[2], f[3]);
+    } else {
+        mma(c[0], a, f[0], f[1]);
+        mma(c[1], a, f[2], f[3]);
+    }
+}
+// barriers of the staging warps and the walking warps
+template <int THREADS>
+__device__ __forceinline__ void bar_sync(int id) { asm volatile("bar.sync %0, %1;" :: "r"(id), "n"(THREADS) : "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void bar_arrive(int id) { asm volatile("bar.arrive %0, %1;" :: "r"(id), "n"(THREADS) : "memory"); }
+constexpr int kBarFull = 1, kBarFree = 3, kBarStage = 5;   // full and free: one for each of two stages
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(full ? 16 : 0) : "memory");
 }
@@ -63,14 +86,12 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_gr
 // (x, y) as NP packed bfloat16 pairs whose sum is the pair to 8 NP bits
 template <int NP>
 __device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[NP]) {
+    F2 v = f2(x, y);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f2lo(v), f2hi(v));
         p[i] = *reinterpret_cast<const uint32_t*>(&h);
-        if (i + 1 < NP) {
-            x -= __uint_as_float(p[i] << 16);
-            y -= __uint_as_float(p[i] & 0xffff0000u);
-        }
+        if (i + 1 < NP) v = fma2(f2(__uint_as_float(p[i] << 16), __uint_as_float(p[i] & 0xffff0000u)), f2s(-1.f), v);
     }
 }
 // Two neighbouring accumulator tiles (16 x 16) as the pieces of an A operand
@@ -115,17 +136,17 @@ __device__ __forceinline__ void copy_rows(IO* dst, const IO* src, int64_t stride
     }
 }
 
-// float32 rows as three arrays of bfloat16 pieces, PIECE elements apart
-template <int BLK, int W, int LDS, int LDD, int THREADS>
+// float32 rows as NP arrays of bfloat16 pieces, `piece` elements apart
+template <int BLK, int W, int LDS, int LDD, int NP, int THREADS>
 __device__ __forceinline__ void split_rows(__nv_bfloat16* dst, int piece, const float* src, int tid) {
 #pragma unroll 4
     for (int i = tid; i < BLK * W / 2; i += THREADS) {
         const int t = i / (W / 2), c = (i % (W / 2)) * 2;
         const float2 x = *reinterpret_cast<const float2*>(src + t * LDS + c);
-        uint32_t p[3];
-        split2<3>(x.x, x.y, p);
+        uint32_t p[NP];
+        split2<NP>(x.x, x.y, p);
 #pragma unroll
-        for (int q = 0; q < 3; ++q) *reinterpret_cast<uint32_t*>(dst + q * piece + t * LDD + c) = p[q];
+        for (int q = 0; q < NP; ++q) *reinterpret_cast<uint32_t*>(dst + q * piece + t * LDD + c) = p[q];
     }
 }
 
@@ -134,11 +155,8 @@ __device__ __forceinline__ void split_rows(__nv_bfloat16* dst, int piece, const 
 template <int N, int KX, int KY, int ORD>
 __device__ __forceinline__ void gram(float (&c)[2][4], const __nv_bfloat16* x, const __nv_bfloat16* y, int piece, int lane) {
     constexpr int LD = N + 8;
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[n][i] = 0.f;
     // A: rows t, keys; B: rows s, keys
+    bool first = true;
     const int ra = (lane & 7) + ((lane >> 3) & 1) * 8, ca = (lane >> 4) * 8;
     const int rb = (lane & 7) + (lane >> 4) * 8, cb = ((lane >> 3) & 1) * 8;
 #pragma unroll
@@ -153,8 +171,8 @@ __device__ __forceinline__ void gram(float (&c)[2][4], const __nv_bfloat16* x, c
 #pragma unroll
             for (int p = 0; p < KX && p <= o; ++p)
                 if (o - p < KY) {
-                    mma(c[0], a[p], b[o - p][0], b[o - p][1]);
-                    mma(c[1], a[p], b[o - p][2], b[o - p][3]);
+                    mma2(c, a[p], b[o - p], first);
+                    first = false;
                 }
     }
 }
@@ -299,74 +317,233 @@ __device__ __forceinline__ void scale_tokens(float (&x)[2][4], const float* f, i
     }
 }
 
-template <int NP>
-__device__ __forceinline__ void sum_orders(float (&x)[2][4], const float (&o)[NP][2][4]) {
+// A product of pieces in two accumulators: the leading order, and all others
+// (2^-8 of it, so what their additions round off is 2^-8 of a float32 step).
+struct Acc {
+    float hi[2][4], lo[2][4];
+    __device__ __forceinline__ void sum(float (&x)[2][4], bool has_lo = true) const {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[n][i] = has_lo ? hi[n][i] + lo[n][i] : hi[n][i];
+    }
+};
+// acc (+)= A (16 x 16) B (16 x 16) of NA and NB pieces, orders below ORD.  B's
+// pieces lie `piece` elements apart; off: this lane's offset (b_plain, b_trans).
+template <int NA, int NB, int ORD, bool TRANS>
+__device__ __forceinline__ void times(Acc& acc, bool first, const uint32_t (&a)[NA][4], const __nv_bfloat16* m, int piece,
+                                      int off) {
+    bool lo_first = first;
+#pragma unroll
+    for (int p = 0; p < NB && p < ORD; ++p) {
+        uint32_t f[4];
+        if constexpr (TRANS) ldsm4t(f, smem_u32(m + p * piece + off));
+        else ldsm4(f, smem_u32(m + p * piece + off));
+#pragma unroll
+        for (int i = 0; i < NA && i + p < ORD; ++i) {
+            if (i + p == 0) {
+                mma2(acc.hi, a[i], f, first);
+            } else {
+                mma2(acc.lo, a[i], f, lo_first);
+                lo_first = false;
+            }
+        }
+    }
+}
+// d (+)= A B into one accumulator, smallest orders first
+template <int NA, int NB>
+__device__ __forceinline__ void times_add(float (&d)[2][4], bool first, const uint32_t (&a)[NA][4], const __nv_bfloat16* m,
+                                          int piece, int off) {
+    uint32_t f[NB][4];
+#pragma unroll
+    for (int p = 0; p < NB; ++p) ldsm4t(f[p], smem_u32(m + p * piece + off));
+#pragma unroll
+    for (int o = 2; o >= 0; --o)
+#pragma unroll
+        for (int p = 0; p < NB && p <= o; ++p)
+            if (o - p < NA) {
+                mma2(d, a[o - p], f[p], first);
+                first = false;
+            }
+}
+// s <- f s + d
+__device__ __forceinline__ void fade_add(float (&s)[4], float f, const float (&d)[4]) {
+    const F2 a = fma2(f2(s[0], s[1]), f2s(f), f2(d[0], d[1])), b = fma2(f2(s[2], s[3]), f2s(f), f2(d[2], d[3]));
+    s[0] = f2lo(a), s[1] = f2hi(a), s[2] = f2lo(b), s[3] = f2hi(b);
+}
+// shared-memory offsets (elements) of this lane in a B operand: rows as they
+// lie (row = column of the product) and transposed (row = its k)
+__device__ __forceinline__ int b_plain(int lane, int ld) { return ((lane & 7) + (lane >> 4) * 8) * ld + ((lane >> 3) & 1) * 8; }
+__device__ __forceinline__ int b_trans(int lane, int ld) { return ((lane & 7) + ((lane >> 3) & 1) * 8) * ld + (lane >> 4) * 8; }
+
+// sum over this warp's 16 lines of x * y for each token of the chunk, to
+// out[token * stride] (tokens below nt)
+__device__ __forceinline__ void token_sums(float* out, int64_t stride, int nt, const float (&x)[2][4], const float (&y)[2][4],
+                                           int lane) {
+    float s[2][2];
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float s = o[NP - 1][n][i];
+        for (int q = 0; q < 2; ++q) s[n][q] = fmaf(x[n][q], y[n][q], x[n][q + 2] * y[n][q + 2]);
+    // lanes 4 apart hold the same tokens: halve what a lane carries, then the lanes
+    const bool b0 = lane & 4, b1 = lane & 8;
+    float u[2];
 #pragma unroll
-            for (int p = NP - 2; p >= 0; --p) s += o[p][n][i];
-            x[n][i] = s;
-        }
+    for (int q = 0; q < 2; ++q) u[q] = (b0 ? s[1][q] : s[0][q]) + __shfl_xor_sync(0xffffffffu, b0 ? s[0][q] : s[1][q], 4);
+    float v = (b1 ? u[1] : u[0]) + __shfl_xor_sync(0xffffffffu, b1 ? u[0] : u[1], 8);
+    v += __shfl_xor_sync(0xffffffffu, v, 16);
+    const int t = (b0 ? 8 : 0) + 2 * (lane % 4) + (b1 ? 1 : 0);
+    if (lane < 16 && t < nt) out[t * stride] = v;
 }
 
-template <typename IO, int N, int NW, bool WANT_Y>
-struct MmaForward {
+// Shared memory of the two walks over value columns: K and R with V (or dY),
+// two stages, each with its chunks' matrices.  ROPS: R is staged too; MATS:
+// 16 x 16 matrices (pieces) a chunk; SCS: factors a token; VT: tiles of values
+// (V or dY, V).
+template <typename IO, int N, int NW, bool ROPS, int MATS, int SCS, int VT = 1>
+struct MmaColumns {
     static constexpr int KP = sizeof(IO) == 2 ? 1 : 3;           // pieces of K and R
-    static constexpr int PP = sizeof(IO) == 2 ? 2 : 3;           // orders of what only reaches y
-    static constexpr int CW = 16 * NW, SLICES = N / CW, THREADS = 32 * NW;
-    // tokens staged at a time: as many as fit
-    static constexpr int BLK = KP == 3 && N == 128 ? 32 : 64;
-    static constexpr int LD = N + 8;
-    static constexpr int PIECE = BLK * LD;
-    static constexpr int OPS = (WANT_Y ? 2 : 1) * KP * PIECE;    // K (and R), bfloat16
-    static constexpr int LDV = KP == 1 ? CW + 8 : CW + 4;
-    static constexpr int VEL = BLK * LDV;                     // V, in the I/O type
-    static constexpr int LDR = N;                                // raw float32 rows
-    static constexpr int MAT = kChunk * kMatLd;
+    static constexpr int CW = 16 * NW, SLICES = N / CW;
+    static constexpr int WALK = 32 * NW, STAGERS = 64, THREADS = WALK + STAGERS;
+    // tokens staged at a time: two CTAs of 64 channels fit an SM
+    static constexpr int BLK = KP == 3 || N == 128 ? 32 : 64;
     static constexpr int NCH = BLK / kChunk;
-    // bytes
-    static constexpr int B_OPS = OPS * 2 * (KP == 1 ? 2 : 1);
-    static constexpr int B_RAW = KP == 1 ? 0 : (WANT_Y ? 2 : 1) * BLK * LDR * 4;
-    static constexpr int B_V = 2 * VEL * int(sizeof(IO));
-    static constexpr int B_MAT = NCH * (3 + (WANT_Y ? PP : 0)) * MAT * 2;
-    static constexpr int B_SC = 2 * 2 * BLK * 4 + 2 * BLK * 4;
-    static constexpr int B_SCR = NW * (16 * 17 + 16 * 20 + 12) * 4;
-    static constexpr int SMEM = B_OPS + B_RAW + B_V + B_MAT + B_SC + B_SCR;
+    static constexpr int LD = N + 8, PIECE = BLK * LD;
+    static constexpr int OPS = (ROPS ? 2 : 1) * KP * PIECE;
+    static constexpr int LDV = KP == 1 ? CW + 8 : CW + 4, VEL = BLK * LDV;   // V in the I/O type
+    static constexpr int LDR = N, ROW = BLK * LDR;                           // raw float32 rows
+    static constexpr int MAT = kChunk * kMatLd;
+    // bytes of a stage, in order
+    static constexpr int S_OPS = OPS * 2, S_V = VT * VEL * int(sizeof(IO)), S_MAT = NCH * MATS * MAT * 2;
+    static constexpr int S_SC = (2 + SCS) * BLK * 4;                         // w, beta, factors
+    static constexpr int STAGE = S_OPS + S_V + S_MAT + S_SC;
+    static constexpr int B_RAW = KP == 1 ? 0 : (ROPS ? 2 : 1) * ROW * 4;
+    static constexpr int SCR = 16 * 17 + 8 + 16 * 20;                        // floats of a staging warp
+    static constexpr int SMEM = 2 * STAGE + B_RAW + STAGERS / 32 * SCR * 4;
+
+    __nv_bfloat16* k;
+    IO* v;
+    __nv_bfloat16* mats;
+    float *w, *beta, *sc;
+    __device__ __forceinline__ MmaColumns(char* smem, int st) {
+        char* p = smem + st * STAGE;
+        k = reinterpret_cast<__nv_bfloat16*>(p);
+        v = reinterpret_cast<IO*>(p + S_OPS);
+        mats = reinterpret_cast<__nv_bfloat16*>(p + S_OPS + S_V);
+        w = reinterpret_cast<float*>(p + S_OPS + S_V + S_MAT);
+        beta = w + BLK;
+        sc = w + 2 * BLK;
+    }
+    __device__ __forceinline__ __nv_bfloat16* r() const { return k + KP * PIECE; }
+    __device__ __forceinline__ float* scratch(char* smem, int i) const {
+        return reinterpret_cast<float*>(smem + 2 * STAGE + B_RAW) + i * SCR;
+    }
+    // rows t0 .. of every tensor (the staging warps)
+    __device__ __forceinline__ void fetch(char* smem, const IO* kp, const IO* rp, int64_t ks, const IO* vp, const IO* vp2,
+                                          int64_t vs, const float* wp, const float* bp, int64_t H, int64_t t0, int nt, bool vec, int tid) {
+        if constexpr (KP == 1) {
+            copy_rows<IO, BLK, N, LD, STAGERS>(reinterpret_cast<IO*>(k), kp + t0 * ks, ks, nt, vec, tid);
+            if constexpr (ROPS) copy_rows<IO, BLK, N, LD, STAGERS>(reinterpret_cast<IO*>(r()), rp + t0 * ks, ks, nt, vec, tid);
+        } else {
+            float* raw = reinterpret_cast<float*>(smem + 2 * STAGE);
+            copy_rows<float, BLK, N, LDR, STAGERS>(raw, reinterpret_cast<const float*>(kp) + t0 * ks, ks, nt, vec, tid);
+            if constexpr (ROPS)
+                copy_rows<float, BLK, N, LDR, STAGERS>(raw + ROW, reinterpret_cast<const float*>(rp) + t0 * ks, ks, nt, vec, tid);
+        }
+        copy_rows<IO, BLK, CW, LDV, STAGERS>(v, vp + t0 * vs, vs, nt, vec, tid);
+        if constexpr (VT == 2) copy_rows<IO, BLK, CW, LDV, STAGERS>(v + VEL, vp2 + t0 * vs, vs, nt, vec, tid);
+        for (int t = tid; t < BLK; t += STAGERS) {
+            w[t] = t < nt ? wp[(t0 + t) * H] : 0.f;
+            beta[t] = t < nt ? bp[(t0 + t) * H] : 0.f;
+        }
+        cp_async_commit();
+        cp_async_wait();
+        bar_sync<STAGERS>(kBarStage);
+        if constexpr (KP == 3) {
+            const float* raw = reinterpret_cast<const float*>(smem + 2 * STAGE);
+            split_rows<BLK, N, LDR, LD, 3, STAGERS>(k, PIECE, raw, tid);
+            if constexpr (ROPS) split_rows<BLK, N, LDR, LD, 3, STAGERS>(r(), PIECE, raw + ROW, tid);
+            bar_sync<STAGERS>(kBarStage);
+        }
+    }
 };
 
-// Outputs y (WANT_Y) or the errors e for the reverse mode (float32).
+// what only reaches y takes this many orders
+template <typename IO>
+constexpr int kOutOrders = sizeof(IO) == 2 ? 2 : 3;
+
+// Outputs y (WANT_Y) or the errors e for the reverse mode (float32).  Two
+// warps stage and prepare a block ahead; the others walk.
 template <typename IO, int N, int NW, bool WANT_Y>
-__global__ void __launch_bounds__(32 * NW) delta_forward_mma_kernel(const Args a) {
-    using G = MmaForward<IO, N, NW, WANT_Y>;
-    constexpr int KP = G::KP, PP = G::PP, LD = G::LD, NT = N / 8, BLK = G::BLK;
-    extern __shared__ __align__(16) char smem_raw[];
-    __nv_bfloat16* ops = reinterpret_cast<__nv_bfloat16*>(smem_raw);
-    float* raw = reinterpret_cast<float*>(smem_raw + G::B_OPS);
-    IO* vbuf = reinterpret_cast<IO*>(smem_raw + G::B_OPS + G::B_RAW);
-    __nv_bfloat16* mats = reinterpret_cast<__nv_bfloat16*>(smem_raw + G::B_OPS + G::B_RAW + G::B_V);
-    float* wb = reinterpret_cast<float*>(smem_raw + G::B_OPS + G::B_RAW + G::B_V + G::B_MAT);   // [2][w, beta][64]
-    float* sc = wb + 4 * BLK;                                                                 // [g, G beta][64]
+using ForwardShape = MmaColumns<IO, N, NW, WANT_Y, 3 + (WANT_Y ? kOutOrders<IO> : 0), 2>;
+
+template <typename IO, int N, int NW, bool WANT_Y>
+__global__ void __launch_bounds__(ForwardShape<IO, N, NW, WANT_Y>::THREADS, N == 64 && sizeof(IO) == 2 ? 2 : 1)
+delta_forward_mma_kernel(const Args a) {
+    using G = ForwardShape<IO, N, NW, WANT_Y>;
+    constexpr int KP = G::KP, PP = kOutOrders<IO>, LD = G::LD, NT = N / 8, BLK = G::BLK, MATS = 3 + (WANT_Y ? PP : 0);
+    extern __shared__ __align__(16) char smem[];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    float* gam = sc + 2 * BLK + warp * (16 * 17 + 16 * 20 + 12);
-    float* amat = gam + 16 * 17 + 8;   // 16-byte aligned: 280 floats on
 
     const int64_t head = blockIdx.x / G::SLICES;
     const int slice = int(blockIdx.x % G::SLICES) * G::CW;
     const int64_t b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
-    const int64_t ks = a.Hk * N, vs = a.H * N;
-    const IO* kp = static_cast<const IO*>(a.k) + (b * a.T * a.Hk + hk) * N;
-    const IO* rp = static_cast<const IO*>(a.r) + (b * a.T * a.Hk + hk) * N;
+    const int64_t vs = a.H * N;
     const int64_t vbase = (b * a.T * a.H + h) * N + slice;
-    const IO* vp = static_cast<const IO*>(a.v) + vbase;
-    const float* wp = a.w + b * a.T * a.H + h;
-    const float* bp = a.beta + b * a.T * a.H + h;
-    const int j0 = warp * 16;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
+    if (warp >= NW) {
+        const int64_t ks = a.Hk * N;
+        const IO* kp = static_cast<const IO*>(a.k) + (b * a.T * a.Hk + hk) * N;
+        const IO* rp = static_cast<const IO*>(a.r) + (b * a.T * a.Hk + hk) * N;
+        const int tl = lane % 16;
+        int st = 0;
+        for (int64_t t0 = 0; t0 < a.T; t0 += BLK, st ^= 1) {
+            const int nt = a.T - t0 < BLK ? int(a.T - t0) : BLK;
+            G g(smem, st);
+            if (t0 >= 2 * BLK) bar_sync<G::THREADS>(kBarFree + st);
+            g.fetch(smem, kp, rp, ks, static_cast<const IO*>(a.v) + vbase, nullptr, vs, a.w + b * a.T * a.H + h,
+                    a.beta + b * a.T * a.H + h, a.H, t0, nt, a.vec, tid - G::WALK);
+            float* gam = g.scratch(smem, warp - NW);
+            float* amat = gam + 16 * 17 + 8;
+            // A, its inverse and P
+            for (int c = warp - NW; c * kChunk < nt; c += G::STAGERS / 32) {
+                const ChunkDecay d = chunk_decay(g.w + c * kChunk, gam, lane);
+                if (lane < 16) {
+                    g.sc[c * kChunk + tl] = d.upto;
+                    g.sc[BLK + c * kChunk + tl] = d.after * g.beta[c * kChunk + tl];
+                }
+                __syncwarp();
+                const __nv_bfloat16* kc = g.k + c * kChunk * LD;
+                float kk[2][4], rk[2][4];
+                gram<N, KP, KP, KP>(kk, kc, kc, G::PIECE, lane);
+                if constexpr (WANT_Y) gram<N, KP, KP, KP>(rk, g.r() + c * kChunk * LD, kc, G::PIECE, lane);
+                __nv_bfloat16* tm = g.mats + c * MATS * G::MAT;
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float2 bs = pair_at(g.beta + c * kChunk, n, lane);
+                    const int s = 8 * n + 2 * (lane % 4);
+#pragma unroll
+                    for (int hrow = 0; hrow < 2; ++hrow) {
+                        const int t = lane / 4 + 8 * hrow;
+                        const float g0 = gam[t * 17 + s] * bs.x, g1 = gam[t * 17 + s + 1] * bs.y;
+                        amat[t * 20 + s] = s < t ? g0 * kk[n][2 * hrow] : 0.f;
+                        amat[t * 20 + s + 1] = s + 1 < t ? g1 * kk[n][2 * hrow + 1] : 0.f;
+                        if constexpr (WANT_Y)
+                            put_pieces<PP>(tm + 3 * G::MAT, t, s, g0 * rk[n][2 * hrow], g1 * rk[n][2 * hrow + 1]);
+                    }
+                }
+                __syncwarp();
+                put_inverse(tm, amat, lane);
+                __syncwarp();
+            }
+            bar_arrive<G::THREADS>(kBarFull + st);
+        }
+        return;
+    }
+
+    const int j0 = warp * 16;
     // S^T: tile n holds keys 8 n .. 8 n + 7 of values j0 + lane / 4 (+ 8)
     float S[NT][4];
     {
@@ -379,205 +556,88 @@ __global__ void __launch_bounds__(32 * NW) delta_forward_mma_kernel(const Args a
                 S[n][i] = a.s_in != nullptr ? s[key * N + (i >> 1) * 8] : 0.f;
             }
     }
-
-    auto fetch = [&](int64_t t0, int st) {
-        const int nt = a.T - t0 < BLK ? int(a.T - t0) : BLK;
-        if constexpr (KP == 1) {
-            copy_rows<IO, BLK, N, LD, G::THREADS>(reinterpret_cast<IO*>(ops + st * G::OPS), kp + t0 * ks, ks, nt, a.vec, tid);
-            if constexpr (WANT_Y)
-                copy_rows<IO, BLK, N, LD, G::THREADS>(reinterpret_cast<IO*>(ops + st * G::OPS + G::PIECE), rp + t0 * ks, ks, nt,
-                                                 a.vec, tid);
-        } else {
-            copy_rows<float, BLK, N, G::LDR, G::THREADS>(raw, reinterpret_cast<const float*>(kp) + t0 * ks, ks, nt, a.vec, tid);
-            if constexpr (WANT_Y)
-                copy_rows<float, BLK, N, G::LDR, G::THREADS>(raw + BLK * G::LDR, reinterpret_cast<const float*>(rp) + t0 * ks,
-                                                        ks, nt, a.vec, tid);
-        }
-        copy_rows<IO, BLK, G::CW, G::LDV, G::THREADS>(vbuf + st * G::VEL, vp + t0 * vs, vs, nt, a.vec, tid);
-        for (int t = tid; t < BLK; t += G::THREADS) {
-            wb[st * 2 * BLK + t] = t < nt ? wp[(t0 + t) * a.H] : 0.f;
-            wb[(st * 2 + 1) * BLK + t] = t < nt ? bp[(t0 + t) * a.H] : 0.f;
-        }
-        cp_async_commit();
-    };
-
-    // A, its inverse and P of one chunk (one warp)
-    auto prepare = [&](int c, const __nv_bfloat16* kb, const __nv_bfloat16* rb, const float* ws) {
-        const int tl = lane % 16;
-        const ChunkDecay d = chunk_decay(ws + c * kChunk, gam, lane);
-        if (lane < 16) {
-            sc[c * kChunk + tl] = d.upto;
-            sc[BLK + c * kChunk + tl] = d.after * ws[BLK + c * kChunk + tl];
-        }
-        __syncwarp();
-        float kk[2][4], rk[2][4];
-        gram<N, KP, KP, KP>(kk, kb + c * kChunk * LD, kb + c * kChunk * LD, G::PIECE, lane);
-        if constexpr (WANT_Y) gram<N, KP, KP, KP>(rk, rb + c * kChunk * LD, kb + c * kChunk * LD, G::PIECE, lane);
-        __nv_bfloat16* tm = mats + c * (3 + (WANT_Y ? PP : 0)) * G::MAT;
-        __nv_bfloat16* pm = tm + 3 * G::MAT;
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const float2 bs = pair_at(ws + BLK + c * kChunk, n, lane);
-            const int s = 8 * n + 2 * (lane % 4);
-#pragma unroll
-            for (int hrow = 0; hrow < 2; ++hrow) {
-                const int t = lane / 4 + 8 * hrow;
-                const float g0 = gam[t * 17 + s] * bs.x, g1 = gam[t * 17 + s + 1] * bs.y;
-                amat[t * 20 + s] = s < t ? g0 * kk[n][2 * hrow] : 0.f;
-                amat[t * 20 + s + 1] = s + 1 < t ? g1 * kk[n][2 * hrow + 1] : 0.f;
-                if constexpr (WANT_Y) put_pieces<PP>(pm, t, s, g0 * rk[n][2 * hrow], g1 * rk[n][2 * hrow + 1]);
-            }
-        }
-        __syncwarp();
-        put_inverse(tm, amat, lane);
-        __syncwarp();
-    };
-
-    const int rb_ = (lane & 7) + (lane >> 4) * 8, cb_ = ((lane >> 3) & 1) * 8;      // B operand rows, plain
-    const int rt_ = (lane & 7) + ((lane >> 3) & 1) * 8, ct_ = (lane >> 4) * 8;      // B operand rows, transposed
-    const uint32_t off_b = uint32_t(rb_ * LD + cb_) * 2, off_t = uint32_t(rt_ * LD + ct_) * 2;
-    const uint32_t off_m = uint32_t(rb_ * kMatLd + cb_) * 2;
-
-    fetch(0, 0);
+    const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = b_plain(lane, kMatLd);
     int st = 0;
     for (int64_t t0 = 0; t0 < a.T; t0 += BLK, st ^= 1) {
         const int nt = a.T - t0 < BLK ? int(a.T - t0) : BLK;
-        const int nch = (nt + kChunk - 1) / kChunk;
-        cp_async_wait();
-        __syncthreads();   // the block is staged, and everyone is done with the one before
-        const __nv_bfloat16* kb = ops + (KP == 1 ? st * G::OPS : 0);
-        const __nv_bfloat16* rb = kb + KP * G::PIECE;
-        if constexpr (KP == 3) {
-            split_rows<BLK, N, G::LDR, LD, G::THREADS>(ops, G::PIECE, raw, tid);
-            if constexpr (WANT_Y)
-                split_rows<BLK, N, G::LDR, LD, G::THREADS>(ops + KP * G::PIECE, G::PIECE, raw + BLK * G::LDR, tid);
-            __syncthreads();
-        }
-        if (t0 + BLK < a.T) fetch(t0 + BLK, st ^ 1);
-        const float* ws = wb + st * 2 * BLK;
-        for (int c = warp; c < nch; c += NW) prepare(c, kb, rb, ws);
-        __syncthreads();
-
-        IO* vb = vbuf + st * G::VEL;
+        G g(smem, st);
+        bar_sync<G::THREADS>(kBarFull + st);
 #pragma unroll 1
-        for (int c = 0; c < nch; ++c) {
-            const uint32_t ka = smem_u32(kb + c * kChunk * LD), ra = smem_u32(rb + c * kChunk * LD);
-            float pa[3][2][4] = {}, qa[PP][2][4] = {};
+        for (int c = 0; c * kChunk < nt; ++c) {
+            const __nv_bfloat16* kc = g.k + c * kChunk * LD;
+            const __nv_bfloat16* rc = g.r() + c * kChunk * LD;
+            const __nv_bfloat16* tm = g.mats + c * MATS * G::MAT;
+            const float* gt = g.sc + c * kChunk;
             // K S and R S, transposed
+            Acc pa, qa;
 #pragma unroll
             for (int kk = 0; kk < N / 16; ++kk) {
                 uint32_t sp[3][4];
                 split_a<3>(S[2 * kk], S[2 * kk + 1], sp);
-#pragma unroll
-                for (int p = 0; p < KP; ++p) {
-                    uint32_t f[4];
-                    ldsm4(f, ka + off_b + (p * G::PIECE + kk * 16) * 2);
-#pragma unroll
-                    for (int i = 0; i + p < 3; ++i) {
-                        mma(pa[i + p][0], sp[i], f[0], f[1]);
-                        mma(pa[i + p][1], sp[i], f[2], f[3]);
-                    }
-                    if constexpr (WANT_Y) {
-                        ldsm4(f, ra + off_b + (p * G::PIECE + kk * 16) * 2);
-#pragma unroll
-                        for (int i = 0; i + p < PP; ++i) {
-                            mma(qa[i + p][0], sp[i], f[0], f[1]);
-                            mma(qa[i + p][1], sp[i], f[2], f[3]);
-                        }
-                    }
-                }
+                times<3, KP, 3, false>(pa, kk == 0, sp, kc + kk * 16, G::PIECE, off_b);
+                if constexpr (WANT_Y) times<3, KP, PP, false>(qa, kk == 0, sp, rc + kk * 16, G::PIECE, off_b);
             }
             // X = V - g K S
-            float x[2][4];
+            float x[2][4], p[2][4];
             float2 gg[2];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) gg[n] = pair_at(sc + c * kChunk, n, lane);
-            load_lines(x, vb + c * kChunk * G::LDV + j0, G::LDV, lane);
+            for (int n = 0; n < 2; ++n) gg[n] = pair_at(gt, n, lane);
+            load_lines(x, g.v + c * kChunk * G::LDV + j0, G::LDV, lane);
+            pa.sum(p);
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[n][i] = fmaf(-((i & 1) ? gg[n].y : gg[n].x), pa[0][n][i] + (pa[1][n][i] + pa[2][n][i]), x[n][i]);
+                for (int i = 0; i < 4; ++i) x[n][i] = fmaf(-((i & 1) ? gg[n].y : gg[n].x), p[n][i], x[n][i]);
             // E = (I + A)^-1 X
-            const __nv_bfloat16* tm = mats + c * (3 + (WANT_Y ? PP : 0)) * G::MAT;
-            uint32_t xp[3][4];
-            split_a<3>(x[0], x[1], xp);
             float e[2][4];
             {
-                float ea[3][2][4] = {};
-#pragma unroll
-                for (int p = 0; p < 3; ++p) {
-                    uint32_t f[4];
-                    ldsm4(f, smem_u32(tm + p * G::MAT) + off_m);
-#pragma unroll
-                    for (int i = 0; i + p < 3; ++i) {
-                        mma(ea[i + p][0], xp[i], f[0], f[1]);
-                        mma(ea[i + p][1], xp[i], f[2], f[3]);
-                    }
-                }
-                sum_orders<3>(e, ea);
+                uint32_t xp[3][4];
+                split_a<3>(x[0], x[1], xp);
+                Acc ea;
+                times<3, 3, 3, false>(ea, true, xp, tm, G::MAT, off_m);
+                ea.sum(e);
             }
             // S <- g_15 S + (G beta E)^T K
             {
                 float u[2][4];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float2 f = pair_at(sc + BLK + c * kChunk, n, lane);
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) u[n][i] = e[n][i] * ((i & 1) ? f.y : f.x);
-                }
+                    for (int i = 0; i < 4; ++i) u[n][i] = e[n][i];
+                scale_tokens(u, gt + BLK, lane);
                 uint32_t up[3][4];
                 split_a<3>(u[0], u[1], up);
-                const float gl = sc[c * kChunk + kChunk - 1];
+                const float gl = gt[kChunk - 1];
 #pragma unroll
                 for (int kk = 0; kk < N / 16; ++kk) {
-                    float d[2][4] = {};
-                    uint32_t f[KP][4];
-#pragma unroll
-                    for (int p = 0; p < KP; ++p) ldsm4t(f[p], ka + off_t + (p * G::PIECE + kk * 16) * 2);
-#pragma unroll
-                    for (int o = 2; o >= 0; --o)
-#pragma unroll
-                        for (int p = 0; p < KP && p <= o; ++p) {
-                            mma(d[0], up[o - p], f[p][0], f[p][1]);
-                            mma(d[1], up[o - p], f[p][2], f[p][3]);
-                        }
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) S[2 * kk + n][i] = fmaf(gl, S[2 * kk + n][i], d[n][i]);
+                    float d[2][4];
+                    times_add<3, KP>(d, true, up, kc + kk * 16, G::PIECE, off_t);
+                    fade_add(S[2 * kk], gl, d[0]);
+                    fade_add(S[2 * kk + 1], gl, d[1]);
                 }
             }
+            const int64_t at = vbase + (t0 + c * kChunk) * vs + j0;
             if constexpr (!WANT_Y) {
-                store_lines(a.e + vbase + (t0 + c * kChunk) * vs + j0, vs, nt - c * kChunk, e, vb, 0, false, lane);
+                store_lines(a.e + at, vs, nt - c * kChunk, e, g.v, 0, false, lane);
             } else {
                 // Y = g R S + P E
                 uint32_t ep[PP][4];
                 split_a<PP>(e[0], e[1], ep);
-                float ya[PP][2][4] = {};
-                const __nv_bfloat16* pm = tm + 3 * G::MAT;
-#pragma unroll
-                for (int p = 0; p < PP; ++p) {
-                    uint32_t f[4];
-                    ldsm4(f, smem_u32(pm + p * G::MAT) + off_m);
-#pragma unroll
-                    for (int i = 0; i + p < PP; ++i) {
-                        mma(ya[i + p][0], ep[i], f[0], f[1]);
-                        mma(ya[i + p][1], ep[i], f[2], f[3]);
-                    }
-                }
+                Acc ya;
+                times<PP, PP, PP, false>(ya, true, ep, tm + 3 * G::MAT, G::MAT, off_m);
                 float y[2][4], q[2][4];
-                sum_orders<PP>(q, qa);
-                sum_orders<PP>(y, ya);
+                qa.sum(q);
+                ya.sum(y);
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) y[n][i] = fmaf((i & 1) ? gg[n].y : gg[n].x, q[n][i], y[n][i]);
                 // through the V tile's columns, which only this warp reads
-                store_lines(static_cast<IO*>(a.y) + vbase + (t0 + c * kChunk) * vs + j0, vs, nt - c * kChunk, y,
-                            vb + c * kChunk * G::LDV + j0, G::LDV, a.vec, lane);
+                store_lines(static_cast<IO*>(a.y) + at, vs, nt - c * kChunk, y, g.v + c * kChunk * G::LDV + j0, G::LDV, a.vec,
+                            lane);
             }
         }
+        if (t0 + 2 * BLK < a.T) bar_arrive<G::THREADS>(kBarFree + st);
     }
     if (WANT_Y && a.s_out != nullptr) {
         float* s = a.s_out + head * N * N + slice + j0 + lane / 4;

@@ -69,7 +69,7 @@ def test_backward_refusals(L):
     assert bwd(L, N=16) == SHAPE
     for name in ("w", "beta", "r", "k", "v", "dy", "dr", "dk", "dv", "dw", "dbeta"):
         assert bwd(L, **{name: None}) == NULLPTR, name
-    need = L.wkv_delta_backward_workspace_bytes(2, 9, 4, 64)
+    need = L.wkv_delta_backward_workspace_bytes(2, 9, 2, 4, 64)
     assert need > 0
     assert bwd(L, nws=need - 1) == WORKSPACE
     assert bwd(L, ws=None) == WORKSPACE
@@ -79,8 +79,8 @@ def test_backward_refusals(L):
     assert bwd(L, dsi=P[7]) == ALIAS     # dstate_out's
     assert bwd(L, dsi=P[5]) == ALIAS     # state_in's
     assert bwd(L, dw=P[20] + 256) == ALIAS
-    assert L.wkv_delta_backward_workspace_bytes(2, 9, 4, 63) == 0
-    assert L.wkv_delta_backward_workspace_bytes(-2, 9, 4, 64) == 0
+    assert L.wkv_delta_backward_workspace_bytes(2, 9, 2, 4, 63) == 0
+    assert L.wkv_delta_backward_workspace_bytes(-2, 9, 2, 4, 64) == 0
 
 
 def norm(L, rows=4, C=96, G=3, dt=BF16, act=1, eps=1e-5, x=P[0], wt=P[1], b=P[2], gate=P[3], y=P[4]):
