@@ -9,59 +9,52 @@ namespace {
 using namespace wkv::host;
 namespace d = wkv::delta;
 
-template <typename IO, int N, int NW, bool WANT_Y>
-int launch_forward_nw(const d::Args& a, cudaStream_t st) {
-    using G = d::ForwardShape<IO, N, NW, WANT_Y>;
-    auto kern = d::delta_forward_mma_kernel<IO, N, NW, WANT_Y>;
-    static bool ready[kMaxDevices] = {false};
-    const int rc = allow_smem(kern, G::SMEM, ready);
-    return rc != WKV_OK ? rc : launch(kern, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, st, a);
+template <typename K>
+int launch_walk(K kern, int64_t blocks, int threads, int smem, bool (&ready)[kMaxDevices], const d::Args& a, cudaStream_t st) {
+    const int rc = allow_smem(kern, smem, ready);
+    return rc != WKV_OK ? rc : launch(kern, blocks, threads, smem, st, a);
 }
 
 template <typename IO, int N, bool WANT_Y>
 int launch_forward(const d::Args& a, cudaStream_t st) {
-    return launch_forward_nw<IO, N, N == 32 ? 2 : 4, WANT_Y>(a, st);
+    using G = d::ForwardShape<IO, N, WANT_Y>;
+    static bool ready[kMaxDevices] = {false};
+    return launch_walk(d::delta_forward_mma_kernel<IO, N, WANT_Y>, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, ready, a, st);
 }
 
 template <typename IO, int N>
 int launch_reverse(const d::Args& a, cudaStream_t st) {
-    constexpr int NW = N == 32 ? 2 : 4;
-    using G = d::ReverseShape<IO, N, NW>;
-    auto kern = d::delta_reverse_mma_kernel<IO, N, NW>;
+    using G = d::ReverseShape<IO, N>;
     static bool ready[kMaxDevices] = {false};
-    const int rc = allow_smem(kern, G::SMEM, ready);
-    return rc != WKV_OK ? rc : launch(kern, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, st, a);
+    return launch_walk(d::delta_reverse_mma_kernel<IO, N>, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, ready, a, st);
 }
 
-template <typename IO, int N, bool GRAD>
-int launch_rows(const d::Args& a, cudaStream_t st) {
-    constexpr int NW = N == 32 ? 2 : 4;
-    using G = d::MmaRows<IO, N, NW, GRAD>;
-    auto kern = d::delta_rows_mma_kernel<IO, N, NW, GRAD>;
+template <typename IO, int N>
+int launch_segments(const d::Args& a, cudaStream_t st) {
+    using G = d::SegmentShape<IO, N>;
     static bool ready[kMaxDevices] = {false};
-    const int rc = allow_smem(kern, G::SMEM, ready);
-    return rc != WKV_OK ? rc : launch(kern, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, st, a);
+    return launch_walk(d::delta_segment_kernel<IO, N>, a.B * a.H * ((a.T + d::kSegment - 1) / d::kSegment), G::THREADS, G::SMEM,
+                       ready, a, st);
 }
 
 struct Layout {
-    size_t e, du, drh, dkh, check, phi, pr, pv, bytes;
+    size_t e, du, s_seg, d_seg, phi, drh, dkh, bytes;
 };
 
-// share: value heads to a key head
+// share: several value heads to a key head
 Layout layout(int64_t B, int64_t T, int64_t H, int64_t N, bool share) {
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     const size_t val = up(size_t(B) * T * H * N * 4), heads = size_t(B) * H;
-    const size_t chunks = size_t((T + d::kCheck - 1) / d::kCheck) + 1, slots = size_t(N) / 16;
+    const size_t borders = heads * (size_t((T + d::kSegment - 1) / d::kSegment) + 1);
     Layout l{};
     l.e = 0;
     l.du = l.e + val;
-    l.dkh = l.du + val;
-    l.drh = l.dkh + val;
-    l.check = l.drh + (share ? val : 0);
-    l.phi = l.check + up(heads * chunks * N * N * 4);
-    l.pr = l.phi + up(heads * chunks * slots * 4);
-    l.pv = l.pr + up(heads * T * slots * 4);
-    l.bytes = l.pv + up(heads * T * slots * 4);
+    l.s_seg = l.du + val;
+    l.d_seg = l.s_seg + up(borders * N * N * 4);
+    l.phi = l.d_seg + up(borders * N * N * 4);
+    l.drh = l.phi + up(borders * (N / 16) * 4);
+    l.dkh = l.drh + (share ? val : 0);
+    l.bytes = l.dkh + (share ? val : 0);
     return l;
 }
 
@@ -69,14 +62,9 @@ template <typename IO, int N>
 int run_backward(const d::Args& a, cudaStream_t st) {
     int rc = launch_forward<IO, N, false>(a, st);
     if (rc == WKV_OK) rc = launch_reverse<IO, N>(a, st);
-    if (rc == WKV_OK) rc = launch_rows<IO, N, false>(a, st);
-    if (rc == WKV_OK) rc = launch_rows<IO, N, true>(a, st);
+    if (rc == WKV_OK) rc = launch_segments<IO, N>(a, st);
     if (rc == WKV_OK && a.H != a.Hk)
         rc = launch(d::delta_share_kernel<IO, N>, (a.B * a.T * a.Hk * (N / 4) + 255) / 256, 256, 0, st, a);
-    if (rc == WKV_OK) {
-        const int64_t n = a.B * ((a.T + d::kCheck - 1) / d::kCheck) * a.H;
-        rc = launch(d::delta_dw_kernel<N / 16>, (n + 63) / 64, 64, 0, st, a);
-    }
     return rc;
 }
 
@@ -215,8 +203,8 @@ int wkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, i
     a.w = w, a.beta = beta, a.r = r, a.k = k, a.v = v, a.dy = dy, a.s_in = state_in, a.ds_out = dstate_out;
     a.dv = dv, a.ds_in = dstate_in;
     a.dr = dr, a.dk = dk, a.dw = dw, a.dbeta = dbeta;
-    a.e = f(l.e), a.du = f(l.du), a.drh = f(l.drh), a.dkh = f(l.dkh), a.check = f(l.check), a.phi = f(l.phi);
-    a.pr = f(l.pr), a.pv = f(l.pv);
+    a.e = f(l.e), a.du = f(l.du), a.s_seg = f(l.s_seg), a.d_seg = f(l.d_seg), a.phi = f(l.phi);
+    a.drh = f(l.drh), a.dkh = f(l.dkh);
     a.vec = aligned(r, 16) && aligned(k, 16) && aligned(v, 16) && aligned(dy, 16) && aligned(dv, 16) &&
             aligned(dr, 16) && aligned(dk, 16);
     rc = with_type(dtype, N, [&](auto tag, auto size) {

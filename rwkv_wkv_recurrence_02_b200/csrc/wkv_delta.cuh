@@ -22,8 +22,12 @@
 namespace wkv {
 namespace delta {
 
-// tokens between the states the reverse mode keeps for dw
-constexpr int kCheck = 64;
+// tokens of a segment: the reverse mode keeps the states between segments
+constexpr int kSegment = 64;
+// parts of the inner product of two states: one for each warp of 16 value
+// columns
+template <int N>
+constexpr int kSlots = N / 16;
 
 template <typename IO>
 __device__ __forceinline__ float to_f32(IO x);
@@ -56,12 +60,11 @@ struct Args {
     // its workspace
     float* e;            // (B, T, H, N)
     float* du;
-    float* drh;          // (B, T, H, N): dr of each value head, where heads share keys
-    float* dkh;          // dk: the state's part, then of each value head
-    float* check;        // (B, H, n + 1, N, N), n = ceil(T / kCheck)
-    float* phi;          // (B, H, n + 1, slots), slots = N / 16
-    float* pr;           // (slots, B, T, H): parts of r . dr
-    float* pv;           // and of dv . v
+    float* s_seg;        // (B, H, n + 1, N, N), n = ceil(T / kSegment): the state entering each segment and the last, [value][key]
+    float* d_seg;        // gradients of those, of what follows
+    float* phi;          // (B, H, n + 1, slots): parts of <D, S> there
+    float* drh;          // (B, T, H, N): dr and dk of each value head, where heads share keys
+    float* dkh;
     bool vec;            // 16-byte loads of every tensor in the I/O type
 };
 

@@ -9,21 +9,21 @@
 // No decay is divided by, so resets and strong decays need no case of their
 // own.
 //
-// A warp owns 16 value columns for the whole key axis and keeps S^T for them
-// as mma accumulators (m = value, n = key).  The accumulator layout of one
-// product is the A-operand layout of the next, so S^T -> K S -> E -> S^T
-// never leaves the registers; K, R and V come from shared memory by ldmatrix.
-// A, its inverse and P do not depend on the state: for each block of 64 or 32
-// tokens the CTA's warps form those of one chunk each, then every warp walks
-// the block's chunks.
+// A warp keeps S^T for 16 value columns and the whole key axis as mma
+// accumulators (m = value, n = key).  The accumulator layout of one product is
+// the A-operand layout of the next, so S^T -> K S -> E -> S^T stays in
+// registers and the walking warps exchange nothing; K, R and V come from shared
+// memory by ldmatrix.  A, its inverse and P do not depend on the state: staging
+// warps, one for each of four stages, fetch a chunk and form them chunks
+// ahead.
 //
 // Accuracy: a float32 operand is the sum of three bfloat16 pieces (24 bits);
-// products of pieces up to 2^-16 of the leading one are taken, each order in
-// its own accumulator.  bfloat16 inputs are one piece, exact: three products
-// for what reaches the state.  What only reaches a bfloat16 output takes the
-// orders up to 2^-8 (an error of 2^-17 against the output's own 2^-9).  The state is
-// updated by a float32 multiply-add of the chunk's sum, so the accumulators'
-// truncation does not add up along T.
+// products of pieces up to 2^-16 of the leading one are taken, the leading one
+// in an accumulator of its own.  bfloat16 inputs are one piece, exact: three
+// products for what reaches the state.  What only reaches a bfloat16 output
+// takes the orders up to 2^-8 (an error of 2^-17 against the output's own
+// 2^-9).  The state is updated by a float32 multiply-add of the chunk's sum, so
+// the accumulators' truncation does not add up along T.
 #pragma once
 
 #include "wkv_delta.cuh"
@@ -32,7 +32,10 @@ namespace wkv {
 namespace delta {
 
 constexpr int kChunk = 16;     // tokens of a chunk: one k step of an mma
-constexpr int kMatLd = 24;     // row pitch of the 16 x 16 matrices (48 bytes: ldmatrix rows in distinct banks)
+constexpr int kMat = kChunk * kChunk;
+// Place of (row, column) in a 16 x 16 bfloat16 matrix: the two halves of rows
+// 4 .. 7 (mod 8) change places, so that eight rows of ldmatrix differ in banks.
+__device__ __forceinline__ int mat_at(int r, int c) { return r * kChunk + (((c >> 3) ^ (r >> 2)) & 1) * 8 + (c & 7); }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -45,9 +48,8 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
-__device__ __forceinline__ void stsm4t(uint32_t addr, const uint32_t (&r)[4]) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
-                 :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+__device__ __forceinline__ void stsm2t(uint32_t addr, const uint32_t (&r)[2]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1,%2};" :: "r"(addr), "r"(r[0]), "r"(r[1]) : "memory");
 }
 // c += A B, or c = A B
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -75,7 +77,8 @@ template <int THREADS>
 __device__ __forceinline__ void bar_sync(int id) { asm volatile("bar.sync %0, %1;" :: "r"(id), "n"(THREADS) : "memory"); }
 template <int THREADS>
 __device__ __forceinline__ void bar_arrive(int id) { asm volatile("bar.arrive %0, %1;" :: "r"(id), "n"(THREADS) : "memory"); }
-constexpr int kBarFull = 1, kBarFree = 3, kBarStage = 5;   // full and free: one for each of two stages
+// ids: one for each of four stages
+constexpr int kBarFull = 1, kBarFree = 5;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(full ? 16 : 0) : "memory");
@@ -112,20 +115,20 @@ __device__ __forceinline__ float2 pair_at(const float* x, int n, int lane) {
     return *reinterpret_cast<const float2*>(x + 8 * n + 2 * (lane % 4));
 }
 
-// Rows t0 .. of W elements to shared rows of LD elements: 16-byte
-// asynchronous copies, or element copies where the addresses do not allow
-// them; rows from nt on are zero.
-template <typename IO, int BLK, int W, int LD, int THREADS>
-__device__ __forceinline__ void copy_rows(IO* dst, const IO* src, int64_t stride, int nt, bool vec, int tid) {
+// One warp's copy of ROWS rows of W elements to shared rows of LD elements:
+// 16-byte asynchronous copies, or element copies where the addresses do not
+// allow them; rows from nt on are zero.
+template <typename IO, int ROWS, int W, int LD>
+__device__ __forceinline__ void copy_rows(IO* dst, const IO* src, int64_t stride, int nt, bool vec, int lane) {
     if (vec) {
         constexpr int PER = 16 / int(sizeof(IO)), ROWV = W / PER;
 #pragma unroll
-        for (int i = tid; i < BLK * ROWV; i += THREADS) {
+        for (int i = lane; i < ROWS * ROWV; i += 32) {
             const int t = i / ROWV, c = (i % ROWV) * PER;
             cp_async16(smem_u32(dst + t * LD + c), src + (t < nt ? t : 0) * stride + c, t < nt);
         }
     } else {
-        for (int i = tid; i < BLK * W; i += THREADS) {
+        for (int i = lane; i < ROWS * W; i += 32) {
             const int t = i / W, c = i % W;
             IO x;
             if constexpr (sizeof(IO) == 4) x = 0.f;
@@ -136,17 +139,36 @@ __device__ __forceinline__ void copy_rows(IO* dst, const IO* src, int64_t stride
     }
 }
 
-// float32 rows as NP arrays of bfloat16 pieces, `piece` elements apart
-template <int BLK, int W, int LDS, int LDD, int NP, int THREADS>
-__device__ __forceinline__ void split_rows(__nv_bfloat16* dst, int piece, const float* src, int tid) {
-#pragma unroll 4
-    for (int i = tid; i < BLK * W / 2; i += THREADS) {
-        const int t = i / (W / 2), c = (i % (W / 2)) * 2;
-        const float2 x = *reinterpret_cast<const float2*>(src + t * LDS + c);
-        uint32_t p[NP];
-        split2<NP>(x.x, x.y, p);
+__device__ __forceinline__ float4 load4(const float* p, bool vec) {
+    return vec ? __ldcg(reinterpret_cast<const float4*>(p)) : make_float4(p[0], p[1], p[2], p[3]);
+}
+// four neighbouring values as NP bfloat16 pieces, `piece` elements apart
+template <int NP>
+__device__ __forceinline__ void put4(__nv_bfloat16* dst, int piece, float4 v) {
+    uint32_t p[NP], q[NP];
+    split2<NP>(v.x, v.y, p);
+    split2<NP>(v.z, v.w, q);
 #pragma unroll
-        for (int q = 0; q < NP; ++q) *reinterpret_cast<uint32_t*>(dst + q * piece + t * LDD + c) = p[q];
+    for (int i = 0; i < NP; ++i) *reinterpret_cast<uint2*>(dst + i * piece) = make_uint2(p[i], q[i]);
+}
+// One warp's copy of ROWS float32 rows as NP arrays of pieces
+template <int ROWS, int W, int LD, int NP>
+__device__ __forceinline__ void split_rows(__nv_bfloat16* dst, int piece, const float* src, int64_t stride, int nt, bool vec,
+                                           int lane) {
+    constexpr int ROWV = W / 4, ALL = ROWS * ROWV / 32, U = ALL < 8 ? ALL : 8;   // U loads in flight
+#pragma unroll 1
+    for (int n = 0; n < ALL; n += U) {
+        float4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = lane + (n + u) * 32, t = i / ROWV, c = (i % ROWV) * 4;
+            v[u] = t < nt ? load4(src + t * stride + c, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = lane + (n + u) * 32, t = i / ROWV, c = (i % ROWV) * 4;
+            put4<NP>(dst + t * LD + c, piece, v[u]);
+        }
     }
 }
 
@@ -196,26 +218,31 @@ __device__ __forceinline__ void invert_column(const float* A, int lane, float (&
     }
 }
 
-// Decays of a chunk (one warp; lane % 16 is a token): gam[t][s] = product of
-// the decays of tokens s + 1 .. t (0 above the diagonal; row pitch 17), the
-// products up to a token and after it.
+// Decays of NTOK tokens (one warp; a lane is a token).  The running sum W of the
+// rates goes to shared memory as two float32 (its 64-bit value to 48 bits), so
+// that W_t - W_s is as exact as a float32 however far in the two tokens lie.
+// e^-kMaxRate is 0.
+constexpr float kMaxRate = 1e4f;
 struct ChunkDecay {
-    float upto, after;
+    float upto, after;   // the products of the decays up to a token, and after it
 };
-__device__ __forceinline__ ChunkDecay chunk_decay(const float* w, float* gam, int lane) {
-    const int tl = lane % 16;
-    const float al = expf(-w[tl]);
-    ChunkDecay d{0.f, 0.f};
-    float run = 1.f;
+__device__ __forceinline__ float decay_of(float2 t, float2 s) { return ex2(-kLog2e * ((t.x - s.x) + (t.y - s.y))); }
+__device__ __forceinline__ float2 two_floats(double x) {
+    const float a = float(x);
+    return make_float2(a, float(x - double(a)));
+}
+template <int NTOK>
+__device__ __forceinline__ ChunkDecay chunk_decay(float w, float2* sums, int lane) {
+    double x = w > kMaxRate ? kMaxRate : w;
 #pragma unroll
-    for (int t = 0; t < kChunk; ++t) {
-        const float at = __shfl_sync(0xffffffffu, al, t);
-        d.after = t == tl ? 1.f : d.after * at;
-        run *= at;
-        if (t == tl) d.upto = run;
-        if (lane < 16) gam[t * 17 + tl] = d.after;
+    for (int o = 1; o < NTOK; o *= 2) {
+        const double y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
     }
-    return d;
+    const float2 v = two_floats(x);
+    if (lane < NTOK) sums[lane] = v;
+    const float2 last = make_float2(__shfl_sync(0xffffffffu, v.x, NTOK - 1), __shfl_sync(0xffffffffu, v.y, NTOK - 1));
+    return ChunkDecay{decay_of(v, make_float2(0.f, 0.f)), decay_of(last, v)};
 }
 
 // (v0, v1) of row t, columns s, s + 1 into the pieces of a 16 x 16 matrix
@@ -224,7 +251,7 @@ __device__ __forceinline__ void put_pieces(__nv_bfloat16* m, int t, int s, float
     uint32_t p[NP];
     split2<NP>(v0, v1, p);
 #pragma unroll
-    for (int q = 0; q < NP; ++q) *reinterpret_cast<uint32_t*>(m + q * kChunk * kMatLd + t * kMatLd + s) = p[q];
+    for (int q = 0; q < NP; ++q) *reinterpret_cast<uint32_t*>(m + q * kMat + mat_at(t, s)) = p[q];
 }
 
 // The inverse of I + A (A in shared memory) as three pieces.
@@ -238,10 +265,17 @@ __device__ __forceinline__ void put_inverse(__nv_bfloat16* m, const float* A, in
         uint32_t p[3];
         split2<3>(v, 0.f, p);
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
-            m[q * kChunk * kMatLd + t * kMatLd + lane % 16] = __ushort_as_bfloat16(static_cast<unsigned short>(p[q]));
+        for (int q = 0; q < 3; ++q) m[q * kMat + mat_at(t, lane % 16)] = __ushort_as_bfloat16(static_cast<unsigned short>(p[q]));
     }
 }
+
+// shared-memory offsets (elements) of this lane in a B operand: rows as they
+// lie (row = column of the product) and transposed (row = its k)
+__device__ __forceinline__ int b_plain(int lane, int ld) { return ((lane & 7) + (lane >> 4) * 8) * ld + ((lane >> 3) & 1) * 8; }
+__device__ __forceinline__ int b_trans(int lane, int ld) { return ((lane & 7) + ((lane >> 3) & 1) * 8) * ld + (lane >> 4) * 8; }
+// and in a 16 x 16 matrix
+__device__ __forceinline__ int m_plain(int lane) { return mat_at((lane & 7) + (lane >> 4) * 8, ((lane >> 3) & 1) * 8); }
+__device__ __forceinline__ int m_trans(int lane) { return mat_at((lane & 7) + ((lane >> 3) & 1) * 8, (lane >> 4) * 8); }
 
 // A 16-token x 16-line tile of staged rows, transposed, in the accumulator
 // layout: x[n][i] is line lane / 4 + 8 (i / 2), token 8 n + 2 (lane % 4) + i % 2.
@@ -265,27 +299,24 @@ __device__ __forceinline__ void load_lines(float (&x)[2][4], const IO* rows, int
     }
 }
 
-// Such a tile to rows of global memory (row t at out + t * stride), rows
-// below nt.  bfloat16 goes through `rows`, a staged tile that only this warp
-// uses, to 16-byte stores.
+// One of its 8-token halves to rows of global memory (row t at out + t *
+// stride), rows below nt.  bfloat16 goes through `rows`, a place of eight
+// staged rows of its own, to 16-byte stores.
 template <typename OUT, typename IO>
-__device__ __forceinline__ void store_lines(OUT* out, int64_t stride, int nt, const float (&x)[2][4], IO* rows, int ld,
-                                            bool vec, int lane) {
+__device__ __forceinline__ void store_half(OUT* out, int64_t stride, int nt, const float (&x)[4], IO* rows, int ld, bool vec,
+                                           int lane) {
     if constexpr (sizeof(OUT) == 2) {
-        uint32_t f[4];
+        uint32_t f[2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int hrow = 0; hrow < 2; ++hrow) {
-                const __nv_bfloat162 v2 = __floats2bfloat162_rn(x[n][2 * hrow], x[n][2 * hrow + 1]);
-                f[2 * n + hrow] = *reinterpret_cast<const uint32_t*>(&v2);
-            }
-        const int m = lane >> 3;
-        stsm4t(smem_u32(rows + ((lane & 7) + (m >> 1) * 8) * ld + (m & 1) * 8), f);
+        for (int q = 0; q < 2; ++q) {
+            const __nv_bfloat162 v2 = __floats2bfloat162_rn(x[2 * q], x[2 * q + 1]);
+            f[q] = *reinterpret_cast<const uint32_t*>(&v2);
+        }
+        stsm2t(smem_u32(rows + (lane & 7) * ld + ((lane >> 3) & 1) * 8), f);
         __syncwarp();
-        const int t = lane / 2, col = (lane % 2) * 8;
+        const int t = (lane / 2) % 8, col = (lane % 2) * 8;
         const uint4 v4 = *reinterpret_cast<const uint4*>(rows + t * ld + col);
-        if (t < nt) {
+        if (lane < 16 && t < nt) {
             OUT* o = out + t * stride + col;
             if (vec) {
                 *reinterpret_cast<uint4*>(o) = v4;
@@ -298,12 +329,10 @@ __device__ __forceinline__ void store_lines(OUT* out, int64_t stride, int nt, co
         }
     } else {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 8 * n + 2 * (lane % 4) + (i & 1);
-                if (t < nt) out[t * stride + lane / 4 + (i >> 1) * 8] = x[n][i];
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int t = 2 * (lane % 4) + (i & 1);
+            if (t < nt) out[t * stride + lane / 4 + (i >> 1) * 8] = x[i];
+        }
     }
 }
 
@@ -371,117 +400,116 @@ __device__ __forceinline__ void fade_add(float (&s)[4], float f, const float (&d
     const F2 a = fma2(f2(s[0], s[1]), f2s(f), f2(d[0], d[1])), b = fma2(f2(s[2], s[3]), f2s(f), f2(d[2], d[3]));
     s[0] = f2lo(a), s[1] = f2hi(a), s[2] = f2lo(b), s[3] = f2hi(b);
 }
-// shared-memory offsets (elements) of this lane in a B operand: rows as they
-// lie (row = column of the product) and transposed (row = its k)
-__device__ __forceinline__ int b_plain(int lane, int ld) { return ((lane & 7) + (lane >> 4) * 8) * ld + ((lane >> 3) & 1) * 8; }
-__device__ __forceinline__ int b_trans(int lane, int ld) { return ((lane & 7) + ((lane >> 3) & 1) * 8) * ld + (lane >> 4) * 8; }
-
-// sum over this warp's 16 lines of x * y for each token of the chunk, to
-// out[token * stride] (tokens below nt)
-__device__ __forceinline__ void token_sums(float* out, int64_t stride, int nt, const float (&x)[2][4], const float (&y)[2][4],
-                                           int lane) {
-    float s[2][2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) s[n][q] = fmaf(x[n][q], y[n][q], x[n][q + 2] * y[n][q + 2]);
-    // lanes 4 apart hold the same tokens: halve what a lane carries, then the lanes
-    const bool b0 = lane & 4, b1 = lane & 8;
-    float u[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) u[q] = (b0 ? s[1][q] : s[0][q]) + __shfl_xor_sync(0xffffffffu, b0 ? s[0][q] : s[1][q], 4);
-    float v = (b1 ? u[1] : u[0]) + __shfl_xor_sync(0xffffffffu, b1 ? u[0] : u[1], 8);
-    v += __shfl_xor_sync(0xffffffffu, v, 16);
-    const int t = (b0 ? 8 : 0) + 2 * (lane % 4) + (b1 ? 1 : 0);
-    if (lane < 16 && t < nt) out[t * stride] = v;
-}
-
-// Shared memory of the two walks over value columns: K and R with V (or dY),
-// two stages, each with its chunks' matrices.  ROPS: R is staged too; MATS:
-// 16 x 16 matrices (pieces) a chunk; SCS: factors a token; VT: tiles of values
-// (V or dY, V).
-template <typename IO, int N, int NW, bool ROPS, int MATS, int SCS, int VT = 1>
-struct MmaColumns {
+// The walks over value columns.  ROPS: R is staged too; MATS: 16 x 16
+// matrices (pieces) a chunk; SCS: factors a token.
+template <typename IO, int N, bool ROPS, int MATS, int SCS>
+struct Columns {
     static constexpr int KP = sizeof(IO) == 2 ? 1 : 3;           // pieces of K and R
-    static constexpr int CW = 16 * NW, SLICES = N / CW;
-    static constexpr int WALK = 32 * NW, STAGERS = 64, THREADS = WALK + STAGERS;
-    // tokens staged at a time: two CTAs of 64 channels fit an SM
-    static constexpr int BLK = KP == 3 || N == 128 ? 32 : 64;
-    static constexpr int NCH = BLK / kChunk;
-    static constexpr int LD = N + 8, PIECE = BLK * LD;
+    static constexpr int NW = N == 32 ? 2 : 4;                   // walking warps
+    static constexpr int CW = 16 * NW, SLICES = N / CW, NST = 4;
+    static constexpr int WALK = 32 * NW, THREADS = WALK + 32 * NST;
+    static constexpr int BAR = WALK + 32;                        // threads of a stage's barriers
+    static constexpr int LD = N + 8, PIECE = kChunk * LD;
     static constexpr int OPS = (ROPS ? 2 : 1) * KP * PIECE;
-    static constexpr int LDV = KP == 1 ? CW + 8 : CW + 4, VEL = BLK * LDV;   // V in the I/O type
-    static constexpr int LDR = N, ROW = BLK * LDR;                           // raw float32 rows
-    static constexpr int MAT = kChunk * kMatLd;
+    static constexpr int LDV = KP == 1 ? CW + 8 : CW + 4, VEL = kChunk * LDV;   // V in the I/O type
     // bytes of a stage, in order
-    static constexpr int S_OPS = OPS * 2, S_V = VT * VEL * int(sizeof(IO)), S_MAT = NCH * MATS * MAT * 2;
-    static constexpr int S_SC = (2 + SCS) * BLK * 4;                         // w, beta, factors
-    static constexpr int STAGE = S_OPS + S_V + S_MAT + S_SC;
-    static constexpr int B_RAW = KP == 1 ? 0 : (ROPS ? 2 : 1) * ROW * 4;
-    static constexpr int SCR = 16 * 17 + 8 + 16 * 20;                        // floats of a staging warp
-    static constexpr int SMEM = 2 * STAGE + B_RAW + STAGERS / 32 * SCR * 4;
+    static constexpr int S_OPS = OPS * 2, S_V = VEL * int(sizeof(IO)), S_MAT = MATS * kMat * 2;
+    static constexpr int S_SC = (SCS + 1) * kChunk * 4;                         // factors, beta
+    static constexpr int S_OWN = kChunk * 8 + 16 * 20 * 4;                      // the staging warp's
+    static constexpr int STAGE = S_OPS + S_V + S_MAT + S_SC + S_OWN;
+    static constexpr int SMEM = NST * STAGE;
 
     __nv_bfloat16* k;
     IO* v;
     __nv_bfloat16* mats;
-    float *w, *beta, *sc;
-    __device__ __forceinline__ MmaColumns(char* smem, int st) {
+    float *sc, *diag, *beta;
+    float2* sums;
+    __device__ __forceinline__ Columns(char* smem, int st) {
         char* p = smem + st * STAGE;
         k = reinterpret_cast<__nv_bfloat16*>(p);
         v = reinterpret_cast<IO*>(p + S_OPS);
         mats = reinterpret_cast<__nv_bfloat16*>(p + S_OPS + S_V);
-        w = reinterpret_cast<float*>(p + S_OPS + S_V + S_MAT);
-        beta = w + BLK;
-        sc = w + 2 * BLK;
+        diag = reinterpret_cast<float*>(p + S_OPS + S_V + S_MAT);
+        sums = reinterpret_cast<float2*>(diag + 16 * 20);
+        beta = reinterpret_cast<float*>(sums + kChunk);
+        sc = beta + kChunk;
     }
     __device__ __forceinline__ __nv_bfloat16* r() const { return k + KP * PIECE; }
-    __device__ __forceinline__ float* scratch(char* smem, int i) const {
-        return reinterpret_cast<float*>(smem + 2 * STAGE + B_RAW) + i * SCR;
-    }
-    // rows t0 .. of every tensor (the staging warps)
-    __device__ __forceinline__ void fetch(char* smem, const IO* kp, const IO* rp, int64_t ks, const IO* vp, const IO* vp2,
-                                          int64_t vs, const float* wp, const float* bp, int64_t H, int64_t t0, int nt, bool vec, int tid) {
+    // a chunk's rows of every tensor (one warp)
+    __device__ __forceinline__ void fetch(const IO* kp, const IO* rp, int64_t ks, const IO* vp, int64_t vs, int nt, bool vec,
+                                          int lane) {
+        copy_rows<IO, kChunk, CW, LDV>(v, vp, vs, nt, vec, lane);
         if constexpr (KP == 1) {
-            copy_rows<IO, BLK, N, LD, STAGERS>(reinterpret_cast<IO*>(k), kp + t0 * ks, ks, nt, vec, tid);
-            if constexpr (ROPS) copy_rows<IO, BLK, N, LD, STAGERS>(reinterpret_cast<IO*>(r()), rp + t0 * ks, ks, nt, vec, tid);
-        } else {
-            float* raw = reinterpret_cast<float*>(smem + 2 * STAGE);
-            copy_rows<float, BLK, N, LDR, STAGERS>(raw, reinterpret_cast<const float*>(kp) + t0 * ks, ks, nt, vec, tid);
-            if constexpr (ROPS)
-                copy_rows<float, BLK, N, LDR, STAGERS>(raw + ROW, reinterpret_cast<const float*>(rp) + t0 * ks, ks, nt, vec, tid);
-        }
-        copy_rows<IO, BLK, CW, LDV, STAGERS>(v, vp + t0 * vs, vs, nt, vec, tid);
-        if constexpr (VT == 2) copy_rows<IO, BLK, CW, LDV, STAGERS>(v + VEL, vp2 + t0 * vs, vs, nt, vec, tid);
-        for (int t = tid; t < BLK; t += STAGERS) {
-            w[t] = t < nt ? wp[(t0 + t) * H] : 0.f;
-            beta[t] = t < nt ? bp[(t0 + t) * H] : 0.f;
+            copy_rows<IO, kChunk, N, LD>(reinterpret_cast<IO*>(k), kp, ks, nt, vec, lane);
+            if constexpr (ROPS) copy_rows<IO, kChunk, N, LD>(reinterpret_cast<IO*>(r()), rp, ks, nt, vec, lane);
         }
         cp_async_commit();
-        cp_async_wait();
-        bar_sync<STAGERS>(kBarStage);
         if constexpr (KP == 3) {
-            const float* raw = reinterpret_cast<const float*>(smem + 2 * STAGE);
-            split_rows<BLK, N, LDR, LD, 3, STAGERS>(k, PIECE, raw, tid);
-            if constexpr (ROPS) split_rows<BLK, N, LDR, LD, 3, STAGERS>(r(), PIECE, raw + ROW, tid);
-            bar_sync<STAGERS>(kBarStage);
+            split_rows<kChunk, N, LD, 3>(k, PIECE, reinterpret_cast<const float*>(kp), ks, nt, vec, lane);
+            if constexpr (ROPS) split_rows<kChunk, N, LD, 3>(r(), PIECE, reinterpret_cast<const float*>(rp), ks, nt, vec, lane);
         }
+        cp_async_wait();
+        __syncwarp();
     }
 };
 
-// what only reaches y takes this many orders
+// S^T of a warp from / to a state S[key][value]: tile n holds keys 8 n .. 8 n + 7
+// of line lane / 4 (+ 8)
+template <int N>
+__device__ __forceinline__ void load_state(float (&S)[N / 8][4], const float* s, int lane) {
+#pragma unroll
+    for (int n = 0; n < N / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            S[n][i] = s != nullptr ? s[(8 * n + 2 * (lane % 4) + (i & 1)) * N + lane / 4 + (i >> 1) * 8] : 0.f;
+}
+template <int N>
+__device__ __forceinline__ void store_state(float* s, const float (&S)[N / 8][4], int lane) {
+#pragma unroll
+    for (int n = 0; n < N / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[(8 * n + 2 * (lane % 4) + (i & 1)) * N + lane / 4 + (i >> 1) * 8] = S[n][i];
+}
+// and as it lies, S^T[value][key], for the reverse mode
+template <int N>
+__device__ __forceinline__ void keep_state(float* s, const float (&S)[N / 8][4], int lane) {
+#pragma unroll
+    for (int n = 0; n < N / 8; ++n)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<float2*>(s + (lane / 4 + 8 * q) * N + 8 * n + 2 * (lane % 4)) = make_float2(S[n][2 * q], S[n][2 * q + 1]);
+}
+
+// what only reaches an output takes this many orders
 template <typename IO>
 constexpr int kOutOrders = sizeof(IO) == 2 ? 2 : 3;
 
-// Outputs y (WANT_Y) or the errors e for the reverse mode (float32).  Two
-// warps stage and prepare a block ahead; the others walk.
-template <typename IO, int N, int NW, bool WANT_Y>
-using ForwardShape = MmaColumns<IO, N, NW, WANT_Y, 3 + (WANT_Y ? kOutOrders<IO> : 0), 2>;
+// CTAs an SM: two where the state's lines and the I/O type leave room
+template <typename IO, int N>
+constexpr int kCtas = N <= 64 && sizeof(IO) == 2 ? 2 : 1;
+// Two walks of heads of 64 in bfloat16 fit an SM with 128 registers a thread on
+// average: the walking warps take 168 and the staging warps keep 88 (four
+// warps each, 128 * 168 + 128 * 88 = 256 * 128, what the CTA has).
+template <typename IO, int N>
+constexpr bool kShareRegs = N == 64 && sizeof(IO) == 2;
+template <typename IO, int N>
+__device__ __forceinline__ void stager_regs() {
+    if constexpr (kShareRegs<IO, N>) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+}
+template <typename IO, int N>
+__device__ __forceinline__ void walker_regs() {
+    if constexpr (kShareRegs<IO, N>) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+}
 
-template <typename IO, int N, int NW, bool WANT_Y>
-__global__ void __launch_bounds__(ForwardShape<IO, N, NW, WANT_Y>::THREADS, N == 64 && sizeof(IO) == 2 ? 2 : 1)
-delta_forward_mma_kernel(const Args a) {
-    using G = ForwardShape<IO, N, NW, WANT_Y>;
-    constexpr int KP = G::KP, PP = kOutOrders<IO>, LD = G::LD, NT = N / 8, BLK = G::BLK, MATS = 3 + (WANT_Y ? PP : 0);
+// Outputs y (WANT_Y), or the errors e and the states between segments for the
+// reverse mode (float32).
+template <typename IO, int N, bool WANT_Y>
+using ForwardShape = Columns<IO, N, WANT_Y, 3 + (WANT_Y ? kOutOrders<IO> : 0), 2>;
+
+template <typename IO, int N, bool WANT_Y>
+__global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO, N>) delta_forward_mma_kernel(const Args a) {
+    using G = ForwardShape<IO, N, WANT_Y>;
+    constexpr int KP = G::KP, PP = kOutOrders<IO>, LD = G::LD;
     extern __shared__ __align__(16) char smem[];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
 
@@ -493,158 +521,150 @@ delta_forward_mma_kernel(const Args a) {
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    if (warp >= NW) {
+    if (warp >= G::NW) {
+        stager_regs<IO, N>();
+        const int st = warp - G::NW;
         const int64_t ks = a.Hk * N;
         const IO* kp = static_cast<const IO*>(a.k) + (b * a.T * a.Hk + hk) * N;
         const IO* rp = static_cast<const IO*>(a.r) + (b * a.T * a.Hk + hk) * N;
-        const int tl = lane % 16;
-        int st = 0;
-        for (int64_t t0 = 0; t0 < a.T; t0 += BLK, st ^= 1) {
-            const int nt = a.T - t0 < BLK ? int(a.T - t0) : BLK;
-            G g(smem, st);
-            if (t0 >= 2 * BLK) bar_sync<G::THREADS>(kBarFree + st);
-            g.fetch(smem, kp, rp, ks, static_cast<const IO*>(a.v) + vbase, nullptr, vs, a.w + b * a.T * a.H + h,
-                    a.beta + b * a.T * a.H + h, a.H, t0, nt, a.vec, tid - G::WALK);
-            float* gam = g.scratch(smem, warp - NW);
-            float* amat = gam + 16 * 17 + 8;
+        const IO* vp = static_cast<const IO*>(a.v) + vbase;
+        const float* wp = a.w + b * a.T * a.H + h;
+        const float* bp = a.beta + b * a.T * a.H + h;
+        G g(smem, st);
+#pragma unroll 1
+        for (int64_t t0 = st * kChunk; t0 < a.T; t0 += G::NST * kChunk) {
+            const int nt = a.T - t0 < kChunk ? int(a.T - t0) : kChunk;
+            if (t0 >= G::NST * kChunk) bar_sync<G::BAR>(kBarFree + st);
+            const float w = lane < nt ? wp[(t0 + lane) * a.H] : 0.f, be = lane < nt ? bp[(t0 + lane) * a.H] : 0.f;
+            g.fetch(kp + t0 * ks, rp + t0 * ks, ks, vp + t0 * vs, vs, nt, a.vec, lane);
             // A, its inverse and P
-            for (int c = warp - NW; c * kChunk < nt; c += G::STAGERS / 32) {
-                const ChunkDecay d = chunk_decay(g.w + c * kChunk, gam, lane);
-                if (lane < 16) {
-                    g.sc[c * kChunk + tl] = d.upto;
-                    g.sc[BLK + c * kChunk + tl] = d.after * g.beta[c * kChunk + tl];
-                }
-                __syncwarp();
-                const __nv_bfloat16* kc = g.k + c * kChunk * LD;
-                float kk[2][4], rk[2][4];
-                gram<N, KP, KP, KP>(kk, kc, kc, G::PIECE, lane);
-                if constexpr (WANT_Y) gram<N, KP, KP, KP>(rk, g.r() + c * kChunk * LD, kc, G::PIECE, lane);
-                __nv_bfloat16* tm = g.mats + c * MATS * G::MAT;
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float2 bs = pair_at(g.beta + c * kChunk, n, lane);
-                    const int s = 8 * n + 2 * (lane % 4);
-#pragma unroll
-                    for (int hrow = 0; hrow < 2; ++hrow) {
-                        const int t = lane / 4 + 8 * hrow;
-                        const float g0 = gam[t * 17 + s] * bs.x, g1 = gam[t * 17 + s + 1] * bs.y;
-                        amat[t * 20 + s] = s < t ? g0 * kk[n][2 * hrow] : 0.f;
-                        amat[t * 20 + s + 1] = s + 1 < t ? g1 * kk[n][2 * hrow + 1] : 0.f;
-                        if constexpr (WANT_Y)
-                            put_pieces<PP>(tm + 3 * G::MAT, t, s, g0 * rk[n][2 * hrow], g1 * rk[n][2 * hrow + 1]);
-                    }
-                }
-                __syncwarp();
-                put_inverse(tm, amat, lane);
-                __syncwarp();
+            const ChunkDecay d = chunk_decay<kChunk>(w, g.sums, lane);
+            if (lane < kChunk) {
+                g.beta[lane] = be;
+                g.sc[lane] = d.upto;
+                g.sc[kChunk + lane] = d.after * be;
             }
-            bar_arrive<G::THREADS>(kBarFull + st);
+            __syncwarp();
+            float kk[2][4], rk[2][4];
+            gram<N, KP, KP, KP>(kk, g.k, g.k, G::PIECE, lane);
+            if constexpr (WANT_Y) gram<N, KP, KP, KP>(rk, g.r(), g.k, G::PIECE, lane);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float2 bs = pair_at(g.beta, n, lane);
+                const int s = 8 * n + 2 * (lane % 4);
+                const float2 s0 = g.sums[s], s1 = g.sums[s + 1];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int t = lane / 4 + 8 * q;
+                    const float2 tt = g.sums[t];
+                    const float g0 = decay_of(tt, s0) * bs.x, g1 = decay_of(tt, s1) * bs.y;
+                    g.diag[t * 20 + s] = s < t ? g0 * kk[n][2 * q] : 0.f;
+                    g.diag[t * 20 + s + 1] = s + 1 < t ? g1 * kk[n][2 * q + 1] : 0.f;
+                    if constexpr (WANT_Y)
+                        put_pieces<PP>(g.mats + 3 * kMat, t, s, s <= t ? g0 * rk[n][2 * q] : 0.f,
+                                       s + 1 <= t ? g1 * rk[n][2 * q + 1] : 0.f);
+                }
+            }
+            __syncwarp();
+            put_inverse(g.mats, g.diag, lane);
+            bar_arrive<G::BAR>(kBarFull + st);
         }
         return;
     }
 
+    walker_regs<IO, N>();
     const int j0 = warp * 16;
-    // S^T: tile n holds keys 8 n .. 8 n + 7 of values j0 + lane / 4 (+ 8)
-    float S[NT][4];
-    {
-        const float* s = a.s_in + head * N * N + slice + j0 + lane / 4;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int key = 8 * n + 2 * (lane % 4) + (i & 1);
-                S[n][i] = a.s_in != nullptr ? s[key * N + (i >> 1) * 8] : 0.f;
-            }
-    }
-    const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = b_plain(lane, kMatLd);
+    const int64_t nseg = (a.T + kSegment - 1) / kSegment;
+    const int64_t place = int64_t(slice + j0) * N;   // in a kept state
+    float* keep = a.s_seg + head * (nseg + 1) * N * N + place;
+    float S[N / 8][4];
+    load_state<N>(S, a.s_in == nullptr ? nullptr : a.s_in + head * N * N + slice + j0, lane);
+    const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = m_plain(lane);
     int st = 0;
-    for (int64_t t0 = 0; t0 < a.T; t0 += BLK, st ^= 1) {
-        const int nt = a.T - t0 < BLK ? int(a.T - t0) : BLK;
-        G g(smem, st);
-        bar_sync<G::THREADS>(kBarFull + st);
 #pragma unroll 1
-        for (int c = 0; c * kChunk < nt; ++c) {
-            const __nv_bfloat16* kc = g.k + c * kChunk * LD;
-            const __nv_bfloat16* rc = g.r() + c * kChunk * LD;
-            const __nv_bfloat16* tm = g.mats + c * MATS * G::MAT;
-            const float* gt = g.sc + c * kChunk;
-            // K S and R S, transposed
+    for (int64_t t0 = 0; t0 < a.T; t0 += kChunk, st = (st + 1) % G::NST) {
+        const int nt = a.T - t0 < kChunk ? int(a.T - t0) : kChunk;
+        G g(smem, st);
+        if (!WANT_Y && t0 % kSegment == 0) keep_state<N>(keep + t0 / kSegment * N * N, S, lane);
+        bar_sync<G::BAR>(kBarFull + st);
+        // K S and R S, transposed
+        float p[2][4], q[2][4], x[2][4];
+        {
             Acc pa, qa;
 #pragma unroll
             for (int kk = 0; kk < N / 16; ++kk) {
                 uint32_t sp[3][4];
                 split_a<3>(S[2 * kk], S[2 * kk + 1], sp);
-                times<3, KP, 3, false>(pa, kk == 0, sp, kc + kk * 16, G::PIECE, off_b);
-                if constexpr (WANT_Y) times<3, KP, PP, false>(qa, kk == 0, sp, rc + kk * 16, G::PIECE, off_b);
+                times<3, KP, 3, false>(pa, kk == 0, sp, g.k + kk * 16, G::PIECE, off_b);
+                if constexpr (WANT_Y) times<3, KP, PP, false>(qa, kk == 0, sp, g.r() + kk * 16, G::PIECE, off_b);
             }
-            // X = V - g K S
-            float x[2][4], p[2][4];
-            float2 gg[2];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) gg[n] = pair_at(gt, n, lane);
-            load_lines(x, g.v + c * kChunk * G::LDV + j0, G::LDV, lane);
             pa.sum(p);
+            if constexpr (WANT_Y) qa.sum(q);
+        }
+        load_lines(x, g.v + j0, G::LDV, lane);
+        // X = V - g K S
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const float2 gg = pair_at(g.sc, n, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[n][i] = fmaf(-((i & 1) ? gg.y : gg.x), p[n][i], x[n][i]);
+        }
+        // E = (I + A)^-1 X
+        float e[2][4];
+        {
+            uint32_t xp[3][4];
+            split_a<3>(x[0], x[1], xp);
+            Acc ea;
+            times<3, 3, 3, false>(ea, true, xp, g.mats, kMat, off_m);
+            ea.sum(e);
+        }
+        // S <- g_15 S + (G beta E)^T K
+        {
+            float u[2][4];
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[n][i] = fmaf(-((i & 1) ? gg[n].y : gg[n].x), p[n][i], x[n][i]);
-            // E = (I + A)^-1 X
-            float e[2][4];
-            {
-                uint32_t xp[3][4];
-                split_a<3>(x[0], x[1], xp);
-                Acc ea;
-                times<3, 3, 3, false>(ea, true, xp, tm, G::MAT, off_m);
-                ea.sum(e);
-            }
-            // S <- g_15 S + (G beta E)^T K
-            {
-                float u[2][4];
+                for (int i = 0; i < 4; ++i) u[n][i] = e[n][i];
+            scale_tokens(u, g.sc + kChunk, lane);
+            uint32_t up[3][4];
+            split_a<3>(u[0], u[1], up);
+            const float gl = g.sc[kChunk - 1];
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) u[n][i] = e[n][i];
-                scale_tokens(u, gt + BLK, lane);
-                uint32_t up[3][4];
-                split_a<3>(u[0], u[1], up);
-                const float gl = gt[kChunk - 1];
-#pragma unroll
-                for (int kk = 0; kk < N / 16; ++kk) {
-                    float d[2][4];
-                    times_add<3, KP>(d, true, up, kc + kk * 16, G::PIECE, off_t);
-                    fade_add(S[2 * kk], gl, d[0]);
-                    fade_add(S[2 * kk + 1], gl, d[1]);
-                }
-            }
-            const int64_t at = vbase + (t0 + c * kChunk) * vs + j0;
-            if constexpr (!WANT_Y) {
-                store_lines(a.e + at, vs, nt - c * kChunk, e, g.v, 0, false, lane);
-            } else {
-                // Y = g R S + P E
-                uint32_t ep[PP][4];
-                split_a<PP>(e[0], e[1], ep);
-                Acc ya;
-                times<PP, PP, PP, false>(ya, true, ep, tm + 3 * G::MAT, G::MAT, off_m);
-                float y[2][4], q[2][4];
-                qa.sum(q);
-                ya.sum(y);
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[n][i] = fmaf((i & 1) ? gg[n].y : gg[n].x, q[n][i], y[n][i]);
-                // through the V tile's columns, which only this warp reads
-                store_lines(static_cast<IO*>(a.y) + at, vs, nt - c * kChunk, y, g.v + c * kChunk * G::LDV + j0, G::LDV, a.vec,
-                            lane);
+            for (int kk = 0; kk < N / 16; ++kk) {
+                float d[2][4];
+                times_add<3, KP>(d, true, up, g.k + kk * 16, G::PIECE, off_t);
+                fade_add(S[2 * kk], gl, d[0]);
+                fade_add(S[2 * kk + 1], gl, d[1]);
             }
         }
-        if (t0 + 2 * BLK < a.T) bar_arrive<G::THREADS>(kBarFree + st);
+        const int64_t at = vbase + t0 * vs + j0;
+        if constexpr (!WANT_Y) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+                store_half(a.e + at + 8 * n * vs, vs, nt - 8 * n, e[n], g.v, 0, false, lane);
+        } else {
+            // Y = g R S + P E
+            uint32_t ep[PP][4];
+            split_a<PP>(e[0], e[1], ep);
+            Acc ya;
+            times<PP, PP, PP, false>(ya, true, ep, g.mats + 3 * kMat, kMat, off_m);
+            float y[2][4];
+            ya.sum(y);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float2 gg = pair_at(g.sc, n, lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[n][i] = fmaf((i & 1) ? gg.y : gg.x, q[n][i], y[n][i]);
+                // through the V tile's columns, which only this warp reads
+                store_half(static_cast<IO*>(a.y) + at + 8 * n * vs, vs, nt - 8 * n, y[n], g.v + 8 * n * G::LDV + j0, G::LDV, a.vec, lane);
+            }
+        }
+        if (t0 + G::NST * kChunk < a.T) bar_arrive<G::BAR>(kBarFree + st);
     }
-    if (WANT_Y && a.s_out != nullptr) {
-        float* s = a.s_out + head * N * N + slice + j0 + lane / 4;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[(8 * n + 2 * (lane % 4) + (i & 1)) * N + (i >> 1) * 8] = S[n][i];
+    if constexpr (WANT_Y) {
+        if (a.s_out != nullptr) store_state<N>(a.s_out + head * N * N + slice + j0, S, lane);
+    } else {
+        keep_state<N>(keep + nseg * N * N, S, lane);
     }
 }
 

@@ -1,22 +1,24 @@
-// wkv_delta_mma_bwd.cuh -- reverse mode of the gated delta rule in chunks of
-// 16 tokens on the tensor cores (wkv_delta_mma.cuh has the notation, the
-// layouts and how float32 accuracy is kept).
+// wkv_delta_mma_bwd.cuh -- reverse mode of the gated delta rule on the tensor
+// cores (wkv_delta_mma.cuh has the notation, the layouts and how float32
+// accuracy is kept).
 //
 // Within a chunk left by gradient state D (of the state after it), G[t][s]
-// the decays of tokens s+1 .. t, g_t those of tokens 0 .. t, q_t those of
-// tokens t+1 .. 15:
+// the decays of tokens s+1 .. t, g_t those up to t, q_t those after t:
 //   (I + B)^T DU = diag(q) D^T K + P^T DY,   B[s][t] = G[s][t] beta_s k_s.k_t  (t < s)
 //                                            P[s][t] = G[s][t] r_s.k_t         (t <= s)
 //   dv = beta du
 //   D  <- g_15 D + R^T diag(g) DY - K^T diag(g beta) DU
-// with the state S that enters the chunk and u = beta e:
+// with the state S that enters and u = beta e:
 //   dr_t = g_t S dy_t + sum_{s<=t} G[t][s] (u_s.dy_t) k_s
 //   dk_t = q_t D u_t + sum_{s>=t} G[s][t] (dy_s.u_t) r_s - sum_{s>t} G[s][t] (dv_s.u_t) k_s
 //          - g_t S dv_t - sum_{s<t} G[t][s] (u_s.dv_t) k_s
-// Four walks: e (the forward kernel), du (value columns, backwards), the
-// state's part of dr and dk (key rows), the gradient state's part of dk (key
-// rows, backwards).  What only reaches dk, rounded to bfloat16, takes the
-// orders up to 2^-8; dr takes them all, as r.dr enters dw.
+// Two walks, for e and the states between segments of 64 tokens (the forward
+// kernel) and for du and the gradient states between them; with those, dr and
+// dk of a segment need nothing from the others, and a third kernel forms them
+// for every segment at once.  The inner product <D, S> between segments
+// comes from the second walk; dw continues from it within a segment.
+// What only reaches dk takes the orders that its type keeps; dr takes them
+// all, as r.dr enters dw.
 #pragma once
 
 #include "wkv_delta_mma.cuh"
@@ -25,16 +27,16 @@ namespace wkv {
 namespace delta {
 
 // ---------------------------------------------------------------------------
-// du, dv, the initial state's gradient, and dv.v for dw (value columns)
+// du, dv, the initial state's gradient and the gradient states between
+// segments (value columns, backwards)
 // ---------------------------------------------------------------------------
-template <typename IO, int N, int NW>
-using ReverseShape = MmaColumns<IO, N, NW, true, 6, 3, 2>;
+template <typename IO, int N>
+using ReverseShape = Columns<IO, N, true, 6, 3>;
 
-template <typename IO, int N, int NW>
-__global__ void __launch_bounds__(ReverseShape<IO, N, NW>::THREADS, N == 64 && sizeof(IO) == 2 ? 2 : 1)
-delta_reverse_mma_kernel(const Args a) {
-    using G = ReverseShape<IO, N, NW>;
-    constexpr int KP = G::KP, LD = G::LD, NT = N / 8, BLK = G::BLK;
+template <typename IO, int N>
+__global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) delta_reverse_mma_kernel(const Args a) {
+    using G = ReverseShape<IO, N>;
+    constexpr int KP = G::KP, LD = G::LD;
     extern __shared__ __align__(16) char smem[];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
 
@@ -43,490 +45,515 @@ delta_reverse_mma_kernel(const Args a) {
     const int64_t b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
     const int64_t vs = a.H * N;
     const int64_t vbase = (b * a.T * a.H + h) * N + slice;
-    const int64_t last = (a.T - 1) / BLK * BLK;
+    const int64_t last = (a.T - 1) / kChunk * kChunk;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    if (warp >= NW) {
+    if (warp >= G::NW) {
+        stager_regs<IO, N>();
+        const int st = warp - G::NW;
         const int64_t ks = a.Hk * N;
         const IO* kp = static_cast<const IO*>(a.k) + (b * a.T * a.Hk + hk) * N;
         const IO* rp = static_cast<const IO*>(a.r) + (b * a.T * a.Hk + hk) * N;
-        const int tl = lane % 16;
-        int st = 0;
-        for (int64_t t0 = last; t0 >= 0; t0 -= BLK, st ^= 1) {
-            const int nt = a.T - t0 < BLK ? int(a.T - t0) : BLK;
-            G g(smem, st);
-            if (last - t0 >= 2 * BLK) bar_sync<G::THREADS>(kBarFree + st);
-            g.fetch(smem, kp, rp, ks, static_cast<const IO*>(a.dy) + vbase, static_cast<const IO*>(a.v) + vbase, vs,
-                    a.w + b * a.T * a.H + h, a.beta + b * a.T * a.H + h, a.H, t0, nt, a.vec, tid - G::WALK);
-            float* gam = g.scratch(smem, warp - NW);
-            float* amat = gam + 16 * 17 + 8;
+        const IO* yp = static_cast<const IO*>(a.dy) + vbase;
+        const float* wp = a.w + b * a.T * a.H + h;
+        const float* bp = a.beta + b * a.T * a.H + h;
+        G g(smem, st);
+#pragma unroll 1
+        for (int64_t t0 = last - st * kChunk; t0 >= 0; t0 -= G::NST * kChunk) {
+            const int nt = a.T - t0 < kChunk ? int(a.T - t0) : kChunk;
+            if (last - t0 >= G::NST * kChunk) bar_sync<G::BAR>(kBarFree + st);
+            const float w = lane < nt ? wp[(t0 + lane) * a.H] : 0.f, be = lane < nt ? bp[(t0 + lane) * a.H] : 0.f;
+            g.fetch(kp + t0 * ks, rp + t0 * ks, ks, yp + t0 * vs, vs, nt, a.vec, lane);
             // B, its inverse and P
-            for (int c = warp - NW; c * kChunk < nt; c += G::STAGERS / 32) {
-                const ChunkDecay d = chunk_decay(g.w + c * kChunk, gam, lane);
-                if (lane < 16) {
-                    g.sc[c * kChunk + tl] = d.after;
-                    g.sc[BLK + c * kChunk + tl] = d.upto;
-                    g.sc[2 * BLK + c * kChunk + tl] = d.upto * g.beta[c * kChunk + tl];
-                }
-                __syncwarp();
-                const __nv_bfloat16* kc = g.k + c * kChunk * LD;
-                float kk[2][4], rk[2][4];
-                gram<N, KP, KP, KP>(kk, kc, kc, G::PIECE, lane);
-                gram<N, KP, KP, KP>(rk, g.r() + c * kChunk * LD, kc, G::PIECE, lane);
-                __nv_bfloat16* tm = g.mats + c * 6 * G::MAT;
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const int t = 8 * n + 2 * (lane % 4);
-#pragma unroll
-                    for (int hrow = 0; hrow < 2; ++hrow) {
-                        const int s = lane / 4 + 8 * hrow;
-                        const float bs = g.beta[c * kChunk + s];
-                        const float g0 = gam[s * 17 + t], g1 = gam[s * 17 + t + 1];
-                        amat[s * 20 + t] = t < s ? g0 * bs * kk[n][2 * hrow] : 0.f;
-                        amat[s * 20 + t + 1] = t + 1 < s ? g1 * bs * kk[n][2 * hrow + 1] : 0.f;
-                        put_pieces<3>(tm + 3 * G::MAT, s, t, g0 * rk[n][2 * hrow], g1 * rk[n][2 * hrow + 1]);
-                    }
-                }
-                __syncwarp();
-                put_inverse(tm, amat, lane);
-                __syncwarp();
+            const ChunkDecay d = chunk_decay<kChunk>(w, g.sums, lane);
+            if (lane < kChunk) {
+                g.beta[lane] = be;
+                g.sc[lane] = d.after;
+                g.sc[kChunk + lane] = d.upto;
+                g.sc[2 * kChunk + lane] = d.upto * be;
             }
-            bar_arrive<G::THREADS>(kBarFull + st);
+            __syncwarp();
+            float kk[2][4], rk[2][4];
+            gram<N, KP, KP, KP>(kk, g.k, g.k, G::PIECE, lane);
+            gram<N, KP, KP, KP>(rk, g.r(), g.k, G::PIECE, lane);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int t = 8 * n + 2 * (lane % 4);
+                const float2 t0s = g.sums[t], t1s = g.sums[t + 1];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int s = lane / 4 + 8 * q;
+                    const float bs = g.beta[s];
+                    const float2 ss = g.sums[s];
+                    const float g0 = decay_of(ss, t0s), g1 = decay_of(ss, t1s);
+                    g.diag[s * 20 + t] = t < s ? g0 * bs * kk[n][2 * q] : 0.f;
+                    g.diag[s * 20 + t + 1] = t + 1 < s ? g1 * bs * kk[n][2 * q + 1] : 0.f;
+                    put_pieces<3>(g.mats + 3 * kMat, s, t, t <= s ? g0 * rk[n][2 * q] : 0.f,
+                                  t + 1 <= s ? g1 * rk[n][2 * q + 1] : 0.f);
+                }
+            }
+            __syncwarp();
+            put_inverse(g.mats, g.diag, lane);
+            bar_arrive<G::BAR>(kBarFull + st);
         }
         return;
     }
 
+    walker_regs<IO, N>();
     const int j0 = warp * 16;
-    float S[NT][4];   // D^T
-    {
-        const float* s = a.ds_out + head * N * N + slice + j0 + lane / 4;
+    const int64_t nseg = (a.T + kSegment - 1) / kSegment;
+    const int64_t place = head * (nseg + 1) * N * N + int64_t(slice + j0) * N;
+    const float* states = a.s_seg + place;
+    float* grads = a.d_seg + place;
+    constexpr int SLOTS = kSlots<N>;
+    float* phi = a.phi + head * (nseg + 1) * SLOTS + slice / 16 + warp;
+    float S[N / 8][4];   // D^T
+    load_state<N>(S, a.ds_out == nullptr ? nullptr : a.ds_out + head * N * N + slice + j0, lane);
+    // the gradient state behind segment c - 1, and its inner product with the state there
+    auto border = [&](int64_t c) {
+        keep_state<N>(grads + c * N * N, S, lane);
+        float x = 0.f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < N / 8; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                S[n][i] = a.ds_out != nullptr ? s[(8 * n + 2 * (lane % 4) + (i & 1)) * N + (i >> 1) * 8] : 0.f;
-    }
-    float* pv = a.pv + (slice / 16 + warp) * (a.B * a.T * a.H) + b * a.T * a.H + h;
-    const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = b_trans(lane, kMatLd);
+            for (int q = 0; q < 2; ++q) {
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(states + c * N * N + (lane / 4 + 8 * q) * N + 8 * n + 2 * (lane % 4)));
+                x = fmaf(S[n][2 * q], v.x, fmaf(S[n][2 * q + 1], v.y, x));
+            }
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane == 0) phi[c * SLOTS] = x;
+    };
+    border(nseg);
+    const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = m_trans(lane);
     int st = 0;
-    for (int64_t t0 = last; t0 >= 0; t0 -= BLK, st ^= 1) {
-        const int nt = a.T - t0 < BLK ? int(a.T - t0) : BLK;
-        G g(smem, st);
-        bar_sync<G::THREADS>(kBarFull + st);
 #pragma unroll 1
-        for (int c = (nt - 1) / kChunk; c >= 0; --c) {
-            const __nv_bfloat16* kc = g.k + c * kChunk * LD;
-            const __nv_bfloat16* rc = g.r() + c * kChunk * LD;
-            const __nv_bfloat16* tm = g.mats + c * 6 * G::MAT;
-            const float* sc = g.sc + c * kChunk;
-            IO* yt = g.v + c * kChunk * G::LDV + j0;
-            // diag(q) D^T K + P^T dY
-            float dy[2][4], x[2][4];
-            {
-                Acc pa;
+    for (int64_t t0 = last; t0 >= 0; t0 -= kChunk, st = (st + 1) % G::NST) {
+        const int nt = a.T - t0 < kChunk ? int(a.T - t0) : kChunk;
+        G g(smem, st);
+        bar_sync<G::BAR>(kBarFull + st);
+        // X = diag(q) D^T K + P^T dY
+        float dy[2][4], x[2][4];
+        {
+            Acc pa;
 #pragma unroll
-                for (int kk = 0; kk < N / 16; ++kk) {
-                    uint32_t sp[3][4];
-                    split_a<3>(S[2 * kk], S[2 * kk + 1], sp);
-                    times<3, KP, 3, false>(pa, kk == 0, sp, kc + kk * 16, G::PIECE, off_b);
-                }
-                pa.sum(x);
-                scale_tokens(x, sc, lane);
+            for (int kk = 0; kk < N / 16; ++kk) {
+                uint32_t sp[3][4];
+                split_a<3>(S[2 * kk], S[2 * kk + 1], sp);
+                times<3, KP, 3, false>(pa, kk == 0, sp, g.k + kk * 16, G::PIECE, off_b);
             }
-            load_lines(dy, yt, G::LDV, lane);
-            {
-                uint32_t yq[KP][4];
-                split_a<KP>(dy[0], dy[1], yq);
-                Acc ya;
-                times<KP, 3, 3, true>(ya, true, yq, tm + 3 * G::MAT, G::MAT, off_m);
-                float p[2][4];
-                ya.sum(p);
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[n][i] += p[n][i];
-            }
-            float du[2][4];
-            {
-                uint32_t xp[3][4];
-                split_a<3>(x[0], x[1], xp);
-                Acc ea;
-                times<3, 3, 3, true>(ea, true, xp, tm, G::MAT, off_m);
-                ea.sum(du);
-            }
-            // D <- g_15 D + (g dy)^T R - (g beta du)^T K
-            {
-                float f1[2][4];
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) f1[n][i] = -du[n][i];
-                scale_tokens(dy, sc + BLK, lane);
-                scale_tokens(f1, sc + 2 * BLK, lane);
-                uint32_t yq[3][4], uq[3][4];
-                split_a<3>(dy[0], dy[1], yq);
-                split_a<3>(f1[0], f1[1], uq);
-                const float gl = sc[BLK + kChunk - 1];
-#pragma unroll
-                for (int kk = 0; kk < N / 16; ++kk) {
-                    float d[2][4];
-                    times_add<3, KP>(d, true, uq, kc + kk * 16, G::PIECE, off_t);
-                    times_add<3, KP>(d, false, yq, rc + kk * 16, G::PIECE, off_t);
-                    fade_add(S[2 * kk], gl, d[0]);
-                    fade_add(S[2 * kk + 1], gl, d[1]);
-                }
-            }
-            const int64_t t = t0 + c * kChunk, at = vbase + t * vs + j0;
-            const int left = nt - c * kChunk;
-            store_lines(a.du + at, vs, left, du, yt, 0, false, lane);
-            scale_tokens(du, g.beta + c * kChunk, lane);
-            float v[2][4];
-            load_lines(v, yt + G::VEL, G::LDV, lane);
-            token_sums(pv + t * a.H, a.H, left, du, v, lane);
-            // dv through dy's columns, which only this warp reads
-            store_lines(static_cast<IO*>(a.dv) + at, vs, left, du, yt, G::LDV, a.vec, lane);
+            pa.sum(x);
         }
-        if (t0 >= 2 * BLK) bar_arrive<G::THREADS>(kBarFree + st);
-    }
-    if (a.ds_in != nullptr) {
-        float* s = a.ds_in + head * N * N + slice + j0 + lane / 4;
+        load_lines(dy, g.v + j0, G::LDV, lane);
+        scale_tokens(x, g.sc, lane);
+        {
+            uint32_t yq[KP][4];
+            split_a<KP>(dy[0], dy[1], yq);
+            Acc ya;
+            times<KP, 3, 3, true>(ya, true, yq, g.mats + 3 * kMat, kMat, off_m);
+            float p[2][4];
+            ya.sum(p);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[(8 * n + 2 * (lane % 4) + (i & 1)) * N + (i >> 1) * 8] = S[n][i];
+                for (int i = 0; i < 4; ++i) x[n][i] += p[n][i];
+        }
+        float du[2][4];
+        {
+            uint32_t xp[3][4];
+            split_a<3>(x[0], x[1], xp);
+            Acc ea;
+            times<3, 3, 3, true>(ea, true, xp, g.mats, kMat, off_m);
+            ea.sum(du);
+        }
+        // D <- g_15 D + (g dy)^T R - (g beta du)^T K
+        {
+            float f1[2][4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f1[n][i] = -du[n][i];
+            scale_tokens(dy, g.sc + kChunk, lane);
+            scale_tokens(f1, g.sc + 2 * kChunk, lane);
+            uint32_t yq[3][4], uq[3][4];
+            split_a<3>(dy[0], dy[1], yq);
+            split_a<3>(f1[0], f1[1], uq);
+            const float gl = g.sc[2 * kChunk - 1];
+#pragma unroll
+            for (int kk = 0; kk < N / 16; ++kk) {
+                float d[2][4];
+                times_add<3, KP>(d, true, uq, g.k + kk * 16, G::PIECE, off_t);
+                times_add<3, KP>(d, false, yq, g.r() + kk * 16, G::PIECE, off_t);
+                fade_add(S[2 * kk], gl, d[0]);
+                fade_add(S[2 * kk + 1], gl, d[1]);
+            }
+        }
+        const int64_t at = vbase + t0 * vs + j0;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            store_half(a.du + at + 8 * n * vs, vs, nt - 8 * n, du[n], g.v, 0, false, lane);
+            const float2 be = pair_at(g.beta, n, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) du[n][i] *= (i & 1) ? be.y : be.x;
+            // dv through dy's columns, which only this warp reads
+            store_half(static_cast<IO*>(a.dv) + at + 8 * n * vs, vs, nt - 8 * n, du[n], g.v + 8 * n * G::LDV + j0, G::LDV, a.vec, lane);
+        }
+        if (t0 >= G::NST * kChunk) bar_arrive<G::BAR>(kBarFree + st);
+        if (t0 % kSegment == 0) border(t0 / kSegment);
     }
+    if (a.ds_in != nullptr) store_state<N>(a.ds_in + head * N * N + slice + j0, S, lane);
 }
 
 // ---------------------------------------------------------------------------
-// Key rows: a warp owns 16 key rows of S (or D) for the whole value axis.
-// GRAD false: the state's walk forwards -- dr, the state's part of dk, dbeta,
-// r.dr for dw and the states at the borders of kCheck tokens.  GRAD true: the
-// gradient state's walk backwards -- the rest of dk and the border products
-// <D, S>.  dr and dk are final where no heads share a key head; otherwise the
-// value heads' own go to the workspace.
+// dr, dk, dbeta and dw of one segment.  A warp takes 16 tokens t and IC
+// channels i: the products with S and D, then the segment's 16 x 16 blocks of
+// (token, token) products, which turn from accumulators to A operands in
+// registers.  A row of blocks has 5 in all, those on the diagonal from both
+// sides, so the warps' work is even.
 // ---------------------------------------------------------------------------
-template <typename IO, int N, int NW, bool GRAD>
-struct MmaRows {
-    static constexpr int KP = sizeof(IO) == 2 ? 1 : 3;
-    static constexpr int PP = kOutOrders<IO>;                      // orders of what only reaches dk
-    static constexpr int KE = GRAD ? PP : 3, KD = GRAD ? 3 : PP;   // pieces of e and du
-    static constexpr int CW = 16 * NW, SLICES = N / CW, SLOTS = N / 16;
-    static constexpr int WALK = 32 * NW, STAGERS = 64, THREADS = WALK + STAGERS;
-    static constexpr int BLK = KP == 3 && N == 128 ? 16 : 32;      // what two stages leave room for
-    static constexpr int LD = N + 8, PIECE = BLK * LD, LDR = N, ROW = BLK * LDR;
-    static constexpr int LDV = KP == 1 ? CW + 8 : CW + 4, VEL = BLK * LDV;
-    static constexpr int MAT = kChunk * kMatLd, NCH = BLK / kChunk;
-    static constexpr int M0 = PP, M1 = GRAD ? PP : 3;              // pieces of the two 16 x 16 matrices
-    // bytes of a stage, in order: e, du, dy; k and r of the CTA's rows; matrices; w, beta, factors
-    static constexpr int S_OPS = (KE + KD + KP) * PIECE * 2, S_V = 2 * VEL * int(sizeof(IO));
-    static constexpr int S_MAT = NCH * (M0 + M1) * MAT * 2, S_SC = 5 * BLK * 4;
-    static constexpr int STAGE = S_OPS + S_V + S_MAT + S_SC;
-    static constexpr int B_RAW = (KP == 1 ? 2 : 3) * ROW * 4;      // e, du (, dy) as they come
-    static constexpr int SCR = 16 * 17;
-    static constexpr int SMEM = 2 * STAGE + B_RAW + STAGERS / 32 * SCR * 4;
-
-    __nv_bfloat16 *e, *du, *dy, *mats;
-    IO *k, *r;
-    float *w, *beta, *sc, *raw;
-    __device__ __forceinline__ MmaRows(char* smem, int st) {
-        char* p = smem + st * STAGE;
-        e = reinterpret_cast<__nv_bfloat16*>(p);
-        du = e + KE * PIECE;
-        dy = du + KD * PIECE;
-        k = reinterpret_cast<IO*>(p + S_OPS);
-        r = k + VEL;
-        mats = reinterpret_cast<__nv_bfloat16*>(p + S_OPS + S_V);
-        w = reinterpret_cast<float*>(p + S_OPS + S_V + S_MAT);
-        beta = w + BLK;
-        sc = w + 2 * BLK;
-        raw = reinterpret_cast<float*>(smem + 2 * STAGE);
-    }
+template <typename IO, int N>
+struct SegmentShape {
+    static constexpr int KP = sizeof(IO) == 2 ? 1 : 3, PP = kOutOrders<IO>;
+    static constexpr int IC = N < 64 ? N : 64, HALVES = N / IC;
+    static constexpr int WARPS = 4 * HALVES, THREADS = 32 * WARPS;
+    static constexpr int LD = N + 8, PIECE = kSegment * LD;
+    static constexpr int JB = N == 64 ? 64 : 32;              // value lines of S and D at a time
+    static constexpr int SPIECE = JB * LD;
+    static constexpr int KR = KP == 3 && N == 128 ? 16 : 64;  // tokens of K and R at a time
+    static constexpr int KPIECE = KR * LD;
+    // e, du, dy; S and D, later K and R; sums, beta and the sums over channels
+    static constexpr int S_ROWS = (3 + PP + KP) * PIECE * 2;
+    static constexpr int A_ = (3 + PP) * SPIECE * 2, B_ = 2 * KP * KPIECE * 2, S_BUF = A_ > B_ ? A_ : B_;
+    static constexpr int S_SUM = kSegment * (8 + 4 + 4 + 4 * HALVES);
+    static constexpr int SMEM = S_ROWS + S_BUF + S_SUM;
 };
 
-template <typename IO, int N, int NW, bool GRAD>
-__global__ void __launch_bounds__(MmaRows<IO, N, NW, GRAD>::THREADS, N == 64 && sizeof(IO) == 2 ? 2 : 1)
-delta_rows_mma_kernel(const Args a) {
-    using G = MmaRows<IO, N, NW, GRAD>;
-    constexpr int KP = G::KP, PP = G::PP, KE = G::KE, KD = G::KD, LD = G::LD, NT = N / 8, BLK = G::BLK;
+template <typename IO, int N>
+__global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, kCtas<IO, N>) delta_segment_kernel(const Args a) {
+    using G = SegmentShape<IO, N>;
+    constexpr int KP = G::KP, PP = G::PP, LD = G::LD, NP = G::IC / 16;
     extern __shared__ __align__(16) char smem[];
+    __nv_bfloat16* eb = reinterpret_cast<__nv_bfloat16*>(smem);
+    __nv_bfloat16* db = eb + 3 * G::PIECE;
+    __nv_bfloat16* yb = db + PP * G::PIECE;
+    __nv_bfloat16* buf = reinterpret_cast<__nv_bfloat16*>(smem + G::S_ROWS);
+    float2* sums = reinterpret_cast<float2*>(smem + G::S_ROWS + G::S_BUF);
+    float* beta = reinterpret_cast<float*>(sums + kSegment);
+    float* duv = beta + kSegment;     // du . v of a token
+    float* rdr = duv + kSegment;      // r . dr, by halves of the channels
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int tb = warp % 4, i0 = warp / 4 * G::IC;
 
-    const int64_t head = blockIdx.x / G::SLICES;
-    const int slice = int(blockIdx.x % G::SLICES) * G::CW;
+    const int64_t nseg = (a.T + kSegment - 1) / kSegment;
+    const int64_t head = blockIdx.x / nseg, seg = blockIdx.x % nseg;
     const int64_t b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
+    const int64_t t0 = seg * kSegment;
+    const int nt = a.T - t0 < kSegment ? int(a.T - t0) : kSegment;
     const int64_t ks = a.Hk * N, vs = a.H * N;
-    const int64_t base = (b * a.T * a.H + h) * N, scalar = b * a.T * a.H + h;
-    const int64_t last = (a.T - 1) / BLK * BLK;
-    const int64_t first = GRAD ? last : 0, step = GRAD ? -BLK : BLK;
-    const int64_t blocks = last / BLK + 1;
+    const int64_t rows = ((b * a.T + t0) * a.H + h) * N, keys = ((b * a.T + t0) * a.Hk + hk) * N;
+    const int64_t scalar = (b * a.T + t0) * a.H + h;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    if (warp >= NW) {
-        const int stid = tid - G::WALK, tl = lane % 16;
-        const IO* kp = static_cast<const IO*>(a.k) + (b * a.T * a.Hk + hk) * N + slice;
-        const IO* rp = static_cast<const IO*>(a.r) + (b * a.T * a.Hk + hk) * N + slice;
-        const IO* yp = static_cast<const IO*>(a.dy) + base;
-        int st = 0;
-        int64_t t0 = first;
-        for (int64_t i = 0; i < blocks; ++i, t0 += step, st ^= 1) {
-            const int nt = a.T - t0 < BLK ? int(a.T - t0) : BLK;
-            G g(smem, st);
-            // the raw rows are the stagers' own; the stage is the walkers' until they leave it
-            copy_rows<float, BLK, N, G::LDR, G::STAGERS>(g.raw, a.e + base + t0 * vs, vs, nt, true, stid);
-            copy_rows<float, BLK, N, G::LDR, G::STAGERS>(g.raw + G::ROW, a.du + base + t0 * vs, vs, nt, true, stid);
-            if constexpr (KP == 3)
-                copy_rows<float, BLK, N, G::LDR, G::STAGERS>(g.raw + 2 * G::ROW, reinterpret_cast<const float*>(yp) + t0 * vs,
-                                                             vs, nt, a.vec, stid);
-            if (i >= 2) bar_sync<G::THREADS>(kBarFree + st);
-            if constexpr (KP == 1)
-                copy_rows<IO, BLK, N, LD, G::STAGERS>(reinterpret_cast<IO*>(g.dy), yp + t0 * vs, vs, nt, a.vec, stid);
-            copy_rows<IO, BLK, G::CW, G::LDV, G::STAGERS>(g.k, kp + t0 * ks, ks, nt, a.vec, stid);
-            copy_rows<IO, BLK, G::CW, G::LDV, G::STAGERS>(g.r, rp + t0 * ks, ks, nt, a.vec, stid);
-            for (int t = stid; t < BLK; t += G::STAGERS) {
-                g.w[t] = t < nt ? a.w[scalar + (t0 + t) * a.H] : 0.f;
-                g.beta[t] = t < nt ? a.beta[scalar + (t0 + t) * a.H] : 0.f;
+    // --- the segment's rows: 16 / HALVES a warp
+    constexpr int RW = 16 / G::HALVES;
+    const int row = warp * RW, left = nt - row;
+    const int64_t rr = left > 0 ? row : 0;   // rows behind the last token: zeros, addressed at one that exists
+    if constexpr (KP == 1) {
+        copy_rows<IO, RW, N, LD>(reinterpret_cast<IO*>(yb) + row * LD, static_cast<const IO*>(a.dy) + rows + rr * vs, vs, left, a.vec,
+                                 lane);
+        cp_async_commit();
+    }
+    {
+        constexpr int ROWV = N / 4, ALL = RW * ROWV / 32, U = ALL < 4 ? ALL : 4;
+#pragma unroll 1
+        for (int n = 0; n < ALL; n += U) {
+            float4 x[U], y[U], v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = lane + (n + u) * 32, t = i / ROWV, c = (i % ROWV) * 4;
+                const int64_t at = rows + (row + t) * vs + c;
+                x[u] = y[u] = v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (t < left) {
+                    x[u] = load4(a.e + at, true);
+                    y[u] = load4(a.du + at, true);
+                    const IO* vp = static_cast<const IO*>(a.v) + at;
+                    if constexpr (KP == 3) {
+                        v[u] = load4(reinterpret_cast<const float*>(vp), a.vec);
+                    } else if (a.vec) {
+                        const uint2 w2 = __ldg(reinterpret_cast<const uint2*>(vp));
+                        v[u] = make_float4(__uint_as_float(w2.x << 16), __uint_as_float(w2.x & 0xffff0000u),
+                                           __uint_as_float(w2.y << 16), __uint_as_float(w2.y & 0xffff0000u));
+                    } else {
+                        v[u] = make_float4(to_f32(vp[0]), to_f32(vp[1]), to_f32(vp[2]), to_f32(vp[3]));
+                    }
+                }
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = lane + (n + u) * 32, t = i / ROWV, c = (i % ROWV) * 4;
+                put4<3>(eb + (row + t) * LD + c, G::PIECE, x[u]);
+                put4<PP>(db + (row + t) * LD + c, G::PIECE, y[u]);
+                float s = fmaf(x[u].x, y[u].x, fmaf(x[u].y, y[u].y, fmaf(x[u].z, y[u].z, x[u].w * y[u].w)));
+                float z = fmaf(v[u].x, y[u].x, fmaf(v[u].y, y[u].y, fmaf(v[u].z, y[u].z, v[u].w * y[u].w)));
+#pragma unroll
+                for (int o = ROWV / 2; o > 0; o /= 2) {
+                    s += __shfl_xor_sync(0xffffffffu, s, o);
+                    z += __shfl_xor_sync(0xffffffffu, z, o);
+                }
+                if (lane % ROWV == 0) {
+                    if (t < left) a.dbeta[scalar + (row + t) * a.H] = s;
+                    duv[row + t] = z;
+                }
+            }
+        }
+    }
+    if constexpr (KP == 3)
+        split_rows<RW, N, LD, 3>(yb + row * LD, G::PIECE, reinterpret_cast<const float*>(a.dy) + rows + row * vs, vs, left, a.vec, lane);
+    if (warp == 0) {   // the decays' running sum, two tokens a lane
+        const int ta = 2 * lane;
+        const float w0 = ta < nt ? a.w[scalar + ta * a.H] : 0.f, w1 = ta + 1 < nt ? a.w[scalar + (ta + 1) * a.H] : 0.f;
+        const double x0 = w0 > kMaxRate ? kMaxRate : w0, x1 = x0 + double(w1 > kMaxRate ? kMaxRate : w1);
+        double x = x1;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const double y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        sums[ta] = two_floats(x - x1 + x0);
+        sums[ta + 1] = two_floats(x);
+        beta[ta] = ta < nt ? a.beta[scalar + ta * a.H] : 0.f;
+        beta[ta + 1] = ta + 1 < nt ? a.beta[scalar + (ta + 1) * a.H] : 0.f;
+    }
+
+    // --- the products with S and D: C[t][i], tiles of 16 channels
+    float dr[NP][2][4], dk[NP][2][4];
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dr[p][n][i] = dk[p][n][i] = 0.f;
+    const int off_a = b_trans(lane, LD) + tb * 16 * LD;   // an A operand's rows lie as a transposed B's
+    const float* s_seg = a.s_seg + (head * (nseg + 1) + seg) * N * N;
+    const float* d_seg = a.d_seg + (head * (nseg + 1) + seg + 1) * N * N;
+    const int t_lo = tb * 16 + lane / 4;                  // this lane's rows: t_lo and t_lo + 8
+#pragma unroll 1
+    for (int jb = 0; jb < N; jb += G::JB) {
+        constexpr int RB = G::JB / G::WARPS;
+        if (jb > 0) __syncthreads();
+        split_rows<RB, N, LD, 3>(buf + warp * RB * LD, G::SPIECE, s_seg + (jb + warp * RB) * N, N, RB, true, lane);
+        split_rows<RB, N, LD, PP>(buf + 3 * G::SPIECE + warp * RB * LD, G::SPIECE, d_seg + (jb + warp * RB) * N, N, RB, true, lane);
+        if (KP == 1 && jb == 0) cp_async_wait();
+        __syncthreads();
+        float2 gq[2];   // of the lane's two rows: g, q
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            gq[q] = make_float2(decay_of(sums[t_lo + 8 * q], make_float2(0.f, 0.f)), decay_of(sums[kSegment - 1], sums[t_lo + 8 * q]));
+        const float b0 = beta[t_lo], b1 = beta[t_lo + 8];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            Acc ra, ka, da;
+#pragma unroll 2
+            for (int kk = 0; kk < G::JB / 16; ++kk) {
+                const int off = off_a + jb + kk * 16, so = b_trans(lane, LD) + kk * 16 * LD + i0 + p * 16;
+                uint32_t yq[KP][4], uq[PP][4], eq[PP][4];
+#pragma unroll
+                for (int c = 0; c < KP; ++c) ldsm4(yq[c], smem_u32(yb + c * G::PIECE + off));
+#pragma unroll
+                for (int c = 0; c < PP; ++c) {
+                    ldsm4(uq[c], smem_u32(db + c * G::PIECE + off));
+                    ldsm4(eq[c], smem_u32(eb + c * G::PIECE + off));
+                }
+                times<KP, 3, 3, true>(ra, kk == 0, yq, buf, G::SPIECE, so);
+                times<PP, 3, PP, true>(ka, kk == 0, uq, buf, G::SPIECE, so);
+                times<PP, PP, PP, true>(da, kk == 0, eq, buf + 3 * G::SPIECE, G::SPIECE, so);
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = gq[i >> 1];
+                    const float bt = (i >> 1) ? b1 : b0;
+                    dr[p][n][i] = fmaf(f.x, ra.hi[n][i] + ra.lo[n][i], dr[p][n][i]);
+                    dk[p][n][i] += bt * (f.y * (da.hi[n][i] + da.lo[n][i]) - f.x * (ka.hi[n][i] + ka.lo[n][i]));
+                }
+        }
+    }
+
+    // --- the blocks of token pairs
+    __nv_bfloat16 *kb = buf, *rb = buf + KP * G::KPIECE;
+    const IO* kp = static_cast<const IO*>(a.k) + keys;
+    const IO* rp = static_cast<const IO*>(a.r) + keys;
+    auto stage_keys = [&](int s0) {   // K and R, tokens s0 .. s0 + KR
+        constexpr int RB = G::KR / G::WARPS > 0 ? G::KR / G::WARPS : 1;
+        const int r0 = warp * RB, l = nt - s0 - r0;
+        if (r0 >= G::KR) return;
+        const int64_t at = l > 0 ? s0 + r0 : 0;
+        if constexpr (KP == 1) {
+            copy_rows<IO, RB, N, LD>(reinterpret_cast<IO*>(kb) + r0 * LD, kp + at * ks, ks, l, a.vec, lane);
+            copy_rows<IO, RB, N, LD>(reinterpret_cast<IO*>(rb) + r0 * LD, rp + at * ks, ks, l, a.vec, lane);
             cp_async_commit();
             cp_async_wait();
-            bar_sync<G::STAGERS>(kBarStage);
-            split_rows<BLK, N, G::LDR, LD, KE, G::STAGERS>(g.e, G::PIECE, g.raw, stid);
-            split_rows<BLK, N, G::LDR, LD, KD, G::STAGERS>(g.du, G::PIECE, g.raw + G::ROW, stid);
-            if constexpr (KP == 3) split_rows<BLK, N, G::LDR, LD, 3, G::STAGERS>(g.dy, G::PIECE, g.raw + 2 * G::ROW, stid);
-            if constexpr (!GRAD) {
-                if (slice == 0) {   // dbeta: du . e, eight lanes a token
-#pragma unroll
-                    for (int t = stid / 8; t < BLK; t += G::STAGERS / 8) {
-                        float x = 0.f;
-#pragma unroll
-                        for (int j = lane % 8; j < N; j += 8) x = fmaf(g.raw[t * G::LDR + j], g.raw[G::ROW + t * G::LDR + j], x);
-                        x += __shfl_xor_sync(0xffffffffu, x, 1);
-                        x += __shfl_xor_sync(0xffffffffu, x, 2);
-                        x += __shfl_xor_sync(0xffffffffu, x, 4);
-                        if (lane % 8 == 0 && t < nt) a.dbeta[scalar + (t0 + t) * a.H] = x;
-                    }
-                }
-            }
-            bar_sync<G::STAGERS>(kBarStage);
-            // the two matrices of each chunk, one a warp at a time
-            float* gam = reinterpret_cast<float*>(smem + 2 * G::STAGE + G::B_RAW) + (warp - NW) * G::SCR;
-            for (int j = warp - NW; j / 2 * kChunk < nt; j += G::STAGERS / 32) {
-                const int c = j / 2, which = j % 2;
-                const float* be = g.beta + c * kChunk;
-                const ChunkDecay d = chunk_decay(g.w + c * kChunk, gam, lane);
-                if (which == 0 && lane < 16) {
-                    g.sc[c * kChunk + tl] = d.upto;
-                    g.sc[BLK + c * kChunk + tl] = d.upto * be[tl];
-                    g.sc[2 * BLK + c * kChunk + tl] = d.after * be[tl];
-                }
-                __syncwarp();
-                const __nv_bfloat16 *ec = g.e + c * kChunk * LD, *dc = g.du + c * kChunk * LD, *yc = g.dy + c * kChunk * LD;
-                __nv_bfloat16* m = g.mats + (c * (G::M0 + G::M1) + (which ? G::M0 : 0)) * G::MAT;
-                float x[2][4];
-                if constexpr (!GRAD) {
-                    // 0: G[t][s] beta_s beta_t e_s.du_t (s < t); 1: G[t][s] beta_s e_s.dy_t (s <= t)
-                    if (which == 0) gram<N, KD, KE, PP>(x, dc, ec, G::PIECE, lane);
-                    else gram<N, KP, KE, 3>(x, yc, ec, G::PIECE, lane);
-                } else {
-                    // 0: G[s][t] beta_t e_t.dy_s (s >= t); 1: -G[s][t] beta_s beta_t e_t.du_s (s > t)
-                    if (which == 0) gram<N, KE, KP, PP>(x, ec, yc, G::PIECE, lane);
-                    else gram<N, KE, PP, PP>(x, ec, dc, G::PIECE, lane);
-                }
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int hrow = 0; hrow < 2; ++hrow) {
-                        const int t = lane / 4 + 8 * hrow, s0 = 8 * n + 2 * (lane % 4);
-                        float v[2];
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const int s = s0 + q;
-                            const float gm = GRAD ? gam[s * 17 + t] : gam[t * 17 + s];
-                            float f;
-                            if constexpr (!GRAD) f = which == 0 ? (s < t ? gm * be[s] * be[t] : 0.f) : gm * be[s];
-                            else f = which == 0 ? gm * be[t] : (s > t ? -gm * be[s] * be[t] : 0.f);
-                            v[q] = f * x[n][2 * hrow + q];
-                        }
-                        if (which == 0) put_pieces<G::M0>(m, t, s0, v[0], v[1]);
-                        else put_pieces<G::M1>(m, t, s0, v[0], v[1]);
-                    }
-                __syncwarp();
-            }
-            bar_arrive<G::THREADS>(kBarFull + st);
+        } else {
+            split_rows<RB, N, LD, 3>(kb + r0 * LD, G::KPIECE, reinterpret_cast<const float*>(kp) + at * ks, ks, l, a.vec, lane);
+            split_rows<RB, N, LD, 3>(rb + r0 * LD, G::KPIECE, reinterpret_cast<const float*>(rp) + at * ks, ks, l, a.vec, lane);
         }
-        return;
-    }
-
-    const int i0 = warp * 16;
-    const int64_t nchunk = (a.T + kCheck - 1) / kCheck;
-    const int slot = slice / 16 + warp;
-    float* ck = a.check + head * (nchunk + 1) * N * N + slot * (N * 16);
-    float* phi = a.phi + head * (nchunk + 1) * G::SLOTS + slot;
-    float* pr = a.pr + slot * (a.B * a.T * a.H) + scalar;
-    // tile n: values 8 n .. 8 n + 7 of key rows i0 + lane / 4 (+ 8)
-    float S[NT][4];
-    const float* s0 = GRAD ? a.ds_out : a.s_in;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            S[n][i] = s0 != nullptr ? s0[head * N * N + (slice + i0 + lane / 4 + (i >> 1) * 8) * N + 8 * n + 2 * (lane % 4) + (i & 1)]
-                                    : 0.f;
-    auto keep = [&](int64_t c) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            reinterpret_cast<float4*>(ck + c * N * N)[n * 32 + lane] = make_float4(S[n][0], S[n][1], S[n][2], S[n][3]);
     };
-    auto border = [&](int64_t c) {
-        float x = 0.f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(ck + c * N * N) + n * 32 + lane);
-            x = fmaf(S[n][0], v.x, x);
-            x = fmaf(S[n][1], v.y, x);
-            x = fmaf(S[n][2], v.z, x);
-            x = fmaf(S[n][3], v.w, x);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0) phi[c * G::SLOTS] = x;
-    };
-    if constexpr (GRAD) {
-        if (s0 != nullptr) border(nchunk);
-        else if (lane == 0) phi[nchunk * G::SLOTS] = 0.f;
-    }
-
-    const bool own = a.H == a.Hk;
-    const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = b_plain(lane, kMatLd);
-    int st = 0;
-    int64_t t0 = first;
-    for (int64_t i = 0; i < blocks; ++i, t0 += step, st ^= 1) {
-        const int nt = a.T - t0 < BLK ? int(a.T - t0) : BLK;
-        const int nch = (nt + kChunk - 1) / kChunk;
-        G g(smem, st);
-        if (!GRAD && t0 % kCheck == 0) keep(t0 / kCheck);
-        bar_sync<G::THREADS>(kBarFull + st);
+    float own[2] = {0.f, 0.f};   // r . dr of the lane's rows
 #pragma unroll 1
-        for (int cc = 0; cc < nch; ++cc) {
-            const int c = GRAD ? nch - 1 - cc : cc;
-            const __nv_bfloat16 *ec = g.e + c * kChunk * LD, *dc = g.du + c * kChunk * LD, *yc = g.dy + c * kChunk * LD;
-            const __nv_bfloat16* m0 = g.mats + c * (G::M0 + G::M1) * G::MAT;
-            const __nv_bfloat16* m1 = m0 + G::M0 * G::MAT;
-            const float* sc = g.sc + c * kChunk;
-            IO *kt = g.k + c * kChunk * G::LDV + i0, *rt = g.r + c * kChunk * G::LDV + i0;
-            const int64_t t = t0 + c * kChunk, at = base + t * vs + slice + i0;
-            const int left = nt - c * kChunk;
-            float k[2][4], r[2][4];
-            load_lines(k, kt, G::LDV, lane);
-            load_lines(r, rt, G::LDV, lane);
-            uint32_t kq[KP][4];
-            split_a<KP>(k[0], k[1], kq);
-            const float gl = sc[kChunk - 1];
-            if constexpr (!GRAD) {
-                float o1[2][4], o2[2][4];
-                {
-                    Acc pa, qa;
+    for (int sb = 0; sb < 4; ++sb) {
+        if (sb == 0 || G::KR == 16) {
+            __syncthreads();
+            stage_keys(sb * 16);
+            __syncthreads();
+        }
+        const int ko = (G::KR == 16 ? 0 : sb * 16) * LD;
+        const __nv_bfloat16 *et = eb + tb * 16 * LD, *dt = db + tb * 16 * LD, *yt = yb + tb * 16 * LD;
+        const __nv_bfloat16 *es = eb + sb * 16 * LD, *ds = db + sb * 16 * LD, *ys = yb + sb * 16 * LD;
+        // kq: -(du_t.e_s below the diagonal, e_t.du_s above), to K; rq: e_t.dy_s, to R; dq: dy_t.e_s, K to dr
+        float kq[2][4], x[2][4];
 #pragma unroll
-                    for (int kk = 0; kk < N / 16; ++kk) {
-                        uint32_t sp[3][4];
-                        split_a<3>(S[2 * kk], S[2 * kk + 1], sp);
-                        times<3, KD, PP, false>(pa, kk == 0, sp, dc + kk * 16, G::PIECE, off_b);
-                        times<3, KP, 3, false>(qa, kk == 0, sp, yc + kk * 16, G::PIECE, off_b);
-                    }
-                    pa.sum(o1);
-                    qa.sum(o2);
-                    scale_tokens(o1, sc + BLK, lane);
-                    scale_tokens(o2, sc, lane);
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kq[n][i] = 0.f;
+        uint32_t dq3[3][4], rq3[PP][4], kq3[PP][4];
+        float2 st[2][2], tt[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) st[n][q] = sums[sb * 16 + 8 * n + 2 * (lane % 4) + q];
+        tt[0] = sums[t_lo], tt[1] = sums[t_lo + 8];
+        auto factor = [&](float (&c)[2][4], bool lower, bool diag, bool both, float sign, bool add) {
+            // times the decay between the tokens and beta (of both, or of e's token)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int s = sb * 16 + 8 * n + 2 * (lane % 4) + (i & 1), t = t_lo + 8 * (i >> 1);
+                    const float gm = lower ? decay_of(tt[i >> 1], st[n][i & 1]) : decay_of(st[n][i & 1], tt[i >> 1]);
+                    const bool in = lower ? (diag ? s <= t : s < t) : (diag ? s >= t : s > t);
+                    float f = both ? beta[s] * beta[t] : lower ? beta[s] : beta[t];
+                    f = in ? sign * gm * f * c[n][i] : 0.f;
+                    c[n][i] = f;
+                    if (add) kq[n][i] += f;
                 }
-                {
-                    Acc pa, qa;
-                    times<KP, G::M0, PP, false>(pa, true, kq, m0, G::MAT, off_m);
-                    times<KP, G::M1, 3, false>(qa, true, kq, m1, G::MAT, off_m);
-                    float p[2][4], q[2][4];
-                    pa.sum(p);
-                    qa.sum(q);
+        };
+        if (sb <= tb) {
+            gram<N, PP, PP, PP>(x, dt, es, G::PIECE, lane);
+            factor(x, true, false, true, -1.f, true);
+            gram<N, KP, 3, 3>(x, yt, es, G::PIECE, lane);
+            factor(x, true, true, false, 1.f, false);
+            split_a<3>(x[0], x[1], dq3);
+        }
+        if (sb >= tb) {
+            gram<N, PP, PP, PP>(x, et, ds, G::PIECE, lane);
+            factor(x, false, false, true, -1.f, true);
+            gram<N, PP, KP, PP>(x, et, ys, G::PIECE, lane);
+            factor(x, false, true, false, 1.f, false);
+            split_a<PP>(x[0], x[1], rq3);
+        }
+        split_a<PP>(kq[0], kq[1], kq3);
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+        for (int p = 0; p < NP; ++p) {
+            const int so = b_trans(lane, LD) + ko + i0 + p * 16;
+            Acc acc;
+            times<PP, KP, PP, true>(acc, true, kq3, kb, G::KPIECE, so);
+            if (sb >= tb) times<PP, KP, PP, true>(acc, false, rq3, rb, G::KPIECE, so);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) o1[n][x] = -(o1[n][x] + p[n][x]), o2[n][x] += q[n][x];
-                }
-                // S <- g_15 S + (G beta k) e^T
-                scale_tokens(k, sc + 2 * BLK, lane);
-                uint32_t k3[3][4];
-                split_a<3>(k[0], k[1], k3);
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int kk = 0; kk < N / 16; ++kk) {
-                    float d[2][4];
-                    times_add<3, 3>(d, true, k3, ec + kk * 16, G::PIECE, off_t);
-                    fade_add(S[2 * kk], gl, d[0]);
-                    fade_add(S[2 * kk + 1], gl, d[1]);
-                }
-                store_lines(a.dkh + at, vs, left, o1, kt, 0, false, lane);
-                token_sums(pr + t * a.H, a.H, left, o2, r, lane);
-                if (own) store_lines(static_cast<IO*>(a.dr) + at, vs, left, o2, rt, G::LDV, a.vec, lane);
-                else store_lines(a.drh + at, vs, left, o2, rt, 0, false, lane);
-            } else {
-                // the state's part of dk, on its way while the rest is formed
-                float o0[2][4];
+                for (int i = 0; i < 4; ++i) dk[p][n][i] += acc.hi[n][i] + acc.lo[n][i];
+            if (sb <= tb) {
+                Acc ra;
+                times<3, KP, 3, true>(ra, true, dq3, kb, G::KPIECE, so);
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int tt = 8 * n + 2 * (lane % 4) + (x & 1);
-                        o0[n][x] = tt < left ? __ldcg(a.dkh + at + tt * vs + lane / 4 + (x >> 1) * 8) : 0.f;
-                    }
-                uint32_t rq[KP][4];
-                split_a<KP>(r[0], r[1], rq);
-                float o[2][4];
-                {
-                    Acc pa;
-#pragma unroll
-                    for (int kk = 0; kk < N / 16; ++kk) {
-                        uint32_t sp[PP][4];
-                        split_a<PP>(S[2 * kk], S[2 * kk + 1], sp);
-                        times<PP, KE, PP, false>(pa, kk == 0, sp, ec + kk * 16, G::PIECE, off_b);
-                    }
-                    pa.sum(o);
-                    scale_tokens(o, sc + 2 * BLK, lane);
-                }
-                {
-                    Acc pa;
-                    times<KP, G::M0, PP, false>(pa, true, rq, m0, G::MAT, off_m);
-                    times<KP, G::M1, PP, false>(pa, false, kq, m1, G::MAT, off_m);
-                    float p[2][4];
-                    pa.sum(p);
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) o[n][x] += p[n][x], k[n][x] = -k[n][x];
-                }
-                // D <- g_15 D + (g r) dy^T - (g beta k) du^T
-                scale_tokens(r, sc, lane);
-                scale_tokens(k, sc + BLK, lane);
-                uint32_t r3[3][4], k3[3][4];
-                split_a<3>(r[0], r[1], r3);
-                split_a<3>(k[0], k[1], k3);
-#pragma unroll
-                for (int kk = 0; kk < N / 16; ++kk) {
-                    float d[2][4];
-                    times_add<3, 3>(d, true, k3, dc + kk * 16, G::PIECE, off_t);
-                    times_add<3, KP>(d, false, r3, yc + kk * 16, G::PIECE, off_t);
-                    fade_add(S[2 * kk], gl, d[0]);
-                    fade_add(S[2 * kk + 1], gl, d[1]);
-                }
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) o[n][x] += o0[n][x];
-                if (own) store_lines(static_cast<IO*>(a.dk) + at, vs, left, o, kt, G::LDV, a.vec, lane);
-                else store_lines(a.dkh + at, vs, left, o, kt, 0, false, lane);
+                    for (int i = 0; i < 4; ++i) dr[p][n][i] += ra.hi[n][i] + ra.lo[n][i];
             }
         }
-        if (GRAD && t0 % kCheck == 0) border(t0 / kCheck);
-        if (i + 2 < blocks) bar_arrive<G::THREADS>(kBarFree + st);
     }
-    if constexpr (!GRAD) keep(nchunk);
+    // --- r . dr, and the outputs
+    const bool whole = a.H == a.Hk;
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int t = t_lo + 8 * q, c = i0 + p * 16 + 8 * n + 2 * (lane % 4);
+                if (t >= nt) continue;
+                const IO* r2 = rp + t * ks + c;
+                own[q] = fmaf(to_f32(r2[0]), dr[p][n][2 * q], fmaf(to_f32(r2[1]), dr[p][n][2 * q + 1], own[q]));
+                const int64_t at = rows + t * vs + c;
+                if (!whole || KP == 3) {
+                    float* orr = whole ? static_cast<float*>(a.dr) : a.drh;
+                    float* ok = whole ? static_cast<float*>(a.dk) : a.dkh;
+                    if (!whole || a.vec) {
+                        *reinterpret_cast<float2*>(orr + at) = make_float2(dr[p][n][2 * q], dr[p][n][2 * q + 1]);
+                        *reinterpret_cast<float2*>(ok + at) = make_float2(dk[p][n][2 * q], dk[p][n][2 * q + 1]);
+                    } else {
+                        orr[at] = dr[p][n][2 * q], orr[at + 1] = dr[p][n][2 * q + 1];
+                        ok[at] = dk[p][n][2 * q], ok[at + 1] = dk[p][n][2 * q + 1];
+                    }
+                } else {
+                    IO* orr = static_cast<IO*>(a.dr) + at;
+                    IO* ok = static_cast<IO*>(a.dk) + at;
+                    if (a.vec) {
+                        *reinterpret_cast<__nv_bfloat162*>(orr) = __floats2bfloat162_rn(dr[p][n][2 * q], dr[p][n][2 * q + 1]);
+                        *reinterpret_cast<__nv_bfloat162*>(ok) = __floats2bfloat162_rn(dk[p][n][2 * q], dk[p][n][2 * q + 1]);
+                    } else {
+                        put(orr, dr[p][n][2 * q]), put(orr + 1, dr[p][n][2 * q + 1]);
+                        put(ok, dk[p][n][2 * q]), put(ok + 1, dk[p][n][2 * q + 1]);
+                    }
+                }
+            }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        own[q] += __shfl_xor_sync(0xffffffffu, own[q], 1);
+        own[q] += __shfl_xor_sync(0xffffffffu, own[q], 2);
+        if (lane % 4 == 0) rdr[(warp / 4) * kSegment + t_lo + 8 * q] = own[q];
+    }
+    __syncthreads();
+    // --- dw: the sum <Dn, S> from the segment's end backwards; its first token's is the border's own
+    if (warp == 0) {
+        constexpr int SLOTS = kSlots<N>;
+        const float* phi = a.phi + (head * (nseg + 1) + seg) * SLOTS;
+        float first = lane < SLOTS ? phi[lane] : 0.f, end = lane < SLOTS ? phi[SLOTS + lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) {
+            first += __shfl_xor_sync(0xffffffffu, first, o);
+            end += __shfl_xor_sync(0xffffffffu, end, o);
+        }
+        const int ta = 2 * lane;
+        float term[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int t = ta + q;
+            float x = rdr[t];
+            if constexpr (G::HALVES == 2) x += rdr[kSegment + t];
+            term[q] = t < nt ? fmaf(-beta[t], duv[t], x) : 0.f;
+        }
+        float x = term[0] + term[1];   // suffix sums over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const float y = __shfl_down_sync(0xffffffffu, x, o);
+            if (lane + o < 32) x += y;
+        }
+        float after = __shfl_down_sync(0xffffffffu, x, 1);
+        if (lane == 31) after = 0.f;
+        const float s1 = end + (after + term[1]), s0 = end + (after + (term[1] + term[0]));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int t = ta + q;
+            if (t >= nt) continue;
+            const int64_t at = scalar + t * a.H;
+            // a state that nothing is left of has no gradient, whatever the sum's rounding left
+            a.dw[at] = t == 0 ? -first : expf(-a.w[at]) == 0.f ? 0.f : -(q ? s1 : s0);
+        }
+    }
 }
 
 // dr and dk of a key head: the sums over the value heads that share it, in
@@ -550,44 +577,6 @@ __global__ void __launch_bounds__(256) delta_share_kernel(const Args a) {
     IO* ok = static_cast<IO*>(a.dk) + key * N + c;
     put(orr, r.x), put(orr + 1, r.y), put(orr + 2, r.z), put(orr + 3, r.w);
     put(ok, k.x), put(ok + 1, k.y), put(ok + 2, k.z), put(ok + 3, k.w);
-}
-
-// dw of a chunk of kCheck tokens: the sum <Dn, S> from the chunk's end
-// backwards; its first token's is the border's own.  One thread per
-// (sequence, chunk, head).
-template <int SLOTS>
-__global__ void __launch_bounds__(64) delta_dw_kernel(const Args a) {
-    const int64_t nchunk = (a.T + kCheck - 1) / kCheck;
-    const int64_t id = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (id >= a.B * nchunk * a.H) return;
-    const int64_t h = id % a.H, c = id / a.H % nchunk, b = id / a.H / nchunk;
-    const float* phi = a.phi + ((b * a.H + h) * (nchunk + 1) + c) * SLOTS;
-    float first = 0.f, x = 0.f;
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s) first += phi[s], x += phi[SLOTS + s];
-    const int64_t t0 = c * kCheck, t1 = t0 + kCheck < a.T ? t0 + kCheck : a.T;
-    const int64_t plane = a.B * a.T * a.H;
-    constexpr int U = 8;   // tokens whose loads are in flight at once
-    for (int64_t t = t1 - 1; t > t0; t -= U) {
-        float term[U], w[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t at = (b * a.T + (t - u > t0 ? t - u : t0)) * a.H + h;
-            float s = 0.f;
-#pragma unroll
-            for (int q = 0; q < SLOTS; ++q) s += a.pr[q * plane + at] - a.pv[q * plane + at];
-            term[u] = s;
-            w[u] = a.w[at];
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            x += term[u];
-            // a state that nothing is left of has no gradient, whatever the sum's rounding left
-            if (t - u > t0) a.dw[(b * a.T + t - u) * a.H + h] = expf(-w[u]) == 0.f ? 0.f : -x;
-        }
-    }
-    a.dw[(b * a.T + t0) * a.H + h] = -first;
 }
 
 }  // namespace delta
