@@ -86,6 +86,8 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool f
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" :: "l"(p)); }
+
 // (x, y) as NP packed bfloat16 pairs whose sum is the pair to 8 NP bits
 template <int NP>
 __device__ __forceinline__ void split2(float x, float y, uint32_t (&p)[NP]) {
@@ -115,17 +117,29 @@ __device__ __forceinline__ float2 pair_at(const float* x, int n, int lane) {
     return *reinterpret_cast<const float2*>(x + 8 * n + 2 * (lane % 4));
 }
 
-// One warp's copy of ROWS rows of W elements to shared rows of LD elements:
-// 16-byte asynchronous copies, or element copies where the addresses do not
+// Places of (row, column) in shared memory: rows of LD elements, or (Swizzled)
+// of W without padding, 16-byte pieces in an order of their own in every row, so
+// that eight rows of ldmatrix differ in banks.
+template <int LD>
+struct Pitched {
+    __device__ __forceinline__ int operator()(int r, int c) const { return r * LD + c; }
+};
+template <int W>
+struct Swizzled {
+    static __device__ __forceinline__ int turn(int r) { return W == 32 ? (r >> 1) & 3 : r & 7; }
+    __device__ __forceinline__ int operator()(int r, int c) const { return r * W + (((c >> 3) ^ turn(r)) << 3) + (c & 7); }
+};
+// One warp's copy of ROWS rows of W elements to shared memory: 16-byte
+// asynchronous copies, or element copies where the addresses do not
 // allow them; rows from nt on are zero.
-template <typename IO, int ROWS, int W, int LD>
-__device__ __forceinline__ void copy_rows(IO* dst, const IO* src, int64_t stride, int nt, bool vec, int lane) {
+template <typename IO, int ROWS, int W, typename AT>
+__device__ __forceinline__ void copy_rows(IO* dst, AT at, const IO* src, int64_t stride, int nt, bool vec, int lane) {
     if (vec) {
         constexpr int PER = 16 / int(sizeof(IO)), ROWV = W / PER;
 #pragma unroll
         for (int i = lane; i < ROWS * ROWV; i += 32) {
             const int t = i / ROWV, c = (i % ROWV) * PER;
-            cp_async16(smem_u32(dst + t * LD + c), src + (t < nt ? t : 0) * stride + c, t < nt);
+            cp_async16(smem_u32(dst + at(t, c)), src + (t < nt ? t : 0) * stride + c, t < nt);
         }
     } else {
         for (int i = lane; i < ROWS * W; i += 32) {
@@ -134,7 +148,7 @@ __device__ __forceinline__ void copy_rows(IO* dst, const IO* src, int64_t stride
             if constexpr (sizeof(IO) == 4) x = 0.f;
             else x = __ushort_as_bfloat16(0);
             if (t < nt) x = src[t * stride + c];
-            dst[t * LD + c] = x;
+            dst[at(t, c)] = x;
         }
     }
 }
@@ -151,9 +165,10 @@ __device__ __forceinline__ void put4(__nv_bfloat16* dst, int piece, float4 v) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) *reinterpret_cast<uint2*>(dst + i * piece) = make_uint2(p[i], q[i]);
 }
-// One warp's copy of ROWS float32 rows as NP arrays of pieces
-template <int ROWS, int W, int LD, int NP>
-__device__ __forceinline__ void split_rows(__nv_bfloat16* dst, int piece, const float* src, int64_t stride, int nt, bool vec,
+// One warp's copy of ROWS float32 rows as NP arrays of pieces, rows from nt on
+// as zeros (src itself is a row that exists)
+template <int ROWS, int W, int NP, typename AT>
+__device__ __forceinline__ void split_rows(__nv_bfloat16* dst, AT at, int piece, const float* src, int64_t stride, int nt, bool vec,
                                            int lane) {
     constexpr int ROWV = W / 4, ALL = ROWS * ROWV / 32, U = ALL < 8 ? ALL : 8;   // U loads in flight
 #pragma unroll 1
@@ -162,40 +177,14 @@ __device__ __forceinline__ void split_rows(__nv_bfloat16* dst, int piece, const 
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = lane + (n + u) * 32, t = i / ROWV, c = (i % ROWV) * 4;
-            v[u] = t < nt ? load4(src + t * stride + c, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[u] = load4(src + (t < nt ? t : 0) * stride + c, vec);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = lane + (n + u) * 32, t = i / ROWV, c = (i % ROWV) * 4;
-            put4<NP>(dst + t * LD + c, piece, v[u]);
+            if (t >= nt) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            put4<NP>(dst + at(t, c), piece, v[u]);
         }
-    }
-}
-
-// (16 tokens x N) (N x 16 tokens)^T of two staged arrays of KX and KY pieces,
-// the products of the first ORD orders: C[t][s] = x_t . y_s
-template <int N, int KX, int KY, int ORD>
-__device__ __forceinline__ void gram(float (&c)[2][4], const __nv_bfloat16* x, const __nv_bfloat16* y, int piece, int lane) {
-    constexpr int LD = N + 8;
-    // A: rows t, keys; B: rows s, keys
-    bool first = true;
-    const int ra = (lane & 7) + ((lane >> 3) & 1) * 8, ca = (lane >> 4) * 8;
-    const int rb = (lane & 7) + (lane >> 4) * 8, cb = ((lane >> 3) & 1) * 8;
-#pragma unroll
-    for (int kk = 0; kk < N / 16; ++kk) {
-        uint32_t a[KX][4], b[KY][4];
-#pragma unroll
-        for (int p = 0; p < KX; ++p) ldsm4(a[p], smem_u32(x + p * piece + ra * LD + kk * 16 + ca));
-#pragma unroll
-        for (int p = 0; p < KY; ++p) ldsm4(b[p], smem_u32(y + p * piece + rb * LD + kk * 16 + cb));
-#pragma unroll
-        for (int o = ORD - 1; o >= 0; --o)
-#pragma unroll
-            for (int p = 0; p < KX && p <= o; ++p)
-                if (o - p < KY) {
-                    mma2(c, a[p], b[o - p], first);
-                    first = false;
-                }
     }
 }
 
@@ -276,6 +265,36 @@ __device__ __forceinline__ int b_trans(int lane, int ld) { return ((lane & 7) + 
 // and in a 16 x 16 matrix
 __device__ __forceinline__ int m_plain(int lane) { return mat_at((lane & 7) + (lane >> 4) * 8, ((lane >> 3) & 1) * 8); }
 __device__ __forceinline__ int m_trans(int lane) { return mat_at((lane & 7) + ((lane >> 3) & 1) * 8, (lane >> 4) * 8); }
+
+// (16 tokens x N) (N x 16 tokens)^T of two staged arrays of KX and KY pieces
+// (`piece` bytes apart), the products of the first ORD orders: C[t][s] = x_t .
+// y_s.  xa, ya: this lane's place in the first 16 columns of x as an A operand,
+// of y as a plain B operand; SWIZZLED: the columns' places by exclusive or.
+template <int N, int KX, int KY, int ORD, bool SWIZZLED>
+__device__ __forceinline__ void gram_at(float (&c)[2][4], uint32_t xa, uint32_t ya, int piece) {
+    bool first = true;
+#pragma unroll
+    for (int kk = 0; kk < N / 16; ++kk) {
+        uint32_t a[KX][4], b[KY][4];
+#pragma unroll
+        for (int p = 0; p < KX; ++p) ldsm4(a[p], (SWIZZLED ? xa ^ (kk * 32) : xa + kk * 32) + p * piece);
+#pragma unroll
+        for (int p = 0; p < KY; ++p) ldsm4(b[p], (SWIZZLED ? ya ^ (kk * 32) : ya + kk * 32) + p * piece);
+#pragma unroll
+        for (int o = ORD - 1; o >= 0; --o)
+#pragma unroll
+            for (int p = 0; p < KX && p <= o; ++p)
+                if (o - p < KY) {
+                    mma2(c, a[p], b[o - p], first);
+                    first = false;
+                }
+    }
+}
+template <int N, int KX, int KY, int ORD>
+__device__ __forceinline__ void gram(float (&c)[2][4], const __nv_bfloat16* x, const __nv_bfloat16* y, int piece, int lane) {
+    constexpr int LD = N + 8;
+    gram_at<N, KX, KY, ORD, false>(c, smem_u32(x + b_trans(lane, LD)), smem_u32(y + b_plain(lane, LD)), piece * 2);
+}
 
 // A 16-token x 16-line tile of staged rows, transposed, in the accumulator
 // layout: x[n][i] is line lane / 4 + 8 (i / 2), token 8 n + 2 (lane % 4) + i % 2.
@@ -358,16 +377,15 @@ struct Acc {
     }
 };
 // acc (+)= A (16 x 16) B (16 x 16) of NA and NB pieces, orders below ORD.  B's
-// pieces lie `piece` elements apart; off: this lane's offset (b_plain, b_trans).
+// pieces lie `piece` bytes apart; addr: this lane's place in the first.
 template <int NA, int NB, int ORD, bool TRANS>
-__device__ __forceinline__ void times(Acc& acc, bool first, const uint32_t (&a)[NA][4], const __nv_bfloat16* m, int piece,
-                                      int off) {
+__device__ __forceinline__ void times_at(Acc& acc, bool first, const uint32_t (&a)[NA][4], uint32_t addr, int piece) {
     bool lo_first = first;
 #pragma unroll
     for (int p = 0; p < NB && p < ORD; ++p) {
         uint32_t f[4];
-        if constexpr (TRANS) ldsm4t(f, smem_u32(m + p * piece + off));
-        else ldsm4(f, smem_u32(m + p * piece + off));
+        if constexpr (TRANS) ldsm4t(f, addr + p * piece);
+        else ldsm4(f, addr + p * piece);
 #pragma unroll
         for (int i = 0; i < NA && i + p < ORD; ++i) {
             if (i + p == 0) {
@@ -378,6 +396,13 @@ __device__ __forceinline__ void times(Acc& acc, bool first, const uint32_t (&a)[
             }
         }
     }
+}
+// the same of staged elements: pieces `piece` elements apart, off: this lane's
+// offset (b_plain, b_trans)
+template <int NA, int NB, int ORD, bool TRANS>
+__device__ __forceinline__ void times(Acc& acc, bool first, const uint32_t (&a)[NA][4], const __nv_bfloat16* m, int piece,
+                                      int off) {
+    times_at<NA, NB, ORD, TRANS>(acc, first, a, smem_u32(m + off), piece * 2);
 }
 // d (+)= A B into one accumulator, smallest orders first
 template <int NA, int NB>
@@ -438,15 +463,15 @@ struct Columns {
     // a chunk's rows of every tensor (one warp)
     __device__ __forceinline__ void fetch(const IO* kp, const IO* rp, int64_t ks, const IO* vp, int64_t vs, int nt, bool vec,
                                           int lane) {
-        copy_rows<IO, kChunk, CW, LDV>(v, vp, vs, nt, vec, lane);
+        copy_rows<IO, kChunk, CW>(v, Pitched<LDV>{}, vp, vs, nt, vec, lane);
         if constexpr (KP == 1) {
-            copy_rows<IO, kChunk, N, LD>(reinterpret_cast<IO*>(k), kp, ks, nt, vec, lane);
-            if constexpr (ROPS) copy_rows<IO, kChunk, N, LD>(reinterpret_cast<IO*>(r()), rp, ks, nt, vec, lane);
+            copy_rows<IO, kChunk, N>(reinterpret_cast<IO*>(k), Pitched<LD>{}, kp, ks, nt, vec, lane);
+            if constexpr (ROPS) copy_rows<IO, kChunk, N>(reinterpret_cast<IO*>(r()), Pitched<LD>{}, rp, ks, nt, vec, lane);
         }
         cp_async_commit();
         if constexpr (KP == 3) {
-            split_rows<kChunk, N, LD, 3>(k, PIECE, reinterpret_cast<const float*>(kp), ks, nt, vec, lane);
-            if constexpr (ROPS) split_rows<kChunk, N, LD, 3>(r(), PIECE, reinterpret_cast<const float*>(rp), ks, nt, vec, lane);
+            split_rows<kChunk, N, 3>(k, Pitched<LD>{}, PIECE, reinterpret_cast<const float*>(kp), ks, nt, vec, lane);
+            if constexpr (ROPS) split_rows<kChunk, N, 3>(r(), Pitched<LD>{}, PIECE, reinterpret_cast<const float*>(rp), ks, nt, vec, lane);
         }
         cp_async_wait();
         __syncwarp();

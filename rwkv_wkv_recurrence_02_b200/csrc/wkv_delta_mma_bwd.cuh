@@ -217,23 +217,26 @@ struct SegmentShape {
     static constexpr int KP = sizeof(IO) == 2 ? 1 : 3, PP = kOutOrders<IO>;
     static constexpr int IC = N < 64 ? N : 64, HALVES = N / IC;
     static constexpr int WARPS = 4 * HALVES, THREADS = 32 * WARPS;
-    static constexpr int LD = N + 8, PIECE = kSegment * LD;
-    static constexpr int JB = N == 64 ? 64 : 32;              // value lines of S and D at a time
-    static constexpr int SPIECE = JB * LD;
+    static constexpr int PIECE = kSegment * N;                // rows without padding (Swizzled)
+    static constexpr int JB = 32;                             // value lines of S and D at a time
+    static constexpr int SPIECE = JB * N;
     static constexpr int KR = KP == 3 && N == 128 ? 16 : 64;  // tokens of K and R at a time
-    static constexpr int KPIECE = KR * LD;
+    static constexpr int KPIECE = KR * N;
     // e, du, dy; S and D, later K and R; sums, beta and the sums over channels
     static constexpr int S_ROWS = (3 + PP + KP) * PIECE * 2;
     static constexpr int A_ = (3 + PP) * SPIECE * 2, B_ = 2 * KP * KPIECE * 2, S_BUF = A_ > B_ ? A_ : B_;
     static constexpr int S_SUM = kSegment * (8 + 4 + 4 + 4 * HALVES);
     static constexpr int SMEM = S_ROWS + S_BUF + S_SUM;
+    // CTAs an SM by shared memory; registers follow
+    static constexpr int CTAS = 227 * 1024 / (SMEM + 1024) > 3 ? 3 : 227 * 1024 / (SMEM + 1024);
 };
 
 template <typename IO, int N>
-__global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, kCtas<IO, N>) delta_segment_kernel(const Args a) {
+__global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO, N>::CTAS) delta_segment_kernel(const Args a) {
     using G = SegmentShape<IO, N>;
-    constexpr int KP = G::KP, PP = G::PP, LD = G::LD, NP = G::IC / 16;
-    extern __shared__ __align__(16) char smem[];
+    constexpr int KP = G::KP, PP = G::PP, NP = G::IC / 16;
+    constexpr Swizzled<N> place{};
+    extern __shared__ __align__(1024) char smem[];
     __nv_bfloat16* eb = reinterpret_cast<__nv_bfloat16*>(smem);
     __nv_bfloat16* db = eb + 3 * G::PIECE;
     __nv_bfloat16* yb = db + PP * G::PIECE;
@@ -256,45 +259,63 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, kCtas<IO, N>) de
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
+    // what is read later, on its way to L2 now
+    const float* s_seg = a.s_seg + (head * (nseg + 1) + seg) * N * N;
+    const float* d_seg = a.d_seg + (head * (nseg + 1) + seg + 1) * N * N;
+    const IO* kp = static_cast<const IO*>(a.k) + keys;
+    const IO* rp = static_cast<const IO*>(a.r) + keys;
+    for (int i = tid; i < N * N / 32; i += G::THREADS) {
+        prefetch_l2(s_seg + i * 32);
+        prefetch_l2(d_seg + i * 32);
+    }
+    constexpr int KL = N * int(sizeof(IO)) / 64;   // 64-byte pieces of a row: rows need not begin a line
+    for (int i = tid; i < nt * KL; i += G::THREADS) {
+        const int64_t at = (i / KL) * ks + (i % KL) * (64 / int(sizeof(IO)));
+        prefetch_l2(kp + at);
+        prefetch_l2(rp + at);
+    }
+
     // --- the segment's rows: 16 / HALVES a warp
     constexpr int RW = 16 / G::HALVES;
     const int row = warp * RW, left = nt - row;
     const int64_t rr = left > 0 ? row : 0;   // rows behind the last token: zeros, addressed at one that exists
     if constexpr (KP == 1) {
-        copy_rows<IO, RW, N, LD>(reinterpret_cast<IO*>(yb) + row * LD, static_cast<const IO*>(a.dy) + rows + rr * vs, vs, left, a.vec,
-                                 lane);
+        copy_rows<IO, RW, N>(reinterpret_cast<IO*>(yb) + row * N, place, static_cast<const IO*>(a.dy) + rows + rr * vs, vs, left, a.vec,
+                             lane);
         cp_async_commit();
     }
     {
-        constexpr int ROWV = N / 4, ALL = RW * ROWV / 32, U = ALL < 4 ? ALL : 4;
+        constexpr int ROWV = N / 4, ALL = RW * ROWV / 32, U = ALL < 8 ? ALL : 8;
 #pragma unroll 1
         for (int n = 0; n < ALL; n += U) {
+            // all loads first, of a row that exists; rows behind the last token are zeroed after
             float4 x[U], y[U], v[U];
+            uint2 vr[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int i = lane + (n + u) * 32, t = i / ROWV, c = (i % ROWV) * 4;
-                const int64_t at = rows + (row + t) * vs + c;
-                x[u] = y[u] = v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (t < left) {
-                    x[u] = load4(a.e + at, true);
-                    y[u] = load4(a.du + at, true);
-                    const IO* vp = static_cast<const IO*>(a.v) + at;
-                    if constexpr (KP == 3) {
-                        v[u] = load4(reinterpret_cast<const float*>(vp), a.vec);
-                    } else if (a.vec) {
-                        const uint2 w2 = __ldg(reinterpret_cast<const uint2*>(vp));
-                        v[u] = make_float4(__uint_as_float(w2.x << 16), __uint_as_float(w2.x & 0xffff0000u),
-                                           __uint_as_float(w2.y << 16), __uint_as_float(w2.y & 0xffff0000u));
-                    } else {
-                        v[u] = make_float4(to_f32(vp[0]), to_f32(vp[1]), to_f32(vp[2]), to_f32(vp[3]));
-                    }
+                const int64_t at = rows + (t < left ? row + t : 0) * vs + c;
+                x[u] = load4(a.e + at, true);
+                y[u] = load4(a.du + at, true);
+                const IO* vp = static_cast<const IO*>(a.v) + at;
+                if constexpr (KP == 3) {
+                    v[u] = load4(reinterpret_cast<const float*>(vp), a.vec);
+                } else if (a.vec) {
+                    vr[u] = __ldg(reinterpret_cast<const uint2*>(vp));
+                } else {
+                    const unsigned short* q = reinterpret_cast<const unsigned short*>(vp);
+                    vr[u] = make_uint2(q[0] | uint32_t(q[1]) << 16, q[2] | uint32_t(q[3]) << 16);
                 }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int i = lane + (n + u) * 32, t = i / ROWV, c = (i % ROWV) * 4;
-                put4<3>(eb + (row + t) * LD + c, G::PIECE, x[u]);
-                put4<PP>(db + (row + t) * LD + c, G::PIECE, y[u]);
+                if constexpr (KP == 1)
+                    v[u] = make_float4(__uint_as_float(vr[u].x << 16), __uint_as_float(vr[u].x & 0xffff0000u),
+                                       __uint_as_float(vr[u].y << 16), __uint_as_float(vr[u].y & 0xffff0000u));
+                if (t >= left) x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                put4<3>(eb + place(row + t, c), G::PIECE, x[u]);
+                put4<PP>(db + place(row + t, c), G::PIECE, y[u]);
                 float s = fmaf(x[u].x, y[u].x, fmaf(x[u].y, y[u].y, fmaf(x[u].z, y[u].z, x[u].w * y[u].w)));
                 float z = fmaf(v[u].x, y[u].x, fmaf(v[u].y, y[u].y, fmaf(v[u].z, y[u].z, v[u].w * y[u].w)));
 #pragma unroll
@@ -310,7 +331,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, kCtas<IO, N>) de
         }
     }
     if constexpr (KP == 3)
-        split_rows<RW, N, LD, 3>(yb + row * LD, G::PIECE, reinterpret_cast<const float*>(a.dy) + rows + row * vs, vs, left, a.vec, lane);
+        split_rows<RW, N, 3>(yb + row * N, place, G::PIECE, reinterpret_cast<const float*>(a.dy) + rows + rr * vs, vs, left, a.vec, lane);
     if (warp == 0) {   // the decays' running sum, two tokens a lane
         const int ta = 2 * lane;
         const float w0 = ta < nt ? a.w[scalar + ta * a.H] : 0.f, w1 = ta + 1 < nt ? a.w[scalar + (ta + 1) * a.H] : 0.f;
@@ -335,16 +356,19 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, kCtas<IO, N>) de
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) dr[p][n][i] = dk[p][n][i] = 0.f;
-    const int off_a = b_trans(lane, LD) + tb * 16 * LD;   // an A operand's rows lie as a transposed B's
-    const float* s_seg = a.s_seg + (head * (nseg + 1) + seg) * N * N;
-    const float* d_seg = a.d_seg + (head * (nseg + 1) + seg + 1) * N * N;
+    // this lane's places (bytes): as an A operand or a transposed B, and as a plain B; the columns' by exclusive or
+    const uint32_t at_t = place((lane & 7) + ((lane >> 3) & 1) * 8, (lane >> 4) * 8) * 2;
+    const uint32_t at_p = place((lane & 7) + (lane >> 4) * 8, ((lane >> 3) & 1) * 8) * 2;
+    const uint32_t eb_a = smem_u32(eb), db_a = smem_u32(db), yb_a = smem_u32(yb), buf_a = smem_u32(buf);
+    constexpr int PB = G::PIECE * 2, SB = G::SPIECE * 2, KB = G::KPIECE * 2, ROWS16 = 16 * N * 2;
     const int t_lo = tb * 16 + lane / 4;                  // this lane's rows: t_lo and t_lo + 8
 #pragma unroll 1
     for (int jb = 0; jb < N; jb += G::JB) {
         constexpr int RB = G::JB / G::WARPS;
+        const auto rows_at = [&](int r, int c) { return place(warp * RB + r, c); };
         if (jb > 0) __syncthreads();
-        split_rows<RB, N, LD, 3>(buf + warp * RB * LD, G::SPIECE, s_seg + (jb + warp * RB) * N, N, RB, true, lane);
-        split_rows<RB, N, LD, PP>(buf + 3 * G::SPIECE + warp * RB * LD, G::SPIECE, d_seg + (jb + warp * RB) * N, N, RB, true, lane);
+        split_rows<RB, N, 3>(buf, rows_at, G::SPIECE, s_seg + (jb + warp * RB) * N, N, RB, true, lane);
+        split_rows<RB, N, PP>(buf + 3 * G::SPIECE, rows_at, G::SPIECE, d_seg + (jb + warp * RB) * N, N, RB, true, lane);
         if (KP == 1 && jb == 0) cp_async_wait();
         __syncthreads();
         float2 gq[2];   // of the lane's two rows: g, q
@@ -355,20 +379,21 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, kCtas<IO, N>) de
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             Acc ra, ka, da;
-#pragma unroll 2
+#pragma unroll
             for (int kk = 0; kk < G::JB / 16; ++kk) {
-                const int off = off_a + jb + kk * 16, so = b_trans(lane, LD) + kk * 16 * LD + i0 + p * 16;
+                const uint32_t off = tb * ROWS16 + (at_t ^ ((jb + kk * 16) * 2));
+                const uint32_t so = buf_a + kk * ROWS16 + (at_t ^ ((i0 + p * 16) * 2));
                 uint32_t yq[KP][4], uq[PP][4], eq[PP][4];
 #pragma unroll
-                for (int c = 0; c < KP; ++c) ldsm4(yq[c], smem_u32(yb + c * G::PIECE + off));
+                for (int c = 0; c < KP; ++c) ldsm4(yq[c], yb_a + c * PB + off);
 #pragma unroll
                 for (int c = 0; c < PP; ++c) {
-                    ldsm4(uq[c], smem_u32(db + c * G::PIECE + off));
-                    ldsm4(eq[c], smem_u32(eb + c * G::PIECE + off));
+                    ldsm4(uq[c], db_a + c * PB + off);
+                    ldsm4(eq[c], eb_a + c * PB + off);
                 }
-                times<KP, 3, 3, true>(ra, kk == 0, yq, buf, G::SPIECE, so);
-                times<PP, 3, PP, true>(ka, kk == 0, uq, buf, G::SPIECE, so);
-                times<PP, PP, PP, true>(da, kk == 0, eq, buf + 3 * G::SPIECE, G::SPIECE, so);
+                times_at<KP, 3, 3, true>(ra, kk == 0, yq, so, SB);
+                times_at<PP, PP, PP, true>(ka, kk == 0, uq, so, SB);
+                times_at<PP, PP, PP, true>(da, kk == 0, eq, so + 3 * SB, SB);
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n)
@@ -384,21 +409,20 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, kCtas<IO, N>) de
 
     // --- the blocks of token pairs
     __nv_bfloat16 *kb = buf, *rb = buf + KP * G::KPIECE;
-    const IO* kp = static_cast<const IO*>(a.k) + keys;
-    const IO* rp = static_cast<const IO*>(a.r) + keys;
     auto stage_keys = [&](int s0) {   // K and R, tokens s0 .. s0 + KR
         constexpr int RB = G::KR / G::WARPS > 0 ? G::KR / G::WARPS : 1;
         const int r0 = warp * RB, l = nt - s0 - r0;
         if (r0 >= G::KR) return;
         const int64_t at = l > 0 ? s0 + r0 : 0;
+        const auto rows_at = [&](int r, int c) { return place(r0 + r, c); };
         if constexpr (KP == 1) {
-            copy_rows<IO, RB, N, LD>(reinterpret_cast<IO*>(kb) + r0 * LD, kp + at * ks, ks, l, a.vec, lane);
-            copy_rows<IO, RB, N, LD>(reinterpret_cast<IO*>(rb) + r0 * LD, rp + at * ks, ks, l, a.vec, lane);
+            copy_rows<IO, RB, N>(reinterpret_cast<IO*>(kb), rows_at, kp + at * ks, ks, l, a.vec, lane);
+            copy_rows<IO, RB, N>(reinterpret_cast<IO*>(rb), rows_at, rp + at * ks, ks, l, a.vec, lane);
             cp_async_commit();
             cp_async_wait();
         } else {
-            split_rows<RB, N, LD, 3>(kb + r0 * LD, G::KPIECE, reinterpret_cast<const float*>(kp) + at * ks, ks, l, a.vec, lane);
-            split_rows<RB, N, LD, 3>(rb + r0 * LD, G::KPIECE, reinterpret_cast<const float*>(rp) + at * ks, ks, l, a.vec, lane);
+            split_rows<RB, N, 3>(kb, rows_at, G::KPIECE, reinterpret_cast<const float*>(kp) + at * ks, ks, l, a.vec, lane);
+            split_rows<RB, N, 3>(rb, rows_at, G::KPIECE, reinterpret_cast<const float*>(rp) + at * ks, ks, l, a.vec, lane);
         }
     };
     float own[2] = {0.f, 0.f};   // r . dr of the lane's rows
@@ -409,9 +433,8 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, kCtas<IO, N>) de
             stage_keys(sb * 16);
             __syncthreads();
         }
-        const int ko = (G::KR == 16 ? 0 : sb * 16) * LD;
-        const __nv_bfloat16 *et = eb + tb * 16 * LD, *dt = db + tb * 16 * LD, *yt = yb + tb * 16 * LD;
-        const __nv_bfloat16 *es = eb + sb * 16 * LD, *ds = db + sb * 16 * LD, *ys = yb + sb * 16 * LD;
+        const int ko = G::KR == 16 ? 0 : sb;   // the block's rows of K and R
+        const uint32_t xt = tb * ROWS16 + at_t, ys = sb * ROWS16 + at_p;
         // kq: -(du_t.e_s below the diagonal, e_t.du_s above), to K; rq: e_t.dy_s, to R; dq: dy_t.e_s, K to dr
         float kq[2][4], x[2][4];
 #pragma unroll
@@ -441,41 +464,56 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, kCtas<IO, N>) de
                 }
         };
         if (sb <= tb) {
-            gram<N, PP, PP, PP>(x, dt, es, G::PIECE, lane);
+            gram_at<N, PP, PP, PP, true>(x, db_a + xt, eb_a + ys, PB);
             factor(x, true, false, true, -1.f, true);
-            gram<N, KP, 3, 3>(x, yt, es, G::PIECE, lane);
+            gram_at<N, KP, 3, 3, true>(x, yb_a + xt, eb_a + ys, PB);
             factor(x, true, true, false, 1.f, false);
             split_a<3>(x[0], x[1], dq3);
         }
         if (sb >= tb) {
-            gram<N, PP, PP, PP>(x, et, ds, G::PIECE, lane);
+            gram_at<N, PP, PP, PP, true>(x, eb_a + xt, db_a + ys, PB);
             factor(x, false, false, true, -1.f, true);
-            gram<N, PP, KP, PP>(x, et, ys, G::PIECE, lane);
+            gram_at<N, PP, KP, PP, true>(x, eb_a + xt, yb_a + ys, PB);
             factor(x, false, true, false, 1.f, false);
             split_a<PP>(x[0], x[1], rq3);
         }
         split_a<PP>(kq[0], kq[1], kq3);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const int so = b_trans(lane, LD) + ko + i0 + p * 16;
+            const uint32_t so = buf_a + ko * ROWS16 + (at_t ^ ((i0 + p * 16) * 2));
             Acc acc;
-            times<PP, KP, PP, true>(acc, true, kq3, kb, G::KPIECE, so);
-            if (sb >= tb) times<PP, KP, PP, true>(acc, false, rq3, rb, G::KPIECE, so);
+            times_at<PP, KP, PP, true>(acc, true, kq3, so, KB);
+            if (sb >= tb) times_at<PP, KP, PP, true>(acc, false, rq3, so + KP * KB, KB);
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) dk[p][n][i] += acc.hi[n][i] + acc.lo[n][i];
             if (sb <= tb) {
                 Acc ra;
-                times<3, KP, 3, true>(ra, true, dq3, kb, G::KPIECE, so);
+                times_at<3, KP, 3, true>(ra, true, dq3, so, KB);
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) dr[p][n][i] += ra.hi[n][i] + ra.lo[n][i];
             }
+            if (sb == tb) {   // dr of these channels is whole, and R's rows are the warp's own
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const __nv_bfloat16* r2 = rb + place(ko * 16 + lane / 4 + 8 * q, i0 + p * 16 + 8 * n + 2 * (lane % 4));
+                        float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+                        for (int c = KP - 1; c >= 0; --c) {
+                            const uint32_t w2 = *reinterpret_cast<const uint32_t*>(r2 + c * G::KPIECE);
+                            x0 += __uint_as_float(w2 << 16), x1 += __uint_as_float(w2 & 0xffff0000u);
+                        }
+                        own[q] = fmaf(x0, dr[p][n][2 * q], fmaf(x1, dr[p][n][2 * q + 1], own[q]));
+                    }
+            }
         }
     }
-    // --- r . dr, and the outputs
+    // --- the outputs
     const bool whole = a.H == a.Hk;
 #pragma unroll
     for (int p = 0; p < NP; ++p)
@@ -485,8 +523,6 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, kCtas<IO, N>) de
             for (int q = 0; q < 2; ++q) {
                 const int t = t_lo + 8 * q, c = i0 + p * 16 + 8 * n + 2 * (lane % 4);
                 if (t >= nt) continue;
-                const IO* r2 = rp + t * ks + c;
-                own[q] = fmaf(to_f32(r2[0]), dr[p][n][2 * q], fmaf(to_f32(r2[1]), dr[p][n][2 * q + 1], own[q]));
                 const int64_t at = rows + t * vs + c;
                 if (!whole || KP == 3) {
                     float* orr = whole ? static_cast<float*>(a.dr) : a.drh;
