@@ -222,10 +222,10 @@ struct SegmentShape {
     static constexpr int SPIECE = JB * N;
     static constexpr int KR = KP == 3 && N == 128 ? 16 : 64;  // tokens of K and R at a time
     static constexpr int KPIECE = KR * N;
-    // e, du, dy; S and D, later K and R; sums, beta and the sums over channels
+    // u, dv, dy; S and D, later K and R; the decays and the sums over channels
     static constexpr int S_ROWS = (3 + PP + KP) * PIECE * 2;
     static constexpr int A_ = (3 + PP) * SPIECE * 2, B_ = 2 * KP * KPIECE * 2, S_BUF = A_ > B_ ? A_ : B_;
-    static constexpr int S_SUM = kSegment * (8 + 4 + 4 + 4 * HALVES);
+    static constexpr int S_SUM = kSegment * (8 + 4 + 4 * HALVES);
     static constexpr int SMEM = S_ROWS + S_BUF + S_SUM;
     // CTAs an SM by shared memory; registers follow
     static constexpr int CTAS = 227 * 1024 / (SMEM + 1024) > 3 ? 3 : 227 * 1024 / (SMEM + 1024);
@@ -237,14 +237,13 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     constexpr int KP = G::KP, PP = G::PP, NP = G::IC / 16;
     constexpr Swizzled<N> place{};
     extern __shared__ __align__(1024) char smem[];
-    __nv_bfloat16* eb = reinterpret_cast<__nv_bfloat16*>(smem);
-    __nv_bfloat16* db = eb + 3 * G::PIECE;
+    __nv_bfloat16* ub = reinterpret_cast<__nv_bfloat16*>(smem);   // u = beta e
+    __nv_bfloat16* db = ub + 3 * G::PIECE;                        // dv = beta du
     __nv_bfloat16* yb = db + PP * G::PIECE;
     __nv_bfloat16* buf = reinterpret_cast<__nv_bfloat16*>(smem + G::S_ROWS);
     float2* sums = reinterpret_cast<float2*>(smem + G::S_ROWS + G::S_BUF);
-    float* beta = reinterpret_cast<float*>(sums + kSegment);
-    float* duv = beta + kSegment;     // du . v of a token
-    float* rdr = duv + kSegment;      // r . dr, by halves of the channels
+    float* dvv = reinterpret_cast<float*>(sums + kSegment);       // dv . v of a token
+    float* rdr = dvv + kSegment;                                  // r . dr, by halves of the channels
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int tb = warp % 4, i0 = warp / 4 * G::IC;
 
@@ -291,10 +290,12 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
             // all loads first, of a row that exists; rows behind the last token are zeroed after
             float4 x[U], y[U], v[U];
             uint2 vr[U];
+            float be[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int i = lane + (n + u) * 32, t = i / ROWV, c = (i % ROWV) * 4;
                 const int64_t at = rows + (t < left ? row + t : 0) * vs + c;
+                be[u] = __ldg(a.beta + scalar + (t < left ? row + t : 0) * a.H);
                 x[u] = load4(a.e + at, true);
                 y[u] = load4(a.du + at, true);
                 const IO* vp = static_cast<const IO*>(a.v) + at;
@@ -314,8 +315,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
                     v[u] = make_float4(__uint_as_float(vr[u].x << 16), __uint_as_float(vr[u].x & 0xffff0000u),
                                        __uint_as_float(vr[u].y << 16), __uint_as_float(vr[u].y & 0xffff0000u));
                 if (t >= left) x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                put4<3>(eb + place(row + t, c), G::PIECE, x[u]);
-                put4<PP>(db + place(row + t, c), G::PIECE, y[u]);
+                const float bt = be[u];
                 float s = fmaf(x[u].x, y[u].x, fmaf(x[u].y, y[u].y, fmaf(x[u].z, y[u].z, x[u].w * y[u].w)));
                 float z = fmaf(v[u].x, y[u].x, fmaf(v[u].y, y[u].y, fmaf(v[u].z, y[u].z, v[u].w * y[u].w)));
 #pragma unroll
@@ -325,8 +325,10 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
                 }
                 if (lane % ROWV == 0) {
                     if (t < left) a.dbeta[scalar + (row + t) * a.H] = s;
-                    duv[row + t] = z;
+                    dvv[row + t] = bt * z;
                 }
+                put4<3>(ub + place(row + t, c), G::PIECE, make_float4(bt * x[u].x, bt * x[u].y, bt * x[u].z, bt * x[u].w));
+                put4<PP>(db + place(row + t, c), G::PIECE, make_float4(bt * y[u].x, bt * y[u].y, bt * y[u].z, bt * y[u].w));
             }
         }
     }
@@ -344,8 +346,6 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         }
         sums[ta] = two_floats(x - x1 + x0);
         sums[ta + 1] = two_floats(x);
-        beta[ta] = ta < nt ? a.beta[scalar + ta * a.H] : 0.f;
-        beta[ta + 1] = ta + 1 < nt ? a.beta[scalar + (ta + 1) * a.H] : 0.f;
     }
 
     // --- the products with S and D: C[t][i], tiles of 16 channels
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     // this lane's places (bytes): as an A operand or a transposed B, and as a plain B; the columns' by exclusive or
     const uint32_t at_t = place((lane & 7) + ((lane >> 3) & 1) * 8, (lane >> 4) * 8) * 2;
     const uint32_t at_p = place((lane & 7) + (lane >> 4) * 8, ((lane >> 3) & 1) * 8) * 2;
-    const uint32_t eb_a = smem_u32(eb), db_a = smem_u32(db), yb_a = smem_u32(yb), buf_a = smem_u32(buf);
+    const uint32_t ub_a = smem_u32(ub), db_a = smem_u32(db), yb_a = smem_u32(yb), buf_a = smem_u32(buf);
     constexpr int PB = G::PIECE * 2, SB = G::SPIECE * 2, KB = G::KPIECE * 2, ROWS16 = 16 * N * 2;
     const int t_lo = tb * 16 + lane / 4;                  // this lane's rows: t_lo and t_lo + 8
 #pragma unroll 1
@@ -375,7 +375,6 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
 #pragma unroll
         for (int q = 0; q < 2; ++q)
             gq[q] = make_float2(decay_of(sums[t_lo + 8 * q], make_float2(0.f, 0.f)), decay_of(sums[kSegment - 1], sums[t_lo + 8 * q]));
-        const float b0 = beta[t_lo], b1 = beta[t_lo + 8];
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             Acc ra, ka, da;
@@ -383,26 +382,25 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
             for (int kk = 0; kk < G::JB / 16; ++kk) {
                 const uint32_t off = tb * ROWS16 + (at_t ^ ((jb + kk * 16) * 2));
                 const uint32_t so = buf_a + kk * ROWS16 + (at_t ^ ((i0 + p * 16) * 2));
-                uint32_t yq[KP][4], uq[PP][4], eq[PP][4];
+                uint32_t yq[KP][4], vq[PP][4], uq[PP][4];
 #pragma unroll
                 for (int c = 0; c < KP; ++c) ldsm4(yq[c], yb_a + c * PB + off);
 #pragma unroll
                 for (int c = 0; c < PP; ++c) {
-                    ldsm4(uq[c], db_a + c * PB + off);
-                    ldsm4(eq[c], eb_a + c * PB + off);
+                    ldsm4(vq[c], db_a + c * PB + off);
+                    ldsm4(uq[c], ub_a + c * PB + off);
                 }
                 times_at<KP, 3, 3, true>(ra, kk == 0, yq, so, SB);
-                times_at<PP, PP, PP, true>(ka, kk == 0, uq, so, SB);
-                times_at<PP, PP, PP, true>(da, kk == 0, eq, so + 3 * SB, SB);
+                times_at<PP, PP, PP, true>(ka, kk == 0, vq, so, SB);
+                times_at<PP, PP, PP, true>(da, kk == 0, uq, so + 3 * SB, SB);
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 f = gq[i >> 1];
-                    const float bt = (i >> 1) ? b1 : b0;
                     dr[p][n][i] = fmaf(f.x, ra.hi[n][i] + ra.lo[n][i], dr[p][n][i]);
-                    dk[p][n][i] += bt * (f.y * (da.hi[n][i] + da.lo[n][i]) - f.x * (ka.hi[n][i] + ka.lo[n][i]));
+                    dk[p][n][i] = fmaf(f.y, da.hi[n][i] + da.lo[n][i], fmaf(-f.x, ka.hi[n][i] + ka.lo[n][i], dk[p][n][i]));
                 }
         }
     }
@@ -435,46 +433,54 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         }
         const int ko = G::KR == 16 ? 0 : sb;   // the block's rows of K and R
         const uint32_t xt = tb * ROWS16 + at_t, ys = sb * ROWS16 + at_p;
-        // kq: -(du_t.e_s below the diagonal, e_t.du_s above), to K; rq: e_t.dy_s, to R; dq: dy_t.e_s, K to dr
+        // with the decay between the tokens -- kq: -(dv_t.u_s below the diagonal, u_t.dv_s above), to K;
+        // rq: u_t.dy_s, to R; dq: dy_t.u_s, K to dr
         float kq[2][4], x[2][4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) kq[n][i] = 0.f;
         uint32_t dq3[3][4], rq3[PP][4], kq3[PP][4];
-        float2 st[2][2], tt[2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) st[n][q] = sums[sb * 16 + 8 * n + 2 * (lane % 4) + q];
-        tt[0] = sums[t_lo], tt[1] = sums[t_lo + 8];
-        auto factor = [&](float (&c)[2][4], bool lower, bool diag, bool both, float sign, bool add) {
-            // times the decay between the tokens and beta (of both, or of e's token)
+        float gm[2][4];
+        auto decays = [&](bool lower) {
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int s = sb * 16 + 8 * n + 2 * (lane % 4) + (i & 1), t = t_lo + 8 * (i >> 1);
-                    const float gm = lower ? decay_of(tt[i >> 1], st[n][i & 1]) : decay_of(st[n][i & 1], tt[i >> 1]);
-                    const bool in = lower ? (diag ? s <= t : s < t) : (diag ? s >= t : s > t);
-                    float f = both ? beta[s] * beta[t] : lower ? beta[s] : beta[t];
-                    f = in ? sign * gm * f * c[n][i] : 0.f;
-                    c[n][i] = f;
-                    if (add) kq[n][i] += f;
+                    const int s = 8 * n + 2 * (lane % 4) + (i & 1), t = lane / 4 + 8 * (i >> 1);   // in their blocks
+                    const float2 ws = sums[sb * 16 + s], wt = sums[tb * 16 + t];
+                    gm[n][i] = lower ? decay_of(wt, ws) : decay_of(ws, wt);
+                    if (sb == tb && (lower ? s > t : s < t)) gm[n][i] = 0.f;
                 }
         };
+        const bool diag = sb == tb;
         if (sb <= tb) {
-            gram_at<N, PP, PP, PP, true>(x, db_a + xt, eb_a + ys, PB);
-            factor(x, true, false, true, -1.f, true);
-            gram_at<N, KP, 3, 3, true>(x, yb_a + xt, eb_a + ys, PB);
-            factor(x, true, true, false, 1.f, false);
+            decays(true);
+            gram_at<N, PP, PP, PP, true>(x, db_a + xt, ub_a + ys, PB);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)   // not the token's own
+                    kq[n][i] = diag && lane / 4 + 8 * (i >> 1) == 8 * n + 2 * (lane % 4) + (i & 1) ? 0.f : -gm[n][i] * x[n][i];
+            gram_at<N, KP, 3, 3, true>(x, yb_a + xt, ub_a + ys, PB);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[n][i] *= gm[n][i];
             split_a<3>(x[0], x[1], dq3);
         }
         if (sb >= tb) {
-            gram_at<N, PP, PP, PP, true>(x, eb_a + xt, db_a + ys, PB);
-            factor(x, false, false, true, -1.f, true);
-            gram_at<N, PP, KP, PP, true>(x, eb_a + xt, yb_a + ys, PB);
-            factor(x, false, true, false, 1.f, false);
+            decays(false);
+            gram_at<N, PP, PP, PP, true>(x, ub_a + xt, db_a + ys, PB);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool self = lane / 4 + 8 * (i >> 1) == 8 * n + 2 * (lane % 4) + (i & 1);
+                    if (!diag) kq[n][i] = -gm[n][i] * x[n][i];
+                    else if (!self) kq[n][i] -= gm[n][i] * x[n][i];
+                }
+            gram_at<N, PP, KP, PP, true>(x, ub_a + xt, yb_a + ys, PB);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[n][i] *= gm[n][i];
             split_a<PP>(x[0], x[1], rq3);
         }
         split_a<PP>(kq[0], kq[1], kq3);
@@ -516,36 +522,41 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     // --- the outputs
     const bool whole = a.H == a.Hk;
 #pragma unroll
-    for (int p = 0; p < NP; ++p)
+    for (int q = 0; q < 2; ++q) {
+        const int t = t_lo + 8 * q;
+        if (t >= nt) continue;
+        const int64_t at = rows + t * vs + i0 + 2 * (lane % 4);
+        if (!whole || KP == 3) {
+            float* orr = (whole ? static_cast<float*>(a.dr) : a.drh) + at;
+            float* ok = (whole ? static_cast<float*>(a.dk) : a.dkh) + at;
+            const bool pairs = !whole || a.vec;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int t = t_lo + 8 * q, c = i0 + p * 16 + 8 * n + 2 * (lane % 4);
-                if (t >= nt) continue;
-                const int64_t at = rows + t * vs + c;
-                if (!whole || KP == 3) {
-                    float* orr = whole ? static_cast<float*>(a.dr) : a.drh;
-                    float* ok = whole ? static_cast<float*>(a.dk) : a.dkh;
-                    if (!whole || a.vec) {
-                        *reinterpret_cast<float2*>(orr + at) = make_float2(dr[p][n][2 * q], dr[p][n][2 * q + 1]);
-                        *reinterpret_cast<float2*>(ok + at) = make_float2(dk[p][n][2 * q], dk[p][n][2 * q + 1]);
-                    } else {
-                        orr[at] = dr[p][n][2 * q], orr[at + 1] = dr[p][n][2 * q + 1];
-                        ok[at] = dk[p][n][2 * q], ok[at + 1] = dk[p][n][2 * q + 1];
-                    }
+            for (int c = 0; c < 2 * NP; ++c) {
+                const float *x = &dr[c / 2][c % 2][2 * q], *y = &dk[c / 2][c % 2][2 * q];
+                if (pairs) {
+                    *reinterpret_cast<float2*>(orr + 8 * c) = make_float2(x[0], x[1]);
+                    *reinterpret_cast<float2*>(ok + 8 * c) = make_float2(y[0], y[1]);
                 } else {
-                    IO* orr = static_cast<IO*>(a.dr) + at;
-                    IO* ok = static_cast<IO*>(a.dk) + at;
-                    if (a.vec) {
-                        *reinterpret_cast<__nv_bfloat162*>(orr) = __floats2bfloat162_rn(dr[p][n][2 * q], dr[p][n][2 * q + 1]);
-                        *reinterpret_cast<__nv_bfloat162*>(ok) = __floats2bfloat162_rn(dk[p][n][2 * q], dk[p][n][2 * q + 1]);
-                    } else {
-                        put(orr, dr[p][n][2 * q]), put(orr + 1, dr[p][n][2 * q + 1]);
-                        put(ok, dk[p][n][2 * q]), put(ok + 1, dk[p][n][2 * q + 1]);
-                    }
+                    orr[8 * c] = x[0], orr[8 * c + 1] = x[1];
+                    ok[8 * c] = y[0], ok[8 * c + 1] = y[1];
                 }
             }
+        } else {
+            IO* orr = static_cast<IO*>(a.dr) + at;
+            IO* ok = static_cast<IO*>(a.dk) + at;
+#pragma unroll
+            for (int c = 0; c < 2 * NP; ++c) {
+                const float *x = &dr[c / 2][c % 2][2 * q], *y = &dk[c / 2][c % 2][2 * q];
+                if (a.vec) {
+                    *reinterpret_cast<__nv_bfloat162*>(orr + 8 * c) = __floats2bfloat162_rn(x[0], x[1]);
+                    *reinterpret_cast<__nv_bfloat162*>(ok + 8 * c) = __floats2bfloat162_rn(y[0], y[1]);
+                } else {
+                    put(orr + 8 * c, x[0]), put(orr + 8 * c + 1, x[1]);
+                    put(ok + 8 * c, y[0]), put(ok + 8 * c + 1, y[1]);
+                }
+            }
+        }
+    }
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         own[q] += __shfl_xor_sync(0xffffffffu, own[q], 1);
@@ -570,7 +581,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
             const int t = ta + q;
             float x = rdr[t];
             if constexpr (G::HALVES == 2) x += rdr[kSegment + t];
-            term[q] = t < nt ? fmaf(-beta[t], duv[t], x) : 0.f;
+            term[q] = t < nt ? x - dvv[t] : 0.f;
         }
         float x = term[0] + term[1];   // suffix sums over the lanes
 #pragma unroll
