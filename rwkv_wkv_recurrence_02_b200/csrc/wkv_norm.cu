@@ -49,7 +49,9 @@ Plan plan(int64_t rows, int64_t C, int64_t group, int elem, int align, bool bwd)
     int64_t span = rows * p.slots / fill;
     if (bwd && span < rows / kChunks) span = rows / kChunks;
     const int64_t most = bwd ? 256 : 32;
-    p.span = int(span < 1 ? 1 : span > most ? most : span);
+    span = span < 1 ? 1 : span > most ? most : span;
+    if (span > 4) span = (span + 3) / 4 * 4;   // whole rounds of the kernels' loop
+    p.span = int(span);
     p.chunks = (rows + p.span - 1) / p.span;
     p.bytes = bwd ? size_t(p.chunks) * C * 8 : 0;
     return p;
@@ -57,9 +59,9 @@ Plan plan(int64_t rows, int64_t C, int64_t group, int elem, int align, bool bwd)
 
 template <typename IO, int PER, int V, bool BWD>
 int launch_small(const nm::Args& a, int64_t chunks, cudaStream_t st) {
-    // tokens in flight: about 64 bytes of each tensor a lane
+    // tokens a lane works on, as many on their way
     constexpr int B = PER * V * int(sizeof(IO));
-    constexpr int U = BWD ? (B >= 32 ? 1 : 2) : (B >= 64 ? 1 : B >= 32 ? 2 : 4);
+    constexpr int U = BWD || B >= 32 ? 1 : 2;
     const int64_t blocks = (chunks * a.slots + 255) / 256;
     if constexpr (BWD)
         return a.gate ? launch(nm::backward_kernel<IO, PER, V, U, true>, blocks, 256, 0, st, a)

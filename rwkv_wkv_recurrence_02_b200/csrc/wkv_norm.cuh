@@ -9,8 +9,8 @@
 // power of two, the lanes behind the group's last channel idle), and keeps
 // its channels over `span` tokens, so weight and bias stay in registers and
 // the reverse mode sums dweight and dbias there.  Mean and variance are two
-// passes over registers: x is read once.  Bound by memory: the rows of
-// kUnroll tokens are in flight at once.
+// passes over registers: x is read once.  Bound by memory, and near it by the
+// instructions, so the arithmetic is in packed pairs.
 #pragma once
 
 #include "wkv_common.cuh"
@@ -130,6 +130,124 @@ struct Place {
     }
 };
 
+// Packed pairs of a lane's channels.  PER == 1 keeps one value a pair, the
+// other half zero throughout.
+template <int PER>
+constexpr int kPairs = PER > 1 ? PER / 2 : 1;
+
+template <typename IO, int PER>
+__device__ __forceinline__ F2 pair_of(const Pack<IO, PER>& v, int i) {
+    return f2(v.get(2 * i), PER > 1 ? v.get(2 * i + 1) : 0.f);
+}
+template <typename IO, int PER>
+__device__ __forceinline__ void put_pair(Pack<IO, PER>& v, int i, F2 x) {
+    if constexpr (PER > 1 && sizeof(IO) == 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f2lo(x), f2hi(x));
+        v.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        v.put(2 * i, f2lo(x));
+        if constexpr (PER > 1) v.put(2 * i + 1, f2hi(x));
+    }
+}
+__device__ __forceinline__ F2 sigmoid2(F2 x) {
+    const F2 e = ex2x2(mul2(x, f2s(-kLog2e)));
+    return rcpx2(add2(e, f2s(1.f)));
+}
+__device__ __forceinline__ F2 neg2(F2 x) { return mul2(x, f2s(-1.f)); }
+
+// weight and bias of a lane's channels
+template <int PER, int V>
+struct Affine {
+    F2 w[V][kPairs<PER>], b[V][kPairs<PER>];
+    __device__ __forceinline__ void load(const Args& a, const Place<PER, V>& at) {
+        const int step = a.lpg * PER;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < kPairs<PER>; ++i) {
+                float x[4] = {1.f, 1.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < (PER > 1 ? 2 : 1); ++q)
+                    if (v < at.n) {
+                        const int64_t c = at.c0 + v * step + 2 * i + q;
+                        if (a.weight != nullptr) x[q] = __ldg(a.weight + c);
+                        if (a.bias != nullptr) x[2 + q] = __ldg(a.bias + c);
+                    }
+                w[v][i] = f2(x[0], x[1]);
+                b[v][i] = f2(x[2], x[3]);
+            }
+    }
+};
+
+// x - mean of a lane's channels (zero where there are none), and 1 / sqrt(var + eps)
+template <typename IO, int PER, int V>
+__device__ __forceinline__ float centre(const Args& a, const Place<PER, V>& at, const Pack<IO, PER> (&x)[V],
+                                        F2 (&d)[V][kPairs<PER>]) {
+    F2 s = f2s(0.f);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < kPairs<PER>; ++i) {
+            d[v][i] = pair_of(x[v], i);
+            s = add2(s, d[v][i]);
+        }
+    const float mean = group_sum(f2lo(s) + f2hi(s), a.lpg) * a.inv_group;
+    s = f2s(0.f);
+    const F2 m = PER > 1 ? f2s(-mean) : f2(-mean, 0.f);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < kPairs<PER>; ++i) {
+            d[v][i] = v < at.n ? add2(d[v][i], m) : f2s(0.f);
+            s = fma2(d[v][i], d[v][i], s);
+        }
+    return rsqrtf(fmaf(group_sum(f2lo(s) + f2hi(s), a.lpg), a.inv_group, a.eps));
+}
+
+// A lane's vectors of one token of each tensor
+template <typename IO, int PER, int V, bool GATE, bool BWD>
+struct Rows {
+    Pack<IO, PER> x[V], gate[V], dy[V];
+    __device__ __forceinline__ void load(const Args& a, const Place<PER, V>& at, int64_t r) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            x[v].clear();
+            if (BWD) dy[v].clear();
+            if (GATE) gate[v].clear();
+            if (v < at.n) {
+                const int64_t off = r * a.C + at.c0 + v * (a.lpg * PER);
+                x[v].load(static_cast<const IO*>(a.x) + off);
+                if constexpr (BWD) dy[v].load(static_cast<const IO*>(a.dy) + off);
+                if constexpr (GATE) gate[v].load(static_cast<const IO*>(a.gate) + off);
+            }
+        }
+    }
+};
+
+template <typename IO, int PER, int V, bool GATE>
+__device__ __forceinline__ void forward_row(const Args& a, const Place<PER, V>& at, const Affine<PER, V>& p,
+                                            const Rows<IO, PER, V, GATE, false>& t, int64_t r) {
+    F2 d[V][kPairs<PER>];
+    const F2 inv = f2s(centre<IO, PER, V>(a, at, t.x, d));
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (v >= at.n) continue;
+        Pack<IO, PER> o;
+#pragma unroll
+        for (int i = 0; i < kPairs<PER>; ++i) {
+            const F2 z = fma2(mul2(d[v][i], inv), p.w[v][i], p.b[v][i]);
+            F2 g = GATE ? pair_of(t.gate[v], i) : z;
+            if (a.act != kNone) {
+                const F2 s = sigmoid2(g);
+                g = a.act == kSilu ? mul2(g, s) : s;
+            }
+            put_pair(o, i, GATE ? mul2(z, g) : g);
+        }
+        o.store(static_cast<IO*>(a.y) + r * a.C + at.c0 + v * (a.lpg * PER));
+    }
+}
+
+// U tokens of a lane are on their way while U others are worked on.
 template <typename IO, int PER, int V, int U, bool GATE>
 __global__ void __launch_bounds__(256) forward_kernel(const Args a) {
     pdl_begin();
@@ -137,170 +255,124 @@ __global__ void __launch_bounds__(256) forward_kernel(const Args a) {
     const int64_t r0 = at.chunk * a.span;
     if (r0 >= a.rows) return;   // whole warps: slots is a multiple of 32
     const int64_t r1 = r0 + a.span < a.rows ? r0 + a.span : a.rows;
-    const int step = a.lpg * PER;
-    float wt[V][PER], bs[V][PER];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int64_t c = at.c0 + v * step + i;
-            wt[v][i] = a.weight != nullptr && v < at.n ? __ldg(a.weight + c) : 1.f;
-            bs[v][i] = a.bias != nullptr && v < at.n ? __ldg(a.bias + c) : 0.f;
-        }
-    for (int64_t r = r0; r < r1; r += U) {
-        Pack<IO, PER> x[U][V], gt[U][V];
+    Rows<IO, PER, V, GATE, false> x[U], y[U];
+    auto load = [&](Rows<IO, PER, V, GATE, false> (&t)[U], int64_t r) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
+            if (r + u < r1) t[u].load(a, at, r + u);
+    };
+    load(x, r0);
+    Affine<PER, V> p;
+    p.load(a, at);
+    auto work = [&](const Rows<IO, PER, V, GATE, false> (&t)[U], int64_t r) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                x[u][v].clear();
-                if (r + u < r1 && v < at.n) {
-                    const int64_t off = (r + u) * a.C + at.c0 + v * step;
-                    x[u][v].load(static_cast<const IO*>(a.x) + off);
-                    if constexpr (GATE) gt[u][v].load(static_cast<const IO*>(a.gate) + off);
-                }
-            }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (r + u >= r1) break;
-            float s = 0.f;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int i = 0; i < PER; ++i) s += x[u][v].get(i);
-            const float mean = group_sum(s, a.lpg) * a.inv_group;
-            s = 0.f;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (v < at.n)
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        const float d = x[u][v].get(i) - mean;
-                        s = fmaf(d, d, s);
-                    }
-            const float inv = rsqrtf(fmaf(group_sum(s, a.lpg), a.inv_group, a.eps));
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (v < at.n) {
-                    Pack<IO, PER> o;
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        const float z = fmaf((x[u][v].get(i) - mean) * inv, wt[v][i], bs[v][i]);
-                        o.put(i, GATE ? z * act(a.act, gt[u][v].get(i)) : act(a.act, z));
-                    }
-                    o.store(static_cast<IO*>(a.y) + (r + u) * a.C + at.c0 + v * step);
-                }
-        }
+        for (int u = 0; u < U; ++u)
+            if (r + u < r1) forward_row<IO, PER, V, GATE>(a, at, p, t[u], r + u);
+    };
+#pragma unroll 1
+    for (int64_t r = r0; r < r1; r += 2 * U) {
+        load(y, r + U);
+        work(x, r);
+        load(x, r + 2 * U);
+        work(y, r + U);
     }
 }
 
 // dz = dy act'(z) without a gate, dy act(gate) with one (dgate = dy z act'(gate));
 // dweight = sum dz hat, dbias = sum dz over the tokens;
 // dx = (h - mean(h) - hat mean(h hat)) / sqrt(var + eps), h = weight dz.
+template <typename IO, int PER, int V, bool GATE>
+__device__ __forceinline__ void backward_row(const Args& a, const Place<PER, V>& at, const Affine<PER, V>& p,
+                                             const Rows<IO, PER, V, GATE, true>& t, int64_t r, F2 (&dw)[V][kPairs<PER>],
+                                             F2 (&db)[V][kPairs<PER>]) {
+    constexpr int P = kPairs<PER>;
+    F2 hat[V][P], h[V][P];
+    const float inv = centre<IO, PER, V>(a, at, t.x, hat);
+    F2 h1 = f2s(0.f), h2 = f2s(0.f);
+    const int64_t row = r * a.C + at.c0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        Pack<IO, PER> o;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            hat[v][i] = mul2(hat[v][i], f2s(inv));
+            const F2 z = fma2(hat[v][i], p.w[v][i], p.b[v][i]);
+            const F2 g = GATE ? pair_of(t.gate[v], i) : z, dy = pair_of(t.dy[v], i);
+            F2 value = g, slope = f2s(1.f);
+            if (a.act != kNone) {
+                const F2 s = sigmoid2(g), rest = fma2(s, f2s(-1.f), f2s(1.f));   // 1 - s
+                value = a.act == kSilu ? mul2(g, s) : s;
+                slope = mul2(s, a.act == kSilu ? fma2(g, rest, f2s(1.f)) : rest);
+            }
+            const F2 dz = mul2(dy, GATE ? value : slope);
+            if constexpr (GATE) put_pair(o, i, mul2(mul2(dy, z), slope));
+            dw[v][i] = fma2(dz, hat[v][i], dw[v][i]);
+            db[v][i] = add2(db[v][i], dz);
+            h[v][i] = mul2(p.w[v][i], dz);
+            h1 = add2(h1, h[v][i]);
+            h2 = fma2(h[v][i], hat[v][i], h2);
+        }
+        if (GATE && v < at.n) o.store(static_cast<IO*>(a.dgate) + row + v * (a.lpg * PER));
+    }
+    const float m1 = group_sum(f2lo(h1) + f2hi(h1), a.lpg) * a.inv_group;
+    const float m2 = group_sum(f2lo(h2) + f2hi(h2), a.lpg) * a.inv_group;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (v >= at.n) continue;
+        Pack<IO, PER> o;
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            put_pair(o, i, mul2(fma2(hat[v][i], f2s(-m2), add2(h[v][i], f2s(-m1))), f2s(inv)));
+        o.store(static_cast<IO*>(a.dx) + row + v * (a.lpg * PER));
+    }
+}
+
 template <typename IO, int PER, int V, int U, bool GATE>
 __global__ void __launch_bounds__(256) backward_kernel(const Args a) {
     pdl_begin();
+    constexpr int P = kPairs<PER>;
     const Place<PER, V> at(a);
     const int64_t r0 = at.chunk * a.span;
     if (r0 >= a.rows) return;
     const int64_t r1 = r0 + a.span < a.rows ? r0 + a.span : a.rows;
-    const int step = a.lpg * PER;
-    float wt[V][PER], bs[V][PER], dw[V][PER], db[V][PER];
+    Rows<IO, PER, V, GATE, true> x[U], y[U];
+    auto load = [&](Rows<IO, PER, V, GATE, true> (&t)[U], int64_t r) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (r + u < r1) t[u].load(a, at, r + u);
+    };
+    load(x, r0);
+    Affine<PER, V> p;
+    p.load(a, at);
+    F2 dw[V][P], db[V][P];
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int64_t c = at.c0 + v * step + i;
-            wt[v][i] = a.weight != nullptr && v < at.n ? __ldg(a.weight + c) : 1.f;
-            bs[v][i] = a.bias != nullptr && v < at.n ? __ldg(a.bias + c) : 0.f;
-            dw[v][i] = db[v][i] = 0.f;
-        }
-    for (int64_t r = r0; r < r1; r += U) {
-        Pack<IO, PER> x[U][V], gt[U][V], dy[U][V];
+        for (int i = 0; i < P; ++i) dw[v][i] = db[v][i] = f2s(0.f);
+    auto work = [&](const Rows<IO, PER, V, GATE, true> (&t)[U], int64_t r) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                x[u][v].clear();
-                dy[u][v].clear();
-                if (r + u < r1 && v < at.n) {
-                    const int64_t off = (r + u) * a.C + at.c0 + v * step;
-                    x[u][v].load(static_cast<const IO*>(a.x) + off);
-                    dy[u][v].load(static_cast<const IO*>(a.dy) + off);
-                    if constexpr (GATE) gt[u][v].load(static_cast<const IO*>(a.gate) + off);
-                }
-            }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (r + u >= r1) break;
-            float s = 0.f;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int i = 0; i < PER; ++i) s += x[u][v].get(i);
-            const float mean = group_sum(s, a.lpg) * a.inv_group;
-            s = 0.f;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (v < at.n)
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        const float d = x[u][v].get(i) - mean;
-                        s = fmaf(d, d, s);
-                    }
-            const float inv = rsqrtf(fmaf(group_sum(s, a.lpg), a.inv_group, a.eps));
-            float h1 = 0.f, h2 = 0.f;
-            float h[V][PER];
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (v < at.n) {
-                    Pack<IO, PER> o;
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        const float hat = (x[u][v].get(i) - mean) * inv;
-                        const float z = fmaf(hat, wt[v][i], bs[v][i]);
-                        const float g = dy[u][v].get(i);
-                        float slope, dz;
-                        if constexpr (GATE) {
-                            dz = g * act_slope(a.act, gt[u][v].get(i), &slope);
-                            o.put(i, g * z * slope);
-                        } else {
-                            act_slope(a.act, z, &slope);
-                            dz = g * slope;
-                        }
-                        dw[v][i] = fmaf(dz, hat, dw[v][i]);
-                        db[v][i] += dz;
-                        h[v][i] = wt[v][i] * dz;
-                        h1 += h[v][i];
-                        h2 = fmaf(h[v][i], hat, h2);
-                    }
-                    if constexpr (GATE) o.store(static_cast<IO*>(a.dgate) + (r + u) * a.C + at.c0 + v * step);
-                }
-            h1 = group_sum(h1, a.lpg) * a.inv_group;
-            h2 = group_sum(h2, a.lpg) * a.inv_group;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (v < at.n) {
-                    Pack<IO, PER> o;
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        const float hat = (x[u][v].get(i) - mean) * inv;
-                        o.put(i, inv * (h[v][i] - h1 - hat * h2));
-                    }
-                    o.store(static_cast<IO*>(a.dx) + (r + u) * a.C + at.c0 + v * step);
-                }
-        }
+            if (r + u < r1) backward_row<IO, PER, V, GATE>(a, at, p, t[u], r + u, dw, db);
+    };
+#pragma unroll 1
+    for (int64_t r = r0; r < r1; r += 2 * U) {
+        load(y, r + U);
+        work(x, r);
+        load(x, r + 2 * U);
+        work(y, r + U);
     }
     if (a.part != nullptr) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (v < at.n)
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int64_t c = at.c0 + v * step + i;
-                    a.part[(at.chunk * 2) * a.C + c] = dw[v][i];
-                    a.part[(at.chunk * 2 + 1) * a.C + c] = db[v][i];
-                }
+                for (int i = 0; i < P; ++i)
+#pragma unroll
+                    for (int q = 0; q < (PER > 1 ? 2 : 1); ++q) {
+                        const int64_t c = at.c0 + v * (a.lpg * PER) + 2 * i + q;
+                        a.part[(at.chunk * 2) * a.C + c] = q ? f2hi(dw[v][i]) : f2lo(dw[v][i]);
+                        a.part[(at.chunk * 2 + 1) * a.C + c] = q ? f2hi(db[v][i]) : f2lo(db[v][i]);
+                    }
     }
 }
 
