@@ -43,32 +43,42 @@ Plan plan(int64_t rows, int64_t C, int64_t group, int elem, int align, bool bwd)
     p.v = 1;
     while (p.v * p.lpg < vecs) p.v *= 2;
     p.slots = (groups * p.lpg + 31) / 32 * 32;
-    // a lane takes enough tokens that its weights pay, and few enough that
-    // the lanes fill the machine several times over
-    const int64_t fill = int64_t(148) * 2048 * 2;
-    int64_t span = rows * p.slots / fill;
-    if (bwd && span < rows / kChunks) span = rows / kChunks;
+    // as many CTAs as the machine holds a few times over (forward), or twice
+    // (reverse: a chunk's partial sums cost 8 bytes a channel), and no more
+    const int64_t fill = int64_t(148) * 256 * (bwd ? 4 : 24);
+    int64_t span = (rows * p.slots + fill - 1) / fill;
     const int64_t most = bwd ? 256 : 32;
     span = span < 1 ? 1 : span > most ? most : span;
-    if (span > 4) span = (span + 3) / 4 * 4;   // whole rounds of the kernels' loop
     p.span = int(span);
     p.chunks = (rows + p.span - 1) / p.span;
     p.bytes = bwd ? size_t(p.chunks) * C * 8 : 0;
     return p;
 }
 
+template <typename R>
+int launch_ring(void (*kern)(nm::Args), int64_t blocks, const nm::Args& a, cudaStream_t st) {
+    int rc = WKV_OK;
+    if constexpr (R::SMEM > 48 * 1024)   // groups of over 8 channels a lane only: set at each call
+        rc = record_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::SMEM));
+    return rc != WKV_OK ? rc : launch(kern, blocks, 256, R::SMEM, st, a);
+}
+
+template <typename IO, int PER, int V, bool GATE>
+int launch_backward(const nm::Args& a, int64_t blocks, cudaStream_t st) {
+    using R = nm::Ring<IO, PER, V, GATE, true>;
+    if (a.act == nm::kSilu) return launch_ring<R>(nm::backward_kernel<IO, PER, V, GATE, nm::kSilu>, blocks, a, st);
+    if (a.act == nm::kSigmoid) return launch_ring<R>(nm::backward_kernel<IO, PER, V, GATE, nm::kSigmoid>, blocks, a, st);
+    return launch_ring<R>(nm::backward_kernel<IO, PER, V, GATE, nm::kNone>, blocks, a, st);
+}
+
 template <typename IO, int PER, int V, bool BWD>
 int launch_small(const nm::Args& a, int64_t chunks, cudaStream_t st) {
-    // tokens a lane works on, as many on their way
-    constexpr int B = PER * V * int(sizeof(IO));
-    constexpr int U = BWD || B >= 32 ? 1 : 2;
     const int64_t blocks = (chunks * a.slots + 255) / 256;
     if constexpr (BWD)
-        return a.gate ? launch(nm::backward_kernel<IO, PER, V, U, true>, blocks, 256, 0, st, a)
-                      : launch(nm::backward_kernel<IO, PER, V, U, false>, blocks, 256, 0, st, a);
+        return a.gate ? launch_backward<IO, PER, V, true>(a, blocks, st) : launch_backward<IO, PER, V, false>(a, blocks, st);
     else
-        return a.gate ? launch(nm::forward_kernel<IO, PER, V, U, true>, blocks, 256, 0, st, a)
-                      : launch(nm::forward_kernel<IO, PER, V, U, false>, blocks, 256, 0, st, a);
+        return a.gate ? launch_ring<nm::Ring<IO, PER, V, true, false>>(nm::forward_kernel<IO, PER, V, true>, blocks, a, st)
+                      : launch_ring<nm::Ring<IO, PER, V, false, false>>(nm::forward_kernel<IO, PER, V, false>, blocks, a, st);
 }
 
 template <typename IO, int PER, bool BWD>
@@ -133,7 +143,7 @@ int run(nm::Args& a, const Plan& p, int64_t groups, float* ws, float* dweight, f
         }
     }
     if (rc == WKV_OK && params)
-        rc = launch(nm::params_kernel, (a.C + 31) / 32, 256, 0, st, a.C, p.chunks, part, dweight, dbias);
+        rc = launch(nm::params_kernel, (a.C + 31) / 32, 1024, 0, st, a.C, p.chunks, part, dweight, dbias);
     return rc;
 }
 

@@ -56,6 +56,14 @@ struct Pack {
             w[0] = __ldcs(reinterpret_cast<const unsigned short*>(p));
         }
     }
+    __device__ __forceinline__ void load_shared(uint32_t addr) {
+        if constexpr (PER * sizeof(IO) == 16)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+        else if constexpr (PER * sizeof(IO) == 8)
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+        else
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+    }
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) w[i] = 0;
@@ -208,19 +216,72 @@ __device__ __forceinline__ float centre(const Args& a, const Place<PER, V>& at, 
 template <typename IO, int PER, int V, bool GATE, bool BWD>
 struct Rows {
     Pack<IO, PER> x[V], gate[V], dy[V];
-    __device__ __forceinline__ void load(const Args& a, const Place<PER, V>& at, int64_t r) {
+};
+
+// The tokens a lane has on their way: a ring in shared memory that the lane
+// fills and reads by itself (asynchronous copies, no barrier), STAGES - 1
+// tokens ahead.  Registers would bound the bytes in flight, and with them the
+// bandwidth.  Vectors of 2 bytes, which such copies cannot take, are read when
+// they are needed.
+template <typename IO, int PER, int V, bool GATE, bool BWD>
+struct Ring {
+    static constexpr int B = PER * int(sizeof(IO)), NT = 1 + GATE + BWD;
+    static constexpr bool ASYNC = B >= 4;
+    static constexpr int STAGE = NT * V * B * 256;
+    static constexpr int FIT = 48 * 1024 / STAGE;
+    static constexpr int STAGES = !ASYNC ? 1 : FIT > 5 ? 5 : FIT < 2 ? 2 : FIT;
+    static constexpr int SMEM = ASYNC ? STAGES * STAGE : 0;
+    uint32_t base;
+    int fill, take;
+    __device__ __forceinline__ Ring() : fill(0), take(0) {
+        extern __shared__ __align__(16) char smem[];
+        base = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * B;
+    }
+    // token r's copies (none behind the last: an empty group keeps the count)
+    __device__ __forceinline__ void ask(const Args& a, const Place<PER, V>& at, int64_t r, int64_t r1) {
+        if constexpr (ASYNC) {
+            if (r < r1) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (v < at.n) {
+                        const int64_t off = r * a.C + at.c0 + v * (a.lpg * PER);
+                        const uint32_t dst = base + fill * STAGE + v * B * 256;
+                        copy(dst, static_cast<const IO*>(a.x) + off);
+                        if constexpr (BWD) copy(dst + V * B * 256, static_cast<const IO*>(a.dy) + off);
+                        if constexpr (GATE) copy(dst + (1 + BWD) * V * B * 256, static_cast<const IO*>(a.gate) + off);
+                    }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            fill = fill + 1 == STAGES ? 0 : fill + 1;
+        }
+    }
+    static __device__ __forceinline__ void copy(uint32_t dst, const void* src) {
+        if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(B >= 4 ? B : 4) : "memory");
+    }
+    // the oldest token asked for (token r)
+    __device__ __forceinline__ void get(const Args& a, const Place<PER, V>& at, int64_t r, Rows<IO, PER, V, GATE, BWD>& t) {
+        if constexpr (ASYNC) asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            x[v].clear();
-            if (BWD) dy[v].clear();
-            if (GATE) gate[v].clear();
+            t.x[v].clear();
+            if (BWD) t.dy[v].clear();
+            if (GATE) t.gate[v].clear();
             if (v < at.n) {
-                const int64_t off = r * a.C + at.c0 + v * (a.lpg * PER);
-                x[v].load(static_cast<const IO*>(a.x) + off);
-                if constexpr (BWD) dy[v].load(static_cast<const IO*>(a.dy) + off);
-                if constexpr (GATE) gate[v].load(static_cast<const IO*>(a.gate) + off);
+                if constexpr (ASYNC) {
+                    const uint32_t src = base + take * STAGE + v * B * 256;
+                    t.x[v].load_shared(src);
+                    if constexpr (BWD) t.dy[v].load_shared(src + V * B * 256);
+                    if constexpr (GATE) t.gate[v].load_shared(src + (1 + BWD) * V * B * 256);
+                } else {
+                    const int64_t off = r * a.C + at.c0 + v * (a.lpg * PER);
+                    t.x[v].load(static_cast<const IO*>(a.x) + off);
+                    if constexpr (BWD) t.dy[v].load(static_cast<const IO*>(a.dy) + off);
+                    if constexpr (GATE) t.gate[v].load(static_cast<const IO*>(a.gate) + off);
+                }
             }
         }
+        take = take + 1 == STAGES ? 0 : take + 1;
     }
 };
 
@@ -247,41 +308,32 @@ __device__ __forceinline__ void forward_row(const Args& a, const Place<PER, V>& 
     }
 }
 
-// U tokens of a lane are on their way while U others are worked on.
-template <typename IO, int PER, int V, int U, bool GATE>
-__global__ void __launch_bounds__(256) forward_kernel(const Args a) {
+template <typename IO, int PER, int V, bool GATE>
+__global__ void __launch_bounds__(256, PER * V <= 8 ? 5 : 2) forward_kernel(const Args a) {
     pdl_begin();
     const Place<PER, V> at(a);
     const int64_t r0 = at.chunk * a.span;
     if (r0 >= a.rows) return;   // whole warps: slots is a multiple of 32
     const int64_t r1 = r0 + a.span < a.rows ? r0 + a.span : a.rows;
-    Rows<IO, PER, V, GATE, false> x[U], y[U];
-    auto load = [&](Rows<IO, PER, V, GATE, false> (&t)[U], int64_t r) {
+    using R = Ring<IO, PER, V, GATE, false>;
+    R ring;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (r + u < r1) t[u].load(a, at, r + u);
-    };
-    load(x, r0);
+    for (int i = 0; i < R::STAGES - 1; ++i) ring.ask(a, at, r0 + i, r1);
     Affine<PER, V> p;
     p.load(a, at);
-    auto work = [&](const Rows<IO, PER, V, GATE, false> (&t)[U], int64_t r) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (r + u < r1) forward_row<IO, PER, V, GATE>(a, at, p, t[u], r + u);
-    };
 #pragma unroll 1
-    for (int64_t r = r0; r < r1; r += 2 * U) {
-        load(y, r + U);
-        work(x, r);
-        load(x, r + 2 * U);
-        work(y, r + U);
+    for (int64_t r = r0; r < r1; ++r) {
+        Rows<IO, PER, V, GATE, false> t;
+        ring.get(a, at, r, t);
+        ring.ask(a, at, r + R::STAGES - 1, r1);   // into the place of the token before this one
+        forward_row<IO, PER, V, GATE>(a, at, p, t, r);
     }
 }
 
 // dz = dy act'(z) without a gate, dy act(gate) with one (dgate = dy z act'(gate));
 // dweight = sum dz hat, dbias = sum dz over the tokens;
 // dx = (h - mean(h) - hat mean(h hat)) / sqrt(var + eps), h = weight dz.
-template <typename IO, int PER, int V, bool GATE>
+template <typename IO, int PER, int V, bool GATE, int ACT>
 __device__ __forceinline__ void backward_row(const Args& a, const Place<PER, V>& at, const Affine<PER, V>& p,
                                              const Rows<IO, PER, V, GATE, true>& t, int64_t r, F2 (&dw)[V][kPairs<PER>],
                                              F2 (&db)[V][kPairs<PER>]) {
@@ -299,10 +351,10 @@ __device__ __forceinline__ void backward_row(const Args& a, const Place<PER, V>&
             const F2 z = fma2(hat[v][i], p.w[v][i], p.b[v][i]);
             const F2 g = GATE ? pair_of(t.gate[v], i) : z, dy = pair_of(t.dy[v], i);
             F2 value = g, slope = f2s(1.f);
-            if (a.act != kNone) {
+            if (ACT != kNone) {
                 const F2 s = sigmoid2(g), rest = fma2(s, f2s(-1.f), f2s(1.f));   // 1 - s
-                value = a.act == kSilu ? mul2(g, s) : s;
-                slope = mul2(s, a.act == kSilu ? fma2(g, rest, f2s(1.f)) : rest);
+                value = ACT == kSilu ? mul2(g, s) : s;
+                slope = mul2(s, ACT == kSilu ? fma2(g, rest, f2s(1.f)) : rest);
             }
             const F2 dz = mul2(dy, GATE ? value : slope);
             if constexpr (GATE) put_pair(o, i, mul2(mul2(dy, z), slope));
@@ -327,21 +379,19 @@ __device__ __forceinline__ void backward_row(const Args& a, const Place<PER, V>&
     }
 }
 
-template <typename IO, int PER, int V, int U, bool GATE>
-__global__ void __launch_bounds__(256) backward_kernel(const Args a) {
+// ACT known to the compiler: a test of it at every pair took an eighth of the time
+template <typename IO, int PER, int V, bool GATE, int ACT>
+__global__ void __launch_bounds__(256, PER * V <= 8 ? 2 : 1) backward_kernel(const Args a) {
     pdl_begin();
     constexpr int P = kPairs<PER>;
     const Place<PER, V> at(a);
     const int64_t r0 = at.chunk * a.span;
     if (r0 >= a.rows) return;
     const int64_t r1 = r0 + a.span < a.rows ? r0 + a.span : a.rows;
-    Rows<IO, PER, V, GATE, true> x[U], y[U];
-    auto load = [&](Rows<IO, PER, V, GATE, true> (&t)[U], int64_t r) {
+    using R = Ring<IO, PER, V, GATE, true>;
+    R ring;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (r + u < r1) t[u].load(a, at, r + u);
-    };
-    load(x, r0);
+    for (int i = 0; i < R::STAGES - 1; ++i) ring.ask(a, at, r0 + i, r1);
     Affine<PER, V> p;
     p.load(a, at);
     F2 dw[V][P], db[V][P];
@@ -349,17 +399,12 @@ __global__ void __launch_bounds__(256) backward_kernel(const Args a) {
     for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < P; ++i) dw[v][i] = db[v][i] = f2s(0.f);
-    auto work = [&](const Rows<IO, PER, V, GATE, true> (&t)[U], int64_t r) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (r + u < r1) backward_row<IO, PER, V, GATE>(a, at, p, t[u], r + u, dw, db);
-    };
 #pragma unroll 1
-    for (int64_t r = r0; r < r1; r += 2 * U) {
-        load(y, r + U);
-        work(x, r);
-        load(x, r + 2 * U);
-        work(y, r + U);
+    for (int64_t r = r0; r < r1; ++r) {
+        Rows<IO, PER, V, GATE, true> t;
+        ring.get(a, at, r, t);
+        ring.ask(a, at, r + R::STAGES - 1, r1);
+        backward_row<IO, PER, V, GATE, ACT>(a, at, p, t, r, dw, db);
     }
     if (a.part != nullptr) {
 #pragma unroll
@@ -481,17 +526,17 @@ __global__ void __launch_bounds__(128) large_params_kernel(const Args a, int64_t
     part[(int64_t(blockIdx.y) * 2 + 1) * a.C + c] = db;
 }
 
-// the chunks' partial sums, in a fixed order: 32 channels x 8 lanes of chunks
-__global__ void __launch_bounds__(256) params_kernel(int64_t C, int64_t chunks, const float* __restrict__ part,
-                                                     float* __restrict__ dweight, float* __restrict__ dbias) {
-    __shared__ float sm[2][8][33];
+// the chunks' partial sums, in a fixed order: 32 channels x 32 warps of chunks
+__global__ void __launch_bounds__(1024) params_kernel(int64_t C, int64_t chunks, const float* __restrict__ part,
+                                                      float* __restrict__ dweight, float* __restrict__ dbias) {
+    __shared__ float sm[2][32][33];
     const int cx = threadIdx.x % 32, k = threadIdx.x / 32;
     const int64_t c = int64_t(blockIdx.x) * 32 + cx;
     pdl_begin();
     float dw = 0.f, db = 0.f;
     if (c < C) {
-#pragma unroll 4
-        for (int64_t i = k; i < chunks; i += 8) {
+#pragma unroll 8
+        for (int64_t i = k; i < chunks; i += 32) {
             dw += part[2 * i * C + c];
             db += part[(2 * i + 1) * C + c];
         }
@@ -499,12 +544,15 @@ __global__ void __launch_bounds__(256) params_kernel(int64_t C, int64_t chunks, 
     sm[0][k][cx] = dw;
     sm[1][k][cx] = db;
     __syncthreads();
-    if (k < 2 && c < C) {
-        float s = 0.f;
+    // warp k: the sums of channel k
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += sm[k][i][cx];
-        float* out = k == 0 ? dweight : dbias;
-        if (out != nullptr) out[c] = s;
+    for (int o = 0; o < 2; ++o) {
+        float s = sm[o][cx][k];
+#pragma unroll
+        for (int w = 16; w > 0; w /= 2) s += __shfl_xor_sync(0xffffffffu, s, w);
+        float* out = o == 0 ? dweight : dbias;
+        const int64_t ch = int64_t(blockIdx.x) * 32 + k;
+        if (cx == 0 && out != nullptr && ch < C) out[ch] = s;
     }
 }
 
