@@ -14,7 +14,6 @@ Two layers:
   ``data_ptr()`` values and the current stream, and raise ``WkvError`` on a
   non-zero status.
 """
-import contextlib
 import ctypes
 import functools
 import os
@@ -506,13 +505,17 @@ def wkv_step(w, u, k, v, state, r=None, *, y=None, stream=None):
     return y
 
 
-def _on_device(dev):
-    """Context in which `dev` is the current device (the library launches on
-    the current one)."""
+def _launch(dev, where, fn, *args):
+    """fn(*args) with `dev` as the current device (the library launches on the
+    current one); raises on a non-zero status."""
     torch = _torch()
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+    if dev.index == torch._C._cuda_getDevice():
+        status = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args)
+    if status != 0:
+        raise WkvError(status, where)
 
 
 def _delta_sizes(k, v, H, where):
@@ -539,23 +542,25 @@ def wkv_delta_forward(w, beta, r, k, v, H, state_in=None, *, y=None, state_out=N
     Returns (y, state_out); state_out may be state_in."""
     torch = _torch()
     B, T, Hk, N = _delta_sizes(k, v, H, "wkv_delta_forward")
-    dev, code = k.device, _dtype_code(k)
-    for t, name in ((r, "r"), (k, "k")):
-        _need(t, name, (B, T, Hk * N), k.dtype, dev)
-    _need(v, "v", (B, T, H * N), k.dtype, dev)
-    for t, name in ((w, "w"), (beta, "beta")):
-        _need(t, name, (B, T, H), torch.float32, dev)
-    _need(state_in, "state_in", (B, H, N, N), torch.float32, dev)
+    dev, dt, f32 = k.device, k.dtype, torch.float32
+    code = _dtype_code(k)
+    keys, values, scalars, states = (B, T, Hk * N), (B, T, H * N), (B, T, H), (B, H, N, N)
+    _need(r, "r", keys, dt, dev)
+    _need(k, "k", keys, dt, dev)
+    _need(v, "v", values, dt, dev)
+    _need(w, "w", scalars, f32, dev)
+    _need(beta, "beta", scalars, f32, dev)
+    _need(state_in, "state_in", states, f32, dev)
     if y is None:
-        y = torch.empty((B, T, H * N), dtype=k.dtype, device=dev)
-    _need(y, "y", (B, T, H * N), k.dtype, dev)
-    if state_out is None and want_state:
-        state_out = torch.empty((B, H, N, N), dtype=torch.float32, device=dev)
-    _need(state_out, "state_out", (B, H, N, N), torch.float32, dev)
-    with _on_device(dev):
-        _check(lib().wkv_delta_forward(B, T, Hk, H, N, code, _ptr(w), _ptr(beta), _ptr(r), _ptr(k), _ptr(v),
-                                       _ptr(state_in), _ptr(y), _ptr(state_out), _stream_ptr(stream, dev)),
-               "wkv_delta_forward")
+        y = torch.empty_like(v)
+    else:
+        _need(y, "y", values, dt, dev)
+    if state_out is not None:
+        _need(state_out, "state_out", states, f32, dev)
+    elif want_state:
+        state_out = torch.empty(states, dtype=f32, device=dev) if state_in is None else torch.empty_like(state_in)
+    _launch(dev, "wkv_delta_forward", lib().wkv_delta_forward, B, T, Hk, H, N, code, _ptr(w), _ptr(beta), _ptr(r), _ptr(k),
+            _ptr(v), _ptr(state_in), _ptr(y), _ptr(state_out), _stream_ptr(stream, dev))
     return y, state_out
 
 
@@ -568,19 +573,21 @@ def wkv_delta_step(w, beta, r, k, v, state, *, y=None, stream=None):
         raise ValueError("state must be (L, B, H, N, N)")
     H = state.shape[2]
     Lr, B, Hk, N = _delta_sizes(k, v, H, "wkv_delta_step")
-    dev, code = k.device, _dtype_code(k)
-    for t, name in ((r, "r"), (k, "k")):
-        _need(t, name, (Lr, B, Hk * N), k.dtype, dev)
-    _need(v, "v", (Lr, B, H * N), k.dtype, dev)
-    for t, name in ((w, "w"), (beta, "beta")):
-        _need(t, name, (Lr, B, H), torch.float32, dev)
-    _need(state, "state", (Lr, B, H, N, N), torch.float32, dev)
+    dev, dt, f32 = k.device, k.dtype, torch.float32
+    code = _dtype_code(k)
+    keys, values, scalars = (Lr, B, Hk * N), (Lr, B, H * N), (Lr, B, H)
+    _need(r, "r", keys, dt, dev)
+    _need(k, "k", keys, dt, dev)
+    _need(v, "v", values, dt, dev)
+    _need(w, "w", scalars, f32, dev)
+    _need(beta, "beta", scalars, f32, dev)
+    _need(state, "state", (Lr, B, H, N, N), f32, dev)
     if y is None:
-        y = torch.empty((Lr, B, H * N), dtype=k.dtype, device=dev)
-    _need(y, "y", (Lr, B, H * N), k.dtype, dev)
-    with _on_device(dev):
-        _check(lib().wkv_delta_step(Lr, B, Hk, H, N, code, _ptr(w), _ptr(beta), _ptr(r), _ptr(k), _ptr(v), _ptr(state),
-                                    _ptr(y), _stream_ptr(stream, dev)), "wkv_delta_step")
+        y = torch.empty_like(v)
+    else:
+        _need(y, "y", values, dt, dev)
+    _launch(dev, "wkv_delta_step", lib().wkv_delta_step, Lr, B, Hk, H, N, code, _ptr(w), _ptr(beta), _ptr(r), _ptr(k), _ptr(v),
+            _ptr(state), _ptr(y), _stream_ptr(stream, dev))
     return y
 
 
@@ -609,31 +616,31 @@ def wkv_delta_backward(w, beta, r, k, v, H, state_in=None, *, dy, dstate_out=Non
     value heads that share a key head, dw and dbeta are (B, T, H) float32."""
     torch = _torch()
     B, T, Hk, N = _delta_sizes(k, v, H, "wkv_delta_backward")
-    dev, code = k.device, _dtype_code(k)
-    empty = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
-    f32 = torch.float32
-    dr = empty((B, T, Hk * N), k.dtype) if dr is None else dr
-    dk = empty((B, T, Hk * N), k.dtype) if dk is None else dk
-    dv = empty((B, T, H * N), k.dtype) if dv is None else dv
-    dw = empty((B, T, H), f32) if dw is None else dw
-    dbeta = empty((B, T, H), f32) if dbeta is None else dbeta
-    if dstate_in is None and want_dstate_in:
-        dstate_in = empty((B, H, N, N), f32)
-    for t, name in ((r, "r"), (k, "k"), (dr, "dr"), (dk, "dk")):
-        _need(t, name, (B, T, Hk * N), k.dtype, dev)
+    dev, dt, f32 = k.device, k.dtype, torch.float32
+    code = _dtype_code(k)
+    keys, values, scalars, states = (B, T, Hk * N), (B, T, H * N), (B, T, H), (B, H, N, N)
+    _need(r, "r", keys, dt, dev)
+    _need(k, "k", keys, dt, dev)
     for t, name in ((v, "v"), (dy, "dy"), (dv, "dv")):
-        _need(t, name, (B, T, H * N), k.dtype, dev)
+        _need(t, name, values, dt, dev)
     for t, name in ((w, "w"), (beta, "beta"), (dw, "dw"), (dbeta, "dbeta")):
-        _need(t, name, (B, T, H), f32, dev)
+        _need(t, name, scalars, f32, dev)
     for t, name in ((state_in, "state_in"), (dstate_out, "dstate_out"), (dstate_in, "dstate_in")):
-        _need(t, name, (B, H, N, N), f32, dev)
-    with _on_device(dev):
-        nbytes = int(lib().wkv_delta_backward_workspace_bytes(B, T, Hk, H, N))
-        ws_ptr, ws_bytes, owner = _scratch(nbytes, workspace, dev, stream)
-        _check(lib().wkv_delta_backward(B, T, Hk, H, N, code, _ptr(w), _ptr(beta), _ptr(r), _ptr(k), _ptr(v),
-                                        _ptr(state_in), _ptr(dy), _ptr(dstate_out), _ptr(dr), _ptr(dk), _ptr(dv),
-                                        _ptr(dw), _ptr(dbeta), _ptr(dstate_in), ws_ptr, ws_bytes,
-                                        _stream_ptr(stream, dev)), "wkv_delta_backward")
+        _need(t, name, states, f32, dev)
+    _need(dr, "dr", keys, dt, dev)
+    _need(dk, "dk", keys, dt, dev)
+    dr = torch.empty_like(k) if dr is None else dr
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    dw = torch.empty_like(w) if dw is None else dw
+    dbeta = torch.empty_like(w) if dbeta is None else dbeta
+    if dstate_in is None and want_dstate_in:
+        dstate_in = torch.empty(states, dtype=f32, device=dev)
+    nbytes = int(lib().wkv_delta_backward_workspace_bytes(B, T, Hk, H, N))
+    ws_ptr, ws_bytes, owner = _scratch(nbytes, workspace, dev, stream)
+    _launch(dev, "wkv_delta_backward", lib().wkv_delta_backward, B, T, Hk, H, N, code, _ptr(w), _ptr(beta), _ptr(r), _ptr(k),
+            _ptr(v), _ptr(state_in), _ptr(dy), _ptr(dstate_out), _ptr(dr), _ptr(dk), _ptr(dv), _ptr(dw), _ptr(dbeta),
+            _ptr(dstate_in), ws_ptr, ws_bytes, _stream_ptr(stream, dev))
     return dr, dk, dv, dw, dbeta, dstate_in
 
 
@@ -641,22 +648,20 @@ _ACTS = {"none": 0, "silu": 1, "sigmoid": 2}
 
 
 def _norm_args(x, G, weight, bias, gate, act, where):
-    torch = _torch()
     if x.dim() < 1 or G <= 0 or x.shape[-1] % G != 0:
         raise ValueError(f"{where}: x's channels are not {G} groups")
     if act not in _ACTS:
         raise ValueError(f"{where}: act must be one of {sorted(_ACTS)}")
-    if x.device.type != "cuda":
+    dev = x.device
+    if dev.type != "cuda":
         raise ValueError(f"{where} runs on CUDA tensors only")
-    C = x.shape[-1]
-    _need(x, "x", x.shape, x.dtype, x.device)
-    _need(gate, "gate", x.shape, x.dtype, x.device)
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        _need(t, name, (C,), torch.float32, x.device)
-    rows = 1
-    for n in x.shape[:-1]:
-        rows *= n
-    return rows, C, x.device, _dtype_code(x)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    C, f32 = x.shape[-1], _torch().float32
+    _need(gate, "gate", x.shape, x.dtype, dev)
+    _need(weight, "weight", (C,), f32, dev)
+    _need(bias, "bias", (C,), f32, dev)
+    return x.numel() // C if C else 0, C, dev, _dtype_code(x)
 
 
 def wkv_group_norm(x, G, weight=None, bias=None, gate=None, *, act="none", eps=1e-5, y=None, stream=None):
@@ -667,11 +672,11 @@ def wkv_group_norm(x, G, weight=None, bias=None, gate=None, *, act="none", eps=1
     "sigmoid".  Returns y."""
     rows, C, dev, code = _norm_args(x, G, weight, bias, gate, act, "wkv_group_norm")
     if y is None:
-        y = _torch().empty(x.shape, dtype=x.dtype, device=dev)
-    _need(y, "y", x.shape, x.dtype, dev)
-    with _on_device(dev):
-        _check(lib().wkv_group_norm(rows, C, G, code, _ACTS[act], eps, _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate),
-                                    _ptr(y), _stream_ptr(stream, dev)), "wkv_group_norm")
+        y = _torch().empty_like(x)
+    else:
+        _need(y, "y", x.shape, x.dtype, dev)
+    _launch(dev, "wkv_group_norm", lib().wkv_group_norm, rows, C, G, code, _ACTS[act], eps, _ptr(x), _ptr(weight), _ptr(bias),
+            _ptr(gate), _ptr(y), _stream_ptr(stream, dev))
     return y
 
 
@@ -698,12 +703,11 @@ def wkv_group_norm_backward(x, G, weight=None, bias=None, gate=None, *, dy, act=
     _need(dgate, "dgate", x.shape, x.dtype, dev)
     for t, name in ((dweight, "dweight"), (dbias, "dbias")):
         _need(t, name, (C,), torch.float32, dev)
-    with _on_device(dev):
-        nbytes = 0
-        if weight is not None or bias is not None:
-            nbytes = int(lib().wkv_group_norm_backward_workspace_bytes(rows, C, G, code))
-        ws_ptr, ws_bytes, owner = _scratch(nbytes, workspace, dev, stream)
-        _check(lib().wkv_group_norm_backward(rows, C, G, code, _ACTS[act], eps, _ptr(x), _ptr(weight), _ptr(bias),
-                                             _ptr(gate), _ptr(dy), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(dgate),
-                                             ws_ptr, ws_bytes, _stream_ptr(stream, dev)), "wkv_group_norm_backward")
+    nbytes = 0
+    if weight is not None or bias is not None:
+        nbytes = int(lib().wkv_group_norm_backward_workspace_bytes(rows, C, G, code))
+    ws_ptr, ws_bytes, owner = _scratch(nbytes, workspace, dev, stream)
+    _launch(dev, "wkv_group_norm_backward", lib().wkv_group_norm_backward, rows, C, G, code, _ACTS[act], eps, _ptr(x),
+            _ptr(weight), _ptr(bias), _ptr(gate), _ptr(dy), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(dgate), ws_ptr, ws_bytes,
+            _stream_ptr(stream, dev))
     return dx, dweight, dbias, dgate
