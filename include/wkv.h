@@ -508,11 +508,22 @@ int wkv_token_shift(int64_t B, int64_t T, int64_t C, int dtype, int nmix,
  * NULL: not wanted; it may equal state_in and must overlap nothing else.
  * Feeding it back chains chunks exactly like one pass.  T == 0: state_out =
  * state_in.  16-byte aligned r, k, v are read in 16-byte pieces.  Errors as
- * wkv5_forward.  Asynchronous on `stream`; no workspace.
+ * wkv5_forward.  Asynchronous on `stream`.
+ *   workspace    256-byte aligned scratch of wkv_delta_forward_workspace_bytes()
+ *                bytes (0 where none is of use), or NULL.  With it, more heads
+ *                than the GPU holds at once are walked in parts of the tokens,
+ *                so that the last wave of heads does not leave it mostly idle;
+ *                the results are the same bits.  It needs no initialisation and
+ *                holds nothing between calls; one that is too small is not
+ *                touched.  A part waits for the one before it, at most the
+ *                library's wait limit: then what follows is NaN and
+ *                wkv_workspace_status() returns WKV_ERR_TIMEOUT.
  */
 int wkv_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int dtype,
                       const float* w, const float* beta, const void* r, const void* k, const void* v,
-                      const float* state_in, void* y, float* state_out, cudaStream_t stream);
+                      const float* state_in, void* y, float* state_out,
+                      void* workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t wkv_delta_forward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t N);
 
 /*
  * wkv_delta_step -- one token for L layers of B sequences: w, beta (L,B,H),
@@ -531,7 +542,7 @@ int wkv_delta_step(int64_t L, int64_t B, int64_t Hk, int64_t H, int64_t N, int d
  * (B,H,N,N) float32 or NULL.  dw is 0 where e^{-w} is 0.  No output may
  * overlap an input, another output or the workspace.  The workspace (256-byte
  * aligned, no initialisation, wkv_delta_backward_workspace_bytes() bytes)
- * holds nothing between calls.  T == 0: dstate_in = dstate_out (zeros if
+ * holds nothing between calls; its walks go in parts as the forward's do.  T == 0: dstate_in = dstate_out (zeros if
  * NULL), nothing else is written.  WKV_ERR_WORKSPACE: NULL or too small.
  */
 size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N);

@@ -33,7 +33,8 @@ STATUS = {
 EXPORTS = ("wkv_forward", "wkv_forward_ex", "wkv_forward_workspace_bytes", "wkv_workspace_init", "wkv_workspace_status",
            "wkv_step", "wkv_forward_noalloc", "wkv_forward_noalloc_scratch_bytes", "wkv_forward_noalloc_status",
            "wkv_backward", "wkv_state", "wkv_state_combine", "wkv5_forward",
-           "wkv_backward_workspace_bytes", "wkv_token_shift", "wkv_delta_forward", "wkv_delta_step",
+           "wkv_backward_workspace_bytes", "wkv_token_shift", "wkv_delta_forward", "wkv_delta_forward_workspace_bytes",
+           "wkv_delta_step",
            "wkv_delta_backward", "wkv_delta_backward_workspace_bytes", "wkv_group_norm", "wkv_group_norm_backward",
            "wkv_group_norm_backward_workspace_bytes", "wkv_strerror", "wkv_last_cuda_error",
            "wkv_abi_version")
@@ -96,8 +97,10 @@ def lib():
         L.wkv_backward.restype = i32
         L.wkv_backward_workspace_bytes.argtypes = [i64, i64, i64, i32]
         L.wkv_backward_workspace_bytes.restype = sz
-        L.wkv_delta_forward.argtypes = [i64] * 5 + [i32] + [vp] * 9
+        L.wkv_delta_forward.argtypes = [i64] * 5 + [i32] + [vp] * 9 + [sz, vp]
         L.wkv_delta_forward.restype = i32
+        L.wkv_delta_forward_workspace_bytes.argtypes = [i64] * 4
+        L.wkv_delta_forward_workspace_bytes.restype = sz
         L.wkv_delta_step.argtypes = [i64] * 5 + [i32] + [vp] * 8
         L.wkv_delta_step.restype = i32
         L.wkv_delta_backward.argtypes = [i64] * 5 + [i32] + [vp] * 15 + [sz, vp]
@@ -532,14 +535,16 @@ def _delta_sizes(k, v, H, where):
     return v.shape[0], v.shape[1], k.shape[2] // N, N
 
 
-def wkv_delta_forward(w, beta, r, k, v, H, state_in=None, *, y=None, state_out=None, want_state=True, stream=None):
+def wkv_delta_forward(w, beta, r, k, v, H, state_in=None, *, y=None, state_out=None, want_state=True,
+                      workspace: Workspace = None, use_workspace=True, stream=None):
     """Gated delta rule over one chunk.  r, k: (B, T, Hk * N), v: (B, T, H * N)
     float32 or bfloat16 CUDA tensors, N in {32, 64, 128} and H a multiple of
     Hk (value head h takes key head h // (H // Hk)); w (decay rates, inf
     forgets the state), beta: (B, T, H) float32; state_in: (B, H, N, N)
     float32 or None (zeros).  Per head
         e_t = v_t - exp(-w_t) S^T k_t,  S <- exp(-w_t) S + beta_t k_t e_t^T,  y_t = S^T r_t.
-    Returns (y, state_out); state_out may be state_in."""
+    Returns (y, state_out); state_out may be state_in.  use_workspace=False
+    passes no workspace (one CTA a head's slice, whatever the number of heads)."""
     torch = _torch()
     B, T, Hk, N = _delta_sizes(k, v, H, "wkv_delta_forward")
     dev, dt, f32 = k.device, k.dtype, torch.float32
@@ -559,8 +564,12 @@ def wkv_delta_forward(w, beta, r, k, v, H, state_in=None, *, y=None, state_out=N
         _need(state_out, "state_out", states, f32, dev)
     elif want_state:
         state_out = torch.empty(states, dtype=f32, device=dev) if state_in is None else torch.empty_like(state_in)
+    ws_ptr, ws_bytes, owner = None, 0, None
+    if use_workspace and B * H > 64:   # fewer heads never need one
+        nbytes = int(lib().wkv_delta_forward_workspace_bytes(B, T, H, N))
+        ws_ptr, ws_bytes, owner = _scratch(nbytes, workspace, dev, stream)
     _launch(dev, "wkv_delta_forward", lib().wkv_delta_forward, B, T, Hk, H, N, code, _ptr(w), _ptr(beta), _ptr(r), _ptr(k),
-            _ptr(v), _ptr(state_in), _ptr(y), _ptr(state_out), _stream_ptr(stream, dev))
+            _ptr(v), _ptr(state_in), _ptr(y), _ptr(state_out), ws_ptr, ws_bytes, _stream_ptr(stream, dev))
     return y, state_out
 
 

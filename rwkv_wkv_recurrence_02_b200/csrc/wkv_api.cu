@@ -92,21 +92,6 @@ constexpr int stream_ls() { return sizeof(IO) == 2 ? 32 : 16; }
 constexpr int64_t stream_pt(int dtype) { return kStreamW * (dtype == WKV_BF16 ? 32 : 16); }
 // Sequences at most this long take the sequential kernel.
 constexpr int64_t kSeqMaxT = 16;
-// Limit of every wait on another CTA's result: 1 s, or WKV_WAIT_LIMIT_NS (read
-// once per process; used by the tests to make waits run out on purpose).
-// Waits for a CTA's own TMA copies have a fixed limit (kCopyWaitNs).
-uint64_t wait_limit_ns() {
-    static const uint64_t v = []() -> uint64_t {
-        const char* e = std::getenv("WKV_WAIT_LIMIT_NS");
-        if (e != nullptr && *e != '\0') {
-            char* end = nullptr;
-            const unsigned long long x = std::strtoull(e, &end, 10);
-            if (end != e) return x;
-        }
-        return 1000000000ull;
-    }();
-    return v;
-}
 
 struct ChunkGeom {
     int64_t nCB, nLB, nchunks, units;

@@ -9,24 +9,71 @@ namespace {
 using namespace wkv::host;
 namespace d = wkv::delta;
 
+// Walks in parts (Task in wkv_delta_mma.cuh) need walks that are not few and
+// tokens for parts of kPartMin or more; kPartMax of them bound the work that
+// the last wave leaves undone to an eighth of a walk.
+constexpr int64_t kPartMin = 256, kPartMax = 8, kSlotsMin = 148;
+
+struct Parts {
+    size_t done, hand, bytes;   // offsets behind the control words; 0 bytes: never in parts
+};
+// walks: heads times slices of their columns
+Parts parts_layout(int64_t walks, int64_t states, int64_t T) {
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    Parts p{};
+    if (walks <= kSlotsMin || T < 2 * kPartMin) return p;
+    p.done = 256;
+    p.hand = p.done + up(size_t(walks) * 4);
+    p.bytes = p.hand + up(size_t(states) * 4);
+    return p;
+}
+int slices(int64_t N) { return N == 128 ? 2 : 1; }
+
+// ws: parts_layout's bytes, or NULL for one walk a CTA
 template <typename K>
-int launch_walk(K kern, int64_t blocks, int threads, int smem, bool (&ready)[kMaxDevices], const d::Args& a, cudaStream_t st) {
-    const int rc = allow_smem(kern, smem, ready);
-    return rc != WKV_OK ? rc : launch(kern, blocks, threads, smem, st, a);
+int launch_walk(K kern, int64_t walks, int threads, int smem, bool (&ready)[kMaxDevices], d::Args a, char* ws, const Parts& p,
+                cudaStream_t st) {
+    int rc = allow_smem(kern, smem, ready);
+    if (rc != WKV_OK) return rc;
+    a.parts = 1, a.part_len = a.T;
+    if (ws != nullptr && p.bytes > 0) {
+        int dev = 0, sms = 0, per = 0;
+        rc = record_cuda(cudaGetDevice(&dev));
+        if (rc == WKV_OK) rc = record_cuda(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+        if (rc == WKV_OK) rc = record_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, threads, size_t(smem)));
+        if (rc != WKV_OK) return rc;
+        // the share of the last wave's places that stay empty, of all waves': parts
+        // pay from about a tenth (they cost a pipeline's fill each)
+        const int64_t slots = int64_t(sms) * per, waves = slots > 0 ? (walks + slots - 1) / slots : 0;
+        if (walks > slots && slots > 0 && (waves * slots - walks) * 10 > waves * slots) {
+            const int64_t n = a.T / kPartMin < kPartMax ? a.T / kPartMin : kPartMax;
+            a.part_len = ((a.T + n - 1) / n + d::kSegment - 1) / d::kSegment * d::kSegment;
+            a.parts = (a.T + a.part_len - 1) / a.part_len;
+            a.control = reinterpret_cast<d::Control*>(ws);
+            a.done = reinterpret_cast<uint32_t*>(ws + p.done);
+            a.hand = reinterpret_cast<float*>(ws + p.hand);
+            a.wait_ns = wait_limit_ns();
+            rc = record_cuda(cudaMemsetAsync(ws, 0, p.hand, st));
+            if (rc != WKV_OK) return rc;
+            kern<<<dim3(unsigned(slots)), threads, smem, st>>>(a);
+            return check_launch();
+        }
+    }
+    return launch(kern, walks, threads, smem, st, a);
 }
 
 template <typename IO, int N, bool WANT_Y>
-int launch_forward(const d::Args& a, cudaStream_t st) {
+int launch_forward(const d::Args& a, char* ws, const Parts& p, cudaStream_t st) {
     using G = d::ForwardShape<IO, N, WANT_Y>;
     static bool ready[kMaxDevices] = {false};
-    return launch_walk(d::delta_forward_mma_kernel<IO, N, WANT_Y>, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, ready, a, st);
+    return launch_walk(d::delta_forward_mma_kernel<IO, N, WANT_Y>, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, ready, a, ws, p, st);
 }
 
 template <typename IO, int N>
-int launch_reverse(const d::Args& a, cudaStream_t st) {
+int launch_reverse(const d::Args& a, char* ws, const Parts& p, cudaStream_t st) {
     using G = d::ReverseShape<IO, N>;
     static bool ready[kMaxDevices] = {false};
-    return launch_walk(d::delta_reverse_mma_kernel<IO, N>, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, ready, a, st);
+    return launch_walk(d::delta_reverse_mma_kernel<IO, N>, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, ready, a, ws, p, st);
 }
 
 template <typename IO, int N>
@@ -34,11 +81,11 @@ int launch_segments(const d::Args& a, cudaStream_t st) {
     using G = d::SegmentShape<IO, N>;
     static bool ready[kMaxDevices] = {false};
     return launch_walk(d::delta_segment_kernel<IO, N>, a.B * a.H * ((a.T + d::kSegment - 1) / d::kSegment), G::THREADS, G::SMEM,
-                       ready, a, st);
+                       ready, a, nullptr, Parts{}, st);
 }
 
 struct Layout {
-    size_t e, du, s_seg, d_seg, phi, drh, dkh, bytes;
+    size_t e, du, s_seg, d_seg, phi, drh, dkh, parts, bytes;
 };
 
 // share: several value heads to a key head
@@ -54,14 +101,15 @@ Layout layout(int64_t B, int64_t T, int64_t H, int64_t N, bool share) {
     l.phi = l.d_seg + up(borders * N * N * 4);
     l.drh = l.phi + up(borders * (N / 16) * 4);
     l.dkh = l.drh + (share ? val : 0);
-    l.bytes = l.dkh + (share ? val : 0);
+    l.parts = l.dkh + (share ? val : 0);
+    l.bytes = l.parts + parts_layout(B * H * slices(N), B * H * N * N, T).bytes;
     return l;
 }
 
 template <typename IO, int N>
-int run_backward(const d::Args& a, cudaStream_t st) {
-    int rc = launch_forward<IO, N, false>(a, st);
-    if (rc == WKV_OK) rc = launch_reverse<IO, N>(a, st);
+int run_backward(const d::Args& a, char* ws, const Parts& p, cudaStream_t st) {
+    int rc = launch_forward<IO, N, false>(a, ws, p, st);
+    if (rc == WKV_OK) rc = launch_reverse<IO, N>(a, ws, p, st);
     if (rc == WKV_OK) rc = launch_segments<IO, N>(a, st);
     if (rc == WKV_OK && a.H != a.Hk)
         rc = launch(d::delta_share_kernel<IO, N>, (a.B * a.T * a.Hk * (N / 4) + 255) / 256, 256, 0, st, a);
@@ -120,7 +168,7 @@ extern "C" {
 
 int wkv_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int dtype, const float* w,
                       const float* beta, const void* r, const void* k, const void* v, const float* state_in, void* y,
-                      float* state_out, cudaStream_t stream) {
+                      float* state_out, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
     if (dtype != WKV_F32 && dtype != WKV_BF16) return WKV_ERR_DTYPE;
     Sizes n{};
     int rc = sizes(B, T, B, Hk, H, N, &n);
@@ -132,17 +180,27 @@ int wkv_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, in
     const Span ins[] = {{w, size_t(n.scalars) * 4, 4}, {beta, size_t(n.scalars) * 4, 4}, {r, size_t(n.keys) * eb, eb},
                         {k, size_t(n.keys) * eb, eb}, {v, size_t(n.values) * eb, eb},
                         {state_in == state_out ? nullptr : state_in, sb, 4}};
-    const Span outs[] = {{y, size_t(n.values) * eb, eb}, {state_out, sb, 4}};
+    // a workspace that is too small is not touched
+    const Parts p = parts_layout(B * H * slices(N), n.states, T);
+    if (p.bytes == 0 || workspace_bytes < p.bytes) workspace = nullptr;
+    const Span outs[] = {{y, size_t(n.values) * eb, eb}, {state_out, sb, 4}, {workspace, p.bytes, 256}};
     rc = check_spans(ins, outs);
     if (rc != WKV_OK) return rc;
+    if (workspace && overlaps(workspace, p.bytes, state_in, sb)) return WKV_ERR_ALIAS;
     d::Args a{};
     a.B = B, a.T = T, a.Hk = Hk, a.H = H;
     a.w = w, a.beta = beta, a.r = r, a.k = k, a.v = v, a.s_in = state_in, a.y = y, a.s_out = state_out;
     a.vec = aligned(r, 16) && aligned(k, 16) && aligned(v, 16) && aligned(y, 16);
     rc = with_type(dtype, N, [&](auto tag, auto size) {
-        return launch_forward<decltype(tag), decltype(size)::value, true>(a, stream);
+        return launch_forward<decltype(tag), decltype(size)::value, true>(a, static_cast<char*>(workspace), p, stream);
     });
     return rc != WKV_OK ? rc : check_launch();
+}
+
+size_t wkv_delta_forward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t N) {
+    Sizes n{};
+    if (sizes(B, T, B, 1, H, N, &n) != WKV_OK) return 0;
+    return parts_layout(B * H * slices(N), n.states, T).bytes;
 }
 
 int wkv_delta_step(int64_t L, int64_t B, int64_t Hk, int64_t H, int64_t N, int dtype, const float* w,
@@ -208,7 +266,8 @@ int wkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, i
     a.vec = aligned(r, 16) && aligned(k, 16) && aligned(v, 16) && aligned(dy, 16) && aligned(dv, 16) &&
             aligned(dr, 16) && aligned(dk, 16);
     rc = with_type(dtype, N, [&](auto tag, auto size) {
-        return run_backward<decltype(tag), decltype(size)::value>(a, stream);
+        return run_backward<decltype(tag), decltype(size)::value>(a, ws + l.parts, parts_layout(B * H * slices(N), n.states, T),
+                                                                  stream);
     });
     return rc != WKV_OK ? rc : check_launch();
 }

@@ -38,6 +38,11 @@ __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// Words of a walk in parts; the error is where wkv_workspace_status() reads it.
+struct Control {
+    uint32_t epoch, finished, error, err_unit, ticket;
+};
+
 struct Args {
     int64_t B, T, Hk, H;
     const float* w;      // (B, T, H)
@@ -66,6 +71,12 @@ struct Args {
     float* drh;          // (B, T, H, N): dr and dk of each value head, where heads share keys
     float* dkh;
     bool vec;            // 16-byte loads of every tensor in the I/O type
+    // a walk in parts of part_len tokens, taken by tickets (parts > 1)
+    int64_t parts, part_len;
+    Control* control;
+    uint32_t* done;      // (walks): parts that are done
+    float* hand;         // (B, H, N, N): the state between a walk's parts, as its warps hold it
+    uint64_t wait_ns;
 };
 
 // ---------------------------------------------------------------------------

@@ -78,7 +78,7 @@ __device__ __forceinline__ void bar_sync(int id) { asm volatile("bar.sync %0, %1
 template <int THREADS>
 __device__ __forceinline__ void bar_arrive(int id) { asm volatile("bar.arrive %0, %1;" :: "r"(id), "n"(THREADS) : "memory"); }
 // ids: one for each of four stages
-constexpr int kBarFull = 1, kBarFree = 5;
+constexpr int kBarFull = 1, kBarFree = 5, kBarTask = 9;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(full ? 16 : 0) : "memory");
@@ -505,6 +505,74 @@ __device__ __forceinline__ void keep_state(float* s, const float (&S)[N / 8][4],
             *reinterpret_cast<float2*>(s + (lane / 4 + 8 * q) * N + 8 * n + 2 * (lane % 4)) = make_float2(S[n][2 * q], S[n][2 * q + 1]);
 }
 
+// The walk's state as a warp holds it, between the parts of a walk
+template <int N>
+__device__ __forceinline__ void hand_on(float* s, const float (&S)[N / 8][4], int lane) {
+#pragma unroll
+    for (int n = 0; n < N / 8; ++n)
+        __stcg(reinterpret_cast<float4*>(s) + n * 32 + lane, make_float4(S[n][0], S[n][1], S[n][2], S[n][3]));
+    __threadfence();
+}
+template <int N>
+__device__ __forceinline__ void take_over(float (&S)[N / 8][4], const float* s, bool lost, int lane) {
+#pragma unroll
+    for (int n = 0; n < N / 8; ++n) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + n * 32 + lane);
+        S[n][0] = v.x, S[n][1] = v.y, S[n][2] = v.z, S[n][3] = v.w;
+        if (lost) S[n][0] = S[n][1] = S[n][2] = S[n][3] = __int_as_float(0x7fffffff);
+    }
+}
+
+// What a CTA works on: one walk (a head's slice of columns) over all tokens,
+// or, where the walks would leave the last of several waves mostly empty, one
+// part of a walk after another.  Tickets go through the first part of every
+// walk, then the second: a part's predecessor was taken earlier, so somebody
+// is at it or done with it, and by then it is nearly always done.  A wait ends
+// after wait_ns; it leaves the error word and NaN in what follows.
+struct Task {
+    int64_t walk, part;
+    bool lost;   // the part before it never came
+};
+// The next task of the CTA (every thread calls; THREADS of them), false: none
+// is left.  Publishes the one before: its state is written and fenced.
+template <int THREADS>
+__device__ __forceinline__ bool next_task(const Args& a, int64_t walks, Task& t, bool first) {
+    if (a.parts <= 1) {
+        t = Task{int64_t(blockIdx.x), 0, false};
+        return first;
+    }
+    __shared__ int64_t s_ticket;
+    __shared__ int s_lost;
+    bar_sync<THREADS>(kBarTask);
+    if (threadIdx.x == 0) {
+        if (!first) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(a.done + t.walk), "r"(uint32_t(t.part + 1)) : "memory");
+        const int64_t id = atomicAdd(&a.control->ticket, 1u);
+        s_ticket = id;
+        s_lost = 0;
+        if (id < walks * a.parts) {
+            const uint32_t want = uint32_t(id / walks);
+            uint64_t begin, now;
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(begin));
+            uint32_t have = 0;
+            while (true) {
+                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(have) : "l"(a.done + id % walks) : "memory");
+                if (have >= want) break;
+                asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+                if (now - begin > a.wait_ns) {
+                    a.control->error = 1u;
+                    a.control->err_unit = uint32_t(id);
+                    s_lost = 1;
+                    break;
+                }
+            }
+        }
+    }
+    __syncwarp();
+    bar_sync<THREADS>(kBarTask);
+    t = Task{s_ticket % walks, s_ticket / walks, s_lost != 0};
+    return t.part < a.parts;
+}
+
 // what only reaches an output takes this many orders
 template <typename IO>
 constexpr int kOutOrders = sizeof(IO) == 2 ? 2 : 3;
@@ -538,11 +606,9 @@ __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO
     extern __shared__ __align__(16) char smem[];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
 
-    const int64_t head = blockIdx.x / G::SLICES;
-    const int slice = int(blockIdx.x % G::SLICES) * G::CW;
-    const int64_t b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
-    const int64_t vs = a.H * N;
-    const int64_t vbase = (b * a.T * a.H + h) * N + slice;
+    const int64_t walks = a.B * a.H * G::SLICES, vs = a.H * N;
+    Task task;
+    bool first = true;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -550,16 +616,19 @@ __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO
         stager_regs<IO, N>();
         const int st = warp - G::NW;
         const int64_t ks = a.Hk * N;
+        G g(smem, st);
+        for (; next_task<G::THREADS>(a, walks, task, first); first = false) {
+        const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
+        const int64_t begin = task.part * a.part_len, end = begin + a.part_len < a.T ? begin + a.part_len : a.T;
         const IO* kp = static_cast<const IO*>(a.k) + (b * a.T * a.Hk + hk) * N;
         const IO* rp = static_cast<const IO*>(a.r) + (b * a.T * a.Hk + hk) * N;
-        const IO* vp = static_cast<const IO*>(a.v) + vbase;
+        const IO* vp = static_cast<const IO*>(a.v) + (b * a.T * a.H + h) * N + task.walk % G::SLICES * G::CW;
         const float* wp = a.w + b * a.T * a.H + h;
         const float* bp = a.beta + b * a.T * a.H + h;
-        G g(smem, st);
 #pragma unroll 1
-        for (int64_t t0 = st * kChunk; t0 < a.T; t0 += G::NST * kChunk) {
-            const int nt = a.T - t0 < kChunk ? int(a.T - t0) : kChunk;
-            if (t0 >= G::NST * kChunk) bar_sync<G::BAR>(kBarFree + st);
+        for (int64_t t0 = begin + st * kChunk; t0 < end; t0 += G::NST * kChunk) {
+            const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
+            if (t0 >= begin + G::NST * kChunk) bar_sync<G::BAR>(kBarFree + st);
             const float w = lane < nt ? wp[(t0 + lane) * a.H] : 0.f, be = lane < nt ? bp[(t0 + lane) * a.H] : 0.f;
             g.fetch(kp + t0 * ks, rp + t0 * ks, ks, vp + t0 * vs, vs, nt, a.vec, lane);
             // A, its inverse and P
@@ -594,21 +663,28 @@ __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO
             put_inverse(g.mats, g.diag, lane);
             bar_arrive<G::BAR>(kBarFull + st);
         }
+        }
         return;
     }
 
     walker_regs<IO, N>();
     const int j0 = warp * 16;
     const int64_t nseg = (a.T + kSegment - 1) / kSegment;
-    const int64_t place = int64_t(slice + j0) * N;   // in a kept state
-    float* keep = a.s_seg + head * (nseg + 1) * N * N + place;
-    float S[N / 8][4];
-    load_state<N>(S, a.s_in == nullptr ? nullptr : a.s_in + head * N * N + slice + j0, lane);
     const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = m_plain(lane);
+    for (; next_task<G::THREADS>(a, walks, task, first); first = false) {
+    const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H;
+    const int slice = int(task.walk % G::SLICES) * G::CW;
+    const int64_t begin = task.part * a.part_len, end = begin + a.part_len < a.T ? begin + a.part_len : a.T;
+    const int64_t vbase = (b * a.T * a.H + h) * N + slice;
+    float* keep = a.s_seg + head * (nseg + 1) * N * N + int64_t(slice + j0) * N;
+    float* hand = a.hand + head * N * N + int64_t(slice + j0) * N;
+    float S[N / 8][4];
+    if (task.part == 0) load_state<N>(S, a.s_in == nullptr ? nullptr : a.s_in + head * N * N + slice + j0, lane);
+    else take_over<N>(S, hand, task.lost, lane);
     int st = 0;
 #pragma unroll 1
-    for (int64_t t0 = 0; t0 < a.T; t0 += kChunk, st = (st + 1) % G::NST) {
-        const int nt = a.T - t0 < kChunk ? int(a.T - t0) : kChunk;
+    for (int64_t t0 = begin; t0 < end; t0 += kChunk, st = (st + 1) % G::NST) {
+        const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
         G g(smem, st);
         if (!WANT_Y && t0 % kSegment == 0) keep_state<N>(keep + t0 / kSegment * N * N, S, lane);
         bar_sync<G::BAR>(kBarFull + st);
@@ -684,12 +760,15 @@ __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO
                 store_half(static_cast<IO*>(a.y) + at + 8 * n * vs, vs, nt - 8 * n, y[n], g.v + 8 * n * G::LDV + j0, G::LDV, a.vec, lane);
             }
         }
-        if (t0 + G::NST * kChunk < a.T) bar_arrive<G::BAR>(kBarFree + st);
+        if (t0 + G::NST * kChunk < end) bar_arrive<G::BAR>(kBarFree + st);
     }
-    if constexpr (WANT_Y) {
+    if (end < a.T) {
+        hand_on<N>(hand, S, lane);
+    } else if constexpr (WANT_Y) {
         if (a.s_out != nullptr) store_state<N>(a.s_out + head * N * N + slice + j0, S, lane);
     } else {
         keep_state<N>(keep + nseg * N * N, S, lane);
+    }
     }
 }
 

@@ -40,12 +40,9 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
     extern __shared__ __align__(16) char smem[];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
 
-    const int64_t head = blockIdx.x / G::SLICES;
-    const int slice = int(blockIdx.x % G::SLICES) * G::CW;
-    const int64_t b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
-    const int64_t vs = a.H * N;
-    const int64_t vbase = (b * a.T * a.H + h) * N + slice;
-    const int64_t last = (a.T - 1) / kChunk * kChunk;
+    const int64_t walks = a.B * a.H * G::SLICES, vs = a.H * N;
+    Task task;
+    bool first = true;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -53,15 +50,20 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
         stager_regs<IO, N>();
         const int st = warp - G::NW;
         const int64_t ks = a.Hk * N;
+        G g(smem, st);
+        for (; next_task<G::THREADS>(a, walks, task, first); first = false) {
+        const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
+        const int64_t begin = (a.parts - 1 - task.part) * a.part_len, end = begin + a.part_len < a.T ? begin + a.part_len : a.T;
+        const int64_t last = begin + (end - 1 - begin) / kChunk * kChunk;
+        const int64_t vbase = (b * a.T * a.H + h) * N + task.walk % G::SLICES * G::CW;
         const IO* kp = static_cast<const IO*>(a.k) + (b * a.T * a.Hk + hk) * N;
         const IO* rp = static_cast<const IO*>(a.r) + (b * a.T * a.Hk + hk) * N;
         const IO* yp = static_cast<const IO*>(a.dy) + vbase;
         const float* wp = a.w + b * a.T * a.H + h;
         const float* bp = a.beta + b * a.T * a.H + h;
-        G g(smem, st);
 #pragma unroll 1
-        for (int64_t t0 = last - st * kChunk; t0 >= 0; t0 -= G::NST * kChunk) {
-            const int nt = a.T - t0 < kChunk ? int(a.T - t0) : kChunk;
+        for (int64_t t0 = last - st * kChunk; t0 >= begin; t0 -= G::NST * kChunk) {
+            const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
             if (last - t0 >= G::NST * kChunk) bar_sync<G::BAR>(kBarFree + st);
             const float w = lane < nt ? wp[(t0 + lane) * a.H] : 0.f, be = lane < nt ? bp[(t0 + lane) * a.H] : 0.f;
             g.fetch(kp + t0 * ks, rp + t0 * ks, ks, yp + t0 * vs, vs, nt, a.vec, lane);
@@ -97,19 +99,29 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
             put_inverse(g.mats, g.diag, lane);
             bar_arrive<G::BAR>(kBarFull + st);
         }
+        }
         return;
     }
 
     walker_regs<IO, N>();
     const int j0 = warp * 16;
     const int64_t nseg = (a.T + kSegment - 1) / kSegment;
+    constexpr int SLOTS = kSlots<N>;
+    const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = m_trans(lane);
+    for (; next_task<G::THREADS>(a, walks, task, first); first = false) {
+    const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H;
+    const int slice = int(task.walk % G::SLICES) * G::CW;
+    const int64_t begin = (a.parts - 1 - task.part) * a.part_len, end = begin + a.part_len < a.T ? begin + a.part_len : a.T;
+    const int64_t last = begin + (end - 1 - begin) / kChunk * kChunk;
+    const int64_t vbase = (b * a.T * a.H + h) * N + slice;
     const int64_t place = head * (nseg + 1) * N * N + int64_t(slice + j0) * N;
     const float* states = a.s_seg + place;
     float* grads = a.d_seg + place;
-    constexpr int SLOTS = kSlots<N>;
     float* phi = a.phi + head * (nseg + 1) * SLOTS + slice / 16 + warp;
+    float* hand = a.hand + head * N * N + int64_t(slice + j0) * N;
     float S[N / 8][4];   // D^T
-    load_state<N>(S, a.ds_out == nullptr ? nullptr : a.ds_out + head * N * N + slice + j0, lane);
+    if (task.part == 0) load_state<N>(S, a.ds_out == nullptr ? nullptr : a.ds_out + head * N * N + slice + j0, lane);
+    else take_over<N>(S, hand, task.lost, lane);
     // the gradient state behind segment c - 1, and its inner product with the state there
     auto border = [&](int64_t c) {
         keep_state<N>(grads + c * N * N, S, lane);
@@ -125,12 +137,11 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
         for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (lane == 0) phi[c * SLOTS] = x;
     };
-    border(nseg);
-    const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = m_trans(lane);
+    if (task.part == 0) border(nseg);
     int st = 0;
 #pragma unroll 1
-    for (int64_t t0 = last; t0 >= 0; t0 -= kChunk, st = (st + 1) % G::NST) {
-        const int nt = a.T - t0 < kChunk ? int(a.T - t0) : kChunk;
+    for (int64_t t0 = last; t0 >= begin; t0 -= kChunk, st = (st + 1) % G::NST) {
+        const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
         G g(smem, st);
         bar_sync<G::BAR>(kBarFull + st);
         // X = diag(q) D^T K + P^T dY
@@ -199,10 +210,12 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
             // dv through dy's columns, which only this warp reads
             store_half(static_cast<IO*>(a.dv) + at + 8 * n * vs, vs, nt - 8 * n, du[n], g.v + 8 * n * G::LDV + j0, G::LDV, a.vec, lane);
         }
-        if (t0 >= G::NST * kChunk) bar_arrive<G::BAR>(kBarFree + st);
+        if (t0 >= begin + G::NST * kChunk) bar_arrive<G::BAR>(kBarFree + st);
         if (t0 % kSegment == 0) border(t0 / kSegment);
     }
-    if (a.ds_in != nullptr) store_state<N>(a.ds_in + head * N * N + slice + j0, S, lane);
+    if (begin > 0) hand_on<N>(hand, S, lane);
+    else if (a.ds_in != nullptr) store_state<N>(a.ds_in + head * N * N + slice + j0, S, lane);
+    }
 }
 
 // ---------------------------------------------------------------------------

@@ -6,6 +6,7 @@
 
 #include <cstdint>
 #include <cstdio>
+#include <cstdlib>
 
 #include "../../include/wkv.h"
 
@@ -44,6 +45,22 @@ inline bool mul_ok(int64_t a, int64_t b, int64_t c, int64_t* out) {
 }
 
 inline size_t elem_bytes(int dtype) { return dtype == WKV_BF16 ? 2 : 4; }
+
+// Limit of every wait on another CTA's result: 1 s, or WKV_WAIT_LIMIT_NS (read
+// once per process; used by the tests to make waits run out on purpose).
+// Waits for a CTA's own TMA copies have a fixed limit (kCopyWaitNs).
+inline uint64_t wait_limit_ns() {
+    static const uint64_t v = []() -> uint64_t {
+        const char* e = std::getenv("WKV_WAIT_LIMIT_NS");
+        if (e != nullptr && *e != '\0') {
+            char* end = nullptr;
+            const unsigned long long x = std::strtoull(e, &end, 10);
+            if (end != e) return x;
+        }
+        return 1000000000ull;
+    }();
+    return v;
+}
 
 // An argument's bytes, for the checks of a call with many of them.
 struct Span {

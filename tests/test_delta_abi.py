@@ -18,8 +18,8 @@ def L():
 
 
 def fwd(L, B=2, T=9, Hk=2, H=4, N=64, dt=BF16, w=P[0], beta=P[1], r=P[2], k=P[3], v=P[4], s_in=None, y=P[6],
-        s_out=None):
-    return L.wkv_delta_forward(B, T, Hk, H, N, dt, w, beta, r, k, v, s_in, y, s_out, None)
+        s_out=None, ws=None, nws=0):
+    return L.wkv_delta_forward(B, T, Hk, H, N, dt, w, beta, r, k, v, s_in, y, s_out, ws, nws, None)
 
 
 def test_forward_refusals(L):
@@ -39,6 +39,13 @@ def test_forward_refusals(L):
     assert fwd(L, s_in=P[5], s_out=P[5] + 64) == ALIAS
     assert fwd(L, B=0, w=None) == OK
     assert fwd(L, T=0) == OK
+    many = dict(B=40, T=2048)      # 160 heads
+    need = L.wkv_delta_forward_workspace_bytes(40, 2048, 4, 64)
+    assert need > 0 and L.wkv_delta_forward_workspace_bytes(2, 2048, 4, 64) == 0
+    assert L.wkv_delta_forward_workspace_bytes(40, 2048, 4, 63) == 0
+    assert fwd(L, ws=P[8] + 8, nws=need, **many) == ALIGN
+    assert fwd(L, ws=P[6], nws=need, **many) == ALIAS
+    assert fwd(L, ws=P[5], nws=need, s_in=P[5], **many) == ALIAS
     assert fwd(L, T=0, s_in=P[5], s_out=P[5]) == OK
 
 

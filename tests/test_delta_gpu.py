@@ -325,3 +325,27 @@ def test_layer_with_norm_and_gate(dtype):
         close(a, b, name)
     for name, a, b in zip(NAMES, got, ref_bwd({**d, "dy": dx}, H)):
         close(a, b, name)
+
+
+@pytest.mark.parametrize("B,T,Hk,H,N,dtype", [(7, 1100, 8, 64, 64, BF16), (11, 777, 16, 16, 128, BF16), (13, 513, 30, 60, 32, F32),
+                                              (6, 2048, 50, 50, 64, F32)])
+def test_walks_in_parts_equal_whole_ones(B, T, Hk, H, N, dtype):
+    """More heads than the GPU holds at once go in parts of the tokens, with
+    the same arithmetic: the same bits as one walk a CTA, on calls that share
+    a workspace, and each sequence's as in a call of its own."""
+    g = torch.Generator(device=DEV).manual_seed(B)
+    n = lambda *s: torch.randn(s, generator=g, device=DEV)  # noqa: E731
+    d = {"w": torch.rand((B, T, H), generator=g, device=DEV), "beta": torch.rand((B, T, H), generator=g, device=DEV),
+         "r": n(B, T, Hk * N).to(dtype), "k": (n(B, T, Hk * N) * N ** -0.5).to(dtype), "v": n(B, T, H * N).to(dtype),
+         "state_in": n(B, H, N, N), "dy": n(B, T, H * N).to(dtype), "ds": n(B, H, N, N)}
+    ws = wkv.Workspace()
+    y, s = forward(d, H, use_workspace=False)
+    for _ in range(2):
+        y1, s1 = forward(d, H, workspace=ws)
+        assert torch.equal(y, y1) and torch.equal(s, s1)
+        assert ws.status() == 0
+    got = backward(d, H)
+    for b in (0, B // 2, B - 1):
+        one = {x: t[b:b + 1].contiguous() for x, t in d.items()}
+        for x, t in zip(NAMES, backward(one, H)):
+            assert torch.equal(got[NAMES.index(x)][b:b + 1], t), (x, b)
