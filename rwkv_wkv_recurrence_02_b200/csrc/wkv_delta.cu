@@ -30,17 +30,18 @@ Parts parts_layout(int64_t walks, int64_t states, int64_t T) {
 int slices(int64_t N) { return N == 128 ? 2 : 1; }
 
 // ws: parts_layout's bytes, or NULL for one walk a CTA
-template <typename K>
-int launch_walk(K kern, int64_t walks, int threads, int smem, bool (&ready)[kMaxDevices], d::Args a, char* ws, const Parts& p,
-                cudaStream_t st) {
-    int rc = allow_smem(kern, smem, ready);
+using Walk = void (*)(d::Args);
+int launch_walk(Walk kern, Walk in_parts, int64_t walks, int threads, int smem, bool (&ready)[2][kMaxDevices], d::Args a, char* ws,
+                const Parts& p, cudaStream_t st) {
+    int rc = allow_smem(kern, smem, ready[0]);
+    if (rc == WKV_OK) rc = allow_smem(in_parts, smem, ready[1]);
     if (rc != WKV_OK) return rc;
     a.parts = 1, a.part_len = a.T;
     if (ws != nullptr && p.bytes > 0) {
         int dev = 0, sms = 0, per = 0;
         rc = record_cuda(cudaGetDevice(&dev));
         if (rc == WKV_OK) rc = record_cuda(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-        if (rc == WKV_OK) rc = record_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, threads, size_t(smem)));
+        if (rc == WKV_OK) rc = record_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, in_parts, threads, size_t(smem)));
         if (rc != WKV_OK) return rc;
         // the share of the last wave's places that stay empty, of all waves': parts
         // pay from about a tenth (they cost a pipeline's fill each)
@@ -55,7 +56,7 @@ int launch_walk(K kern, int64_t walks, int threads, int smem, bool (&ready)[kMax
             a.wait_ns = wait_limit_ns();
             rc = record_cuda(cudaMemsetAsync(ws, 0, p.hand, st));
             if (rc != WKV_OK) return rc;
-            kern<<<dim3(unsigned(slots)), threads, smem, st>>>(a);
+            in_parts<<<dim3(unsigned(slots)), threads, smem, st>>>(a);
             return check_launch();
         }
     }
@@ -65,23 +66,25 @@ int launch_walk(K kern, int64_t walks, int threads, int smem, bool (&ready)[kMax
 template <typename IO, int N, bool WANT_Y>
 int launch_forward(const d::Args& a, char* ws, const Parts& p, cudaStream_t st) {
     using G = d::ForwardShape<IO, N, WANT_Y>;
-    static bool ready[kMaxDevices] = {false};
-    return launch_walk(d::delta_forward_mma_kernel<IO, N, WANT_Y>, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, ready, a, ws, p, st);
+    static bool ready[2][kMaxDevices] = {{false}};
+    return launch_walk(d::delta_forward_mma_kernel<IO, N, WANT_Y, false>, d::delta_forward_mma_kernel<IO, N, WANT_Y, true>, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, ready, a, ws, p, st);
 }
 
 template <typename IO, int N>
 int launch_reverse(const d::Args& a, char* ws, const Parts& p, cudaStream_t st) {
     using G = d::ReverseShape<IO, N>;
-    static bool ready[kMaxDevices] = {false};
-    return launch_walk(d::delta_reverse_mma_kernel<IO, N>, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, ready, a, ws, p, st);
+    static bool ready[2][kMaxDevices] = {{false}};
+    return launch_walk(d::delta_reverse_mma_kernel<IO, N, false>, d::delta_reverse_mma_kernel<IO, N, true>, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, ready, a, ws, p, st);
 }
 
 template <typename IO, int N>
 int launch_segments(const d::Args& a, cudaStream_t st) {
     using G = d::SegmentShape<IO, N>;
     static bool ready[kMaxDevices] = {false};
-    return launch_walk(d::delta_segment_kernel<IO, N>, a.B * a.H * ((a.T + d::kSegment - 1) / d::kSegment), G::THREADS, G::SMEM,
-                       ready, a, nullptr, Parts{}, st);
+    auto kern = d::delta_segment_kernel<IO, N>;
+    const int rc = allow_smem(kern, G::SMEM, ready);
+    const int64_t segments = a.B * a.H * ((a.T + d::kSegment - 1) / d::kSegment);
+    return rc != WKV_OK ? rc : launch(kern, segments, G::THREADS, G::SMEM, st, a);
 }
 
 struct Layout {

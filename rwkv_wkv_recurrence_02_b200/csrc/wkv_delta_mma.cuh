@@ -535,9 +535,9 @@ struct Task {
 };
 // The next task of the CTA (every thread calls; THREADS of them), false: none
 // is left.  Publishes the one before: its state is written and fenced.
-template <int THREADS>
+template <bool PARTS, int THREADS>
 __device__ __forceinline__ bool next_task(const Args& a, int64_t walks, Task& t, bool first) {
-    if (a.parts <= 1) {
+    if constexpr (!PARTS) {
         t = Task{int64_t(blockIdx.x), 0, false};
         return first;
     }
@@ -599,7 +599,7 @@ __device__ __forceinline__ void walker_regs() {
 template <typename IO, int N, bool WANT_Y>
 using ForwardShape = Columns<IO, N, WANT_Y, 3 + (WANT_Y ? kOutOrders<IO> : 0), 2>;
 
-template <typename IO, int N, bool WANT_Y>
+template <typename IO, int N, bool WANT_Y, bool PARTS>
 __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO, N>) delta_forward_mma_kernel(const Args a) {
     using G = ForwardShape<IO, N, WANT_Y>;
     constexpr int KP = G::KP, PP = kOutOrders<IO>, LD = G::LD;
@@ -617,9 +617,10 @@ __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO
         const int st = warp - G::NW;
         const int64_t ks = a.Hk * N;
         G g(smem, st);
-        for (; next_task<G::THREADS>(a, walks, task, first); first = false) {
+        for (; next_task<PARTS, G::THREADS>(a, walks, task, first); first = false) {
         const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
-        const int64_t begin = task.part * a.part_len, end = begin + a.part_len < a.T ? begin + a.part_len : a.T;
+        const int64_t begin = PARTS ? task.part * a.part_len : 0;
+    const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
         const IO* kp = static_cast<const IO*>(a.k) + (b * a.T * a.Hk + hk) * N;
         const IO* rp = static_cast<const IO*>(a.r) + (b * a.T * a.Hk + hk) * N;
         const IO* vp = static_cast<const IO*>(a.v) + (b * a.T * a.H + h) * N + task.walk % G::SLICES * G::CW;
@@ -671,15 +672,16 @@ __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO
     const int j0 = warp * 16;
     const int64_t nseg = (a.T + kSegment - 1) / kSegment;
     const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = m_plain(lane);
-    for (; next_task<G::THREADS>(a, walks, task, first); first = false) {
+    for (; next_task<PARTS, G::THREADS>(a, walks, task, first); first = false) {
     const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H;
     const int slice = int(task.walk % G::SLICES) * G::CW;
-    const int64_t begin = task.part * a.part_len, end = begin + a.part_len < a.T ? begin + a.part_len : a.T;
+    const int64_t begin = PARTS ? task.part * a.part_len : 0;
+    const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
     const int64_t vbase = (b * a.T * a.H + h) * N + slice;
     float* keep = a.s_seg + head * (nseg + 1) * N * N + int64_t(slice + j0) * N;
     float* hand = a.hand + head * N * N + int64_t(slice + j0) * N;
     float S[N / 8][4];
-    if (task.part == 0) load_state<N>(S, a.s_in == nullptr ? nullptr : a.s_in + head * N * N + slice + j0, lane);
+    if (!PARTS || task.part == 0) load_state<N>(S, a.s_in == nullptr ? nullptr : a.s_in + head * N * N + slice + j0, lane);
     else take_over<N>(S, hand, task.lost, lane);
     int st = 0;
 #pragma unroll 1
@@ -762,7 +764,7 @@ __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO
         }
         if (t0 + G::NST * kChunk < end) bar_arrive<G::BAR>(kBarFree + st);
     }
-    if (end < a.T) {
+    if (PARTS && end < a.T) {
         hand_on<N>(hand, S, lane);
     } else if constexpr (WANT_Y) {
         if (a.s_out != nullptr) store_state<N>(a.s_out + head * N * N + slice + j0, S, lane);

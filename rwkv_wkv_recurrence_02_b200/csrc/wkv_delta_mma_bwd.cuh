@@ -33,7 +33,7 @@ namespace delta {
 template <typename IO, int N>
 using ReverseShape = Columns<IO, N, true, 6, 3>;
 
-template <typename IO, int N>
+template <typename IO, int N, bool PARTS>
 __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) delta_reverse_mma_kernel(const Args a) {
     using G = ReverseShape<IO, N>;
     constexpr int KP = G::KP, LD = G::LD;
@@ -51,9 +51,10 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
         const int st = warp - G::NW;
         const int64_t ks = a.Hk * N;
         G g(smem, st);
-        for (; next_task<G::THREADS>(a, walks, task, first); first = false) {
+        for (; next_task<PARTS, G::THREADS>(a, walks, task, first); first = false) {
         const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
-        const int64_t begin = (a.parts - 1 - task.part) * a.part_len, end = begin + a.part_len < a.T ? begin + a.part_len : a.T;
+        const int64_t begin = PARTS ? (a.parts - 1 - task.part) * a.part_len : 0;
+    const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
         const int64_t last = begin + (end - 1 - begin) / kChunk * kChunk;
         const int64_t vbase = (b * a.T * a.H + h) * N + task.walk % G::SLICES * G::CW;
         const IO* kp = static_cast<const IO*>(a.k) + (b * a.T * a.Hk + hk) * N;
@@ -108,10 +109,11 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
     const int64_t nseg = (a.T + kSegment - 1) / kSegment;
     constexpr int SLOTS = kSlots<N>;
     const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = m_trans(lane);
-    for (; next_task<G::THREADS>(a, walks, task, first); first = false) {
+    for (; next_task<PARTS, G::THREADS>(a, walks, task, first); first = false) {
     const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H;
     const int slice = int(task.walk % G::SLICES) * G::CW;
-    const int64_t begin = (a.parts - 1 - task.part) * a.part_len, end = begin + a.part_len < a.T ? begin + a.part_len : a.T;
+    const int64_t begin = PARTS ? (a.parts - 1 - task.part) * a.part_len : 0;
+    const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
     const int64_t last = begin + (end - 1 - begin) / kChunk * kChunk;
     const int64_t vbase = (b * a.T * a.H + h) * N + slice;
     const int64_t place = head * (nseg + 1) * N * N + int64_t(slice + j0) * N;
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
     float* phi = a.phi + head * (nseg + 1) * SLOTS + slice / 16 + warp;
     float* hand = a.hand + head * N * N + int64_t(slice + j0) * N;
     float S[N / 8][4];   // D^T
-    if (task.part == 0) load_state<N>(S, a.ds_out == nullptr ? nullptr : a.ds_out + head * N * N + slice + j0, lane);
+    if (!PARTS || task.part == 0) load_state<N>(S, a.ds_out == nullptr ? nullptr : a.ds_out + head * N * N + slice + j0, lane);
     else take_over<N>(S, hand, task.lost, lane);
     // the gradient state behind segment c - 1, and its inner product with the state there
     auto border = [&](int64_t c) {
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
         for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (lane == 0) phi[c * SLOTS] = x;
     };
-    if (task.part == 0) border(nseg);
+    if (!PARTS || task.part == 0) border(nseg);
     int st = 0;
 #pragma unroll 1
     for (int64_t t0 = last; t0 >= begin; t0 -= kChunk, st = (st + 1) % G::NST) {
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
         if (t0 >= begin + G::NST * kChunk) bar_arrive<G::BAR>(kBarFree + st);
         if (t0 % kSegment == 0) border(t0 / kSegment);
     }
-    if (begin > 0) hand_on<N>(hand, S, lane);
+    if (PARTS && begin > 0) hand_on<N>(hand, S, lane);
     else if (a.ds_in != nullptr) store_state<N>(a.ds_in + head * N * N + slice + j0, S, lane);
     }
 }
