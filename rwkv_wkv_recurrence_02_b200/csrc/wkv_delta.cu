@@ -88,7 +88,7 @@ int launch_segments(const d::Args& a, cudaStream_t st) {
 }
 
 struct Layout {
-    size_t e, du, s_seg, d_seg, phi, drh, dkh, parts, bytes;
+    size_t e, du, s_seg, d_seg, drh, dkh, parts, bytes;
 };
 
 // share: several value heads to a key head
@@ -101,8 +101,7 @@ Layout layout(int64_t B, int64_t T, int64_t H, int64_t N, bool share) {
     l.du = l.e + val;
     l.s_seg = l.du + val;
     l.d_seg = l.s_seg + up(borders * N * N * 4);
-    l.phi = l.d_seg + up(borders * N * N * 4);
-    l.drh = l.phi + up(borders * (N / 16) * 4);
+    l.drh = l.d_seg + up(borders * N * N * 4);
     l.dkh = l.drh + (share ? val : 0);
     l.parts = l.dkh + (share ? val : 0);
     l.bytes = l.parts + parts_layout(B * H * slices(N), B * H * N * N, T).bytes;
@@ -264,7 +263,7 @@ int wkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, i
     a.w = w, a.beta = beta, a.r = r, a.k = k, a.v = v, a.dy = dy, a.s_in = state_in, a.ds_out = dstate_out;
     a.dv = dv, a.ds_in = dstate_in;
     a.dr = dr, a.dk = dk, a.dw = dw, a.dbeta = dbeta;
-    a.e = f(l.e), a.du = f(l.du), a.s_seg = f(l.s_seg), a.d_seg = f(l.d_seg), a.phi = f(l.phi);
+    a.e = f(l.e), a.du = f(l.du), a.s_seg = f(l.s_seg), a.d_seg = f(l.d_seg);
     a.drh = f(l.drh), a.dkh = f(l.dkh);
     a.vec = aligned(r, 16) && aligned(k, 16) && aligned(v, 16) && aligned(dy, 16) && aligned(dv, 16) &&
             aligned(dr, 16) && aligned(dk, 16);

@@ -24,11 +24,6 @@ namespace delta {
 
 // tokens of a segment: the reverse mode keeps the states between segments
 constexpr int kSegment = 64;
-// parts of the inner product of two states: one for each warp of 16 value
-// columns
-template <int N>
-constexpr int kSlots = N / 16;
-
 template <typename IO>
 __device__ __forceinline__ float to_f32(IO x);
 template <>
@@ -67,7 +62,6 @@ struct Args {
     float* du;
     float* s_seg;        // (B, H, n + 1, N, N), n = ceil(T / kSegment): the state entering each segment and the last, [value][key]
     float* d_seg;        // gradients of those, of what follows
-    float* phi;          // (B, H, n + 1, slots): parts of <D, S> there
     float* drh;          // (B, T, H, N): dr and dk of each value head, where heads share keys
     float* dkh;
     bool vec;            // 16-byte loads of every tensor in the I/O type

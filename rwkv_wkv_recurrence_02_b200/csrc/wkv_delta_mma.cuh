@@ -611,6 +611,8 @@ __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO
     bool first = true;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the reverse mode's other walk may start: what it reads is finished
+    if constexpr (!WANT_Y && !PARTS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp >= G::NW) {
         stager_regs<IO, N>();

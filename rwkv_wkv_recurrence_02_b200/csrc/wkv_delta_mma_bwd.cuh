@@ -15,8 +15,9 @@
 // Two walks, for e and the states between segments of 64 tokens (the forward
 // kernel) and for du and the gradient states between them; with those, dr and
 // dk of a segment need nothing from the others, and a third kernel forms them
-// for every segment at once.  The inner product <D, S> between segments
-// comes from the second walk; dw continues from it within a segment.
+// for every segment at once.  It starts dw from the inner
+// products <D, S> at the segment's borders.  The two walks need nothing of
+// each other and run at the same time where the GPU has room.
 // What only reaches dk takes the orders that its type keeps; dr takes them
 // all, as r.dr enters dw.
 #pragma once
@@ -44,7 +45,10 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
     Task task;
     bool first = true;
 
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // In parts, after the memset of the tickets.  Otherwise the forward walk,
+    // which this one needs nothing of, has let it start once its own CTAs knew
+    // everything before them finished; the two end together (below).
+    if constexpr (PARTS) asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp >= G::NW) {
         stager_regs<IO, N>();
@@ -107,7 +111,6 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
     walker_regs<IO, N>();
     const int j0 = warp * 16;
     const int64_t nseg = (a.T + kSegment - 1) / kSegment;
-    constexpr int SLOTS = kSlots<N>;
     const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = m_trans(lane);
     for (; next_task<PARTS, G::THREADS>(a, walks, task, first); first = false) {
     const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H;
@@ -117,29 +120,13 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
     const int64_t last = begin + (end - 1 - begin) / kChunk * kChunk;
     const int64_t vbase = (b * a.T * a.H + h) * N + slice;
     const int64_t place = head * (nseg + 1) * N * N + int64_t(slice + j0) * N;
-    const float* states = a.s_seg + place;
     float* grads = a.d_seg + place;
-    float* phi = a.phi + head * (nseg + 1) * SLOTS + slice / 16 + warp;
     float* hand = a.hand + head * N * N + int64_t(slice + j0) * N;
     float S[N / 8][4];   // D^T
     if (!PARTS || task.part == 0) load_state<N>(S, a.ds_out == nullptr ? nullptr : a.ds_out + head * N * N + slice + j0, lane);
     else take_over<N>(S, hand, task.lost, lane);
-    // the gradient state behind segment c - 1, and its inner product with the state there
-    auto border = [&](int64_t c) {
-        keep_state<N>(grads + c * N * N, S, lane);
-        float x = 0.f;
-#pragma unroll
-        for (int n = 0; n < N / 8; ++n)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const float2 v = __ldcg(reinterpret_cast<const float2*>(states + c * N * N + (lane / 4 + 8 * q) * N + 8 * n + 2 * (lane % 4)));
-                x = fmaf(S[n][2 * q], v.x, fmaf(S[n][2 * q + 1], v.y, x));
-            }
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0) phi[c * SLOTS] = x;
-    };
-    if (!PARTS || task.part == 0) border(nseg);
+    // gradient states between segments, as S^T's
+    if (!PARTS || task.part == 0) keep_state<N>(grads + nseg * N * N, S, lane);
     int st = 0;
 #pragma unroll 1
     for (int64_t t0 = last; t0 >= begin; t0 -= kChunk, st = (st + 1) % G::NST) {
@@ -213,11 +200,13 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
             store_half(static_cast<IO*>(a.dv) + at + 8 * n * vs, vs, nt - 8 * n, du[n], g.v + 8 * n * G::LDV + j0, G::LDV, a.vec, lane);
         }
         if (t0 >= begin + G::NST * kChunk) bar_arrive<G::BAR>(kBarFree + st);
-        if (t0 % kSegment == 0) border(t0 / kSegment);
+        if (t0 % kSegment == 0) keep_state<N>(grads + t0 / kSegment * N * N, S, lane);
     }
     if (PARTS && begin > 0) hand_on<N>(hand, S, lane);
     else if (a.ds_in != nullptr) store_state<N>(a.ds_in + head * N * N + slice + j0, S, lane);
     }
+    // what follows this kernel reads the forward walk's results too
+    if constexpr (!PARTS) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -240,7 +229,7 @@ struct SegmentShape {
     // u, dv, dy; S and D, later K and R; the decays and the sums over channels
     static constexpr int S_ROWS = (3 + PP + KP) * PIECE * 2;
     static constexpr int A_ = (3 + PP) * SPIECE * 2, B_ = 2 * KP * KPIECE * 2, S_BUF = A_ > B_ ? A_ : B_;
-    static constexpr int S_SUM = kSegment * (8 + 4 + 4 * HALVES);
+    static constexpr int S_SUM = kSegment * (8 + 4 + 4 * HALVES) + WARPS * 8;
     static constexpr int SMEM = S_ROWS + S_BUF + S_SUM;
     // CTAs an SM by shared memory; registers follow
     static constexpr int CTAS = 227 * 1024 / (SMEM + 1024) > 3 ? 3 : 227 * 1024 / (SMEM + 1024);
@@ -259,6 +248,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     float2* sums = reinterpret_cast<float2*>(smem + G::S_ROWS + G::S_BUF);
     float* dvv = reinterpret_cast<float*>(sums + kSegment);       // dv . v of a token
     float* rdr = dvv + kSegment;                                  // r . dr, by halves of the channels
+    float* inner = rdr + kSegment * G::HALVES;                    // <D, S> at the borders, by warps
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int tb = warp % 4, i0 = warp / 4 * G::IC;
 
@@ -280,6 +270,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     const IO* rp = static_cast<const IO*>(a.r) + keys;
     for (int i = tid; i < N * N / 32; i += G::THREADS) {
         prefetch_l2(s_seg + i * 32);
+        prefetch_l2(s_seg + N * N + i * 32);
         prefetch_l2(d_seg + i * 32);
     }
     constexpr int KL = N * int(sizeof(IO)) / 64;   // 64-byte pieces of a row: rows need not begin a line
@@ -578,17 +569,30 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         own[q] += __shfl_xor_sync(0xffffffffu, own[q], 2);
         if (lane % 4 == 0) rdr[(warp / 4) * kSegment + t_lo + 8 * q] = own[q];
     }
-    __syncthreads();
-    // --- dw: the sum <Dn, S> from the segment's end backwards; its first token's is the border's own
-    if (warp == 0) {
-        constexpr int SLOTS = kSlots<N>;
-        const float* phi = a.phi + (head * (nseg + 1) + seg) * SLOTS;
-        float first = lane < SLOTS ? phi[lane] : 0.f, end = lane < SLOTS ? phi[SLOTS + lane] : 0.f;
+    // the inner product <D, S> at the segment's end; at its begin it follows from
+    // the segment's terms, but for the first segment, where it is formed too: with
+    // an empty state it is zero, and not what rounding leaves of the terms
+    float x[2] = {0.f, 0.f};
 #pragma unroll
-        for (int o = 16; o > 0; o /= 2) {
-            first += __shfl_xor_sync(0xffffffffu, first, o);
-            end += __shfl_xor_sync(0xffffffffu, end, o);
+    for (int q = 1; q >= 0; --q) {
+        if (q == 0 && seg > 0) break;
+        const float4* ps = reinterpret_cast<const float4*>(s_seg + q * N * N);
+        const float4* pd = reinterpret_cast<const float4*>(d_seg + (q - 1) * N * N);
+#pragma unroll 8
+        for (int i = tid; i < N * N / 4; i += G::THREADS) {
+            const float4 u = __ldcg(ps + i), v = __ldcg(pd + i);
+            x[q] = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, x[q]))));
         }
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) x[q] += __shfl_xor_sync(0xffffffffu, x[q], o);
+    }
+    if (lane == 0) inner[2 * warp] = x[0], inner[2 * warp + 1] = x[1];
+    __syncthreads();
+    // --- dw: the sum <Dn, S> from the segment's end backwards
+    if (warp == 0) {
+        float first = 0.f, end = 0.f;
+#pragma unroll
+        for (int i = 0; i < G::WARPS; ++i) first += inner[2 * i], end += inner[2 * i + 1];
         const int ta = 2 * lane;
         float term[2];
 #pragma unroll
@@ -613,7 +617,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
             if (t >= nt) continue;
             const int64_t at = scalar + t * a.H;
             // a state that nothing is left of has no gradient, whatever the sum's rounding left
-            a.dw[at] = t == 0 ? -first : expf(-a.w[at]) == 0.f ? 0.f : -(q ? s1 : s0);
+            a.dw[at] = expf(-a.w[at]) == 0.f ? 0.f : t == 0 && seg == 0 ? -first : -(q ? s1 : s0);
         }
     }
 }
