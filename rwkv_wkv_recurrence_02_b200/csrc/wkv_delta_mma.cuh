@@ -266,36 +266,6 @@ __device__ __forceinline__ int b_trans(int lane, int ld) { return ((lane & 7) + 
 __device__ __forceinline__ int m_plain(int lane) { return mat_at((lane & 7) + (lane >> 4) * 8, ((lane >> 3) & 1) * 8); }
 __device__ __forceinline__ int m_trans(int lane) { return mat_at((lane & 7) + ((lane >> 3) & 1) * 8, (lane >> 4) * 8); }
 
-// (16 tokens x N) (N x 16 tokens)^T of two staged arrays of KX and KY pieces
-// (`piece` bytes apart), the products of the first ORD orders: C[t][s] = x_t .
-// y_s.  xa, ya: this lane's place in the first 16 columns of x as an A operand,
-// of y as a plain B operand; SWIZZLED: the columns' places by exclusive or.
-template <int N, int KX, int KY, int ORD, bool SWIZZLED>
-__device__ __forceinline__ void gram_at(float (&c)[2][4], uint32_t xa, uint32_t ya, int piece) {
-    bool first = true;
-#pragma unroll
-    for (int kk = 0; kk < N / 16; ++kk) {
-        uint32_t a[KX][4], b[KY][4];
-#pragma unroll
-        for (int p = 0; p < KX; ++p) ldsm4(a[p], (SWIZZLED ? xa ^ (kk * 32) : xa + kk * 32) + p * piece);
-#pragma unroll
-        for (int p = 0; p < KY; ++p) ldsm4(b[p], (SWIZZLED ? ya ^ (kk * 32) : ya + kk * 32) + p * piece);
-#pragma unroll
-        for (int o = ORD - 1; o >= 0; --o)
-#pragma unroll
-            for (int p = 0; p < KX && p <= o; ++p)
-                if (o - p < KY) {
-                    mma2(c, a[p], b[o - p], first);
-                    first = false;
-                }
-    }
-}
-template <int N, int KX, int KY, int ORD>
-__device__ __forceinline__ void gram(float (&c)[2][4], const __nv_bfloat16* x, const __nv_bfloat16* y, int piece, int lane) {
-    constexpr int LD = N + 8;
-    gram_at<N, KX, KY, ORD, false>(c, smem_u32(x + b_trans(lane, LD)), smem_u32(y + b_plain(lane, LD)), piece * 2);
-}
-
 // A 16-token x 16-line tile of staged rows, transposed, in the accumulator
 // layout: x[n][i] is line lane / 4 + 8 (i / 2), token 8 n + 2 (lane % 4) + i % 2.
 template <typename IO>
@@ -366,21 +336,68 @@ __device__ __forceinline__ void scale_tokens(float (&x)[2][4], const float* f, i
 }
 
 // A product of pieces in two accumulators: the leading order, and all others
-// (2^-8 of it, so what their additions round off is 2^-8 of a float32 step).
+// (2^-8 of it, so what their additions cut off is 2^-8 of a float32 step).  The
+// leading one is added to a float32 sum every CHAIN steps of 16: the tensor
+// cores cut off what a rounded addition would keep half of, so errors of a long
+// chain have one sign and grow with its length.
 struct Acc {
     float hi[2][4], lo[2][4];
-    __device__ __forceinline__ void sum(float (&x)[2][4], bool has_lo = true) const {
+    // before k step kk: does the leading order begin anew?  x: the sum of the steps before
+    template <int CHAIN>
+    __device__ __forceinline__ bool start(float (&x)[2][4], int kk) const {
+        if (kk > 0 && kk % CHAIN == 0) add(x, hi, kk == CHAIN);
+        return kk % CHAIN == 0;
+    }
+    // after the last of `steps`
+    template <int CHAIN>
+    __device__ __forceinline__ void finish(float (&x)[2][4], int steps, bool has_lo = true) const {
+        add(x, hi, steps <= CHAIN);
+        if (has_lo) add(x, lo, false);
+    }
+    __device__ __forceinline__ void sum(float (&x)[2][4]) const { finish<1>(x, 1); }
+    static __device__ __forceinline__ void add(float (&x)[2][4], const float (&y)[2][4], bool first) {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[n][i] = has_lo ? hi[n][i] + lo[n][i] : hi[n][i];
+            for (int i = 0; i < 4; ++i) x[n][i] = first ? y[n][i] : x[n][i] + y[n][i];
     }
 };
+// (16 tokens x N) (N x 16 tokens)^T of two staged arrays of KX and KY pieces
+// (`piece` bytes apart), the products of the first ORD orders: C[t][s] = x_t .
+// y_s.  xa, ya: this lane's place in the first 16 columns of x as an A operand,
+// of y as a plain B operand; SWIZZLED: the columns' places by exclusive or.
+template <int N, int KX, int KY, int ORD, int CHAIN, bool SWIZZLED>
+__device__ __forceinline__ void gram_at(float (&c)[2][4], uint32_t xa, uint32_t ya, int piece) {
+    Acc acc;
+#pragma unroll
+    for (int kk = 0; kk < N / 16; ++kk) {
+        uint32_t a[KX][4], b[KY][4];
+#pragma unroll
+        for (int p = 0; p < KX; ++p) ldsm4(a[p], (SWIZZLED ? xa ^ (kk * 32) : xa + kk * 32) + p * piece);
+#pragma unroll
+        for (int p = 0; p < KY; ++p) ldsm4(b[p], (SWIZZLED ? ya ^ (kk * 32) : ya + kk * 32) + p * piece);
+        const bool hi_first = acc.start<CHAIN>(c, kk);
+        bool lo_first = kk == 0;
+#pragma unroll
+        for (int p = 0; p < KX && p < ORD; ++p)
+#pragma unroll
+            for (int q = 0; q < KY && p + q < ORD; ++q) {
+                mma2(p + q == 0 ? acc.hi : acc.lo, a[p], b[q], p + q == 0 ? hi_first : lo_first);
+                if (p + q > 0) lo_first = false;
+            }
+    }
+    acc.finish<CHAIN>(c, N / 16, ORD > 1 && KX * KY > 1);
+}
+template <int N, int KX, int KY, int ORD, int CHAIN>
+__device__ __forceinline__ void gram(float (&c)[2][4], const __nv_bfloat16* x, const __nv_bfloat16* y, int piece, int lane) {
+    constexpr int LD = N + 8;
+    gram_at<N, KX, KY, ORD, CHAIN, false>(c, smem_u32(x + b_trans(lane, LD)), smem_u32(y + b_plain(lane, LD)), piece * 2);
+}
+
 // acc (+)= A (16 x 16) B (16 x 16) of NA and NB pieces, orders below ORD.  B's
 // pieces lie `piece` bytes apart; addr: this lane's place in the first.
 template <int NA, int NB, int ORD, bool TRANS>
-__device__ __forceinline__ void times_at(Acc& acc, bool first, const uint32_t (&a)[NA][4], uint32_t addr, int piece) {
-    bool lo_first = first;
+__device__ __forceinline__ void times_at(Acc& acc, bool first, bool lo_first, const uint32_t (&a)[NA][4], uint32_t addr, int piece) {
 #pragma unroll
     for (int p = 0; p < NB && p < ORD; ++p) {
         uint32_t f[4];
@@ -400,9 +417,9 @@ __device__ __forceinline__ void times_at(Acc& acc, bool first, const uint32_t (&
 // the same of staged elements: pieces `piece` elements apart, off: this lane's
 // offset (b_plain, b_trans)
 template <int NA, int NB, int ORD, bool TRANS>
-__device__ __forceinline__ void times(Acc& acc, bool first, const uint32_t (&a)[NA][4], const __nv_bfloat16* m, int piece,
-                                      int off) {
-    times_at<NA, NB, ORD, TRANS>(acc, first, a, smem_u32(m + off), piece * 2);
+__device__ __forceinline__ void times(Acc& acc, bool first, bool lo_first, const uint32_t (&a)[NA][4], const __nv_bfloat16* m,
+                                      int piece, int off) {
+    times_at<NA, NB, ORD, TRANS>(acc, first, lo_first, a, smem_u32(m + off), piece * 2);
 }
 // d (+)= A B into one accumulator, smallest orders first
 template <int NA, int NB>
@@ -576,6 +593,9 @@ __device__ __forceinline__ bool next_task(const Args& a, int64_t walks, Task& t,
 // what only reaches an output takes this many orders
 template <typename IO>
 constexpr int kOutOrders = sizeof(IO) == 2 ? 2 : 3;
+// steps of 16 in a chain of the tensor cores' additions
+template <typename IO>
+constexpr int kChain = sizeof(IO) == 2 ? 4 : 1;
 
 // CTAs an SM: two where the state's lines and the I/O type leave room
 template <typename IO, int N>
@@ -602,7 +622,7 @@ using ForwardShape = Columns<IO, N, WANT_Y, 3 + (WANT_Y ? kOutOrders<IO> : 0), 2
 template <typename IO, int N, bool WANT_Y, bool PARTS>
 __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO, N>) delta_forward_mma_kernel(const Args a) {
     using G = ForwardShape<IO, N, WANT_Y>;
-    constexpr int KP = G::KP, PP = kOutOrders<IO>, LD = G::LD;
+    constexpr int KP = G::KP, PP = kOutOrders<IO>, LD = G::LD, C = kChain<IO>;
     extern __shared__ __align__(16) char smem[];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
 
@@ -643,8 +663,8 @@ __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO
             }
             __syncwarp();
             float kk[2][4], rk[2][4];
-            gram<N, KP, KP, KP>(kk, g.k, g.k, G::PIECE, lane);
-            if constexpr (WANT_Y) gram<N, KP, KP, KP>(rk, g.r(), g.k, G::PIECE, lane);
+            gram<N, KP, KP, KP, kChain<IO>>(kk, g.k, g.k, G::PIECE, lane);
+            if constexpr (WANT_Y) gram<N, KP, KP, KP, kChain<IO>>(rk, g.r(), g.k, G::PIECE, lane);
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const float2 bs = pair_at(g.beta, n, lane);
@@ -700,11 +720,12 @@ __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO
             for (int kk = 0; kk < N / 16; ++kk) {
                 uint32_t sp[3][4];
                 split_a<3>(S[2 * kk], S[2 * kk + 1], sp);
-                times<3, KP, 3, false>(pa, kk == 0, sp, g.k + kk * 16, G::PIECE, off_b);
-                if constexpr (WANT_Y) times<3, KP, PP, false>(qa, kk == 0, sp, g.r() + kk * 16, G::PIECE, off_b);
+                times<3, KP, 3, false>(pa, pa.template start<C>(p, kk), kk == 0, sp, g.k + kk * 16, G::PIECE, off_b);
+                if constexpr (WANT_Y)
+                    times<3, KP, PP, false>(qa, qa.template start<C>(q, kk), kk == 0, sp, g.r() + kk * 16, G::PIECE, off_b);
             }
-            pa.sum(p);
-            if constexpr (WANT_Y) qa.sum(q);
+            pa.template finish<C>(p, N / 16);
+            if constexpr (WANT_Y) qa.template finish<C>(q, N / 16);
         }
         load_lines(x, g.v + j0, G::LDV, lane);
         // X = V - g K S
@@ -720,7 +741,7 @@ __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO
             uint32_t xp[3][4];
             split_a<3>(x[0], x[1], xp);
             Acc ea;
-            times<3, 3, 3, false>(ea, true, xp, g.mats, kMat, off_m);
+            times<3, 3, 3, false>(ea, true, true, xp, g.mats, kMat, off_m);
             ea.sum(e);
         }
         // S <- g_15 S + (G beta E)^T K
@@ -752,7 +773,7 @@ __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO
             uint32_t ep[PP][4];
             split_a<PP>(e[0], e[1], ep);
             Acc ya;
-            times<PP, PP, PP, false>(ya, true, ep, g.mats + 3 * kMat, kMat, off_m);
+            times<PP, PP, PP, false>(ya, true, true, ep, g.mats + 3 * kMat, kMat, off_m);
             float y[2][4];
             ya.sum(y);
 #pragma unroll

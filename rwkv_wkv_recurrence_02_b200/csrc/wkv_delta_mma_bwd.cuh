@@ -82,8 +82,8 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
             }
             __syncwarp();
             float kk[2][4], rk[2][4];
-            gram<N, KP, KP, KP>(kk, g.k, g.k, G::PIECE, lane);
-            gram<N, KP, KP, KP>(rk, g.r(), g.k, G::PIECE, lane);
+            gram<N, KP, KP, KP, kChain<IO>>(kk, g.k, g.k, G::PIECE, lane);
+            gram<N, KP, KP, KP, kChain<IO>>(rk, g.r(), g.k, G::PIECE, lane);
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int t = 8 * n + 2 * (lane % 4);
@@ -141,9 +141,9 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
             for (int kk = 0; kk < N / 16; ++kk) {
                 uint32_t sp[3][4];
                 split_a<3>(S[2 * kk], S[2 * kk + 1], sp);
-                times<3, KP, 3, false>(pa, kk == 0, sp, g.k + kk * 16, G::PIECE, off_b);
+                times<3, KP, 3, false>(pa, pa.template start<kChain<IO>>(x, kk), kk == 0, sp, g.k + kk * 16, G::PIECE, off_b);
             }
-            pa.sum(x);
+            pa.template finish<kChain<IO>>(x, N / 16);
         }
         load_lines(dy, g.v + j0, G::LDV, lane);
         scale_tokens(x, g.sc, lane);
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
             uint32_t yq[KP][4];
             split_a<KP>(dy[0], dy[1], yq);
             Acc ya;
-            times<KP, 3, 3, true>(ya, true, yq, g.mats + 3 * kMat, kMat, off_m);
+            times<KP, 3, 3, true>(ya, true, true, yq, g.mats + 3 * kMat, kMat, off_m);
             float p[2][4];
             ya.sum(p);
 #pragma unroll
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
             uint32_t xp[3][4];
             split_a<3>(x[0], x[1], xp);
             Acc ea;
-            times<3, 3, 3, true>(ea, true, xp, g.mats, kMat, off_m);
+            times<3, 3, 3, true>(ea, true, true, xp, g.mats, kMat, off_m);
             ea.sum(du);
         }
         // D <- g_15 D + (g dy)^T R - (g beta du)^T K
@@ -396,9 +396,9 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
                     ldsm4(vq[c], db_a + c * PB + off);
                     ldsm4(uq[c], ub_a + c * PB + off);
                 }
-                times_at<KP, 3, 3, true>(ra, kk == 0, yq, so, SB);
-                times_at<PP, PP, PP, true>(ka, kk == 0, vq, so, SB);
-                times_at<PP, PP, PP, true>(da, kk == 0, uq, so + 3 * SB, SB);
+                times_at<KP, 3, 3, true>(ra, kk == 0, kk == 0, yq, so, SB);
+                times_at<PP, PP, PP, true>(ka, kk == 0, kk == 0, vq, so, SB);
+                times_at<PP, PP, PP, true>(da, kk == 0, kk == 0, uq, so + 3 * SB, SB);
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n)
@@ -458,13 +458,13 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         const bool diag = sb == tb;
         if (sb <= tb) {
             decays(true);
-            gram_at<N, PP, PP, PP, true>(x, db_a + xt, ub_a + ys, PB);
+            gram_at<N, PP, PP, PP, kChain<IO>, true>(x, db_a + xt, ub_a + ys, PB);
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)   // not the token's own
                     kq[n][i] = diag && lane / 4 + 8 * (i >> 1) == 8 * n + 2 * (lane % 4) + (i & 1) ? 0.f : -gm[n][i] * x[n][i];
-            gram_at<N, KP, 3, 3, true>(x, yb_a + xt, ub_a + ys, PB);
+            gram_at<N, KP, 3, 3, kChain<IO>, true>(x, yb_a + xt, ub_a + ys, PB);
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         }
         if (sb >= tb) {
             decays(false);
-            gram_at<N, PP, PP, PP, true>(x, ub_a + xt, db_a + ys, PB);
+            gram_at<N, PP, PP, PP, kChain<IO>, true>(x, ub_a + xt, db_a + ys, PB);
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
                     if (!diag) kq[n][i] = -gm[n][i] * x[n][i];
                     else if (!self) kq[n][i] -= gm[n][i] * x[n][i];
                 }
-            gram_at<N, PP, KP, PP, true>(x, ub_a + xt, yb_a + ys, PB);
+            gram_at<N, PP, KP, PP, kChain<IO>, true>(x, ub_a + xt, yb_a + ys, PB);
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -494,15 +494,15 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         for (int p = 0; p < NP; ++p) {
             const uint32_t so = buf_a + ko * ROWS16 + (at_t ^ ((i0 + p * 16) * 2));
             Acc acc;
-            times_at<PP, KP, PP, true>(acc, true, kq3, so, KB);
-            if (sb >= tb) times_at<PP, KP, PP, true>(acc, false, rq3, so + KP * KB, KB);
+            times_at<PP, KP, PP, true>(acc, true, true, kq3, so, KB);
+            if (sb >= tb) times_at<PP, KP, PP, true>(acc, false, false, rq3, so + KP * KB, KB);
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) dk[p][n][i] += acc.hi[n][i] + acc.lo[n][i];
             if (sb <= tb) {
                 Acc ra;
-                times_at<3, KP, 3, true>(ra, true, dq3, so, KB);
+                times_at<3, KP, 3, true>(ra, true, true, dq3, so, KB);
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
