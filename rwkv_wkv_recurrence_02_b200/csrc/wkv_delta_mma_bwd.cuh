@@ -354,6 +354,11 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         sums[ta + 1] = two_floats(x);
     }
 
+    // the inner products <D, S> at the segment's borders.  The one at its begin
+    // follows from the one at its end and the segment's terms, but in the first
+    // segment it is formed too: with an empty state it is zero, and not what
+    // rounding leaves of the terms.
+    float border[2] = {0.f, 0.f};
     // --- the products with S and D: C[t][i], tiles of 16 channels
     float dr[NP][2][4], dk[NP][2][4];
 #pragma unroll
@@ -370,11 +375,23 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     const int t_lo = tb * 16 + lane / 4;                  // this lane's rows: t_lo and t_lo + 8
 #pragma unroll 1
     for (int jb = 0; jb < N; jb += G::JB) {
-        constexpr int RB = G::JB / G::WARPS;
-        const auto rows_at = [&](int r, int c) { return place(warp * RB + r, c); };
+        constexpr int RB = G::JB / G::WARPS, U = RB * N / 128;   // lines and loads of a warp
+        float4 s[U], d[U], z[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = (jb + warp * RB) * N + (lane + u * 32) * 4;
+            s[u] = load4(s_seg + at, true);
+            d[u] = load4(d_seg + at, true);
+            z[u] = load4(s_seg + N * N + at, true);
+        }
         if (jb > 0) __syncthreads();
-        split_rows<RB, N, 3>(buf, rows_at, G::SPIECE, s_seg + (jb + warp * RB) * N, N, RB, true, lane);
-        split_rows<RB, N, PP>(buf + 3 * G::SPIECE, rows_at, G::SPIECE, d_seg + (jb + warp * RB) * N, N, RB, true, lane);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = lane + u * 32, at = place(warp * RB + i / (N / 4), i % (N / 4) * 4);
+            put4<3>(buf + at, G::SPIECE, s[u]);
+            put4<PP>(buf + 3 * G::SPIECE + at, G::SPIECE, d[u]);
+            border[1] += fmaf(d[u].x, z[u].x, d[u].y * z[u].y) + fmaf(d[u].z, z[u].z, d[u].w * z[u].w);
+        }
         if (KP == 1 && jb == 0) cp_async_wait();
         __syncthreads();
         float2 gq[2];   // of the lane's two rows: g, q
@@ -569,24 +586,20 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         own[q] += __shfl_xor_sync(0xffffffffu, own[q], 2);
         if (lane % 4 == 0) rdr[(warp / 4) * kSegment + t_lo + 8 * q] = own[q];
     }
-    // the inner product <D, S> at the segment's end; at its begin it follows from
-    // the segment's terms, but for the first segment, where it is formed too: with
-    // an empty state it is zero, and not what rounding leaves of the terms
-    float x[2] = {0.f, 0.f};
-#pragma unroll
-    for (int q = 1; q >= 0; --q) {
-        if (q == 0 && seg > 0) break;
-        const float4* ps = reinterpret_cast<const float4*>(s_seg + q * N * N);
-        const float4* pd = reinterpret_cast<const float4*>(d_seg + (q - 1) * N * N);
-#pragma unroll 8
+    if (seg == 0) {
+        const float4* ps = reinterpret_cast<const float4*>(s_seg);
+        const float4* pd = reinterpret_cast<const float4*>(d_seg - N * N);
+#pragma unroll 4
         for (int i = tid; i < N * N / 4; i += G::THREADS) {
             const float4 u = __ldcg(ps + i), v = __ldcg(pd + i);
-            x[q] = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, x[q]))));
+            border[0] = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, border[0]))));
         }
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) x[q] += __shfl_xor_sync(0xffffffffu, x[q], o);
     }
-    if (lane == 0) inner[2 * warp] = x[0], inner[2 * warp + 1] = x[1];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) border[q] += __shfl_xor_sync(0xffffffffu, border[q], o);
+    if (lane == 0) inner[2 * warp] = border[0], inner[2 * warp + 1] = border[1];
     __syncthreads();
     // --- dw: the sum <Dn, S> from the segment's end backwards
     if (warp == 0) {
