@@ -394,25 +394,32 @@ __device__ __forceinline__ void gram(float (&c)[2][4], const __nv_bfloat16* x, c
     gram_at<N, KX, KY, ORD, CHAIN, false>(c, smem_u32(x + b_trans(lane, LD)), smem_u32(y + b_plain(lane, LD)), piece * 2);
 }
 
-// acc (+)= A (16 x 16) B (16 x 16) of NA and NB pieces, orders below ORD.  B's
-// pieces lie `piece` bytes apart; addr: this lane's place in the first.
-template <int NA, int NB, int ORD, bool TRANS>
-__device__ __forceinline__ void times_at(Acc& acc, bool first, bool lo_first, const uint32_t (&a)[NA][4], uint32_t addr, int piece) {
+// acc (+)= A (16 x 16) B (16 x 16) of NA and NB pieces, orders below ORD
+template <int NA, int NB, int ORD>
+__device__ __forceinline__ void times_of(Acc& acc, bool first, bool lo_first, const uint32_t (&a)[NA][4], const uint32_t (&f)[NB][4]) {
 #pragma unroll
-    for (int p = 0; p < NB && p < ORD; ++p) {
-        uint32_t f[4];
-        if constexpr (TRANS) ldsm4t(f, addr + p * piece);
-        else ldsm4(f, addr + p * piece);
+    for (int p = 0; p < NB && p < ORD; ++p)
 #pragma unroll
         for (int i = 0; i < NA && i + p < ORD; ++i) {
             if (i + p == 0) {
-                mma2(acc.hi, a[i], f, first);
+                mma2(acc.hi, a[i], f[p], first);
             } else {
-                mma2(acc.lo, a[i], f, lo_first);
+                mma2(acc.lo, a[i], f[p], lo_first);
                 lo_first = false;
             }
         }
+}
+// B's pieces in shared memory, `piece` bytes apart; addr: this lane's place in the first
+template <int NA, int NB, int ORD, bool TRANS>
+__device__ __forceinline__ void times_at(Acc& acc, bool first, bool lo_first, const uint32_t (&a)[NA][4], uint32_t addr, int piece) {
+    constexpr int NF = NB < ORD ? NB : ORD;
+    uint32_t f[NF][4];
+#pragma unroll
+    for (int p = 0; p < NF; ++p) {
+        if constexpr (TRANS) ldsm4t(f[p], addr + p * piece);
+        else ldsm4(f[p], addr + p * piece);
     }
+    times_of<NA, NF, ORD>(acc, first, lo_first, a, f);
 }
 // the same of staged elements: pieces `piece` elements apart, off: this lane's
 // offset (b_plain, b_trans)

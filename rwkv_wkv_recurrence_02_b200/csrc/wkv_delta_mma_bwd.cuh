@@ -211,10 +211,9 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
 
 // ---------------------------------------------------------------------------
 // dr, dk, dbeta and dw of one segment.  A warp takes 16 tokens t and IC
-// channels i: the products with S and D, then the segment's 16 x 16 blocks of
-// (token, token) products, which turn from accumulators to A operands in
-// registers.  A row of blocks has 5 in all, those on the diagonal from both
-// sides, so the warps' work is even.
+// channels i: the products with S and D, then those with K and R of the
+// segment's 16 x 16 blocks of (token, token) products.  A block is formed once,
+// by one warp, and read from shared memory as it lies and transposed.
 // ---------------------------------------------------------------------------
 template <typename IO, int N>
 struct SegmentShape {
@@ -224,11 +223,10 @@ struct SegmentShape {
     static constexpr int PIECE = kSegment * N;                // rows without padding (Swizzled)
     static constexpr int JB = 32;                             // value lines of S and D at a time
     static constexpr int SPIECE = JB * N;
-    static constexpr int KR = KP == 3 && N == 128 ? 16 : 64;  // tokens of K and R at a time
-    static constexpr int KPIECE = KR * N;
-    // u, dv, dy; S and D, later K and R; the decays and the sums over channels
+    static constexpr int BLOCKS = 10, MATS = 3 + PP;          // blocks of token pairs on and below the diagonal, pieces of each
+    // u, dv, dy, later K and R; S and D, later the blocks; the decays and the sums over channels
     static constexpr int S_ROWS = (3 + PP + KP) * PIECE * 2;
-    static constexpr int A_ = (3 + PP) * SPIECE * 2, B_ = 2 * KP * KPIECE * 2, S_BUF = A_ > B_ ? A_ : B_;
+    static constexpr int A_ = (3 + PP) * SPIECE * 2, B_ = BLOCKS * MATS * kMat * 2, S_BUF = A_ > B_ ? A_ : B_;
     static constexpr int S_SUM = kSegment * (8 + 4 + 4 * HALVES) + WARPS * 8;
     static constexpr int SMEM = S_ROWS + S_BUF + S_SUM;
     // CTAs an SM by shared memory; registers follow
@@ -240,7 +238,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     using G = SegmentShape<IO, N>;
     constexpr int KP = G::KP, PP = G::PP, NP = G::IC / 16;
     constexpr Swizzled<N> place{};
-    extern __shared__ __align__(1024) char smem[];
+    extern __shared__ __align__(16) char smem[];
     __nv_bfloat16* ub = reinterpret_cast<__nv_bfloat16*>(smem);   // u = beta e
     __nv_bfloat16* db = ub + 3 * G::PIECE;                        // dv = beta du
     __nv_bfloat16* yb = db + PP * G::PIECE;
@@ -371,7 +369,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     const uint32_t at_t = place((lane & 7) + ((lane >> 3) & 1) * 8, (lane >> 4) * 8) * 2;
     const uint32_t at_p = place((lane & 7) + (lane >> 4) * 8, ((lane >> 3) & 1) * 8) * 2;
     const uint32_t ub_a = smem_u32(ub), db_a = smem_u32(db), yb_a = smem_u32(yb), buf_a = smem_u32(buf);
-    constexpr int PB = G::PIECE * 2, SB = G::SPIECE * 2, KB = G::KPIECE * 2, ROWS16 = 16 * N * 2;
+    constexpr int PB = G::PIECE * 2, SB = G::SPIECE * 2, ROWS16 = 16 * N * 2;
     const int t_lo = tb * 16 + lane / 4;                  // this lane's rows: t_lo and t_lo + 8
 #pragma unroll 1
     for (int jb = 0; jb < N; jb += G::JB) {
@@ -428,120 +426,110 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         }
     }
 
-    // --- the blocks of token pairs
-    __nv_bfloat16 *kb = buf, *rb = buf + KP * G::KPIECE;
-    auto stage_keys = [&](int s0) {   // K and R, tokens s0 .. s0 + KR
-        constexpr int RB = G::KR / G::WARPS > 0 ? G::KR / G::WARPS : 1;
-        const int r0 = warp * RB, l = nt - s0 - r0;
-        if (r0 >= G::KR) return;
-        const int64_t at = l > 0 ? s0 + r0 : 0;
-        const auto rows_at = [&](int r, int c) { return place(r0 + r, c); };
+    // --- the blocks of token pairs s <= t, with the decays between the tokens: dy_t.u_s, and
+    // -dv_t.u_s for s < t
+    __syncthreads();
+#pragma unroll 1
+    for (int blk = warp; blk < G::BLOCKS; blk += G::WARPS) {
+        const int bt = blk < 1 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, bs = blk - bt * (bt + 1) / 2;
+        __nv_bfloat16* m = buf + blk * G::MATS * kMat;
+        const uint32_t xt = bt * ROWS16 + at_t, ys = bs * ROWS16 + at_p;
+        float y[2][4], x[2][4];
+        gram_at<N, KP, 3, 3, kChain<IO>, true>(y, yb_a + xt, ub_a + ys, PB);
+        gram_at<N, PP, PP, PP, kChain<IO>, true>(x, db_a + xt, ub_a + ys, PB);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int t = lane / 4 + 8 * q, c = 8 * n + 2 * (lane % 4), far = bt > bs ? kChunk : 0;
+                const float2 wt = sums[bt * 16 + t], w0 = sums[bs * 16 + c], w1 = sums[bs * 16 + c + 1];
+                const float g0 = c <= t + far ? decay_of(wt, w0) : 0.f, g1 = c + 1 <= t + far ? decay_of(wt, w1) : 0.f;
+                put_pieces<3>(m, t, c, g0 * y[n][2 * q], g1 * y[n][2 * q + 1]);
+                put_pieces<PP>(m + 3 * kMat, t, c, c < t + far ? -g0 * x[n][2 * q] : 0.f,
+                               c + 1 < t + far ? -g1 * x[n][2 * q + 1] : 0.f);
+            }
+    }
+    __syncthreads();
+    // K and R over the rows that are done with
+    __nv_bfloat16 *kb = ub, *rb = ub + KP * G::PIECE;
+    {
+        const auto rows_at = [&](int r, int c) { return place(row + r, c); };
         if constexpr (KP == 1) {
-            copy_rows<IO, RB, N>(reinterpret_cast<IO*>(kb), rows_at, kp + at * ks, ks, l, a.vec, lane);
-            copy_rows<IO, RB, N>(reinterpret_cast<IO*>(rb), rows_at, rp + at * ks, ks, l, a.vec, lane);
+            copy_rows<IO, RW, N>(reinterpret_cast<IO*>(kb), rows_at, kp + rr * ks, ks, left, a.vec, lane);
+            copy_rows<IO, RW, N>(reinterpret_cast<IO*>(rb), rows_at, rp + rr * ks, ks, left, a.vec, lane);
             cp_async_commit();
             cp_async_wait();
         } else {
-            split_rows<RB, N, 3>(kb, rows_at, G::KPIECE, reinterpret_cast<const float*>(kp) + at * ks, ks, l, a.vec, lane);
-            split_rows<RB, N, 3>(rb, rows_at, G::KPIECE, reinterpret_cast<const float*>(rp) + at * ks, ks, l, a.vec, lane);
+            split_rows<RW, N, 3>(kb, rows_at, G::PIECE, reinterpret_cast<const float*>(kp) + rr * ks, ks, left, a.vec, lane);
+            split_rows<RW, N, 3>(rb, rows_at, G::PIECE, reinterpret_cast<const float*>(rp) + rr * ks, ks, left, a.vec, lane);
         }
-    };
-    float own[2] = {0.f, 0.f};   // r . dr of the lane's rows
+    }
+    __syncthreads();
+    // dr takes K by the rows of the blocks, dk K by rows and columns and R by columns
 #pragma unroll 1
     for (int sb = 0; sb < 4; ++sb) {
-        if (sb == 0 || G::KR == 16) {
-            __syncthreads();
-            stage_keys(sb * 16);
-            __syncthreads();
+        const bool low = sb <= tb, up = sb >= tb;
+        uint32_t dq[3][4], kq[PP][4], rq[PP][4], kt[PP][4];
+        if (low) {
+            const uint32_t m = buf_a + ((tb * (tb + 1) / 2 + sb) * G::MATS * kMat + m_trans(lane)) * 2;
+#pragma unroll
+            for (int c = 0; c < 3; ++c) ldsm4(dq[c], m + c * kMat * 2);
+#pragma unroll
+            for (int c = 0; c < PP; ++c) ldsm4(kq[c], m + (3 + c) * kMat * 2);
         }
-        const int ko = G::KR == 16 ? 0 : sb;   // the block's rows of K and R
-        const uint32_t xt = tb * ROWS16 + at_t, ys = sb * ROWS16 + at_p;
-        // with the decay between the tokens -- kq: -(dv_t.u_s below the diagonal, u_t.dv_s above), to K;
-        // rq: u_t.dy_s, to R; dq: dy_t.u_s, K to dr
-        float kq[2][4], x[2][4];
-        uint32_t dq3[3][4], rq3[PP][4], kq3[PP][4];
-        float gm[2][4];
-        auto decays = [&](bool lower) {
+        if (up) {
+            const uint32_t m = buf_a + ((sb * (sb + 1) / 2 + tb) * G::MATS * kMat + m_plain(lane)) * 2;
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int s = 8 * n + 2 * (lane % 4) + (i & 1), t = lane / 4 + 8 * (i >> 1);   // in their blocks
-                    const float2 ws = sums[sb * 16 + s], wt = sums[tb * 16 + t];
-                    gm[n][i] = lower ? decay_of(wt, ws) : decay_of(ws, wt);
-                    if (sb == tb && (lower ? s > t : s < t)) gm[n][i] = 0.f;
-                }
-        };
-        const bool diag = sb == tb;
-        if (sb <= tb) {
-            decays(true);
-            gram_at<N, PP, PP, PP, kChain<IO>, true>(x, db_a + xt, ub_a + ys, PB);
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)   // not the token's own
-                    kq[n][i] = diag && lane / 4 + 8 * (i >> 1) == 8 * n + 2 * (lane % 4) + (i & 1) ? 0.f : -gm[n][i] * x[n][i];
-            gram_at<N, KP, 3, 3, kChain<IO>, true>(x, yb_a + xt, ub_a + ys, PB);
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[n][i] *= gm[n][i];
-            split_a<3>(x[0], x[1], dq3);
+            for (int c = 0; c < PP; ++c) {
+                ldsm4t(rq[c], m + c * kMat * 2);
+                ldsm4t(kt[c], m + (3 + c) * kMat * 2);
+            }
         }
-        if (sb >= tb) {
-            decays(false);
-            gram_at<N, PP, PP, PP, kChain<IO>, true>(x, ub_a + xt, db_a + ys, PB);
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool self = lane / 4 + 8 * (i >> 1) == 8 * n + 2 * (lane % 4) + (i & 1);
-                    if (!diag) kq[n][i] = -gm[n][i] * x[n][i];
-                    else if (!self) kq[n][i] -= gm[n][i] * x[n][i];
-                }
-            gram_at<N, PP, KP, PP, kChain<IO>, true>(x, ub_a + xt, yb_a + ys, PB);
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[n][i] *= gm[n][i];
-            split_a<PP>(x[0], x[1], rq3);
-        }
-        split_a<PP>(kq[0], kq[1], kq3);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const uint32_t so = buf_a + ko * ROWS16 + (at_t ^ ((i0 + p * 16) * 2));
-            Acc acc;
-            times_at<PP, KP, PP, true>(acc, true, true, kq3, so, KB);
-            if (sb >= tb) times_at<PP, KP, PP, true>(acc, false, false, rq3, so + KP * KB, KB);
+            const uint32_t so = ub_a + sb * ROWS16 + (at_t ^ ((i0 + p * 16) * 2));
+            uint32_t fk[KP][4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dk[p][n][i] += acc.hi[n][i] + acc.lo[n][i];
-            if (sb <= tb) {
+            for (int c = 0; c < KP; ++c) ldsm4t(fk[c], so + c * PB);
+            Acc ka;
+            if (low) {
                 Acc ra;
-                times_at<3, KP, 3, true>(ra, true, true, dq3, so, KB);
+                times_of<3, KP, 3>(ra, true, true, dq, fk);
+                times_of<PP, KP, PP>(ka, true, true, kq, fk);
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) dr[p][n][i] += ra.hi[n][i] + ra.lo[n][i];
+                    for (int i = 0; i < 4; ++i) dr[p][n][i] += ra.hi[n][i] + ra.lo[n][i], dk[p][n][i] += ka.hi[n][i] + ka.lo[n][i];
             }
-            if (sb == tb) {   // dr of these channels is whole, and R's rows are the warp's own
+            if (up) {
+                uint32_t fr[KP][4];
+#pragma unroll
+                for (int c = 0; c < KP; ++c) ldsm4t(fr[c], so + (KP + c) * PB);
+                times_of<PP, KP, PP>(ka, true, true, kt, fk);
+                times_of<PP, KP, PP>(ka, false, false, rq, fr);
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const __nv_bfloat16* r2 = rb + place(ko * 16 + lane / 4 + 8 * q, i0 + p * 16 + 8 * n + 2 * (lane % 4));
-                        float x0 = 0.f, x1 = 0.f;
-#pragma unroll
-                        for (int c = KP - 1; c >= 0; --c) {
-                            const uint32_t w2 = *reinterpret_cast<const uint32_t*>(r2 + c * G::KPIECE);
-                            x0 += __uint_as_float(w2 << 16), x1 += __uint_as_float(w2 & 0xffff0000u);
-                        }
-                        own[q] = fmaf(x0, dr[p][n][2 * q], fmaf(x1, dr[p][n][2 * q + 1], own[q]));
-                    }
+                    for (int i = 0; i < 4; ++i) dk[p][n][i] += ka.hi[n][i] + ka.lo[n][i];
             }
         }
     }
+    float own[2] = {0.f, 0.f};   // r . dr of the lane's rows
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const __nv_bfloat16* r2 = rb + place(t_lo + 8 * q, i0 + p * 16 + 8 * n + 2 * (lane % 4));
+                float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+                for (int c = KP - 1; c >= 0; --c) {
+                    const uint32_t w2 = *reinterpret_cast<const uint32_t*>(r2 + c * G::PIECE);
+                    x0 += __uint_as_float(w2 << 16), x1 += __uint_as_float(w2 & 0xffff0000u);
+                }
+                own[q] = fmaf(x0, dr[p][n][2 * q], fmaf(x1, dr[p][n][2 * q + 1], own[q]));
+            }
     // --- the outputs
     const bool whole = a.H == a.Hk;
 #pragma unroll
