@@ -51,6 +51,16 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
 __device__ __forceinline__ void stsm2t(uint32_t addr, const uint32_t (&r)[2]) {
     asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1,%2};" :: "r"(addr), "r"(r[0]), "r"(r[1]) : "memory");
 }
+// a 16 x 16 accumulator as bfloat16, rows as they lie
+__device__ __forceinline__ void stsm_tile(uint32_t addr, const float (&c)[2][4]) {
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(c[i / 2][i % 2 * 2], c[i / 2][i % 2 * 2 + 1]);
+        r[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
 // c += A B, or c = A B
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -359,7 +369,10 @@ struct Acc {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[n][i] = first ? y[n][i] : x[n][i] + y[n][i];
+            for (int i = 0; i < 4; i += 2) {
+                const F2 v = first ? f2(y[n][i], y[n][i + 1]) : add2(f2(x[n][i], x[n][i + 1]), f2(y[n][i], y[n][i + 1]));
+                x[n][i] = f2lo(v), x[n][i + 1] = f2hi(v);
+            }
     }
 };
 // (16 tokens x N) (N x 16 tokens)^T of two staged arrays of KX and KY pieces
@@ -394,55 +407,48 @@ __device__ __forceinline__ void gram(float (&c)[2][4], const __nv_bfloat16* x, c
     gram_at<N, KX, KY, ORD, CHAIN, false>(c, smem_u32(x + b_trans(lane, LD)), smem_u32(y + b_plain(lane, LD)), piece * 2);
 }
 
-// acc (+)= A (16 x 16) B (16 x 16) of NA and NB pieces, orders below ORD
-template <int NA, int NB, int ORD>
-__device__ __forceinline__ void times_of(Acc& acc, bool first, bool lo_first, const uint32_t (&a)[NA][4], const uint32_t (&f)[NB][4]) {
-#pragma unroll
-    for (int p = 0; p < NB && p < ORD; ++p)
-#pragma unroll
-        for (int i = 0; i < NA && i + p < ORD; ++i) {
-            if (i + p == 0) {
-                mma2(acc.hi, a[i], f[p], first);
-            } else {
-                mma2(acc.lo, a[i], f[p], lo_first);
-                lo_first = false;
-            }
-        }
-}
-// B's pieces in shared memory, `piece` bytes apart; addr: this lane's place in the first
-template <int NA, int NB, int ORD, bool TRANS>
-__device__ __forceinline__ void times_at(Acc& acc, bool first, bool lo_first, const uint32_t (&a)[NA][4], uint32_t addr, int piece) {
-    constexpr int NF = NB < ORD ? NB : ORD;
-    uint32_t f[NF][4];
-#pragma unroll
-    for (int p = 0; p < NF; ++p) {
-        if constexpr (TRANS) ldsm4t(f[p], addr + p * piece);
-        else ldsm4(f[p], addr + p * piece);
-    }
-    times_of<NA, NF, ORD>(acc, first, lo_first, a, f);
-}
-// the same of staged elements: pieces `piece` elements apart, off: this lane's
-// offset (b_plain, b_trans)
+// acc (+)= A (16 x 16) B (16 x 16) of NA and NB pieces, orders below ORD.  B's
+// pieces lie `piece` elements apart, off: this lane's offset (b_plain, b_trans)
 template <int NA, int NB, int ORD, bool TRANS>
 __device__ __forceinline__ void times(Acc& acc, bool first, bool lo_first, const uint32_t (&a)[NA][4], const __nv_bfloat16* m,
                                       int piece, int off) {
-    times_at<NA, NB, ORD, TRANS>(acc, first, lo_first, a, smem_u32(m + off), piece * 2);
+    const uint32_t addr = smem_u32(m + off);
+#pragma unroll
+    for (int p = 0; p < NB && p < ORD; ++p) {
+        uint32_t f[4];
+        if constexpr (TRANS) ldsm4t(f, addr + p * piece * 2);
+        else ldsm4(f, addr + p * piece * 2);
+#pragma unroll
+        for (int i = 0; i < NA && i + p < ORD; ++i) {
+            mma2(i + p == 0 ? acc.hi : acc.lo, a[i], f, i + p == 0 ? first : lo_first);
+            if (i + p > 0) lo_first = false;
+        }
+    }
 }
 // d (+)= A B into one accumulator, smallest orders first
-template <int NA, int NB>
-__device__ __forceinline__ void times_add(float (&d)[2][4], bool first, const uint32_t (&a)[NA][4], const __nv_bfloat16* m,
-                                          int piece, int off) {
-    uint32_t f[NB][4];
+template <int NA, int NB, int ORD>
+__device__ __forceinline__ void times_sum(float (&d)[2][4], bool first, const uint32_t (&a)[NA][4], const uint32_t (&f)[NB][4]) {
 #pragma unroll
-    for (int p = 0; p < NB; ++p) ldsm4t(f[p], smem_u32(m + p * piece + off));
-#pragma unroll
-    for (int o = 2; o >= 0; --o)
+    for (int o = ORD - 1; o >= 0; --o)
 #pragma unroll
         for (int p = 0; p < NB && p <= o; ++p)
             if (o - p < NA) {
                 mma2(d, a[o - p], f[p], first);
                 first = false;
             }
+}
+template <int NA, int NB>
+__device__ __forceinline__ void times_add(float (&d)[2][4], bool first, const uint32_t (&a)[NA][4], const __nv_bfloat16* m,
+                                          int piece, int off) {
+    uint32_t f[NB][4];
+#pragma unroll
+    for (int p = 0; p < NB; ++p) ldsm4t(f[p], smem_u32(m + p * piece + off));
+    times_sum<NA, NB, 3>(d, first, a, f);
+}
+// (d0, d1) <- f (x0, x1) + (d0, d1)
+__device__ __forceinline__ void fma_pair(float& d0, float& d1, float f, float x0, float x1) {
+    const F2 v = fma2(f2s(f), f2(x0, x1), f2(d0, d1));
+    d0 = f2lo(v), d1 = f2hi(v);
 }
 // s <- f s + d
 __device__ __forceinline__ void fade_add(float (&s)[4], float f, const float (&d)[4]) {

@@ -218,20 +218,60 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
 template <typename IO, int N>
 struct SegmentShape {
     static constexpr int KP = sizeof(IO) == 2 ? 1 : 3, PP = kOutOrders<IO>;
-    static constexpr int IC = N < 64 ? N : 64, HALVES = N / IC;
-    static constexpr int WARPS = 4 * HALVES, THREADS = 32 * WARPS;
+    static constexpr int IC = 32, PARTS = N / IC;
+    static constexpr int WARPS = 4 * PARTS, THREADS = 32 * WARPS;
     static constexpr int PIECE = kSegment * N;                // rows without padding (Swizzled)
     static constexpr int JB = 32;                             // value lines of S and D at a time
     static constexpr int SPIECE = JB * N;
     static constexpr int BLOCKS = 10, MATS = 3 + PP;          // blocks of token pairs on and below the diagonal, pieces of each
-    // u, dv, dy, later K and R; S and D, later the blocks; the decays and the sums over channels
+    // u, dv, dy; S and D, later the blocks; K and R (float32's over the rows when
+    // those are done with); the decays and the sums over channels
     static constexpr int S_ROWS = (3 + PP + KP) * PIECE * 2;
     static constexpr int A_ = (3 + PP) * SPIECE * 2, B_ = BLOCKS * MATS * kMat * 2, S_BUF = A_ > B_ ? A_ : B_;
-    static constexpr int S_SUM = kSegment * (8 + 4 + 4 * HALVES) + WARPS * 8;
-    static constexpr int SMEM = S_ROWS + S_BUF + S_SUM;
+    static constexpr int S_KEYS = KP == 1 ? 2 * PIECE * 2 : 0;
+    static constexpr int S_SUM = kSegment * (8 + 4 + 4 * PARTS) + WARPS * 8;
+    static constexpr int SMEM = S_ROWS + S_BUF + S_KEYS + S_SUM;
     // CTAs an SM by shared memory; registers follow
     static constexpr int CTAS = 227 * 1024 / (SMEM + 1024) > 3 ? 3 : 227 * 1024 / (SMEM + 1024);
 };
+
+// d[p] += f (A B), f0 and f1 the factors of the lane's two rows: A 16 tokens and
+// 32 columns (NA pieces from a_at on, `ap` bytes apart; col: the lane's place in
+// them), B 32 lines (NB pieces from b_at on, `bp` apart; ch: its place in channels)
+template <int N, int NA, int NB, int ORD, int NP>
+__device__ __forceinline__ void add_lines(float (&d)[NP][2][4], float f0, float f1, uint32_t a_at, int ap, uint32_t col,
+                                          uint32_t b_at, int bp, uint32_t ch) {
+    uint32_t a[2][NA][4];
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int c = 0; c < NA; ++c) ldsm4(a[kk][c], a_at + (col ^ (kk * 32)) + c * ap);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        float x[2][4];
+        bool first = true;
+        uint32_t b[2][NB][4];
+#pragma unroll
+        for (int c = NB - 1; c >= 0; --c)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) ldsm4t(b[kk][c], b_at + (ch ^ (p * 32)) + kk * (16 * N * 2) + c * bp);
+#pragma unroll
+        for (int o = ORD - 1; o >= 0; --o)   // smallest orders first
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int c = 0; c < NA && c <= o; ++c)
+                    if (o - c < NB) {
+                        mma2(x, a[kk][c], b[kk][o - c], first);
+                        first = false;
+                    }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            fma_pair(d[p][n][0], d[p][n][1], f0, x[n][0], x[n][1]);
+            fma_pair(d[p][n][2], d[p][n][3], f1, x[n][2], x[n][3]);
+        }
+    }
+}
 
 template <typename IO, int N>
 __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO, N>::CTAS) delta_segment_kernel(const Args a) {
@@ -243,10 +283,12 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     __nv_bfloat16* db = ub + 3 * G::PIECE;                        // dv = beta du
     __nv_bfloat16* yb = db + PP * G::PIECE;
     __nv_bfloat16* buf = reinterpret_cast<__nv_bfloat16*>(smem + G::S_ROWS);
-    float2* sums = reinterpret_cast<float2*>(smem + G::S_ROWS + G::S_BUF);
+    __nv_bfloat16* kb = KP == 1 ? reinterpret_cast<__nv_bfloat16*>(smem + G::S_ROWS + G::S_BUF) : ub;
+    __nv_bfloat16* rb = kb + KP * G::PIECE;
+    float2* sums = reinterpret_cast<float2*>(smem + G::S_ROWS + G::S_BUF + G::S_KEYS);
     float* dvv = reinterpret_cast<float*>(sums + kSegment);       // dv . v of a token
-    float* rdr = dvv + kSegment;                                  // r . dr, by halves of the channels
-    float* inner = rdr + kSegment * G::HALVES;                    // <D, S> at the borders, by warps
+    float* rdr = dvv + kSegment;                                  // r . dr, by parts of the channels
+    float* inner = rdr + kSegment * G::PARTS;                    // <D, S> at the borders, by warps
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int tb = warp % 4, i0 = warp / 4 * G::IC;
 
@@ -266,25 +308,33 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     const float* d_seg = a.d_seg + (head * (nseg + 1) + seg + 1) * N * N;
     const IO* kp = static_cast<const IO*>(a.k) + keys;
     const IO* rp = static_cast<const IO*>(a.r) + keys;
-    for (int i = tid; i < N * N / 32; i += G::THREADS) {
+    for (int i = G::JB * N / 32 + tid; i < N * N / 32; i += G::THREADS) {
         prefetch_l2(s_seg + i * 32);
         prefetch_l2(s_seg + N * N + i * 32);
         prefetch_l2(d_seg + i * 32);
     }
-    constexpr int KL = N * int(sizeof(IO)) / 64;   // 64-byte pieces of a row: rows need not begin a line
-    for (int i = tid; i < nt * KL; i += G::THREADS) {
-        const int64_t at = (i / KL) * ks + (i % KL) * (64 / int(sizeof(IO)));
-        prefetch_l2(kp + at);
-        prefetch_l2(rp + at);
-    }
+    constexpr int LW = G::JB / G::WARPS, LU = LW * N / 128;   // lines of S and D of a warp, and its loads
+    float4 ls[LU], ld[LU], le[LU];                            // S, D, S at the segment's end
+    const auto load_lines_at = [&](int jb) {
+#pragma unroll
+        for (int u = 0; u < LU; ++u) {
+            const int at = (jb + warp * LW) * N + (lane + u * 32) * 4;
+            ls[u] = load4(s_seg + at, true);
+            ld[u] = load4(d_seg + at, true);
+            le[u] = load4(s_seg + N * N + at, true);
+        }
+    };
+    load_lines_at(0);
 
-    // --- the segment's rows: 16 / HALVES a warp
-    constexpr int RW = 16 / G::HALVES;
+    // --- the segment's rows: 16 / PARTS a warp
+    constexpr int RW = 16 / G::PARTS;
     const int row = warp * RW, left = nt - row;
     const int64_t rr = left > 0 ? row : 0;   // rows behind the last token: zeros, addressed at one that exists
+    const auto rows_at = [&](int r, int c) { return place(row + r, c); };
     if constexpr (KP == 1) {
-        copy_rows<IO, RW, N>(reinterpret_cast<IO*>(yb) + row * N, place, static_cast<const IO*>(a.dy) + rows + rr * vs, vs, left, a.vec,
-                             lane);
+        copy_rows<IO, RW, N>(reinterpret_cast<IO*>(yb), rows_at, static_cast<const IO*>(a.dy) + rows + rr * vs, vs, left, a.vec, lane);
+        copy_rows<IO, RW, N>(reinterpret_cast<IO*>(kb), rows_at, kp + rr * ks, ks, left, a.vec, lane);
+        copy_rows<IO, RW, N>(reinterpret_cast<IO*>(rb), rows_at, rp + rr * ks, ks, left, a.vec, lane);
         cp_async_commit();
     }
     {
@@ -337,7 +387,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         }
     }
     if constexpr (KP == 3)
-        split_rows<RW, N, 3>(yb + row * N, place, G::PIECE, reinterpret_cast<const float*>(a.dy) + rows + rr * vs, vs, left, a.vec, lane);
+        split_rows<RW, N, 3>(yb, rows_at, G::PIECE, reinterpret_cast<const float*>(a.dy) + rows + rr * vs, vs, left, a.vec, lane);
     if (warp == 0) {   // the decays' running sum, two tokens a lane
         const int ta = 2 * lane;
         const float w0 = ta < nt ? a.w[scalar + ta * a.H] : 0.f, w1 = ta + 1 < nt ? a.w[scalar + (ta + 1) * a.H] : 0.f;
@@ -368,104 +418,77 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     // this lane's places (bytes): as an A operand or a transposed B, and as a plain B; the columns' by exclusive or
     const uint32_t at_t = place((lane & 7) + ((lane >> 3) & 1) * 8, (lane >> 4) * 8) * 2;
     const uint32_t at_p = place((lane & 7) + (lane >> 4) * 8, ((lane >> 3) & 1) * 8) * 2;
-    const uint32_t ub_a = smem_u32(ub), db_a = smem_u32(db), yb_a = smem_u32(yb), buf_a = smem_u32(buf);
     constexpr int PB = G::PIECE * 2, SB = G::SPIECE * 2, ROWS16 = 16 * N * 2;
+    const uint32_t ub_a = smem_u32(ub), db_a = ub_a + 3 * PB, yb_a = db_a + PP * PB, buf_a = ub_a + G::S_ROWS,
+                   kb_a = KP == 1 ? buf_a + G::S_BUF : ub_a;
+    const uint32_t own_a = ub_a + tb * ROWS16, at_i = at_t ^ (i0 * 2);   // the warp's tokens, its channels
     const int t_lo = tb * 16 + lane / 4;                  // this lane's rows: t_lo and t_lo + 8
+    float2 gq[2];   // of the lane's two rows: g, q
 #pragma unroll 1
     for (int jb = 0; jb < N; jb += G::JB) {
-        constexpr int RB = G::JB / G::WARPS, U = RB * N / 128;   // lines and loads of a warp
-        float4 s[U], d[U], z[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int at = (jb + warp * RB) * N + (lane + u * 32) * 4;
-            s[u] = load4(s_seg + at, true);
-            d[u] = load4(d_seg + at, true);
-            z[u] = load4(s_seg + N * N + at, true);
-        }
         if (jb > 0) __syncthreads();
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = lane + u * 32, at = place(warp * RB + i / (N / 4), i % (N / 4) * 4);
-            put4<3>(buf + at, G::SPIECE, s[u]);
-            put4<PP>(buf + 3 * G::SPIECE + at, G::SPIECE, d[u]);
-            border[1] += fmaf(d[u].x, z[u].x, d[u].y * z[u].y) + fmaf(d[u].z, z[u].z, d[u].w * z[u].w);
+        for (int u = 0; u < LU; ++u) {
+            const int i = lane + u * 32, at = place(warp * LW + i / (N / 4), i % (N / 4) * 4);
+            put4<3>(buf + at, G::SPIECE, ls[u]);
+            put4<PP>(buf + 3 * G::SPIECE + at, G::SPIECE, ld[u]);
+            border[1] += fmaf(ld[u].x, le[u].x, ld[u].y * le[u].y) + fmaf(ld[u].z, le[u].z, ld[u].w * le[u].w);
         }
         if (KP == 1 && jb == 0) cp_async_wait();
         __syncthreads();
-        float2 gq[2];   // of the lane's two rows: g, q
+        if (jb + G::JB < N) load_lines_at(jb + G::JB);
+        if (jb == 0) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-            gq[q] = make_float2(decay_of(sums[t_lo + 8 * q], make_float2(0.f, 0.f)), decay_of(sums[kSegment - 1], sums[t_lo + 8 * q]));
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            Acc ra, ka, da;
-#pragma unroll
-            for (int kk = 0; kk < G::JB / 16; ++kk) {
-                const uint32_t off = tb * ROWS16 + (at_t ^ ((jb + kk * 16) * 2));
-                const uint32_t so = buf_a + kk * ROWS16 + (at_t ^ ((i0 + p * 16) * 2));
-                uint32_t yq[KP][4], vq[PP][4], uq[PP][4];
-#pragma unroll
-                for (int c = 0; c < KP; ++c) ldsm4(yq[c], yb_a + c * PB + off);
-#pragma unroll
-                for (int c = 0; c < PP; ++c) {
-                    ldsm4(vq[c], db_a + c * PB + off);
-                    ldsm4(uq[c], ub_a + c * PB + off);
-                }
-                times_at<KP, 3, 3, true>(ra, kk == 0, kk == 0, yq, so, SB);
-                times_at<PP, PP, PP, true>(ka, kk == 0, kk == 0, vq, so, SB);
-                times_at<PP, PP, PP, true>(da, kk == 0, kk == 0, uq, so + 3 * SB, SB);
-            }
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = gq[i >> 1];
-                    dr[p][n][i] = fmaf(f.x, ra.hi[n][i] + ra.lo[n][i], dr[p][n][i]);
-                    dk[p][n][i] = fmaf(f.y, da.hi[n][i] + da.lo[n][i], fmaf(-f.x, ka.hi[n][i] + ka.lo[n][i], dk[p][n][i]));
-                }
+            for (int q = 0; q < 2; ++q)
+                gq[q] = make_float2(decay_of(sums[t_lo + 8 * q], make_float2(0.f, 0.f)), decay_of(sums[kSegment - 1], sums[t_lo + 8 * q]));
         }
+        const uint32_t col = at_t ^ (jb * 2);
+        add_lines<N, KP, 3, 3>(dr, gq[0].x, gq[1].x, own_a + (3 + PP) * PB, PB, col, buf_a, SB, at_i);
+        add_lines<N, PP, PP, PP>(dk, -gq[0].x, -gq[1].x, own_a + 3 * PB, PB, col, buf_a, SB, at_i);
+        add_lines<N, PP, PP, PP>(dk, gq[0].y, gq[1].y, own_a, PB, col, buf_a + 3 * SB, SB, at_i);
     }
 
     // --- the blocks of token pairs s <= t, with the decays between the tokens: dy_t.u_s, and
     // -dv_t.u_s for s < t
     __syncthreads();
 #pragma unroll 1
-    for (int blk = warp; blk < G::BLOCKS; blk += G::WARPS) {
-        const int bt = blk < 1 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, bs = blk - bt * (bt + 1) / 2;
-        __nv_bfloat16* m = buf + blk * G::MATS * kMat;
-        const uint32_t xt = bt * ROWS16 + at_t, ys = bs * ROWS16 + at_p;
-        float y[2][4], x[2][4];
-        gram_at<N, KP, 3, 3, kChain<IO>, true>(y, yb_a + xt, ub_a + ys, PB);
-        gram_at<N, PP, PP, PP, kChain<IO>, true>(x, db_a + xt, ub_a + ys, PB);
+    for (int task = warp; task < 2 * G::BLOCKS; task += G::WARPS) {
+        const int blk = task >> 1, bt = blk < 1 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, bs = blk - bt * (bt + 1) / 2;
+        const bool ofv = task & 1;
+        __nv_bfloat16* m = buf + (blk * G::MATS + (ofv ? 3 : 0)) * kMat;
+        const uint32_t xt = bt * ROWS16 + at_t, ys = ub_a + bs * ROWS16 + at_p;
+        const int far = (bt > bs ? kChunk : 0) - ofv;   // s <= t + far
+        float x[2][4];
+        if (ofv) gram_at<N, PP, PP, PP, kChain<IO>, true>(x, db_a + xt, ys, PB);
+        else gram_at<N, KP, 3, 3, kChain<IO>, true>(x, yb_a + xt, ys, PB);
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int t = lane / 4 + 8 * q, c = 8 * n + 2 * (lane % 4), far = bt > bs ? kChunk : 0;
+                const int t = lane / 4 + 8 * q, c = 8 * n + 2 * (lane % 4);
                 const float2 wt = sums[bt * 16 + t], w0 = sums[bs * 16 + c], w1 = sums[bs * 16 + c + 1];
-                const float g0 = c <= t + far ? decay_of(wt, w0) : 0.f, g1 = c + 1 <= t + far ? decay_of(wt, w1) : 0.f;
-                put_pieces<3>(m, t, c, g0 * y[n][2 * q], g1 * y[n][2 * q + 1]);
-                put_pieces<PP>(m + 3 * kMat, t, c, c < t + far ? -g0 * x[n][2 * q] : 0.f,
-                               c + 1 < t + far ? -g1 * x[n][2 * q + 1] : 0.f);
+                const float y0 = c <= t + far ? decay_of(wt, w0) * x[n][2 * q] : 0.f;
+                const float y1 = c + 1 <= t + far ? decay_of(wt, w1) * x[n][2 * q + 1] : 0.f;
+                if (ofv) put_pieces<PP>(m, t, c, -y0, -y1);
+                else put_pieces<3>(m, t, c, y0, y1);
             }
     }
     __syncthreads();
-    // K and R over the rows that are done with
-    __nv_bfloat16 *kb = ub, *rb = ub + KP * G::PIECE;
-    {
-        const auto rows_at = [&](int r, int c) { return place(row + r, c); };
-        if constexpr (KP == 1) {
-            copy_rows<IO, RW, N>(reinterpret_cast<IO*>(kb), rows_at, kp + rr * ks, ks, left, a.vec, lane);
-            copy_rows<IO, RW, N>(reinterpret_cast<IO*>(rb), rows_at, rp + rr * ks, ks, left, a.vec, lane);
-            cp_async_commit();
-            cp_async_wait();
-        } else {
-            split_rows<RW, N, 3>(kb, rows_at, G::PIECE, reinterpret_cast<const float*>(kp) + rr * ks, ks, left, a.vec, lane);
-            split_rows<RW, N, 3>(rb, rows_at, G::PIECE, reinterpret_cast<const float*>(rp) + rr * ks, ks, left, a.vec, lane);
-        }
+    if constexpr (KP == 3) {   // K and R over the rows
+        split_rows<RW, N, 3>(kb, rows_at, G::PIECE, reinterpret_cast<const float*>(kp) + rr * ks, ks, left, a.vec, lane);
+        split_rows<RW, N, 3>(rb, rows_at, G::PIECE, reinterpret_cast<const float*>(rp) + rr * ks, ks, left, a.vec, lane);
+        __syncthreads();
     }
-    __syncthreads();
     // dr takes K by the rows of the blocks, dk K by rows and columns and R by columns
+    const auto times_dk = [&](float (&d)[2][4], const uint32_t (&a)[PP][4], const uint32_t (&f)[KP][4]) {
+        if constexpr (KP == 1) {   // a bfloat16 output: into its sum at once
+            times_sum<PP, KP, PP>(d, false, a, f);
+        } else {
+            float x[2][4];
+            times_sum<PP, KP, PP>(x, true, a, f);
+            Acc::add(d, x, false);
+        }
+    };
 #pragma unroll 1
     for (int sb = 0; sb < 4; ++sb) {
         const bool low = sb <= tb, up = sb >= tb;
@@ -487,30 +510,22 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const uint32_t so = ub_a + sb * ROWS16 + (at_t ^ ((i0 + p * 16) * 2));
+            const uint32_t so = kb_a + sb * ROWS16 + (at_t ^ ((i0 + p * 16) * 2));
             uint32_t fk[KP][4];
 #pragma unroll
             for (int c = 0; c < KP; ++c) ldsm4t(fk[c], so + c * PB);
-            Acc ka;
+            float x[2][4];
             if (low) {
-                Acc ra;
-                times_of<3, KP, 3>(ra, true, true, dq, fk);
-                times_of<PP, KP, PP>(ka, true, true, kq, fk);
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) dr[p][n][i] += ra.hi[n][i] + ra.lo[n][i], dk[p][n][i] += ka.hi[n][i] + ka.lo[n][i];
+                times_sum<3, KP, 3>(x, true, dq, fk);
+                Acc::add(dr[p], x, false);
+                times_dk(dk[p], kq, fk);
             }
             if (up) {
                 uint32_t fr[KP][4];
 #pragma unroll
                 for (int c = 0; c < KP; ++c) ldsm4t(fr[c], so + (KP + c) * PB);
-                times_of<PP, KP, PP>(ka, true, true, kt, fk);
-                times_of<PP, KP, PP>(ka, false, false, rq, fr);
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) dk[p][n][i] += ka.hi[n][i] + ka.lo[n][i];
+                times_dk(dk[p], kt, fk);
+                times_dk(dk[p], rq, fr);
             }
         }
     }
@@ -532,12 +547,12 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
             }
     // --- the outputs
     const bool whole = a.H == a.Hk;
+    if (!whole || KP == 3) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int t = t_lo + 8 * q;
-        if (t >= nt) continue;
-        const int64_t at = rows + t * vs + i0 + 2 * (lane % 4);
-        if (!whole || KP == 3) {
+        for (int q = 0; q < 2; ++q) {
+            const int t = t_lo + 8 * q;
+            if (t >= nt) continue;
+            const int64_t at = rows + t * vs + i0 + 2 * (lane % 4);
             float* orr = (whole ? static_cast<float*>(a.dr) : a.drh) + at;
             float* ok = (whole ? static_cast<float*>(a.dk) : a.dkh) + at;
             const bool pairs = !whole || a.vec;
@@ -552,19 +567,30 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
                     ok[8 * c] = y[0], ok[8 * c + 1] = y[1];
                 }
             }
-        } else {
-            IO* orr = static_cast<IO*>(a.dr) + at;
-            IO* ok = static_cast<IO*>(a.dk) + at;
+        }
+    } else if constexpr (KP == 1) {   // through rows of the warp's own (where u was) to 16-byte stores
+        constexpr int LD = G::IC + 8;
+        __nv_bfloat16* tile = ub + warp * 2 * 16 * LD;
+        const uint32_t to = smem_u32(tile + ((lane & 7) + ((lane >> 3) & 1) * 8) * LD + (lane >> 4) * 8);
 #pragma unroll
-            for (int c = 0; c < 2 * NP; ++c) {
-                const float *x = &dr[c / 2][c % 2][2 * q], *y = &dk[c / 2][c % 2][2 * q];
-                if (a.vec) {
-                    *reinterpret_cast<__nv_bfloat162*>(orr + 8 * c) = __floats2bfloat162_rn(x[0], x[1]);
-                    *reinterpret_cast<__nv_bfloat162*>(ok + 8 * c) = __floats2bfloat162_rn(y[0], y[1]);
-                } else {
-                    put(orr + 8 * c, x[0]), put(orr + 8 * c + 1, x[1]);
-                    put(ok + 8 * c, y[0]), put(ok + 8 * c + 1, y[1]);
-                }
+        for (int p = 0; p < NP; ++p) {
+            stsm_tile(to + p * 32, dr[p]);
+            stsm_tile(to + (16 * LD + p * 16) * 2, dk[p]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int t = n % 2 * 8 + lane / 4, c = lane % 4 * 8;
+            const uint4 v = *reinterpret_cast<const uint4*>(tile + (n / 2 * 16 + t) * LD + c);
+            if (tb * 16 + t >= nt) continue;
+            IO* o = static_cast<IO*>(n < 2 ? a.dr : a.dk) + rows + (tb * 16 + t) * vs + i0 + c;
+            if (a.vec) {
+                *reinterpret_cast<uint4*>(o) = v;
+            } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    reinterpret_cast<unsigned short*>(o)[i] = static_cast<unsigned short>(w[i / 2] >> (16 * (i & 1)));
             }
         }
     }
@@ -600,7 +626,8 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         for (int q = 0; q < 2; ++q) {
             const int t = ta + q;
             float x = rdr[t];
-            if constexpr (G::HALVES == 2) x += rdr[kSegment + t];
+#pragma unroll
+            for (int p = 1; p < G::PARTS; ++p) x += rdr[p * kSegment + t];
             term[q] = t < nt ? x - dvv[t] : 0.f;
         }
         float x = term[0] + term[1];   // suffix sums over the lanes
