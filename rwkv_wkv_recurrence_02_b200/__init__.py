@@ -630,21 +630,25 @@ def wkv_delta_backward(w, beta, r, k, v, H, state_in=None, *, dy, dstate_out=Non
     keys, values, scalars, states = (B, T, Hk * N), (B, T, H * N), (B, T, H), (B, H, N, N)
     _need(r, "r", keys, dt, dev)
     _need(k, "k", keys, dt, dev)
-    for t, name in ((v, "v"), (dy, "dy"), (dv, "dv")):
-        _need(t, name, values, dt, dev)
-    for t, name in ((w, "w"), (beta, "beta"), (dw, "dw"), (dbeta, "dbeta")):
-        _need(t, name, scalars, f32, dev)
-    for t, name in ((state_in, "state_in"), (dstate_out, "dstate_out"), (dstate_in, "dstate_in")):
-        _need(t, name, states, f32, dev)
-    _need(dr, "dr", keys, dt, dev)
-    _need(dk, "dk", keys, dt, dev)
-    dr = torch.empty_like(k) if dr is None else dr
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    dw = torch.empty_like(w) if dw is None else dw
-    dbeta = torch.empty_like(w) if dbeta is None else dbeta
-    if dstate_in is None and want_dstate_in:
-        dstate_in = torch.empty(states, dtype=f32, device=dev)
+    _need(v, "v", values, dt, dev)
+    _need(dy, "dy", values, dt, dev)
+    _need(w, "w", scalars, f32, dev)
+    _need(beta, "beta", scalars, f32, dev)
+    _need(state_in, "state_in", states, f32, dev)
+    _need(dstate_out, "dstate_out", states, f32, dev)
+
+    def out(t, name, shape, dtype, like):
+        if t is None:
+            return torch.empty_like(like)
+        _need(t, name, shape, dtype, dev)
+        return t
+
+    dr, dk, dv = out(dr, "dr", keys, dt, k), out(dk, "dk", keys, dt, k), out(dv, "dv", values, dt, v)
+    dw, dbeta = out(dw, "dw", scalars, f32, w), out(dbeta, "dbeta", scalars, f32, w)
+    if dstate_in is not None:
+        _need(dstate_in, "dstate_in", states, f32, dev)
+    elif want_dstate_in:
+        dstate_in = torch.empty(states, dtype=f32, device=dev) if state_in is None else torch.empty_like(state_in)
     nbytes = int(lib().wkv_delta_backward_workspace_bytes(B, T, Hk, H, N))
     ws_ptr, ws_bytes, owner = _scratch(nbytes, workspace, dev, stream)
     _launch(dev, "wkv_delta_backward", lib().wkv_delta_backward, B, T, Hk, H, N, code, _ptr(w), _ptr(beta), _ptr(r), _ptr(k),
