@@ -513,11 +513,18 @@ int wkv_token_shift(int64_t B, int64_t T, int64_t C, int dtype, int nmix,
  *                bytes (0 where none is of use), or NULL.  With it, more heads
  *                than the GPU holds at once are walked in parts of the tokens,
  *                so that the last wave of heads does not leave it mostly idle;
- *                the results are the same bits.  It needs no initialisation and
- *                holds nothing between calls; one that is too small is not
- *                touched.  A part waits for the one before it, at most the
- *                library's wait limit: then what follows is NaN and
- *                wkv_workspace_status() returns WKV_ERR_TIMEOUT.
+ *                the results are the same bits.  It holds nothing between
+ *                calls; one that is too small is not touched.  A part waits
+ *                for the one before it, at most the library's wait limit:
+ *                then that part of the sequence and all that follow are NaN
+ *                and wkv_workspace_status() returns WKV_ERR_TIMEOUT.
+ *
+ * Workspaces of wkv_delta_* and wkv_group_norm_backward need no
+ * initialisation, but of the first 256 bytes (wkv_workspace_init once) where
+ * wkv_workspace_status() is to be asked: calls leave those as they are until
+ * there is an error.  The rest holds anything after a call: wkv_forward,
+ * wkv_state and wkv_backward may take such a workspace only after another
+ * wkv_workspace_init of it.  Calls that share one must be ordered on the GPU.
  */
 int wkv_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int dtype,
                       const float* w, const float* beta, const void* r, const void* k, const void* v,
@@ -541,8 +548,8 @@ int wkv_delta_step(int64_t L, int64_t B, int64_t Hk, int64_t H, int64_t N, int d
  * value heads that share a key head; dw, dbeta (B,T,H) float32; dstate_in
  * (B,H,N,N) float32 or NULL.  dw is 0 where e^{-w} is 0.  No output may
  * overlap an input, another output or the workspace.  The workspace (256-byte
- * aligned, no initialisation, wkv_delta_backward_workspace_bytes() bytes)
- * holds nothing between calls; its walks go in parts as the forward's do.  T == 0: dstate_in = dstate_out (zeros if
+ * aligned, wkv_delta_backward_workspace_bytes() bytes) is as above; the walks
+ * go in parts as the forward's do.  T == 0: dstate_in = dstate_out (zeros if
  * NULL), nothing else is written.  WKV_ERR_WORKSPACE: NULL or too small.
  */
 size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N);
@@ -574,8 +581,8 @@ int wkv_group_norm(int64_t rows, int64_t C, int64_t G, int dtype, int act, float
  * wkv_group_norm_backward -- gradients of wkv_group_norm given dy (rows, C):
  * dx (and dgate, exactly when gate is given) in dtype, dweight and dbias (C,)
  * float32 sums over the rows in a fixed order, each NULL if not wanted.  The
- * workspace (256-byte aligned, uninitialised, _workspace_bytes()) is needed
- * for dweight or dbias only.  No output may overlap anything else.
+ * workspace (256-byte aligned, _workspace_bytes(), as wkv_delta_forward's) is
+ * needed for dweight or dbias only.  No output may overlap anything else.
  */
 size_t wkv_group_norm_backward_workspace_bytes(int64_t rows, int64_t C, int64_t G, int dtype);
 int wkv_group_norm_backward(int64_t rows, int64_t C, int64_t G, int dtype, int act, float eps,

@@ -178,36 +178,56 @@ class Workspace:
 
     Zeroed once per allocation (wkv_workspace_init); afterwards calls reuse it
     without clearing.  Calls that share one Workspace must be ordered on the
-    GPU (the default: the current stream)."""
+    GPU (the default: the current stream).  The delta rule's and the group
+    norm's calls have a buffer of their own in it, whose contents mean nothing
+    between calls."""
 
     def __init__(self, device=None):
         self.device = device
         self.buf = None
+        self.plain = None
 
     def get(self, nbytes: int, stream=None):
-        torch = _torch()
         if nbytes == 0:
             return None, 0
-        if self.buf is None or self.buf.numel() < nbytes:
-            dev = self.device if self.device is not None else torch.device("cuda", torch.cuda.current_device())
-            self.buf = torch.empty(int(nbytes) + 256, dtype=torch.uint8, device=dev)
-            _check(lib().wkv_workspace_init(self._aligned_ptr(), self.buf.numel() - 256, _stream_ptr(stream, self.buf.device)),
-                   "wkv_workspace_init")
-        return self._aligned_ptr(), self.buf.numel() - 256
+        if self.buf is None or self.buf.numel() - 256 < nbytes:
+            self.buf = self._new(nbytes)
+            self._init(self.buf, self.buf.numel() - 256, stream)
+        return self._aligned_ptr(self.buf), self.buf.numel() - 256
 
-    def _aligned_ptr(self):
-        p = self.buf.data_ptr()
-        return (p + 255) & ~255
+    def scratch(self, nbytes: int, stream=None, device=None):
+        """The other buffer: only its header (the error word) is cleared."""
+        if self.plain is None or self.plain.numel() - 256 < nbytes:
+            self.plain = self._new(nbytes, device)
+            self._init(self.plain, 256, stream)
+        return self._aligned_ptr(self.plain), self.plain.numel() - 256
+
+    def _new(self, nbytes, device=None):
+        torch = _torch()
+        dev = self.device or device or torch.device("cuda", torch.cuda.current_device())
+        return torch.empty(int(nbytes) + 256, dtype=torch.uint8, device=dev)
+
+    def _init(self, buf, nbytes, stream):
+        _launch(buf.device, "wkv_workspace_init", lib().wkv_workspace_init, self._aligned_ptr(buf), nbytes,
+                _stream_ptr(stream, buf.device))
+
+    @staticmethod
+    def _aligned_ptr(buf):
+        return (buf.data_ptr() + 255) & ~255
 
     def status(self, stream=None) -> int:
-        if self.buf is None:
-            return 0
-        return lib().wkv_workspace_status(self._aligned_ptr(), _stream_ptr(stream, self.buf.device))
+        for buf in (self.buf, self.plain):
+            if buf is not None:
+                rc = lib().wkv_workspace_status(self._aligned_ptr(buf), _stream_ptr(stream, buf.device))
+                if rc != 0:
+                    return rc
+        return 0
 
     def reset(self, stream=None):
         if self.buf is not None:
-            _check(lib().wkv_workspace_init(self._aligned_ptr(), self.buf.numel() - 256, _stream_ptr(stream, self.buf.device)),
-                   "wkv_workspace_init")
+            self._init(self.buf, self.buf.numel() - 256, stream)
+        if self.plain is not None:
+            self._init(self.plain, 256, stream)
 
 
 _workspaces = {}
@@ -607,7 +627,7 @@ def _scratch(nbytes, workspace, dev, stream):
     if nbytes == 0:
         return None, 0, None
     if workspace is not None:
-        return (*workspace.get(nbytes, stream), None)
+        return (*workspace.scratch(nbytes, stream, dev), None)
     torch = _torch()
     if stream is not None:
         with torch.cuda.stream(stream):

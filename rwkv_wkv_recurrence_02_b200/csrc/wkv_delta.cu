@@ -4,6 +4,8 @@
 #include "wkv_delta_mma_bwd.cuh"
 #include "wkv_host.cuh"
 
+#include <cstddef>
+
 namespace {
 
 using namespace wkv::host;
@@ -22,59 +24,86 @@ Parts parts_layout(int64_t walks, int64_t states, int64_t T) {
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     Parts p{};
     if (walks <= kSlotsMin || T < 2 * kPartMin) return p;
-    p.done = 256;
+    p.done = kHeader;
     p.hand = p.done + up(size_t(walks) * 4);
     p.bytes = p.hand + up(size_t(states) * 4);
     return p;
 }
 int slices(int64_t N) { return N == 128 ? 2 : 1; }
 
-// ws: parts_layout's bytes, or NULL for one walk a CTA
 using Walk = void (*)(d::Args);
-int launch_walk(Walk kern, Walk in_parts, int64_t walks, int threads, int smem, bool (&ready)[2][kMaxDevices], d::Args a, char* ws,
-                const Parts& p, cudaStream_t st) {
-    int rc = allow_smem(kern, smem, ready[0]);
-    if (rc == WKV_OK) rc = allow_smem(in_parts, smem, ready[1]);
+// CTAs of `kern` that the GPU holds
+int walk_slots(Walk kern, int threads, int smem, int64_t* slots) {
+    int dev = 0, sms = 0, per = 0;
+    int rc = record_cuda(cudaGetDevice(&dev));
+    if (rc == WKV_OK) rc = record_cuda(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    if (rc == WKV_OK) rc = record_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, threads, size_t(smem)));
+    *slots = int64_t(sms) * per;
+    return rc;
+}
+// Do walks go in parts?  Where the share of the last wave's places that stay
+// empty, of all waves', is above a tenth (a part costs a pipeline's fill).
+bool in_parts(int64_t walks, int64_t slots) {
+    const int64_t waves = slots > 0 ? (walks + slots - 1) / slots : 0;
+    return waves > 1 && (waves * slots - walks) * 10 > waves * slots;
+}
+int launch_parts(Walk kern, int64_t slots, int threads, int smem, d::Args a, char* ws, const Parts& p, cudaStream_t st) {
+    const int64_t n = a.T / kPartMin < kPartMax ? a.T / kPartMin : kPartMax;
+    a.part_len = ((a.T + n - 1) / n + d::kSegment - 1) / d::kSegment * d::kSegment;
+    a.parts = (a.T + a.part_len - 1) / a.part_len;
+    a.control = reinterpret_cast<d::Control*>(ws);
+    a.done = reinterpret_cast<uint32_t*>(ws + p.done);
+    a.hand = reinterpret_cast<float*>(ws + p.hand);
+    a.wait_ns = wait_limit_ns();
+    // the tickets and the parts that are done; the error word stays
+    const size_t from = offsetof(d::Control, ticket);
+    const int rc = record_cuda(cudaMemsetAsync(ws + from, 0, p.hand - from, st));
     if (rc != WKV_OK) return rc;
-    a.parts = 1, a.part_len = a.T;
-    if (ws != nullptr && p.bytes > 0) {
-        int dev = 0, sms = 0, per = 0;
-        rc = record_cuda(cudaGetDevice(&dev));
-        if (rc == WKV_OK) rc = record_cuda(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-        if (rc == WKV_OK) rc = record_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, in_parts, threads, size_t(smem)));
-        if (rc != WKV_OK) return rc;
-        // the share of the last wave's places that stay empty, of all waves': parts
-        // pay from about a tenth (they cost a pipeline's fill each)
-        const int64_t slots = int64_t(sms) * per, waves = slots > 0 ? (walks + slots - 1) / slots : 0;
-        if (walks > slots && slots > 0 && (waves * slots - walks) * 10 > waves * slots) {
-            const int64_t n = a.T / kPartMin < kPartMax ? a.T / kPartMin : kPartMax;
-            a.part_len = ((a.T + n - 1) / n + d::kSegment - 1) / d::kSegment * d::kSegment;
-            a.parts = (a.T + a.part_len - 1) / a.part_len;
-            a.control = reinterpret_cast<d::Control*>(ws);
-            a.done = reinterpret_cast<uint32_t*>(ws + p.done);
-            a.hand = reinterpret_cast<float*>(ws + p.hand);
-            a.wait_ns = wait_limit_ns();
-            rc = record_cuda(cudaMemsetAsync(ws, 0, p.hand, st));
-            if (rc != WKV_OK) return rc;
-            in_parts<<<dim3(unsigned(slots)), threads, smem, st>>>(a);
-            return check_launch();
-        }
-    }
-    return launch(kern, walks, threads, smem, st, a);
+    kern<<<dim3(unsigned(slots)), threads, smem, st>>>(a);
+    return check_launch();
 }
 
 template <typename IO, int N, bool WANT_Y>
-int launch_forward(const d::Args& a, char* ws, const Parts& p, cudaStream_t st) {
+int launch_forward_parts(int64_t slots, const d::Args& a, char* ws, const Parts& p, cudaStream_t st) {
     using G = d::ForwardShape<IO, N, WANT_Y>;
-    static bool ready[2][kMaxDevices] = {{false}};
-    return launch_walk(d::delta_forward_mma_kernel<IO, N, WANT_Y, false>, d::delta_forward_mma_kernel<IO, N, WANT_Y, true>, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, ready, a, ws, p, st);
+    static bool ready[kMaxDevices] = {false};
+    const auto kern = d::delta_forward_mma_kernel<IO, N, WANT_Y, true>;
+    const int rc = allow_smem(kern, G::SMEM, ready);
+    return rc != WKV_OK ? rc : launch_parts(kern, slots, G::THREADS, G::SMEM, a, ws, p, st);
+}
+// ws: parts_layout's bytes, or NULL
+template <typename IO, int N>
+int launch_forward(d::Args a, char* ws, const Parts& p, cudaStream_t st) {
+    using G = d::ForwardShape<IO, N, true>;
+    static bool ready[kMaxDevices] = {false};
+    const auto kern = d::delta_forward_mma_kernel<IO, N, true, false>;
+    const int64_t walks = a.B * a.H * G::SLICES;
+    int64_t slots = 0;
+    int rc = allow_smem(kern, G::SMEM, ready);
+    if (rc == WKV_OK && ws != nullptr && p.bytes > 0) rc = walk_slots(kern, G::THREADS, G::SMEM, &slots);
+    if (rc != WKV_OK) return rc;
+    if (in_parts(walks, slots)) return launch_forward_parts<IO, N, true>(slots, a, ws, p, st);
+    return launch(kern, walks, G::THREADS, G::SMEM, st, a);
 }
 
+// both walks of the reverse mode
 template <typename IO, int N>
-int launch_reverse(const d::Args& a, char* ws, const Parts& p, cudaStream_t st) {
-    using G = d::ReverseShape<IO, N>;
+int launch_walks(d::Args a, char* ws, const Parts& p, cudaStream_t st) {
+    using F = d::ForwardShape<IO, N, false>;
+    using R = d::ReverseShape<IO, N>;
+    static_assert(F::THREADS == R::THREADS && F::SMEM <= R::SMEM && F::SLICES == R::SLICES, "one kernel for both");
     static bool ready[2][kMaxDevices] = {{false}};
-    return launch_walk(d::delta_reverse_mma_kernel<IO, N, false>, d::delta_reverse_mma_kernel<IO, N, true>, a.B * a.H * G::SLICES, G::THREADS, G::SMEM, ready, a, ws, p, st);
+    const auto kern = d::delta_walks_kernel<IO, N>;
+    const auto reverse = d::delta_reverse_mma_kernel<IO, N>;
+    const int64_t walks = a.B * a.H * R::SLICES;
+    int64_t slots = 0;
+    int rc = allow_smem(kern, R::SMEM, ready[0]);
+    if (rc == WKV_OK) rc = allow_smem(reverse, R::SMEM, ready[1]);
+    if (rc == WKV_OK && p.bytes > 0) rc = walk_slots(reverse, R::THREADS, R::SMEM, &slots);
+    if (rc != WKV_OK) return rc;
+    if (!in_parts(walks, slots)) return launch(kern, 2 * walks, R::THREADS, R::SMEM, st, a);
+    rc = launch_forward_parts<IO, N, false>(slots, a, ws, p, st);
+    return rc != WKV_OK ? rc : launch_parts(reverse, slots, R::THREADS, R::SMEM, a, ws, p, st);
 }
 
 template <typename IO, int N>
@@ -88,7 +117,7 @@ int launch_segments(const d::Args& a, cudaStream_t st) {
 }
 
 struct Layout {
-    size_t e, du, s_seg, d_seg, drh, dkh, parts, bytes;
+    size_t e, du, s_seg, d_seg, drh, dkh, bytes;
 };
 
 // share: several value heads to a key head
@@ -97,21 +126,20 @@ Layout layout(int64_t B, int64_t T, int64_t H, int64_t N, bool share) {
     const size_t val = up(size_t(B) * T * H * N * 4), heads = size_t(B) * H;
     const size_t borders = heads * (size_t((T + d::kSegment - 1) / d::kSegment) + 1);
     Layout l{};
-    l.e = 0;
+    const size_t parts = parts_layout(B * H * slices(N), B * H * N * N, T).bytes;
+    l.e = parts > 0 ? parts : kHeader;
     l.du = l.e + val;
     l.s_seg = l.du + val;
     l.d_seg = l.s_seg + up(borders * N * N * 4);
     l.drh = l.d_seg + up(borders * N * N * 4);
     l.dkh = l.drh + (share ? val : 0);
-    l.parts = l.dkh + (share ? val : 0);
-    l.bytes = l.parts + parts_layout(B * H * slices(N), B * H * N * N, T).bytes;
+    l.bytes = l.dkh + (share ? val : 0);
     return l;
 }
 
 template <typename IO, int N>
 int run_backward(const d::Args& a, char* ws, const Parts& p, cudaStream_t st) {
-    int rc = launch_forward<IO, N, false>(a, ws, p, st);
-    if (rc == WKV_OK) rc = launch_reverse<IO, N>(a, ws, p, st);
+    int rc = launch_walks<IO, N>(a, ws, p, st);
     if (rc == WKV_OK) rc = launch_segments<IO, N>(a, st);
     if (rc == WKV_OK && a.H != a.Hk)
         rc = launch(d::delta_share_kernel<IO, N>, (a.B * a.T * a.Hk * (N / 4) + 255) / 256, 256, 0, st, a);
@@ -194,7 +222,7 @@ int wkv_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, in
     a.w = w, a.beta = beta, a.r = r, a.k = k, a.v = v, a.s_in = state_in, a.y = y, a.s_out = state_out;
     a.vec = aligned(r, 16) && aligned(k, 16) && aligned(v, 16) && aligned(y, 16);
     rc = with_type(dtype, N, [&](auto tag, auto size) {
-        return launch_forward<decltype(tag), decltype(size)::value, true>(a, static_cast<char*>(workspace), p, stream);
+        return launch_forward<decltype(tag), decltype(size)::value>(a, static_cast<char*>(workspace), p, stream);
     });
     return rc != WKV_OK ? rc : check_launch();
 }
@@ -268,8 +296,7 @@ int wkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, i
     a.vec = aligned(r, 16) && aligned(k, 16) && aligned(v, 16) && aligned(dy, 16) && aligned(dv, 16) &&
             aligned(dr, 16) && aligned(dk, 16);
     rc = with_type(dtype, N, [&](auto tag, auto size) {
-        return run_backward<decltype(tag), decltype(size)::value>(a, ws + l.parts, parts_layout(B * H * slices(N), n.states, T),
-                                                                  stream);
+        return run_backward<decltype(tag), decltype(size)::value>(a, ws, parts_layout(B * H * slices(N), n.states, T), stream);
     });
     return rc != WKV_OK ? rc : check_launch();
 }

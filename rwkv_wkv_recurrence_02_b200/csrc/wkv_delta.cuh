@@ -38,6 +38,8 @@ struct Control {
     uint32_t epoch, finished, error, err_unit, ticket;
 };
 
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct Args {
     int64_t B, T, Hk, H;
     const float* w;      // (B, T, H)

@@ -558,7 +558,9 @@ __device__ __forceinline__ void take_over(float (&S)[N / 8][4], const float* s, 
 // part of a walk after another.  Tickets go through the first part of every
 // walk, then the second: a part's predecessor was taken earlier, so somebody
 // is at it or done with it, and by then it is nearly always done.  A wait ends
-// after wait_ns; it leaves the error word and NaN in what follows.
+// after wait_ns; it leaves the error word, and NaN in that part and all that
+// follow it.
+constexpr uint32_t kLost = 0xffffffffu;   // of the parts that are done: one was given up
 struct Task {
     int64_t walk, part;
     bool lost;   // the part before it never came
@@ -566,16 +568,17 @@ struct Task {
 // The next task of the CTA (every thread calls; THREADS of them), false: none
 // is left.  Publishes the one before: its state is written and fenced.
 template <bool PARTS, int THREADS>
-__device__ __forceinline__ bool next_task(const Args& a, int64_t walks, Task& t, bool first) {
+__device__ __forceinline__ bool next_task(const Args& a, int64_t walks, int64_t block, Task& t, bool first) {
     if constexpr (!PARTS) {
-        t = Task{int64_t(blockIdx.x), 0, false};
+        t = Task{block, 0, false};
         return first;
     }
     __shared__ int64_t s_ticket;
     __shared__ int s_lost;
     bar_sync<THREADS>(kBarTask);
     if (threadIdx.x == 0) {
-        if (!first) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(a.done + t.walk), "r"(uint32_t(t.part + 1)) : "memory");
+        if (!first)
+            asm volatile("red.release.gpu.global.max.u32 [%0], %1;" ::"l"(a.done + t.walk), "r"(t.lost ? kLost : uint32_t(t.part + 1)) : "memory");
         const int64_t id = atomicAdd(&a.control->ticket, 1u);
         s_ticket = id;
         s_lost = 0;
@@ -591,10 +594,11 @@ __device__ __forceinline__ bool next_task(const Args& a, int64_t walks, Task& t,
                 if (now - begin > a.wait_ns) {
                     a.control->error = 1u;
                     a.control->err_unit = uint32_t(id);
-                    s_lost = 1;
+                    have = kLost;
                     break;
                 }
             }
+            s_lost = have == kLost;
         }
     }
     __syncwarp();
@@ -633,26 +637,21 @@ template <typename IO, int N, bool WANT_Y>
 using ForwardShape = Columns<IO, N, WANT_Y, 3 + (WANT_Y ? kOutOrders<IO> : 0), 2>;
 
 template <typename IO, int N, bool WANT_Y, bool PARTS>
-__global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO, N>) delta_forward_mma_kernel(const Args a) {
+__device__ __forceinline__ void forward_walk(const Args& a, char* smem, int64_t block) {
     using G = ForwardShape<IO, N, WANT_Y>;
     constexpr int KP = G::KP, PP = kOutOrders<IO>, LD = G::LD, C = kChain<IO>;
-    extern __shared__ __align__(16) char smem[];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
 
     const int64_t walks = a.B * a.H * G::SLICES, vs = a.H * N;
     Task task;
     bool first = true;
 
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    // the reverse mode's other walk may start: what it reads is finished
-    if constexpr (!WANT_Y && !PARTS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
     if (warp >= G::NW) {
         stager_regs<IO, N>();
         const int st = warp - G::NW;
         const int64_t ks = a.Hk * N;
         G g(smem, st);
-        for (; next_task<PARTS, G::THREADS>(a, walks, task, first); first = false) {
+        for (; next_task<PARTS, G::THREADS>(a, walks, block, task, first); first = false) {
         const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
         const int64_t begin = PARTS ? task.part * a.part_len : 0;
     const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
@@ -707,7 +706,7 @@ __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO
     const int j0 = warp * 16;
     const int64_t nseg = (a.T + kSegment - 1) / kSegment;
     const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = m_plain(lane);
-    for (; next_task<PARTS, G::THREADS>(a, walks, task, first); first = false) {
+    for (; next_task<PARTS, G::THREADS>(a, walks, block, task, first); first = false) {
     const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H;
     const int slice = int(task.walk % G::SLICES) * G::CW;
     const int64_t begin = PARTS ? task.part * a.part_len : 0;
@@ -808,6 +807,13 @@ __global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO
         keep_state<N>(keep + nseg * N * N, S, lane);
     }
     }
+}
+
+template <typename IO, int N, bool WANT_Y, bool PARTS>
+__global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO, N>) delta_forward_mma_kernel(const Args a) {
+    extern __shared__ __align__(16) char smem[];
+    pdl_wait();
+    forward_walk<IO, N, WANT_Y, PARTS>(a, smem, blockIdx.x);
 }
 
 }  // namespace delta

@@ -15,9 +15,8 @@
 // Two walks, for e and the states between segments of 64 tokens (the forward
 // kernel) and for du and the gradient states between them; with those, dr and
 // dk of a segment need nothing from the others, and a third kernel forms them
-// for every segment at once.  It starts dw from the inner
-// products <D, S> at the segment's borders.  The two walks need nothing of
-// each other and run at the same time where the GPU has room.
+// for every segment at once.  It starts dw from the inner product <D, S> at the
+// segment's end.  The two walks run side by side in one kernel.
 // What only reaches dk takes the orders that its type keeps; dr takes them
 // all, as r.dr enters dw.
 #pragma once
@@ -35,27 +34,21 @@ template <typename IO, int N>
 using ReverseShape = Columns<IO, N, true, 6, 3>;
 
 template <typename IO, int N, bool PARTS>
-__global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) delta_reverse_mma_kernel(const Args a) {
+__device__ __forceinline__ void reverse_walk(const Args& a, char* smem, int64_t block) {
     using G = ReverseShape<IO, N>;
     constexpr int KP = G::KP, LD = G::LD;
-    extern __shared__ __align__(16) char smem[];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
 
     const int64_t walks = a.B * a.H * G::SLICES, vs = a.H * N;
     Task task;
     bool first = true;
 
-    // In parts, after the memset of the tickets.  Otherwise the forward walk,
-    // which this one needs nothing of, has let it start once its own CTAs knew
-    // everything before them finished; the two end together (below).
-    if constexpr (PARTS) asm volatile("griddepcontrol.wait;" ::: "memory");
-
     if (warp >= G::NW) {
         stager_regs<IO, N>();
         const int st = warp - G::NW;
         const int64_t ks = a.Hk * N;
         G g(smem, st);
-        for (; next_task<PARTS, G::THREADS>(a, walks, task, first); first = false) {
+        for (; next_task<PARTS, G::THREADS>(a, walks, block, task, first); first = false) {
         const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
         const int64_t begin = PARTS ? (a.parts - 1 - task.part) * a.part_len : 0;
     const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
@@ -112,7 +105,7 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
     const int j0 = warp * 16;
     const int64_t nseg = (a.T + kSegment - 1) / kSegment;
     const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = m_trans(lane);
-    for (; next_task<PARTS, G::THREADS>(a, walks, task, first); first = false) {
+    for (; next_task<PARTS, G::THREADS>(a, walks, block, task, first); first = false) {
     const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H;
     const int slice = int(task.walk % G::SLICES) * G::CW;
     const int64_t begin = PARTS ? (a.parts - 1 - task.part) * a.part_len : 0;
@@ -205,8 +198,23 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
     if (PARTS && begin > 0) hand_on<N>(hand, S, lane);
     else if (a.ds_in != nullptr) store_state<N>(a.ds_in + head * N * N + slice + j0, S, lane);
     }
-    // what follows this kernel reads the forward walk's results too
-    if constexpr (!PARTS) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <typename IO, int N>
+__global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) delta_reverse_mma_kernel(const Args a) {
+    extern __shared__ __align__(16) char smem[];
+    pdl_wait();
+    reverse_walk<IO, N, true>(a, smem, blockIdx.x);
+}
+// Whole walks of both kinds: they need nothing of each other.  The reverse
+// ones, which take longer, first.
+template <typename IO, int N>
+__global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) delta_walks_kernel(const Args a) {
+    extern __shared__ __align__(16) char smem[];
+    const int64_t walks = a.B * a.H * ReverseShape<IO, N>::SLICES;
+    pdl_wait();
+    if (blockIdx.x < walks) reverse_walk<IO, N, false>(a, smem, blockIdx.x);
+    else forward_walk<IO, N, false, false>(a, smem, blockIdx.x - walks);
 }
 
 // ---------------------------------------------------------------------------
@@ -301,7 +309,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     const int64_t rows = ((b * a.T + t0) * a.H + h) * N, keys = ((b * a.T + t0) * a.Hk + hk) * N;
     const int64_t scalar = (b * a.T + t0) * a.H + h;
 
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    pdl_wait();
 
     // what is read later, on its way to L2 now
     const float* s_seg = a.s_seg + (head * (nseg + 1) + seg) * N * N;
@@ -655,7 +663,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
 template <typename IO, int N>
 __global__ void __launch_bounds__(256) delta_share_kernel(const Args a) {
     const int64_t id = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    pdl_wait();
     if (id >= a.B * a.T * a.Hk * (N / 4)) return;
     const int64_t key = id / (N / 4);   // (sequence, token, key head)
     const int share = int(a.H / a.Hk), c = int(id % (N / 4)) * 4;

@@ -18,6 +18,10 @@ inline thread_local char g_last_cuda_error[256] = "";
 constexpr int64_t kMaxElems = int64_t(1) << 62;
 constexpr int kMaxDevices = 64;
 
+// A workspace's first bytes: the error word that wkv_workspace_status() reads
+// is among them, so what a call keeps of its own lies behind them.
+constexpr size_t kHeader = 256;
+
 inline int record_cuda(cudaError_t e) {
     if (e == cudaSuccess) return WKV_OK;
     std::snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "%s: %s", cudaGetErrorName(e),

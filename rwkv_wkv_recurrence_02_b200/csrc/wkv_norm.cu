@@ -197,7 +197,7 @@ size_t wkv_group_norm_backward_workspace_bytes(int64_t rows, int64_t C, int64_t 
         const size_t b = plan(rows, C, C / G, int(elem_bytes(dtype)), align, true).bytes;
         if (b > most) most = b;
     }
-    return most;
+    return most > 0 ? kHeader + most : 0;
 }
 
 int wkv_group_norm_backward(int64_t rows, int64_t C, int64_t G, int dtype, int act, float eps, const void* x,
@@ -230,7 +230,7 @@ int wkv_group_norm_backward(int64_t rows, int64_t C, int64_t G, int dtype, int a
     a.rows = rows, a.C = C, a.group = int(C / G), a.lpg = p.lpg, a.lpg_log2 = p.lpg_log2, a.slots = p.slots;
     a.span = p.span, a.act = act, a.eps = eps, a.inv_group = 1.f / float(C / G);
     a.x = x, a.gate = gate, a.weight = weight, a.bias = bias, a.dy = dy, a.dx = dx, a.dgate = dgate;
-    float* ws = static_cast<float*>(workspace);
+    float* ws = need > 0 ? static_cast<float*>(workspace) + kHeader / 4 : nullptr;
     rc = dtype == WKV_F32 ? run<float, true>(a, p, G, ws, dweight, dbias, stream)
                           : run<__nv_bfloat16, true>(a, p, G, ws, dweight, dbias, stream);
     return rc != WKV_OK ? rc : check_launch();
