@@ -24,6 +24,18 @@
 // takes the orders up to 2^-8 (an error of 2^-17 against the output's own
 // 2^-9).  The state is updated by a float32 multiply-add of the chunk's sum, so
 // the accumulators' truncation does not add up along T.
+//
+// What bounds it: issue.  An mma.sync of 16 x 8 x 16 holds its scheduler for 8.3
+// cycles here and other instructions (1.1 each) do not issue meanwhile; 82 of
+// the ones and about 500 of the others a chunk and warp (bfloat16 heads of 64),
+// with the staging warps' share, are 93% of the time.  Measured: 8 x 4096 tokens
+// of 32 heads of 64 in bfloat16 398 us (reads and writes alone: 85; the same
+// recurrence token by token in float32 multiply-adds: 1798).  With few heads a
+// chunk's chain of dependent products bounds it: 32 heads x 4096 tokens 228 us
+// (0.9 us a chunk), 32 heads of 128 363 us.  Chunks of 32 tokens were no faster
+// (the code outgrows the instruction cache), 2 or 4 warps sharing a head's keys
+// slower (583 us, exchange in shared memory), fp16 pieces slower (428 us, the
+// scaling).
 #pragma once
 
 #include "wkv_delta.cuh"
@@ -610,11 +622,16 @@ __device__ __forceinline__ bool next_task(const Args& a, int64_t walks, int64_t 
 // what only reaches an output takes this many orders
 template <typename IO>
 constexpr int kOutOrders = sizeof(IO) == 2 ? 2 : 3;
-// steps of 16 in a chain of the tensor cores' additions
+// steps of 16 in a chain of the tensor cores' additions.  float32 heads of 128
+// with whole chains: y within 6.8e-7 of 64 bits, dw 2e-6; with chains of one
+// 1.3e-7 and 5e-7.  bfloat16 keeps chains of 4 (heads of 64 whole; heads of 128
+// dw 4e-7, was 8e-7, for 2% of the time).
 template <typename IO>
 constexpr int kChain = sizeof(IO) == 2 ? 4 : 1;
 
-// CTAs an SM: two where the state's lines and the I/O type leave room
+// CTAs an SM: two where the state's lines and the I/O type leave room (8 x 4096
+// tokens of 32 heads of 64: two walks an SM share its issue slots, 398 us for
+// 1.73 walks an SM where one walk alone takes 228)
 template <typename IO, int N>
 constexpr int kCtas = N <= 64 && sizeof(IO) == 2 ? 2 : 1;
 // Two walks of heads of 64 in bfloat16 fit an SM with 128 registers a thread on

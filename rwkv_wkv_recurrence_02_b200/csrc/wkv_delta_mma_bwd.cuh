@@ -19,6 +19,13 @@
 // segment's end.  The two walks run side by side in one kernel.
 // What only reaches dk takes the orders that its type keeps; dr takes them
 // all, as r.dr enters dw.
+//
+// Measured, bfloat16: 8 x 4096 tokens of 32 heads of 64 1630 us (reads and writes
+// alone: 150), the walks 820 to 880 of it, bound as the forward is, the segments
+// the rest: shared memory's wavefronts (67% of their peak) and latency at 16
+// warps an SM, DRAM 26%.  2047 tokens of 16 heads of 128, 8 key heads: 317 us.
+// The two walks one after the other took 671 us on 4096 tokens of 32 heads of
+// 64; side by side all three kernels take 396.
 #pragma once
 
 #include "wkv_delta_mma.cuh"
@@ -223,6 +230,9 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
 // segment's 16 x 16 blocks of (token, token) products.  A block is formed once,
 // by one warp, and read from shared memory as it lies and transposed.
 // ---------------------------------------------------------------------------
+// 16 x 32 of a warp's (8 warps a CTA, two CTAs an SM for heads of 64) is as fast
+// as 16 x 64 (4 warps, three CTAs: 410 us for 8 x 2048 tokens of 32 heads) and
+// faster for heads of 128 (319 against 330 us for the whole call).
 template <typename IO, int N>
 struct SegmentShape {
     static constexpr int KP = sizeof(IO) == 2 ? 1 : 3, PP = kOutOrders<IO>;
