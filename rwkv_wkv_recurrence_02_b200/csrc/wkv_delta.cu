@@ -1,7 +1,7 @@
 // wkv_delta.cu -- host side of the gated delta rule's entry points
 // (wkv_delta_forward, wkv_delta_step, wkv_delta_backward): argument checks,
 // the workspace's layout and the launches.
-#include "wkv_delta_mma_bwd.cuh"
+#include "wkv_delta_tc.cuh"
 #include "wkv_host.cuh"
 
 #include <cstddef>
@@ -111,12 +111,18 @@ int launch_walks(d::Args a, char* ws, const Parts& p, cudaStream_t st) {
 
 template <typename IO, int N>
 int launch_segments(const d::Args& a, cudaStream_t st) {
-    using G = d::SegmentShape<IO, N>;
     static bool ready[kMaxDevices] = {false};
-    auto kern = d::delta_segment_kernel<IO, N>;
-    const int rc = allow_smem(kern, G::SMEM, ready);
     const int64_t segments = a.B * a.H * ((a.T + d::kSegment - 1) / d::kSegment);
-    return rc != WKV_OK ? rc : launch(kern, segments, G::THREADS, G::SMEM, st, a);
+    if constexpr (d::kTcSegments<IO, N>) {
+        using G = d::TcSegment;
+        const int rc = allow_smem(d::delta_segment_tc_kernel, G::SMEM, ready);
+        return rc != WKV_OK ? rc : launch(d::delta_segment_tc_kernel, segments, G::THREADS, G::SMEM, st, a);
+    } else {
+        using G = d::SegmentShape<IO, N>;
+        const auto kern = d::delta_segment_kernel<IO, N>;
+        const int rc = allow_smem(kern, G::SMEM, ready);
+        return rc != WKV_OK ? rc : launch(kern, segments, G::THREADS, G::SMEM, st, a);
+    }
 }
 
 struct Layout {

@@ -537,14 +537,24 @@ __device__ __forceinline__ void store_state(float* s, const float (&S)[N / 8][4]
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[(8 * n + 2 * (lane % 4) + (i & 1)) * N + lane / 4 + (i >> 1) * 8] = S[n][i];
 }
-// and as it lies, S^T[value][key], for the reverse mode
-template <int N>
-__device__ __forceinline__ void keep_state(float* s, const float (&S)[N / 8][4], int lane) {
+// The segments' kernel of the reverse mode: tcgen05.mma (wkv_delta_tc.cuh), or
+// mma.sync, as heads of other sizes and float32 take.
+template <typename IO, int N>
+constexpr bool kTcSegments = N == 64 && sizeof(IO) == 2;
+// The states between segments as that kernel reads them: S[key][value], or
+// S^T[value][key].  j: the warp's first value column.
+template <typename IO, int N>
+__device__ __forceinline__ void keep_state(float* s, int j, const float (&S)[N / 8][4], int lane) {
+    if constexpr (kTcSegments<IO, N>) {
+        store_state<N>(s + j, S, lane);
+    } else {
 #pragma unroll
-    for (int n = 0; n < N / 8; ++n)
+        for (int n = 0; n < N / 8; ++n)
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-            *reinterpret_cast<float2*>(s + (lane / 4 + 8 * q) * N + 8 * n + 2 * (lane % 4)) = make_float2(S[n][2 * q], S[n][2 * q + 1]);
+            for (int q = 0; q < 2; ++q)
+                *reinterpret_cast<float2*>(s + (j + lane / 4 + 8 * q) * N + 8 * n + 2 * (lane % 4)) =
+                    make_float2(S[n][2 * q], S[n][2 * q + 1]);
+    }
 }
 
 // The walk's state as a warp holds it, between the parts of a walk
@@ -729,7 +739,7 @@ __device__ __forceinline__ void forward_walk(const Args& a, char* smem, int64_t 
     const int64_t begin = PARTS ? task.part * a.part_len : 0;
     const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
     const int64_t vbase = (b * a.T * a.H + h) * N + slice;
-    float* keep = a.s_seg + head * (nseg + 1) * N * N + int64_t(slice + j0) * N;
+    float* keep = a.s_seg + head * (nseg + 1) * N * N;
     float* hand = a.hand + head * N * N + int64_t(slice + j0) * N;
     float S[N / 8][4];
     if (!PARTS || task.part == 0) load_state<N>(S, a.s_in == nullptr ? nullptr : a.s_in + head * N * N + slice + j0, lane);
@@ -739,7 +749,7 @@ __device__ __forceinline__ void forward_walk(const Args& a, char* smem, int64_t 
     for (int64_t t0 = begin; t0 < end; t0 += kChunk, st = (st + 1) % G::NST) {
         const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
         G g(smem, st);
-        if (!WANT_Y && t0 % kSegment == 0) keep_state<N>(keep + t0 / kSegment * N * N, S, lane);
+        if (!WANT_Y && t0 % kSegment == 0) keep_state<IO, N>(keep + t0 / kSegment * N * N, slice + j0, S, lane);
         bar_sync<G::BAR>(kBarFull + st);
         // K S and R S, transposed
         float p[2][4], q[2][4], x[2][4];
@@ -821,7 +831,7 @@ __device__ __forceinline__ void forward_walk(const Args& a, char* smem, int64_t 
     } else if constexpr (WANT_Y) {
         if (a.s_out != nullptr) store_state<N>(a.s_out + head * N * N + slice + j0, S, lane);
     } else {
-        keep_state<N>(keep + nseg * N * N, S, lane);
+        keep_state<IO, N>(keep + nseg * N * N, slice + j0, S, lane);
     }
     }
 }

@@ -119,14 +119,13 @@ __device__ __forceinline__ void reverse_walk(const Args& a, char* smem, int64_t 
     const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
     const int64_t last = begin + (end - 1 - begin) / kChunk * kChunk;
     const int64_t vbase = (b * a.T * a.H + h) * N + slice;
-    const int64_t place = head * (nseg + 1) * N * N + int64_t(slice + j0) * N;
-    float* grads = a.d_seg + place;
+    float* grads = a.d_seg + head * (nseg + 1) * N * N;
     float* hand = a.hand + head * N * N + int64_t(slice + j0) * N;
     float S[N / 8][4];   // D^T
     if (!PARTS || task.part == 0) load_state<N>(S, a.ds_out == nullptr ? nullptr : a.ds_out + head * N * N + slice + j0, lane);
     else take_over<N>(S, hand, task.lost, lane);
     // gradient states between segments, as S^T's
-    if (!PARTS || task.part == 0) keep_state<N>(grads + nseg * N * N, S, lane);
+    if (!PARTS || task.part == 0) keep_state<IO, N>(grads + nseg * N * N, slice + j0, S, lane);
     int st = 0;
 #pragma unroll 1
     for (int64_t t0 = last; t0 >= begin; t0 -= kChunk, st = (st + 1) % G::NST) {
@@ -200,7 +199,7 @@ __device__ __forceinline__ void reverse_walk(const Args& a, char* smem, int64_t 
             store_half(static_cast<IO*>(a.dv) + at + 8 * n * vs, vs, nt - 8 * n, du[n], g.v + 8 * n * G::LDV + j0, G::LDV, a.vec, lane);
         }
         if (t0 >= begin + G::NST * kChunk) bar_arrive<G::BAR>(kBarFree + st);
-        if (t0 % kSegment == 0) keep_state<N>(grads + t0 / kSegment * N * N, S, lane);
+        if (t0 % kSegment == 0) keep_state<IO, N>(grads + t0 / kSegment * N * N, slice + j0, S, lane);
     }
     if (PARTS && begin > 0) hand_on<N>(hand, S, lane);
     else if (a.ds_in != nullptr) store_state<N>(a.ds_in + head * N * N + slice + j0, S, lane);
@@ -291,6 +290,244 @@ __device__ __forceinline__ void add_lines(float (&d)[NP][2][4], float f0, float 
     }
 }
 
+// what a CTA of the segments' kernels works on
+struct Segment {
+    int64_t head, seg, ks, vs;   // strides of a token in keys and values
+    int64_t state;               // of its first state among those between segments
+    int64_t rows, keys, scalar;  // of its first token in values, keys and per-head scalars
+    int nt;                      // tokens
+    __device__ __forceinline__ Segment(const Args& a, int N) {
+        const int64_t nseg = (a.T + kSegment - 1) / kSegment;
+        head = blockIdx.x / nseg, seg = blockIdx.x % nseg;
+        const int64_t b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk), t0 = seg * kSegment;
+        nt = a.T - t0 < kSegment ? int(a.T - t0) : kSegment;
+        ks = a.Hk * N, vs = a.H * N;
+        state = (head * (nseg + 1) + seg) * N * N;
+        rows = ((b * a.T + t0) * a.H + h) * N, keys = ((b * a.T + t0) * a.Hk + hk) * N;
+        scalar = (b * a.T + t0) * a.H + h;
+    }
+};
+
+// A warp's RW rows of u = beta e (three pieces) and dv = beta du (PP pieces), at
+// their places in shared memory; dbeta, and dv . v of a token.
+template <typename IO, int N, int RW, int PP, typename AT>
+__device__ __forceinline__ void stage_values(const Args& a, const Segment& sg, __nv_bfloat16* ub, __nv_bfloat16* db, int piece, AT place,
+                                             int row, float* dvv, int lane) {
+    constexpr int KP = sizeof(IO) == 2 ? 1 : 3;
+    const int left = sg.nt - row;
+    const int64_t rows = sg.rows, vs = sg.vs, scalar = sg.scalar;
+    constexpr int ROWV = N / 4, ALL = RW * ROWV / 32, U = ALL < 8 ? ALL : 8;
+#pragma unroll 1
+    for (int n = 0; n < ALL; n += U) {
+        // all loads first, of a row that exists; rows behind the last token are zeroed after
+        float4 x[U], y[U], v[U];
+        uint2 vr[U];
+        float be[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = lane + (n + u) * 32, t = i / ROWV, c = (i % ROWV) * 4;
+            const int64_t at = rows + (t < left ? row + t : 0) * vs + c;
+            be[u] = __ldg(a.beta + scalar + (t < left ? row + t : 0) * a.H);
+            x[u] = load4(a.e + at, true);
+            y[u] = load4(a.du + at, true);
+            const IO* vp = static_cast<const IO*>(a.v) + at;
+            if constexpr (KP == 3) {
+                v[u] = load4(reinterpret_cast<const float*>(vp), a.vec);
+            } else if (a.vec) {
+                vr[u] = __ldg(reinterpret_cast<const uint2*>(vp));
+            } else {
+                const unsigned short* q = reinterpret_cast<const unsigned short*>(vp);
+                vr[u] = make_uint2(q[0] | uint32_t(q[1]) << 16, q[2] | uint32_t(q[3]) << 16);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = lane + (n + u) * 32, t = i / ROWV, c = (i % ROWV) * 4;
+            if constexpr (KP == 1)
+                v[u] = make_float4(__uint_as_float(vr[u].x << 16), __uint_as_float(vr[u].x & 0xffff0000u),
+                                   __uint_as_float(vr[u].y << 16), __uint_as_float(vr[u].y & 0xffff0000u));
+            if (t >= left) x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float bt = be[u];
+            float s = fmaf(x[u].x, y[u].x, fmaf(x[u].y, y[u].y, fmaf(x[u].z, y[u].z, x[u].w * y[u].w)));
+            float z = fmaf(v[u].x, y[u].x, fmaf(v[u].y, y[u].y, fmaf(v[u].z, y[u].z, v[u].w * y[u].w)));
+#pragma unroll
+            for (int o = ROWV / 2; o > 0; o /= 2) {
+                s += __shfl_xor_sync(0xffffffffu, s, o);
+                z += __shfl_xor_sync(0xffffffffu, z, o);
+            }
+            if (lane % ROWV == 0) {
+                if (t < left) a.dbeta[scalar + (row + t) * a.H] = s;
+                dvv[row + t] = bt * z;
+            }
+            put4<3>(ub + place(row + t, c), piece, make_float4(bt * x[u].x, bt * x[u].y, bt * x[u].z, bt * x[u].w));
+            put4<PP>(db + place(row + t, c), piece, make_float4(bt * y[u].x, bt * y[u].y, bt * y[u].z, bt * y[u].w));
+        }
+    }
+}
+
+// the decays' running sum, two tokens a lane (one warp)
+__device__ __forceinline__ void segment_sums(const Args& a, const Segment& sg, float2* sums, int lane) {
+    const int64_t scalar = sg.scalar;
+    const int nt = sg.nt;
+    const int ta = 2 * lane;
+    const float w0 = ta < nt ? a.w[scalar + ta * a.H] : 0.f, w1 = ta + 1 < nt ? a.w[scalar + (ta + 1) * a.H] : 0.f;
+    const double x0 = w0 > kMaxRate ? kMaxRate : w0, x1 = x0 + double(w1 > kMaxRate ? kMaxRate : w1);
+    double x = x1;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const double y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    sums[ta] = two_floats(x - x1 + x0);
+    sums[ta + 1] = two_floats(x);
+}
+
+// own: r . dr of the lane's two rows over its warp's channels (R's pieces staged)
+template <int N, int NP, int KP>
+__device__ __forceinline__ void row_products(float (&own)[2], const __nv_bfloat16* rb, int piece, const float (&dr)[NP][2][4], int t_lo,
+                                             int i0, int lane) {
+    constexpr Swizzled<N> place{};
+    own[0] = own[1] = 0.f;
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const __nv_bfloat16* r2 = rb + place(t_lo + 8 * q, i0 + p * 16 + 8 * n + 2 * (lane % 4));
+                float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+                for (int c = KP - 1; c >= 0; --c) {
+                    const uint32_t w2 = *reinterpret_cast<const uint32_t*>(r2 + c * piece);
+                    x0 += __uint_as_float(w2 << 16), x1 += __uint_as_float(w2 & 0xffff0000u);
+                }
+                own[q] = fmaf(x0, dr[p][n][2 * q], fmaf(x1, dr[p][n][2 * q + 1], own[q]));
+            }
+}
+
+// dr and dk of a warp's 16 tokens and its channels; tile: shared memory of the
+// warp's own for bfloat16's 16-byte stores
+template <typename IO, int N, int NP>
+__device__ __forceinline__ void store_rows(const Args& a, const Segment& sg, const float (&dr)[NP][2][4], const float (&dk)[NP][2][4],
+                                           __nv_bfloat16* tile, int tb, int i0, int lane) {
+    constexpr int KP = sizeof(IO) == 2 ? 1 : 3;
+    const int64_t rows = sg.rows, vs = sg.vs;
+    const int nt = sg.nt, t_lo = tb * 16 + lane / 4;
+    const bool whole = a.H == a.Hk;
+    if (!whole || KP == 3) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int t = t_lo + 8 * q;
+            if (t >= nt) continue;
+            const int64_t at = rows + t * vs + i0 + 2 * (lane % 4);
+            float* orr = (whole ? static_cast<float*>(a.dr) : a.drh) + at;
+            float* ok = (whole ? static_cast<float*>(a.dk) : a.dkh) + at;
+            const bool pairs = !whole || a.vec;
+#pragma unroll
+            for (int c = 0; c < 2 * NP; ++c) {
+                const float *x = &dr[c / 2][c % 2][2 * q], *y = &dk[c / 2][c % 2][2 * q];
+                if (pairs) {
+                    *reinterpret_cast<float2*>(orr + 8 * c) = make_float2(x[0], x[1]);
+                    *reinterpret_cast<float2*>(ok + 8 * c) = make_float2(y[0], y[1]);
+                } else {
+                    orr[8 * c] = x[0], orr[8 * c + 1] = x[1];
+                    ok[8 * c] = y[0], ok[8 * c + 1] = y[1];
+                }
+            }
+        }
+    } else if constexpr (KP == 1) {   // through rows of the warp's own (where u was) to 16-byte stores
+        constexpr int LD = 16 * NP + 8;
+                const uint32_t to = smem_u32(tile + ((lane & 7) + ((lane >> 3) & 1) * 8) * LD + (lane >> 4) * 8);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            stsm_tile(to + p * 32, dr[p]);
+            stsm_tile(to + (16 * LD + p * 16) * 2, dk[p]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int t = n % 2 * 8 + lane / 4, c = lane % 4 * 8;
+            const uint4 v = *reinterpret_cast<const uint4*>(tile + (n / 2 * 16 + t) * LD + c);
+            if (tb * 16 + t >= nt) continue;
+            IO* o = static_cast<IO*>(n < 2 ? a.dr : a.dk) + rows + (tb * 16 + t) * vs + i0 + c;
+            if (a.vec) {
+                *reinterpret_cast<uint4*>(o) = v;
+            } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    reinterpret_cast<unsigned short*>(o)[i] = static_cast<unsigned short>(w[i / 2] >> (16 * (i & 1)));
+            }
+        }
+    }
+}
+
+// dw of a segment from r . dr by the warps' rows (own), dv . v and <D, S> at its
+// end (border[1], a thread's share); all threads of the CTA.  <D, S> at its begin
+// follows from those, but in the first segment it is formed too: with an empty
+// state it is zero, and not what rounding leaves of the terms.
+template <int N, int PARTS>
+__device__ __forceinline__ void segment_rates(const Args& a, const Segment& sg, float (&own)[2], float (&border)[2], float* rdr,
+                                              const float* dvv, float* inner, const float* s_seg, const float* d_seg, int t_lo, int tid) {
+    constexpr int WARPS = 4 * PARTS, THREADS = 32 * WARPS;
+    const int lane = tid % 32, warp = tid / 32, nt = sg.nt;
+    const int64_t scalar = sg.scalar, seg = sg.seg;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        own[q] += __shfl_xor_sync(0xffffffffu, own[q], 1);
+        own[q] += __shfl_xor_sync(0xffffffffu, own[q], 2);
+        if (lane % 4 == 0) rdr[(warp / 4) * kSegment + t_lo + 8 * q] = own[q];
+    }
+    if (seg == 0) {
+        const float4* ps = reinterpret_cast<const float4*>(s_seg);
+        const float4* pd = reinterpret_cast<const float4*>(d_seg - N * N);
+#pragma unroll 4
+        for (int i = tid; i < N * N / 4; i += THREADS) {
+            const float4 u = __ldcg(ps + i), v = __ldcg(pd + i);
+            border[0] = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, border[0]))));
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) border[q] += __shfl_xor_sync(0xffffffffu, border[q], o);
+    if (lane == 0) inner[2 * warp] = border[0], inner[2 * warp + 1] = border[1];
+    __syncthreads();
+    // --- dw: the sum <Dn, S> from the segment's end backwards
+    if (warp == 0) {
+        float first = 0.f, end = 0.f;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) first += inner[2 * i], end += inner[2 * i + 1];
+        const int ta = 2 * lane;
+        float term[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int t = ta + q;
+            float x = rdr[t];
+#pragma unroll
+            for (int p = 1; p < PARTS; ++p) x += rdr[p * kSegment + t];
+            term[q] = t < nt ? x - dvv[t] : 0.f;
+        }
+        float x = term[0] + term[1];   // suffix sums over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const float y = __shfl_down_sync(0xffffffffu, x, o);
+            if (lane + o < 32) x += y;
+        }
+        float after = __shfl_down_sync(0xffffffffu, x, 1);
+        if (lane == 31) after = 0.f;
+        const float s1 = end + (after + term[1]), s0 = end + (after + (term[1] + term[0]));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int t = ta + q;
+            if (t >= nt) continue;
+            const int64_t at = scalar + t * a.H;
+            // a state that nothing is left of has no gradient, whatever the sum's rounding left
+            a.dw[at] = expf(-a.w[at]) == 0.f ? 0.f : t == 0 && seg == 0 ? -first : -(q ? s1 : s0);
+        }
+    }
+}
+
 template <typename IO, int N>
 __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO, N>::CTAS) delta_segment_kernel(const Args a) {
     using G = SegmentShape<IO, N>;
@@ -310,22 +547,15 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int tb = warp % 4, i0 = warp / 4 * G::IC;
 
-    const int64_t nseg = (a.T + kSegment - 1) / kSegment;
-    const int64_t head = blockIdx.x / nseg, seg = blockIdx.x % nseg;
-    const int64_t b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
-    const int64_t t0 = seg * kSegment;
-    const int nt = a.T - t0 < kSegment ? int(a.T - t0) : kSegment;
-    const int64_t ks = a.Hk * N, vs = a.H * N;
-    const int64_t rows = ((b * a.T + t0) * a.H + h) * N, keys = ((b * a.T + t0) * a.Hk + hk) * N;
-    const int64_t scalar = (b * a.T + t0) * a.H + h;
+    const Segment sg(a, N);
 
     pdl_wait();
 
     // what is read later, on its way to L2 now
-    const float* s_seg = a.s_seg + (head * (nseg + 1) + seg) * N * N;
-    const float* d_seg = a.d_seg + (head * (nseg + 1) + seg + 1) * N * N;
-    const IO* kp = static_cast<const IO*>(a.k) + keys;
-    const IO* rp = static_cast<const IO*>(a.r) + keys;
+    const float* s_seg = a.s_seg + sg.state;
+    const float* d_seg = a.d_seg + sg.state + N * N;
+    const IO* kp = static_cast<const IO*>(a.k) + sg.keys;
+    const IO* rp = static_cast<const IO*>(a.r) + sg.keys;
     for (int i = G::JB * N / 32 + tid; i < N * N / 32; i += G::THREADS) {
         prefetch_l2(s_seg + i * 32);
         prefetch_l2(s_seg + N * N + i * 32);
@@ -346,84 +576,20 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
 
     // --- the segment's rows: 16 / PARTS a warp
     constexpr int RW = 16 / G::PARTS;
-    const int row = warp * RW, left = nt - row;
+    const int row = warp * RW, left = sg.nt - row;
     const int64_t rr = left > 0 ? row : 0;   // rows behind the last token: zeros, addressed at one that exists
     const auto rows_at = [&](int r, int c) { return place(row + r, c); };
     if constexpr (KP == 1) {
-        copy_rows<IO, RW, N>(reinterpret_cast<IO*>(yb), rows_at, static_cast<const IO*>(a.dy) + rows + rr * vs, vs, left, a.vec, lane);
-        copy_rows<IO, RW, N>(reinterpret_cast<IO*>(kb), rows_at, kp + rr * ks, ks, left, a.vec, lane);
-        copy_rows<IO, RW, N>(reinterpret_cast<IO*>(rb), rows_at, rp + rr * ks, ks, left, a.vec, lane);
+        copy_rows<IO, RW, N>(reinterpret_cast<IO*>(yb), rows_at, static_cast<const IO*>(a.dy) + sg.rows + rr * sg.vs, sg.vs, left, a.vec, lane);
+        copy_rows<IO, RW, N>(reinterpret_cast<IO*>(kb), rows_at, kp + rr * sg.ks, sg.ks, left, a.vec, lane);
+        copy_rows<IO, RW, N>(reinterpret_cast<IO*>(rb), rows_at, rp + rr * sg.ks, sg.ks, left, a.vec, lane);
         cp_async_commit();
     }
-    {
-        constexpr int ROWV = N / 4, ALL = RW * ROWV / 32, U = ALL < 8 ? ALL : 8;
-#pragma unroll 1
-        for (int n = 0; n < ALL; n += U) {
-            // all loads first, of a row that exists; rows behind the last token are zeroed after
-            float4 x[U], y[U], v[U];
-            uint2 vr[U];
-            float be[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = lane + (n + u) * 32, t = i / ROWV, c = (i % ROWV) * 4;
-                const int64_t at = rows + (t < left ? row + t : 0) * vs + c;
-                be[u] = __ldg(a.beta + scalar + (t < left ? row + t : 0) * a.H);
-                x[u] = load4(a.e + at, true);
-                y[u] = load4(a.du + at, true);
-                const IO* vp = static_cast<const IO*>(a.v) + at;
-                if constexpr (KP == 3) {
-                    v[u] = load4(reinterpret_cast<const float*>(vp), a.vec);
-                } else if (a.vec) {
-                    vr[u] = __ldg(reinterpret_cast<const uint2*>(vp));
-                } else {
-                    const unsigned short* q = reinterpret_cast<const unsigned short*>(vp);
-                    vr[u] = make_uint2(q[0] | uint32_t(q[1]) << 16, q[2] | uint32_t(q[3]) << 16);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = lane + (n + u) * 32, t = i / ROWV, c = (i % ROWV) * 4;
-                if constexpr (KP == 1)
-                    v[u] = make_float4(__uint_as_float(vr[u].x << 16), __uint_as_float(vr[u].x & 0xffff0000u),
-                                       __uint_as_float(vr[u].y << 16), __uint_as_float(vr[u].y & 0xffff0000u));
-                if (t >= left) x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                const float bt = be[u];
-                float s = fmaf(x[u].x, y[u].x, fmaf(x[u].y, y[u].y, fmaf(x[u].z, y[u].z, x[u].w * y[u].w)));
-                float z = fmaf(v[u].x, y[u].x, fmaf(v[u].y, y[u].y, fmaf(v[u].z, y[u].z, v[u].w * y[u].w)));
-#pragma unroll
-                for (int o = ROWV / 2; o > 0; o /= 2) {
-                    s += __shfl_xor_sync(0xffffffffu, s, o);
-                    z += __shfl_xor_sync(0xffffffffu, z, o);
-                }
-                if (lane % ROWV == 0) {
-                    if (t < left) a.dbeta[scalar + (row + t) * a.H] = s;
-                    dvv[row + t] = bt * z;
-                }
-                put4<3>(ub + place(row + t, c), G::PIECE, make_float4(bt * x[u].x, bt * x[u].y, bt * x[u].z, bt * x[u].w));
-                put4<PP>(db + place(row + t, c), G::PIECE, make_float4(bt * y[u].x, bt * y[u].y, bt * y[u].z, bt * y[u].w));
-            }
-        }
-    }
+    stage_values<IO, N, RW, PP>(a, sg, ub, db, G::PIECE, place, row, dvv, lane);
     if constexpr (KP == 3)
-        split_rows<RW, N, 3>(yb, rows_at, G::PIECE, reinterpret_cast<const float*>(a.dy) + rows + rr * vs, vs, left, a.vec, lane);
-    if (warp == 0) {   // the decays' running sum, two tokens a lane
-        const int ta = 2 * lane;
-        const float w0 = ta < nt ? a.w[scalar + ta * a.H] : 0.f, w1 = ta + 1 < nt ? a.w[scalar + (ta + 1) * a.H] : 0.f;
-        const double x0 = w0 > kMaxRate ? kMaxRate : w0, x1 = x0 + double(w1 > kMaxRate ? kMaxRate : w1);
-        double x = x1;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const double y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        sums[ta] = two_floats(x - x1 + x0);
-        sums[ta + 1] = two_floats(x);
-    }
+        split_rows<RW, N, 3>(yb, rows_at, G::PIECE, reinterpret_cast<const float*>(a.dy) + sg.rows + rr * sg.vs, sg.vs, left, a.vec, lane);
+    if (warp == 0) segment_sums(a, sg, sums, lane);
 
-    // the inner products <D, S> at the segment's borders.  The one at its begin
-    // follows from the one at its end and the segment's terms, but in the first
-    // segment it is formed too: with an empty state it is zero, and not what
-    // rounding leaves of the terms.
     float border[2] = {0.f, 0.f};
     // --- the products with S and D: C[t][i], tiles of 16 channels
     float dr[NP][2][4], dk[NP][2][4];
@@ -492,12 +658,12 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
             }
     }
     __syncthreads();
-    if constexpr (KP == 3) {   // K and R over the rows
-        split_rows<RW, N, 3>(kb, rows_at, G::PIECE, reinterpret_cast<const float*>(kp) + rr * ks, ks, left, a.vec, lane);
-        split_rows<RW, N, 3>(rb, rows_at, G::PIECE, reinterpret_cast<const float*>(rp) + rr * ks, ks, left, a.vec, lane);
+    if constexpr (KP == 3) {   // K and R over the sg.rows
+        split_rows<RW, N, 3>(kb, rows_at, G::PIECE, reinterpret_cast<const float*>(kp) + rr * sg.ks, sg.ks, left, a.vec, lane);
+        split_rows<RW, N, 3>(rb, rows_at, G::PIECE, reinterpret_cast<const float*>(rp) + rr * sg.ks, sg.ks, left, a.vec, lane);
         __syncthreads();
     }
-    // dr takes K by the rows of the blocks, dk K by rows and columns and R by columns
+    // dr takes K by the sg.rows of the blocks, dk K by sg.rows and columns and R by columns
     const auto times_dk = [&](float (&d)[2][4], const uint32_t (&a)[PP][4], const uint32_t (&f)[KP][4]) {
         if constexpr (KP == 1) {   // a bfloat16 output: into its sum at once
             times_sum<PP, KP, PP>(d, false, a, f);
@@ -547,125 +713,10 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
             }
         }
     }
-    float own[2] = {0.f, 0.f};   // r . dr of the lane's rows
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const __nv_bfloat16* r2 = rb + place(t_lo + 8 * q, i0 + p * 16 + 8 * n + 2 * (lane % 4));
-                float x0 = 0.f, x1 = 0.f;
-#pragma unroll
-                for (int c = KP - 1; c >= 0; --c) {
-                    const uint32_t w2 = *reinterpret_cast<const uint32_t*>(r2 + c * G::PIECE);
-                    x0 += __uint_as_float(w2 << 16), x1 += __uint_as_float(w2 & 0xffff0000u);
-                }
-                own[q] = fmaf(x0, dr[p][n][2 * q], fmaf(x1, dr[p][n][2 * q + 1], own[q]));
-            }
-    // --- the outputs
-    const bool whole = a.H == a.Hk;
-    if (!whole || KP == 3) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int t = t_lo + 8 * q;
-            if (t >= nt) continue;
-            const int64_t at = rows + t * vs + i0 + 2 * (lane % 4);
-            float* orr = (whole ? static_cast<float*>(a.dr) : a.drh) + at;
-            float* ok = (whole ? static_cast<float*>(a.dk) : a.dkh) + at;
-            const bool pairs = !whole || a.vec;
-#pragma unroll
-            for (int c = 0; c < 2 * NP; ++c) {
-                const float *x = &dr[c / 2][c % 2][2 * q], *y = &dk[c / 2][c % 2][2 * q];
-                if (pairs) {
-                    *reinterpret_cast<float2*>(orr + 8 * c) = make_float2(x[0], x[1]);
-                    *reinterpret_cast<float2*>(ok + 8 * c) = make_float2(y[0], y[1]);
-                } else {
-                    orr[8 * c] = x[0], orr[8 * c + 1] = x[1];
-                    ok[8 * c] = y[0], ok[8 * c + 1] = y[1];
-                }
-            }
-        }
-    } else if constexpr (KP == 1) {   // through rows of the warp's own (where u was) to 16-byte stores
-        constexpr int LD = G::IC + 8;
-        __nv_bfloat16* tile = ub + warp * 2 * 16 * LD;
-        const uint32_t to = smem_u32(tile + ((lane & 7) + ((lane >> 3) & 1) * 8) * LD + (lane >> 4) * 8);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            stsm_tile(to + p * 32, dr[p]);
-            stsm_tile(to + (16 * LD + p * 16) * 2, dk[p]);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int t = n % 2 * 8 + lane / 4, c = lane % 4 * 8;
-            const uint4 v = *reinterpret_cast<const uint4*>(tile + (n / 2 * 16 + t) * LD + c);
-            if (tb * 16 + t >= nt) continue;
-            IO* o = static_cast<IO*>(n < 2 ? a.dr : a.dk) + rows + (tb * 16 + t) * vs + i0 + c;
-            if (a.vec) {
-                *reinterpret_cast<uint4*>(o) = v;
-            } else {
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    reinterpret_cast<unsigned short*>(o)[i] = static_cast<unsigned short>(w[i / 2] >> (16 * (i & 1)));
-            }
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        own[q] += __shfl_xor_sync(0xffffffffu, own[q], 1);
-        own[q] += __shfl_xor_sync(0xffffffffu, own[q], 2);
-        if (lane % 4 == 0) rdr[(warp / 4) * kSegment + t_lo + 8 * q] = own[q];
-    }
-    if (seg == 0) {
-        const float4* ps = reinterpret_cast<const float4*>(s_seg);
-        const float4* pd = reinterpret_cast<const float4*>(d_seg - N * N);
-#pragma unroll 4
-        for (int i = tid; i < N * N / 4; i += G::THREADS) {
-            const float4 u = __ldcg(ps + i), v = __ldcg(pd + i);
-            border[0] = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, border[0]))));
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) border[q] += __shfl_xor_sync(0xffffffffu, border[q], o);
-    if (lane == 0) inner[2 * warp] = border[0], inner[2 * warp + 1] = border[1];
-    __syncthreads();
-    // --- dw: the sum <Dn, S> from the segment's end backwards
-    if (warp == 0) {
-        float first = 0.f, end = 0.f;
-#pragma unroll
-        for (int i = 0; i < G::WARPS; ++i) first += inner[2 * i], end += inner[2 * i + 1];
-        const int ta = 2 * lane;
-        float term[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int t = ta + q;
-            float x = rdr[t];
-#pragma unroll
-            for (int p = 1; p < G::PARTS; ++p) x += rdr[p * kSegment + t];
-            term[q] = t < nt ? x - dvv[t] : 0.f;
-        }
-        float x = term[0] + term[1];   // suffix sums over the lanes
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const float y = __shfl_down_sync(0xffffffffu, x, o);
-            if (lane + o < 32) x += y;
-        }
-        float after = __shfl_down_sync(0xffffffffu, x, 1);
-        if (lane == 31) after = 0.f;
-        const float s1 = end + (after + term[1]), s0 = end + (after + (term[1] + term[0]));
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int t = ta + q;
-            if (t >= nt) continue;
-            const int64_t at = scalar + t * a.H;
-            // a state that nothing is left of has no gradient, whatever the sum's rounding left
-            a.dw[at] = expf(-a.w[at]) == 0.f ? 0.f : t == 0 && seg == 0 ? -first : -(q ? s1 : s0);
-        }
-    }
+    float own[2];
+    row_products<N, NP, KP>(own, rb, G::PIECE, dr, t_lo, i0, lane);
+    store_rows<IO, N, NP>(a, sg, dr, dk, ub + warp * 2 * 16 * (G::IC + 8), tb, i0, lane);
+    segment_rates<N, G::PARTS>(a, sg, own, border, rdr, dvv, inner, s_seg, d_seg, t_lo, tid);
 }
 
 // dr and dk of a key head: the sums over the value heads that share it, in
