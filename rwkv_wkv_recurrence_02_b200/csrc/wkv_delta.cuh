@@ -62,7 +62,7 @@ struct Args {
     // its workspace
     float* e;            // (B, T, H, N)
     float* du;
-    float* s_seg;        // (B, H, n + 1, N, N), n = ceil(T / kSegment): the state entering each segment and the last, [value][key]
+    float* s_seg;        // (B, H, n + 1, N, N), n = ceil(T / kSegment): the state entering each segment and the last (keep_state)
     float* d_seg;        // gradients of those, of what follows
     float* drh;          // (B, T, H, N): dr and dk of each value head, where heads share keys
     float* dkh;

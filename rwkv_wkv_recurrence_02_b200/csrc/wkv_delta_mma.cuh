@@ -537,8 +537,9 @@ __device__ __forceinline__ void store_state(float* s, const float (&S)[N / 8][4]
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[(8 * n + 2 * (lane % 4) + (i & 1)) * N + lane / 4 + (i >> 1) * 8] = S[n][i];
 }
-// The segments' kernel of the reverse mode: tcgen05.mma (wkv_delta_tc.cuh), or
-// mma.sync, as heads of other sizes and float32 take.
+// The segments' kernel of the reverse mode: tcgen05.mma (wkv_delta_tc.cuh; 1580 us
+// for 8 x 4096 tokens of 32 heads, 1656 with mma.sync), or mma.sync, as heads of
+// other sizes and float32 take: their tiles are half empty or do not fit two CTAs.
 template <typename IO, int N>
 constexpr bool kTcSegments = N == 64 && sizeof(IO) == 2;
 // The states between segments as that kernel reads them: S[key][value], or

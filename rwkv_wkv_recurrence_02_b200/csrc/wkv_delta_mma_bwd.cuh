@@ -20,12 +20,12 @@
 // What only reaches dk takes the orders that its type keeps; dr takes them
 // all, as r.dr enters dw.
 //
-// Measured, bfloat16: 8 x 4096 tokens of 32 heads of 64 1630 us (reads and writes
+// Measured, bfloat16: 8 x 4096 tokens of 32 heads of 64 1580 us (reads and writes
 // alone: 150), the walks 820 to 880 of it, bound as the forward is, the segments
-// the rest: shared memory's wavefronts (67% of their peak) and latency at 16
-// warps an SM, DRAM 26%.  2047 tokens of 16 heads of 128, 8 key heads: 317 us.
+// the rest (wkv_delta_tc.cuh).  2047 tokens of 16 heads of 128, 8 key heads: 317 us,
+// its segments bound by shared memory's wavefronts (67% of their peak) and latency.
 // The two walks one after the other took 671 us on 4096 tokens of 32 heads of
-// 64; side by side all three kernels take 396.
+// 64; side by side all three kernels take 383.
 #pragma once
 
 #include "wkv_delta_mma.cuh"
@@ -229,9 +229,9 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
 // segment's 16 x 16 blocks of (token, token) products.  A block is formed once,
 // by one warp, and read from shared memory as it lies and transposed.
 // ---------------------------------------------------------------------------
-// 16 x 32 of a warp's (8 warps a CTA, two CTAs an SM for heads of 64) is as fast
-// as 16 x 64 (4 warps, three CTAs: 410 us for 8 x 2048 tokens of 32 heads) and
-// faster for heads of 128 (319 against 330 us for the whole call).
+// 16 x 32 of a warp's: 319 us for 2047 tokens of 16 heads of 128 (the whole call),
+// 330 with 16 x 64, whose warps are half as many.  Bfloat16 heads of 64 take
+// wkv_delta_tc.cuh's kernel.
 template <typename IO, int N>
 struct SegmentShape {
     static constexpr int KP = sizeof(IO) == 2 ? 1 : 3, PP = kOutOrders<IO>;
@@ -296,10 +296,12 @@ struct Segment {
     int64_t state;               // of its first state among those between segments
     int64_t rows, keys, scalar;  // of its first token in values, keys and per-head scalars
     int nt;                      // tokens
-    __device__ __forceinline__ Segment(const Args& a, int N) {
+    __device__ __forceinline__ Segment(const Args& a, int N, int64_t block) {
         const int64_t nseg = (a.T + kSegment - 1) / kSegment;
-        head = blockIdx.x / nseg, seg = blockIdx.x % nseg;
-        const int64_t b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk), t0 = seg * kSegment;
+        // heads first: neighbours in memory are worked on at the same time
+        seg = block / a.H % nseg;
+        const int64_t b = block / (a.H * nseg), h = block % a.H, hk = h / (a.H / a.Hk), t0 = seg * kSegment;
+        head = b * a.H + h;
         nt = a.T - t0 < kSegment ? int(a.T - t0) : kSegment;
         ks = a.Hk * N, vs = a.H * N;
         state = (head * (nseg + 1) + seg) * N * N;
@@ -365,8 +367,8 @@ __device__ __forceinline__ void stage_values(const Args& a, const Segment& sg, _
     }
 }
 
-// the decays' running sum, two tokens a lane (one warp)
-__device__ __forceinline__ void segment_sums(const Args& a, const Segment& sg, float2* sums, int lane) {
+// the decays' running sum, two tokens a lane (one warp); returns their rates
+__device__ __forceinline__ float2 segment_sums(const Args& a, const Segment& sg, float2* sums, int lane) {
     const int64_t scalar = sg.scalar;
     const int nt = sg.nt;
     const int ta = 2 * lane;
@@ -380,6 +382,7 @@ __device__ __forceinline__ void segment_sums(const Args& a, const Segment& sg, f
     }
     sums[ta] = two_floats(x - x1 + x0);
     sums[ta + 1] = two_floats(x);
+    return make_float2(w0, w1);
 }
 
 // own: r . dr of the lane's two rows over its warp's channels (R's pieces staged)
@@ -463,12 +466,14 @@ __device__ __forceinline__ void store_rows(const Args& a, const Segment& sg, con
 }
 
 // dw of a segment from r . dr by the warps' rows (own), dv . v and <D, S> at its
-// end (border[1], a thread's share); all threads of the CTA.  <D, S> at its begin
+// end (border[1], a thread's share); rates: warp 0's, of two tokens a lane.  All
+// threads of the CTA.  <D, S> at its begin
 // follows from those, but in the first segment it is formed too: with an empty
 // state it is zero, and not what rounding leaves of the terms.
 template <int N, int PARTS>
 __device__ __forceinline__ void segment_rates(const Args& a, const Segment& sg, float (&own)[2], float (&border)[2], float* rdr,
-                                              const float* dvv, float* inner, const float* s_seg, const float* d_seg, int t_lo, int tid) {
+                                              const float* dvv, float* inner, const float* s_seg, const float* d_seg, int t_lo, float2 rates,
+                                              int tid) {
     constexpr int WARPS = 4 * PARTS, THREADS = 32 * WARPS;
     const int lane = tid % 32, warp = tid / 32, nt = sg.nt;
     const int64_t scalar = sg.scalar, seg = sg.seg;
@@ -523,7 +528,7 @@ __device__ __forceinline__ void segment_rates(const Args& a, const Segment& sg, 
             if (t >= nt) continue;
             const int64_t at = scalar + t * a.H;
             // a state that nothing is left of has no gradient, whatever the sum's rounding left
-            a.dw[at] = expf(-a.w[at]) == 0.f ? 0.f : t == 0 && seg == 0 ? -first : -(q ? s1 : s0);
+            a.dw[at] = expf(-(q ? rates.y : rates.x)) == 0.f ? 0.f : t == 0 && seg == 0 ? -first : -(q ? s1 : s0);
         }
     }
 }
@@ -547,7 +552,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int tb = warp % 4, i0 = warp / 4 * G::IC;
 
-    const Segment sg(a, N);
+    const Segment sg(a, N, blockIdx.x);
 
     pdl_wait();
 
@@ -588,7 +593,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     stage_values<IO, N, RW, PP>(a, sg, ub, db, G::PIECE, place, row, dvv, lane);
     if constexpr (KP == 3)
         split_rows<RW, N, 3>(yb, rows_at, G::PIECE, reinterpret_cast<const float*>(a.dy) + sg.rows + rr * sg.vs, sg.vs, left, a.vec, lane);
-    if (warp == 0) segment_sums(a, sg, sums, lane);
+    const float2 rates = warp == 0 ? segment_sums(a, sg, sums, lane) : make_float2(0.f, 0.f);
 
     float border[2] = {0.f, 0.f};
     // --- the products with S and D: C[t][i], tiles of 16 channels
@@ -716,7 +721,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     float own[2];
     row_products<N, NP, KP>(own, rb, G::PIECE, dr, t_lo, i0, lane);
     store_rows<IO, N, NP>(a, sg, dr, dk, ub + warp * 2 * 16 * (G::IC + 8), tb, i0, lane);
-    segment_rates<N, G::PARTS>(a, sg, own, border, rdr, dvv, inner, s_seg, d_seg, t_lo, tid);
+    segment_rates<N, G::PARTS>(a, sg, own, border, rdr, dvv, inner, s_seg, d_seg, t_lo, rates, tid);
 }
 
 // dr and dk of a key head: the sums over the value heads that share it, in

@@ -13,8 +13,20 @@
 // Operands are bfloat16 pieces (u and S three, dv and D two, dy, k and r exact),
 // products of pieces smallest first into one accumulator, as many as the mma.sync
 // form takes.  All tiles are K-major without swizzle: 16-byte slots of 8 values,
-// core matrices of 8 rows; a slot of padding behind each pair of core matrices and two
-// behind each k step keep the stores of a warp in different banks.
+// core matrices of 8 rows; a slot of padding behind each pair of core matrices and
+// two behind each k step keep the stores of a warp in different banks.
+//
+// Measured for 8 x 2048 tokens of 32 heads (8192 segments): 395 us, as mma.sync 423;
+// the whole call on 8 x 4096 tokens 1580 us against 1656.  What bounds it is a
+// CTA's chain at two CTAs an SM, about 22,000 cycles: loads and their conversion
+// 9,000, the three batches 6,500 (an M = 64 product of 16 columns reads 4 KB of shared
+// memory), scores 2,500, outputs 3,500; DRAM is at 28%, issue at 36%.  Four steps of
+// it: descriptors by sums (68 to 50 cycles a product issued), the rates kept from
+// the sums for dw, the next CTA's data prefetched while batch 1 runs (404 to 395;
+// at the start of the CTA, with its own loads, no gain), heads before segments in
+// the grid's order (neighbours in memory at the same time, 430 to 417 as it was
+// then).  The scores first and S and D staged under them was slower (413 against
+// 408), and so were more loads in flight (405 against 395).
 #pragma once
 
 #include "wkv_chunk.cuh"
@@ -46,15 +58,15 @@ struct TcSegment {
 __device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
     return uint64_t((addr >> 4) & 0x3fffu) | uint64_t(TcSegment::LBO) << 16 | uint64_t(TcSegment::SBO) << 32 | uint64_t(1) << 46;
 }
-// d (+)= A B^T, tiles at shared addresses a and b (one thread)
-__device__ __forceinline__ void tile_product(uint32_t d, uint32_t a, uint32_t b, bool first) {
+// d (+)= A B^T, a and b the tiles' descriptors (one thread).  A descriptor's
+// address is its low field, in slots: those of other tiles and k steps are sums.
+__device__ __forceinline__ void tile_product(uint32_t d, uint64_t a, uint64_t b, bool first) {
 #pragma unroll
     for (int s = 0; s < 4; ++s)
         asm volatile(
             "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
             "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(tile_desc(a + TcSegment::KS * 16 * s)), "l"(tile_desc(b + TcSegment::KS * 16 * s)), "r"(TcSegment::IDESC),
-            "r"(first && s == 0 ? 0u : 1u)
+            "l"(a + TcSegment::KS * s), "l"(b + TcSegment::KS * s), "r"(TcSegment::IDESC), "r"(first && s == 0 ? 0u : 1u)
             : "memory");
 }
 __device__ __forceinline__ void tile_commit(uint64_t* bar) {
@@ -89,6 +101,9 @@ __device__ __forceinline__ void load_tile(uint32_t addr, float (&x)[2][2][4]) {
         for (int i = 0; i < 4; ++i) x[g / 2][g % 2][i] = __uint_as_float(r[4 * g + i]);
 }
 
+// the CTA that follows this one on its SM, about: two CTAs on each of 148 SMs
+constexpr int kAhead = 296;
+
 __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel(const Args a) {
     using G = TcSegment;
     using IO = __nv_bfloat16;
@@ -108,7 +123,7 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     // the warp's tokens and channels (and, of scores, columns)
     const int tb = warp % 4, i0 = warp / 4 * 32, t_lo = tb * 16 + lane / 4;
-    const Segment sg(a, N);
+    const Segment sg(a, N, blockIdx.x);
 
     if (tid == 0) {
 #pragma unroll
@@ -145,7 +160,7 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
     copy_rows<IO, 8, N>(rr, raw_at, static_cast<const IO*>(a.r) + sg.keys + first * sg.ks, sg.ks, left, a.vec, lane);
     cp_async_commit();
     stage_values<IO, N, 8, 2>(a, sg, tiles + G::U * PC, tiles + G::V * PC, PC, at, row, dvv, lane);
-    if (warp == 0) segment_sums(a, sg, sums, lane);
+    const float2 rates = warp == 0 ? segment_sums(a, sg, sums, lane) : make_float2(0.f, 0.f);
     float border[2] = {0.f, 0.f};
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -162,8 +177,8 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
     before_batch();
 
     const uint32_t acc = slot, mine = acc + (uint32_t(32 * tb) << 16) + i0;   // this warp's rows and columns
-    const uint32_t t0 = smem_u32(tiles);
-    const auto tile = [&](int i) { return t0 + i * G::TILE; };
+    const uint64_t t0 = tile_desc(smem_u32(tiles));
+    const auto tile = [&](int i) { return t0 + i * (G::TILE / 16); };
     if (tid == 0) {
 #pragma unroll
         for (int p = 2; p >= 0; --p) tile_product(acc, tile(G::Y), tile(G::S + p), p == 2);
@@ -176,6 +191,20 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
 #pragma unroll
         for (int p = 2; p >= 0; --p) tile_product(acc + 192, tile(G::Y), tile(G::U + p), p == 2);
         tile_commit(&bar[0]);
+    }
+    // what that CTA will read, on its way to L2
+    {
+        const Segment nx(a, N, int64_t(blockIdx.x) + kAhead);
+        if (nx.head < a.B * a.H) {
+            const float* lines[2] = {a.s_seg + nx.state, a.d_seg + nx.state + N * N};
+            prefetch_l2(lines[tid / 128] + tid % 128 * 32);
+            const int t = tid / 4;
+            if (t < nx.nt) {
+                prefetch_l2((tid & 2 ? a.du : a.e) + nx.rows + t * nx.vs + (tid & 1) * 32);
+                prefetch_l2(static_cast<const IO*>(tid & 2 ? (tid & 1 ? a.k : a.r) : (tid & 1 ? a.v : a.dy)) +
+                            (tid & 2 ? nx.keys + t * nx.ks : nx.rows + t * nx.vs));
+            }
+        }
     }
     float g[2], q[2];   // decays of the lane's two rows, up to them and after
 #pragma unroll
@@ -303,7 +332,7 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
     row_products<N, 2, 1>(own, rr, 0, dr, t_lo, i0, lane);
     store_rows<IO, N, 2>(a, sg, dr, dk, tiles + G::U * PC + warp * 2 * 16 * 40, tb, i0, lane);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    segment_rates<N, G::PARTS>(a, sg, own, border, rdr, dvv, inner, s_seg, d_seg, t_lo, tid);
+    segment_rates<N, G::PARTS>(a, sg, own, border, rdr, dvv, inner, s_seg, d_seg, t_lo, rates, tid);
     if (warp == 0) {   // every warp's loads are done: the barrier in segment_rates
         after_batch();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(acc), "r"(G::COLS) : "memory");
