@@ -539,7 +539,8 @@ __device__ __forceinline__ void store_state(float* s, const float (&S)[N / 8][4]
 }
 // The segments' kernel of the reverse mode: tcgen05.mma (wkv_delta_tc.cuh; 1580 us
 // for 8 x 4096 tokens of 32 heads, 1656 with mma.sync), or mma.sync, as heads of
-// other sizes and float32 take: their tiles are half empty or do not fit two CTAs.
+// other sizes and float32 take: heads of 128 and float32's pieces need more tiles
+// than two CTAs an SM have room for, heads of 32 would leave half of each unused.
 template <typename IO, int N>
 constexpr bool kTcSegments = N == 64 && sizeof(IO) == 2;
 // The states between segments as that kernel reads them: S[key][value], or

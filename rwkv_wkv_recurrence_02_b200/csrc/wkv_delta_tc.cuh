@@ -20,13 +20,13 @@
 // the whole call on 8 x 4096 tokens 1580 us against 1656.  What bounds it is a
 // CTA's chain at two CTAs an SM, about 22,000 cycles: loads and their conversion
 // 9,000, the three batches 6,500 (an M = 64 product of 16 columns reads 4 KB of shared
-// memory), scores 2,500, outputs 3,500; DRAM is at 28%, issue at 36%.  Four steps of
-// it: descriptors by sums (68 to 50 cycles a product issued), the rates kept from
-// the sums for dw, the next CTA's data prefetched while batch 1 runs (404 to 395;
-// at the start of the CTA, with its own loads, no gain), heads before segments in
-// the grid's order (neighbours in memory at the same time, 430 to 417 as it was
-// then).  The scores first and S and D staged under them was slower (413 against
-// 408), and so were more loads in flight (405 against 395).
+// memory), scores 2,500, outputs 3,500; DRAM is at 28%, issue at 36%.  Steps, as
+// the whole call's time: heads before segments in the grid's order (neighbours in
+// memory at the same time) 1665 to 1637, descriptors by sums 1637 to 1617, dw's rates
+// kept from the decays' sums 1617 to 1600, the next CTA's data prefetched while
+// batch 1 runs 1600 to 1587 (with the CTA's own loads: no gain).  The scores' batch
+// first, with S and D staged under it, was slower (413 against 408 us of this
+// kernel), and so were more loads in flight (405 against 395).
 #pragma once
 
 #include "wkv_chunk.cuh"
