@@ -94,7 +94,9 @@ delta_step_kernel(int64_t heads, int64_t Hk, int64_t H, const float* __restrict_
     if (id >= heads * PARTS) return;
     const int64_t hh = id / PARTS;
     const int col = int(id % PARTS) * CW + (lane % CL) * 4, row = lane / CL * R;
-    const int64_t hk = hh / H * Hk + hh % H / (H / Hk);
+    // 32-bit divisions: 2^32 heads' states would be 16 TB
+    const uint32_t h32 = uint32_t(hh), H32 = uint32_t(H), row0 = h32 / H32;
+    const int64_t hk = int64_t(row0) * Hk + (h32 - row0 * H32) / (H32 / uint32_t(Hk));
     float* sp = state + hh * N * N + row * N + col;
     float4 s[R];
     if (vec) {

@@ -537,8 +537,8 @@ __device__ __forceinline__ void store_state(float* s, const float (&S)[N / 8][4]
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[(8 * n + 2 * (lane % 4) + (i & 1)) * N + lane / 4 + (i >> 1) * 8] = S[n][i];
 }
-// The segments' kernel of the reverse mode: tcgen05.mma (wkv_delta_tc.cuh; 1580 us
-// for 8 x 4096 tokens of 32 heads, 1656 with mma.sync), or mma.sync, as heads of
+// The segments' kernel of the reverse mode: tcgen05.mma (wkv_delta_tc.cuh; 1587 us
+// for 8 x 4096 tokens of 32 heads where mma.sync took 1656), or mma.sync, as heads of
 // other sizes and float32 take: heads of 128 and float32's pieces need more tiles
 // than two CTAs an SM have room for, heads of 32 would leave half of each unused.
 template <typename IO, int N>

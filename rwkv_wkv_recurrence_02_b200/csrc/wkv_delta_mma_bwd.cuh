@@ -20,12 +20,12 @@
 // What only reaches dk takes the orders that its type keeps; dr takes them
 // all, as r.dr enters dw.
 //
-// Measured, bfloat16: 8 x 4096 tokens of 32 heads of 64 1580 us (reads and writes
+// Measured, bfloat16: 8 x 4096 tokens of 32 heads of 64 1540 us (reads and writes
 // alone: 150), the walks 820 to 880 of it, bound as the forward is, the segments
-// the rest (wkv_delta_tc.cuh).  2047 tokens of 16 heads of 128, 8 key heads: 317 us,
+// the rest (wkv_delta_tc.cuh).  2047 tokens of 16 heads of 128, 8 key heads: 312 us,
 // its segments bound by shared memory's wavefronts (67% of their peak) and latency.
 // The two walks one after the other took 671 us on 4096 tokens of 32 heads of
-// 64; side by side all three kernels take 383.
+// 64; side by side all three kernels take 379.
 #pragma once
 
 #include "wkv_delta_mma.cuh"
@@ -297,10 +297,12 @@ struct Segment {
     int64_t rows, keys, scalar;  // of its first token in values, keys and per-head scalars
     int nt;                      // tokens
     __device__ __forceinline__ Segment(const Args& a, int N, int64_t block) {
-        const int64_t nseg = (a.T + kSegment - 1) / kSegment;
-        // heads first: neighbours in memory are worked on at the same time
-        seg = block / a.H % nseg;
-        const int64_t b = block / (a.H * nseg), h = block % a.H, hk = h / (a.H / a.Hk), t0 = seg * kSegment;
+        // heads first: neighbours in memory are worked on at the same time.  All of
+        // these fit 32 bits, as the grid does.
+        const uint32_t H = uint32_t(a.H), nseg = uint32_t((a.T + kSegment - 1) / kSegment), id = uint32_t(block);
+        const uint32_t q = id / H, h = id - q * H, hk = h / (H / uint32_t(a.Hk)), b32 = q / nseg;
+        seg = q - b32 * nseg;
+        const int64_t b = b32, t0 = seg * kSegment;
         head = b * a.H + h;
         nt = a.T - t0 < kSegment ? int(a.T - t0) : kSegment;
         ks = a.Hk * N, vs = a.H * N;
@@ -732,7 +734,7 @@ __global__ void __launch_bounds__(256) delta_share_kernel(const Args a) {
     pdl_wait();
     if (id >= a.B * a.T * a.Hk * (N / 4)) return;
     const int64_t key = id / (N / 4);   // (sequence, token, key head)
-    const int share = int(a.H / a.Hk), c = int(id % (N / 4)) * 4;
+    const int share = int(uint32_t(a.H) / uint32_t(a.Hk)), c = int(id % (N / 4)) * 4;
     const float* pr = a.drh + key * share * N + c;
     const float* pk = a.dkh + key * share * N + c;
     float4 r = make_float4(0.f, 0.f, 0.f, 0.f), k = r;

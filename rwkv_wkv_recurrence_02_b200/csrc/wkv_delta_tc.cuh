@@ -17,14 +17,15 @@
 // two behind each k step keep the stores of a warp in different banks.
 //
 // Measured for 8 x 2048 tokens of 32 heads (8192 segments): 395 us, as mma.sync 423;
-// the whole call on 8 x 4096 tokens 1580 us against 1656.  What bounds it is a
+// the whole call on 8 x 4096 tokens 1587 us against 1656, and 1542 since.  What bounds it is a
 // CTA's chain at two CTAs an SM, about 22,000 cycles: loads and their conversion
 // 9,000, the three batches 6,500 (an M = 64 product of 16 columns reads 4 KB of shared
 // memory), scores 2,500, outputs 3,500; DRAM is at 28%, issue at 36%.  Steps, as
 // the whole call's time: heads before segments in the grid's order (neighbours in
 // memory at the same time) 1665 to 1637, descriptors by sums 1637 to 1617, dw's rates
 // kept from the decays' sums 1617 to 1600, the next CTA's data prefetched while
-// batch 1 runs 1600 to 1587 (with the CTA's own loads: no gain).  The scores' batch
+// batch 1 runs 1600 to 1587 (with the CTA's own loads: no gain), 32-bit divisions
+// for the CTA's place 1581 to 1542.  The scores' batch
 // first, with S and D staged under it, was slower (413 against 408 us of this
 // kernel), and so were more loads in flight (405 against 395).
 #pragma once
