@@ -211,9 +211,8 @@ class Workspace:
         _launch(buf.device, "wkv_workspace_init", lib().wkv_workspace_init, self._aligned_ptr(buf), nbytes,
                 _stream_ptr(stream, buf.device))
 
-    @staticmethod
-    def _aligned_ptr(buf):
-        return (buf.data_ptr() + 255) & ~255
+    def _aligned_ptr(self, buf=None):
+        return ((self.buf if buf is None else buf).data_ptr() + 255) & ~255
 
     def status(self, stream=None) -> int:
         for buf in (self.buf, self.plain):
