@@ -1,4 +1,5 @@
-"""B200 (sm_100a) RWKV-4 WKV operator: Python binding of libwkv.so.
+"""B200 (sm_100a) RWKV WKV operators, gated delta rule and group norm: Python
+binding of libwkv.so.
 
 The binding only marshals arguments: every step of the operator runs in the
 CUDA kernels behind the C ABI declared in ``include/wkv.h``.  There is no CPU
@@ -180,7 +181,8 @@ class Workspace:
     without clearing.  Calls that share one Workspace must be ordered on the
     GPU (the default: the current stream).  The delta rule's and the group
     norm's calls have a buffer of their own in it, whose contents mean nothing
-    between calls."""
+    between calls.  A call that needs more than a buffer holds replaces it: a
+    CUDA graph captured with the old one has to be captured again."""
 
     def __init__(self, device=None):
         self.device = device
