@@ -681,52 +681,52 @@ __device__ __forceinline__ void forward_walk(const Args& a, char* smem, int64_t 
         const int64_t ks = a.Hk * N;
         G g(smem, st);
         for (; next_task<PARTS, G::THREADS>(a, walks, block, task, first); first = false) {
-        const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
-        const int64_t begin = PARTS ? task.part * a.part_len : 0;
-    const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
-        const IO* kp = static_cast<const IO*>(a.k) + (b * a.T * a.Hk + hk) * N;
-        const IO* rp = static_cast<const IO*>(a.r) + (b * a.T * a.Hk + hk) * N;
-        const IO* vp = static_cast<const IO*>(a.v) + (b * a.T * a.H + h) * N + task.walk % G::SLICES * G::CW;
-        const float* wp = a.w + b * a.T * a.H + h;
-        const float* bp = a.beta + b * a.T * a.H + h;
+            const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
+            const int64_t begin = PARTS ? task.part * a.part_len : 0;
+            const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
+            const IO* kp = static_cast<const IO*>(a.k) + (b * a.T * a.Hk + hk) * N;
+            const IO* rp = static_cast<const IO*>(a.r) + (b * a.T * a.Hk + hk) * N;
+            const IO* vp = static_cast<const IO*>(a.v) + (b * a.T * a.H + h) * N + task.walk % G::SLICES * G::CW;
+            const float* wp = a.w + b * a.T * a.H + h;
+            const float* bp = a.beta + b * a.T * a.H + h;
 #pragma unroll 1
-        for (int64_t t0 = begin + st * kChunk; t0 < end; t0 += G::NST * kChunk) {
-            const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
-            if (t0 >= begin + G::NST * kChunk) bar_sync<G::BAR>(kBarFree + st);
-            const float w = lane < nt ? wp[(t0 + lane) * a.H] : 0.f, be = lane < nt ? bp[(t0 + lane) * a.H] : 0.f;
-            g.fetch(kp + t0 * ks, rp + t0 * ks, ks, vp + t0 * vs, vs, nt, a.vec, lane);
-            // A, its inverse and P
-            const ChunkDecay d = chunk_decay<kChunk>(w, g.sums, lane);
-            if (lane < kChunk) {
-                g.beta[lane] = be;
-                g.sc[lane] = d.upto;
-                g.sc[kChunk + lane] = d.after * be;
-            }
-            __syncwarp();
-            float kk[2][4], rk[2][4];
-            gram<N, KP, KP, KP, kChain<IO>>(kk, g.k, g.k, G::PIECE, lane);
-            if constexpr (WANT_Y) gram<N, KP, KP, KP, kChain<IO>>(rk, g.r(), g.k, G::PIECE, lane);
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const float2 bs = pair_at(g.beta, n, lane);
-                const int s = 8 * n + 2 * (lane % 4);
-                const float2 s0 = g.sums[s], s1 = g.sums[s + 1];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int t = lane / 4 + 8 * q;
-                    const float2 tt = g.sums[t];
-                    const float g0 = decay_of(tt, s0) * bs.x, g1 = decay_of(tt, s1) * bs.y;
-                    g.diag[t * 20 + s] = s < t ? g0 * kk[n][2 * q] : 0.f;
-                    g.diag[t * 20 + s + 1] = s + 1 < t ? g1 * kk[n][2 * q + 1] : 0.f;
-                    if constexpr (WANT_Y)
-                        put_pieces<PP>(g.mats + 3 * kMat, t, s, s <= t ? g0 * rk[n][2 * q] : 0.f,
-                                       s + 1 <= t ? g1 * rk[n][2 * q + 1] : 0.f);
+            for (int64_t t0 = begin + st * kChunk; t0 < end; t0 += G::NST * kChunk) {
+                const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
+                if (t0 >= begin + G::NST * kChunk) bar_sync<G::BAR>(kBarFree + st);
+                const float w = lane < nt ? wp[(t0 + lane) * a.H] : 0.f, be = lane < nt ? bp[(t0 + lane) * a.H] : 0.f;
+                g.fetch(kp + t0 * ks, rp + t0 * ks, ks, vp + t0 * vs, vs, nt, a.vec, lane);
+                // A, its inverse and P
+                const ChunkDecay d = chunk_decay<kChunk>(w, g.sums, lane);
+                if (lane < kChunk) {
+                    g.beta[lane] = be;
+                    g.sc[lane] = d.upto;
+                    g.sc[kChunk + lane] = d.after * be;
                 }
+                __syncwarp();
+                float kk[2][4], rk[2][4];
+                gram<N, KP, KP, KP, kChain<IO>>(kk, g.k, g.k, G::PIECE, lane);
+                if constexpr (WANT_Y) gram<N, KP, KP, KP, kChain<IO>>(rk, g.r(), g.k, G::PIECE, lane);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float2 bs = pair_at(g.beta, n, lane);
+                    const int s = 8 * n + 2 * (lane % 4);
+                    const float2 s0 = g.sums[s], s1 = g.sums[s + 1];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int t = lane / 4 + 8 * q;
+                        const float2 tt = g.sums[t];
+                        const float g0 = decay_of(tt, s0) * bs.x, g1 = decay_of(tt, s1) * bs.y;
+                        g.diag[t * 20 + s] = s < t ? g0 * kk[n][2 * q] : 0.f;
+                        g.diag[t * 20 + s + 1] = s + 1 < t ? g1 * kk[n][2 * q + 1] : 0.f;
+                        if constexpr (WANT_Y)
+                            put_pieces<PP>(g.mats + 3 * kMat, t, s, s <= t ? g0 * rk[n][2 * q] : 0.f,
+                                           s + 1 <= t ? g1 * rk[n][2 * q + 1] : 0.f);
+                    }
+                }
+                __syncwarp();
+                put_inverse(g.mats, g.diag, lane);
+                bar_arrive<G::BAR>(kBarFull + st);
             }
-            __syncwarp();
-            put_inverse(g.mats, g.diag, lane);
-            bar_arrive<G::BAR>(kBarFull + st);
-        }
         }
         return;
     }
@@ -736,105 +736,105 @@ __device__ __forceinline__ void forward_walk(const Args& a, char* smem, int64_t 
     const int64_t nseg = (a.T + kSegment - 1) / kSegment;
     const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = m_plain(lane);
     for (; next_task<PARTS, G::THREADS>(a, walks, block, task, first); first = false) {
-    const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H;
-    const int slice = int(task.walk % G::SLICES) * G::CW;
-    const int64_t begin = PARTS ? task.part * a.part_len : 0;
-    const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
-    const int64_t vbase = (b * a.T * a.H + h) * N + slice;
-    float* keep = a.s_seg + head * (nseg + 1) * N * N;
-    float* hand = a.hand + head * N * N + int64_t(slice + j0) * N;
-    float S[N / 8][4];
-    if (!PARTS || task.part == 0) load_state<N>(S, a.s_in == nullptr ? nullptr : a.s_in + head * N * N + slice + j0, lane);
-    else take_over<N>(S, hand, task.lost, lane);
-    int st = 0;
+        const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H;
+        const int slice = int(task.walk % G::SLICES) * G::CW;
+        const int64_t begin = PARTS ? task.part * a.part_len : 0;
+        const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
+        const int64_t vbase = (b * a.T * a.H + h) * N + slice;
+        float* keep = a.s_seg + head * (nseg + 1) * N * N;
+        float* hand = a.hand + head * N * N + int64_t(slice + j0) * N;
+        float S[N / 8][4];
+        if (!PARTS || task.part == 0) load_state<N>(S, a.s_in == nullptr ? nullptr : a.s_in + head * N * N + slice + j0, lane);
+        else take_over<N>(S, hand, task.lost, lane);
+        int st = 0;
 #pragma unroll 1
-    for (int64_t t0 = begin; t0 < end; t0 += kChunk, st = (st + 1) % G::NST) {
-        const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
-        G g(smem, st);
-        if (!WANT_Y && t0 % kSegment == 0) keep_state<IO, N>(keep + t0 / kSegment * N * N, slice + j0, S, lane);
-        bar_sync<G::BAR>(kBarFull + st);
-        // K S and R S, transposed
-        float p[2][4], q[2][4], x[2][4];
-        {
-            Acc pa, qa;
+        for (int64_t t0 = begin; t0 < end; t0 += kChunk, st = (st + 1) % G::NST) {
+            const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
+            G g(smem, st);
+            if (!WANT_Y && t0 % kSegment == 0) keep_state<IO, N>(keep + t0 / kSegment * N * N, slice + j0, S, lane);
+            bar_sync<G::BAR>(kBarFull + st);
+            // K S and R S, transposed
+            float p[2][4], q[2][4], x[2][4];
+            {
+                Acc pa, qa;
 #pragma unroll
-            for (int kk = 0; kk < N / 16; ++kk) {
-                uint32_t sp[3][4];
-                split_a<3>(S[2 * kk], S[2 * kk + 1], sp);
-                times<3, KP, 3, false>(pa, pa.template start<C>(p, kk), kk == 0, sp, g.k + kk * 16, G::PIECE, off_b);
-                if constexpr (WANT_Y)
-                    times<3, KP, PP, false>(qa, qa.template start<C>(q, kk), kk == 0, sp, g.r() + kk * 16, G::PIECE, off_b);
+                for (int kk = 0; kk < N / 16; ++kk) {
+                    uint32_t sp[3][4];
+                    split_a<3>(S[2 * kk], S[2 * kk + 1], sp);
+                    times<3, KP, 3, false>(pa, pa.template start<C>(p, kk), kk == 0, sp, g.k + kk * 16, G::PIECE, off_b);
+                    if constexpr (WANT_Y)
+                        times<3, KP, PP, false>(qa, qa.template start<C>(q, kk), kk == 0, sp, g.r() + kk * 16, G::PIECE, off_b);
+                }
+                pa.template finish<C>(p, N / 16);
+                if constexpr (WANT_Y) qa.template finish<C>(q, N / 16);
             }
-            pa.template finish<C>(p, N / 16);
-            if constexpr (WANT_Y) qa.template finish<C>(q, N / 16);
-        }
-        load_lines(x, g.v + j0, G::LDV, lane);
-        // X = V - g K S
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const float2 gg = pair_at(g.sc, n, lane);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[n][i] = fmaf(-((i & 1) ? gg.y : gg.x), p[n][i], x[n][i]);
-        }
-        // E = (I + A)^-1 X
-        float e[2][4];
-        {
-            uint32_t xp[3][4];
-            split_a<3>(x[0], x[1], xp);
-            Acc ea;
-            times<3, 3, 3, false>(ea, true, true, xp, g.mats, kMat, off_m);
-            ea.sum(e);
-        }
-        // S <- g_15 S + (G beta E)^T K
-        {
-            float u[2][4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) u[n][i] = e[n][i];
-            scale_tokens(u, g.sc + kChunk, lane);
-            uint32_t up[3][4];
-            split_a<3>(u[0], u[1], up);
-            const float gl = g.sc[kChunk - 1];
-#pragma unroll
-            for (int kk = 0; kk < N / 16; ++kk) {
-                float d[2][4];
-                times_add<3, KP>(d, true, up, g.k + kk * 16, G::PIECE, off_t);
-                fade_add(S[2 * kk], gl, d[0]);
-                fade_add(S[2 * kk + 1], gl, d[1]);
-            }
-        }
-        const int64_t at = vbase + t0 * vs + j0;
-        if constexpr (!WANT_Y) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-                store_half(a.e + at + 8 * n * vs, vs, nt - 8 * n, e[n], g.v, 0, false, lane);
-        } else {
-            // Y = g R S + P E
-            uint32_t ep[PP][4];
-            split_a<PP>(e[0], e[1], ep);
-            Acc ya;
-            times<PP, PP, PP, false>(ya, true, true, ep, g.mats + 3 * kMat, kMat, off_m);
-            float y[2][4];
-            ya.sum(y);
+            load_lines(x, g.v + j0, G::LDV, lane);
+            // X = V - g K S
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const float2 gg = pair_at(g.sc, n, lane);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[n][i] = fmaf((i & 1) ? gg.y : gg.x, q[n][i], y[n][i]);
-                // through the V tile's columns, which only this warp reads
-                store_half(static_cast<IO*>(a.y) + at + 8 * n * vs, vs, nt - 8 * n, y[n], g.v + 8 * n * G::LDV + j0, G::LDV, a.vec, lane);
+                for (int i = 0; i < 4; ++i) x[n][i] = fmaf(-((i & 1) ? gg.y : gg.x), p[n][i], x[n][i]);
             }
+            // E = (I + A)^-1 X
+            float e[2][4];
+            {
+                uint32_t xp[3][4];
+                split_a<3>(x[0], x[1], xp);
+                Acc ea;
+                times<3, 3, 3, false>(ea, true, true, xp, g.mats, kMat, off_m);
+                ea.sum(e);
+            }
+            // S <- g_15 S + (G beta E)^T K
+            {
+                float u[2][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) u[n][i] = e[n][i];
+                scale_tokens(u, g.sc + kChunk, lane);
+                uint32_t up[3][4];
+                split_a<3>(u[0], u[1], up);
+                const float gl = g.sc[kChunk - 1];
+#pragma unroll
+                for (int kk = 0; kk < N / 16; ++kk) {
+                    float d[2][4];
+                    times_add<3, KP>(d, true, up, g.k + kk * 16, G::PIECE, off_t);
+                    fade_add(S[2 * kk], gl, d[0]);
+                    fade_add(S[2 * kk + 1], gl, d[1]);
+                }
+            }
+            const int64_t at = vbase + t0 * vs + j0;
+            if constexpr (!WANT_Y) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+                    store_half(a.e + at + 8 * n * vs, vs, nt - 8 * n, e[n], g.v, 0, false, lane);
+            } else {
+                // Y = g R S + P E
+                uint32_t ep[PP][4];
+                split_a<PP>(e[0], e[1], ep);
+                Acc ya;
+                times<PP, PP, PP, false>(ya, true, true, ep, g.mats + 3 * kMat, kMat, off_m);
+                float y[2][4];
+                ya.sum(y);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float2 gg = pair_at(g.sc, n, lane);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[n][i] = fmaf((i & 1) ? gg.y : gg.x, q[n][i], y[n][i]);
+                    // through the V tile's columns, which only this warp reads
+                    store_half(static_cast<IO*>(a.y) + at + 8 * n * vs, vs, nt - 8 * n, y[n], g.v + 8 * n * G::LDV + j0, G::LDV, a.vec, lane);
+                }
+            }
+            if (t0 + G::NST * kChunk < end) bar_arrive<G::BAR>(kBarFree + st);
         }
-        if (t0 + G::NST * kChunk < end) bar_arrive<G::BAR>(kBarFree + st);
-    }
-    if (PARTS && end < a.T) {
-        hand_on<N>(hand, S, lane);
-    } else if constexpr (WANT_Y) {
-        if (a.s_out != nullptr) store_state<N>(a.s_out + head * N * N + slice + j0, S, lane);
-    } else {
-        keep_state<IO, N>(keep + nseg * N * N, slice + j0, S, lane);
-    }
+        if (PARTS && end < a.T) {
+            hand_on<N>(hand, S, lane);
+        } else if constexpr (WANT_Y) {
+            if (a.s_out != nullptr) store_state<N>(a.s_out + head * N * N + slice + j0, S, lane);
+        } else {
+            keep_state<IO, N>(keep + nseg * N * N, slice + j0, S, lane);
+        }
     }
 }
 

@@ -56,54 +56,54 @@ __device__ __forceinline__ void reverse_walk(const Args& a, char* smem, int64_t 
         const int64_t ks = a.Hk * N;
         G g(smem, st);
         for (; next_task<PARTS, G::THREADS>(a, walks, block, task, first); first = false) {
-        const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
-        const int64_t begin = PARTS ? (a.parts - 1 - task.part) * a.part_len : 0;
-    const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
-        const int64_t last = begin + (end - 1 - begin) / kChunk * kChunk;
-        const int64_t vbase = (b * a.T * a.H + h) * N + task.walk % G::SLICES * G::CW;
-        const IO* kp = static_cast<const IO*>(a.k) + (b * a.T * a.Hk + hk) * N;
-        const IO* rp = static_cast<const IO*>(a.r) + (b * a.T * a.Hk + hk) * N;
-        const IO* yp = static_cast<const IO*>(a.dy) + vbase;
-        const float* wp = a.w + b * a.T * a.H + h;
-        const float* bp = a.beta + b * a.T * a.H + h;
+            const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H, hk = h / (a.H / a.Hk);
+            const int64_t begin = PARTS ? (a.parts - 1 - task.part) * a.part_len : 0;
+            const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
+            const int64_t last = begin + (end - 1 - begin) / kChunk * kChunk;
+            const int64_t vbase = (b * a.T * a.H + h) * N + task.walk % G::SLICES * G::CW;
+            const IO* kp = static_cast<const IO*>(a.k) + (b * a.T * a.Hk + hk) * N;
+            const IO* rp = static_cast<const IO*>(a.r) + (b * a.T * a.Hk + hk) * N;
+            const IO* yp = static_cast<const IO*>(a.dy) + vbase;
+            const float* wp = a.w + b * a.T * a.H + h;
+            const float* bp = a.beta + b * a.T * a.H + h;
 #pragma unroll 1
-        for (int64_t t0 = last - st * kChunk; t0 >= begin; t0 -= G::NST * kChunk) {
-            const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
-            if (last - t0 >= G::NST * kChunk) bar_sync<G::BAR>(kBarFree + st);
-            const float w = lane < nt ? wp[(t0 + lane) * a.H] : 0.f, be = lane < nt ? bp[(t0 + lane) * a.H] : 0.f;
-            g.fetch(kp + t0 * ks, rp + t0 * ks, ks, yp + t0 * vs, vs, nt, a.vec, lane);
-            // B, its inverse and P
-            const ChunkDecay d = chunk_decay<kChunk>(w, g.sums, lane);
-            if (lane < kChunk) {
-                g.beta[lane] = be;
-                g.sc[lane] = d.after;
-                g.sc[kChunk + lane] = d.upto;
-                g.sc[2 * kChunk + lane] = d.upto * be;
-            }
-            __syncwarp();
-            float kk[2][4], rk[2][4];
-            gram<N, KP, KP, KP, kChain<IO>>(kk, g.k, g.k, G::PIECE, lane);
-            gram<N, KP, KP, KP, kChain<IO>>(rk, g.r(), g.k, G::PIECE, lane);
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int t = 8 * n + 2 * (lane % 4);
-                const float2 t0s = g.sums[t], t1s = g.sums[t + 1];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int s = lane / 4 + 8 * q;
-                    const float bs = g.beta[s];
-                    const float2 ss = g.sums[s];
-                    const float g0 = decay_of(ss, t0s), g1 = decay_of(ss, t1s);
-                    g.diag[s * 20 + t] = t < s ? g0 * bs * kk[n][2 * q] : 0.f;
-                    g.diag[s * 20 + t + 1] = t + 1 < s ? g1 * bs * kk[n][2 * q + 1] : 0.f;
-                    put_pieces<3>(g.mats + 3 * kMat, s, t, t <= s ? g0 * rk[n][2 * q] : 0.f,
-                                  t + 1 <= s ? g1 * rk[n][2 * q + 1] : 0.f);
+            for (int64_t t0 = last - st * kChunk; t0 >= begin; t0 -= G::NST * kChunk) {
+                const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
+                if (last - t0 >= G::NST * kChunk) bar_sync<G::BAR>(kBarFree + st);
+                const float w = lane < nt ? wp[(t0 + lane) * a.H] : 0.f, be = lane < nt ? bp[(t0 + lane) * a.H] : 0.f;
+                g.fetch(kp + t0 * ks, rp + t0 * ks, ks, yp + t0 * vs, vs, nt, a.vec, lane);
+                // B, its inverse and P
+                const ChunkDecay d = chunk_decay<kChunk>(w, g.sums, lane);
+                if (lane < kChunk) {
+                    g.beta[lane] = be;
+                    g.sc[lane] = d.after;
+                    g.sc[kChunk + lane] = d.upto;
+                    g.sc[2 * kChunk + lane] = d.upto * be;
                 }
+                __syncwarp();
+                float kk[2][4], rk[2][4];
+                gram<N, KP, KP, KP, kChain<IO>>(kk, g.k, g.k, G::PIECE, lane);
+                gram<N, KP, KP, KP, kChain<IO>>(rk, g.r(), g.k, G::PIECE, lane);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int t = 8 * n + 2 * (lane % 4);
+                    const float2 t0s = g.sums[t], t1s = g.sums[t + 1];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int s = lane / 4 + 8 * q;
+                        const float bs = g.beta[s];
+                        const float2 ss = g.sums[s];
+                        const float g0 = decay_of(ss, t0s), g1 = decay_of(ss, t1s);
+                        g.diag[s * 20 + t] = t < s ? g0 * bs * kk[n][2 * q] : 0.f;
+                        g.diag[s * 20 + t + 1] = t + 1 < s ? g1 * bs * kk[n][2 * q + 1] : 0.f;
+                        put_pieces<3>(g.mats + 3 * kMat, s, t, t <= s ? g0 * rk[n][2 * q] : 0.f,
+                                      t + 1 <= s ? g1 * rk[n][2 * q + 1] : 0.f);
+                    }
+                }
+                __syncwarp();
+                put_inverse(g.mats, g.diag, lane);
+                bar_arrive<G::BAR>(kBarFull + st);
             }
-            __syncwarp();
-            put_inverse(g.mats, g.diag, lane);
-            bar_arrive<G::BAR>(kBarFull + st);
-        }
         }
         return;
     }
@@ -113,96 +113,96 @@ __device__ __forceinline__ void reverse_walk(const Args& a, char* smem, int64_t 
     const int64_t nseg = (a.T + kSegment - 1) / kSegment;
     const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = m_trans(lane);
     for (; next_task<PARTS, G::THREADS>(a, walks, block, task, first); first = false) {
-    const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H;
-    const int slice = int(task.walk % G::SLICES) * G::CW;
-    const int64_t begin = PARTS ? (a.parts - 1 - task.part) * a.part_len : 0;
-    const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
-    const int64_t last = begin + (end - 1 - begin) / kChunk * kChunk;
-    const int64_t vbase = (b * a.T * a.H + h) * N + slice;
-    float* grads = a.d_seg + head * (nseg + 1) * N * N;
-    float* hand = a.hand + head * N * N + int64_t(slice + j0) * N;
-    float S[N / 8][4];   // D^T
-    if (!PARTS || task.part == 0) load_state<N>(S, a.ds_out == nullptr ? nullptr : a.ds_out + head * N * N + slice + j0, lane);
-    else take_over<N>(S, hand, task.lost, lane);
-    // gradient states between segments, as S^T's
-    if (!PARTS || task.part == 0) keep_state<IO, N>(grads + nseg * N * N, slice + j0, S, lane);
-    int st = 0;
+        const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H;
+        const int slice = int(task.walk % G::SLICES) * G::CW;
+        const int64_t begin = PARTS ? (a.parts - 1 - task.part) * a.part_len : 0;
+        const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
+        const int64_t last = begin + (end - 1 - begin) / kChunk * kChunk;
+        const int64_t vbase = (b * a.T * a.H + h) * N + slice;
+        float* grads = a.d_seg + head * (nseg + 1) * N * N;
+        float* hand = a.hand + head * N * N + int64_t(slice + j0) * N;
+        float S[N / 8][4];   // D^T
+        if (!PARTS || task.part == 0) load_state<N>(S, a.ds_out == nullptr ? nullptr : a.ds_out + head * N * N + slice + j0, lane);
+        else take_over<N>(S, hand, task.lost, lane);
+        // gradient states between segments, as S^T's
+        if (!PARTS || task.part == 0) keep_state<IO, N>(grads + nseg * N * N, slice + j0, S, lane);
+        int st = 0;
 #pragma unroll 1
-    for (int64_t t0 = last; t0 >= begin; t0 -= kChunk, st = (st + 1) % G::NST) {
-        const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
-        G g(smem, st);
-        bar_sync<G::BAR>(kBarFull + st);
-        // X = diag(q) D^T K + P^T dY
-        float dy[2][4], x[2][4];
-        {
-            Acc pa;
+        for (int64_t t0 = last; t0 >= begin; t0 -= kChunk, st = (st + 1) % G::NST) {
+            const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
+            G g(smem, st);
+            bar_sync<G::BAR>(kBarFull + st);
+            // X = diag(q) D^T K + P^T dY
+            float dy[2][4], x[2][4];
+            {
+                Acc pa;
 #pragma unroll
-            for (int kk = 0; kk < N / 16; ++kk) {
-                uint32_t sp[3][4];
-                split_a<3>(S[2 * kk], S[2 * kk + 1], sp);
-                times<3, KP, 3, false>(pa, pa.template start<kChain<IO>>(x, kk), kk == 0, sp, g.k + kk * 16, G::PIECE, off_b);
+                for (int kk = 0; kk < N / 16; ++kk) {
+                    uint32_t sp[3][4];
+                    split_a<3>(S[2 * kk], S[2 * kk + 1], sp);
+                    times<3, KP, 3, false>(pa, pa.template start<kChain<IO>>(x, kk), kk == 0, sp, g.k + kk * 16, G::PIECE, off_b);
+                }
+                pa.template finish<kChain<IO>>(x, N / 16);
             }
-            pa.template finish<kChain<IO>>(x, N / 16);
-        }
-        load_lines(dy, g.v + j0, G::LDV, lane);
-        scale_tokens(x, g.sc, lane);
-        {
-            uint32_t yq[KP][4];
-            split_a<KP>(dy[0], dy[1], yq);
-            Acc ya;
-            times<KP, 3, 3, true>(ya, true, true, yq, g.mats + 3 * kMat, kMat, off_m);
-            float p[2][4];
-            ya.sum(p);
+            load_lines(dy, g.v + j0, G::LDV, lane);
+            scale_tokens(x, g.sc, lane);
+            {
+                uint32_t yq[KP][4];
+                split_a<KP>(dy[0], dy[1], yq);
+                Acc ya;
+                times<KP, 3, 3, true>(ya, true, true, yq, g.mats + 3 * kMat, kMat, off_m);
+                float p[2][4];
+                ya.sum(p);
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[n][i] += p[n][i];
-        }
-        float du[2][4];
-        {
-            uint32_t xp[3][4];
-            split_a<3>(x[0], x[1], xp);
-            Acc ea;
-            times<3, 3, 3, true>(ea, true, true, xp, g.mats, kMat, off_m);
-            ea.sum(du);
-        }
-        // D <- g_15 D + (g dy)^T R - (g beta du)^T K
-        {
-            float f1[2][4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f1[n][i] = -du[n][i];
-            scale_tokens(dy, g.sc + kChunk, lane);
-            scale_tokens(f1, g.sc + 2 * kChunk, lane);
-            uint32_t yq[3][4], uq[3][4];
-            split_a<3>(dy[0], dy[1], yq);
-            split_a<3>(f1[0], f1[1], uq);
-            const float gl = g.sc[2 * kChunk - 1];
-#pragma unroll
-            for (int kk = 0; kk < N / 16; ++kk) {
-                float d[2][4];
-                times_add<3, KP>(d, true, uq, g.k + kk * 16, G::PIECE, off_t);
-                times_add<3, KP>(d, false, yq, g.r() + kk * 16, G::PIECE, off_t);
-                fade_add(S[2 * kk], gl, d[0]);
-                fade_add(S[2 * kk + 1], gl, d[1]);
+                    for (int i = 0; i < 4; ++i) x[n][i] += p[n][i];
             }
-        }
-        const int64_t at = vbase + t0 * vs + j0;
+            float du[2][4];
+            {
+                uint32_t xp[3][4];
+                split_a<3>(x[0], x[1], xp);
+                Acc ea;
+                times<3, 3, 3, true>(ea, true, true, xp, g.mats, kMat, off_m);
+                ea.sum(du);
+            }
+            // D <- g_15 D + (g dy)^T R - (g beta du)^T K
+            {
+                float f1[2][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            store_half(a.du + at + 8 * n * vs, vs, nt - 8 * n, du[n], g.v, 0, false, lane);
-            const float2 be = pair_at(g.beta, n, lane);
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) du[n][i] *= (i & 1) ? be.y : be.x;
-            // dv through dy's columns, which only this warp reads
-            store_half(static_cast<IO*>(a.dv) + at + 8 * n * vs, vs, nt - 8 * n, du[n], g.v + 8 * n * G::LDV + j0, G::LDV, a.vec, lane);
+                    for (int i = 0; i < 4; ++i) f1[n][i] = -du[n][i];
+                scale_tokens(dy, g.sc + kChunk, lane);
+                scale_tokens(f1, g.sc + 2 * kChunk, lane);
+                uint32_t yq[3][4], uq[3][4];
+                split_a<3>(dy[0], dy[1], yq);
+                split_a<3>(f1[0], f1[1], uq);
+                const float gl = g.sc[2 * kChunk - 1];
+#pragma unroll
+                for (int kk = 0; kk < N / 16; ++kk) {
+                    float d[2][4];
+                    times_add<3, KP>(d, true, uq, g.k + kk * 16, G::PIECE, off_t);
+                    times_add<3, KP>(d, false, yq, g.r() + kk * 16, G::PIECE, off_t);
+                    fade_add(S[2 * kk], gl, d[0]);
+                    fade_add(S[2 * kk + 1], gl, d[1]);
+                }
+            }
+            const int64_t at = vbase + t0 * vs + j0;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                store_half(a.du + at + 8 * n * vs, vs, nt - 8 * n, du[n], g.v, 0, false, lane);
+                const float2 be = pair_at(g.beta, n, lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) du[n][i] *= (i & 1) ? be.y : be.x;
+                // dv through dy's columns, which only this warp reads
+                store_half(static_cast<IO*>(a.dv) + at + 8 * n * vs, vs, nt - 8 * n, du[n], g.v + 8 * n * G::LDV + j0, G::LDV, a.vec, lane);
+            }
+            if (t0 >= begin + G::NST * kChunk) bar_arrive<G::BAR>(kBarFree + st);
+            if (t0 % kSegment == 0) keep_state<IO, N>(grads + t0 / kSegment * N * N, slice + j0, S, lane);
         }
-        if (t0 >= begin + G::NST * kChunk) bar_arrive<G::BAR>(kBarFree + st);
-        if (t0 % kSegment == 0) keep_state<IO, N>(grads + t0 / kSegment * N * N, slice + j0, S, lane);
-    }
-    if (PARTS && begin > 0) hand_on<N>(hand, S, lane);
-    else if (a.ds_in != nullptr) store_state<N>(a.ds_in + head * N * N + slice + j0, S, lane);
+        if (PARTS && begin > 0) hand_on<N>(hand, S, lane);
+        else if (a.ds_in != nullptr) store_state<N>(a.ds_in + head * N * N + slice + j0, S, lane);
     }
 }
 
