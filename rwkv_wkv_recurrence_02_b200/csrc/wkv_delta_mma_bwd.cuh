@@ -213,7 +213,10 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
     reverse_walk<IO, N, true>(a, smem, blockIdx.x);
 }
 // Whole walks of both kinds: they need nothing of each other.  The reverse
-// ones, which take longer, first.
+// ones, which take longer, first: 4 x 4096 tokens of 24 heads of 64 663 us, 737 the
+// other way round (8 x 4096 of 32 heads 1548 and 1528).  In turn they took 858 and
+// 1830 us, and 449 where 32 heads of one sequence take 379: both codes in one
+// instruction cache.
 template <typename IO, int N>
 __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) delta_walks_kernel(const Args a) {
     extern __shared__ __align__(16) char smem[];
