@@ -20,9 +20,8 @@
 // Accuracy: a float32 operand is the sum of three bfloat16 pieces (24 bits);
 // products of pieces up to 2^-16 of the leading one are taken, the leading one
 // in an accumulator of its own.  bfloat16 inputs are one piece, exact: three
-// products for what reaches the state.  What only reaches a bfloat16 output
-// takes the orders up to 2^-8 (an error of 2^-17 against the output's own
-// 2^-9).  The state is updated by a float32 multiply-add of the chunk's sum, so
+// products with a float32 operand.  So a bfloat16 output is a float32 sum rounded
+// once.  The state is updated by a float32 multiply-add of the chunk's sum, so
 // the accumulators' truncation does not add up along T.
 //
 // What bounds it: issue.  An mma.sync of 16 x 8 x 16 holds its scheduler for 8.3
@@ -631,9 +630,6 @@ __device__ __forceinline__ bool next_task(const Args& a, int64_t walks, int64_t 
     return t.part < a.parts;
 }
 
-// what only reaches an output takes this many orders
-template <typename IO>
-constexpr int kOutOrders = sizeof(IO) == 2 ? 2 : 3;
 // steps of 16 in a chain of the tensor cores' additions.  float32 heads of 128
 // with whole chains: y within 6.8e-7 of 64 bits, dw 2e-6; with chains of one
 // 1.3e-7 and 5e-7.  bfloat16 keeps chains of 4 (heads of 64 whole; heads of 128
@@ -663,12 +659,12 @@ __device__ __forceinline__ void walker_regs() {
 // Outputs y (WANT_Y), or the errors e and the states between segments for the
 // reverse mode (float32).
 template <typename IO, int N, bool WANT_Y>
-using ForwardShape = Columns<IO, N, WANT_Y, 3 + (WANT_Y ? kOutOrders<IO> : 0), 2>;
+using ForwardShape = Columns<IO, N, WANT_Y, WANT_Y ? 6 : 3, 2>;
 
 template <typename IO, int N, bool WANT_Y, bool PARTS>
 __device__ __forceinline__ void forward_walk(const Args& a, char* smem, int64_t block) {
     using G = ForwardShape<IO, N, WANT_Y>;
-    constexpr int KP = G::KP, PP = kOutOrders<IO>, LD = G::LD, C = kChain<IO>;
+    constexpr int KP = G::KP, LD = G::LD, C = kChain<IO>;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
 
     const int64_t walks = a.B * a.H * G::SLICES, vs = a.H * N;
@@ -719,8 +715,8 @@ __device__ __forceinline__ void forward_walk(const Args& a, char* smem, int64_t 
                         g.diag[t * 20 + s] = s < t ? g0 * kk[n][2 * q] : 0.f;
                         g.diag[t * 20 + s + 1] = s + 1 < t ? g1 * kk[n][2 * q + 1] : 0.f;
                         if constexpr (WANT_Y)
-                            put_pieces<PP>(g.mats + 3 * kMat, t, s, s <= t ? g0 * rk[n][2 * q] : 0.f,
-                                           s + 1 <= t ? g1 * rk[n][2 * q + 1] : 0.f);
+                            put_pieces<3>(g.mats + 3 * kMat, t, s, s <= t ? g0 * rk[n][2 * q] : 0.f,
+                                          s + 1 <= t ? g1 * rk[n][2 * q + 1] : 0.f);
                     }
                 }
                 __syncwarp();
@@ -763,7 +759,7 @@ __device__ __forceinline__ void forward_walk(const Args& a, char* smem, int64_t 
                     split_a<3>(S[2 * kk], S[2 * kk + 1], sp);
                     times<3, KP, 3, false>(pa, pa.template start<C>(p, kk), kk == 0, sp, g.k + kk * 16, G::PIECE, off_b);
                     if constexpr (WANT_Y)
-                        times<3, KP, PP, false>(qa, qa.template start<C>(q, kk), kk == 0, sp, g.r() + kk * 16, G::PIECE, off_b);
+                        times<3, KP, 3, false>(qa, qa.template start<C>(q, kk), kk == 0, sp, g.r() + kk * 16, G::PIECE, off_b);
                 }
                 pa.template finish<C>(p, N / 16);
                 if constexpr (WANT_Y) qa.template finish<C>(q, N / 16);
@@ -811,10 +807,10 @@ __device__ __forceinline__ void forward_walk(const Args& a, char* smem, int64_t 
                     store_half(a.e + at + 8 * n * vs, vs, nt - 8 * n, e[n], g.v, 0, false, lane);
             } else {
                 // Y = g R S + P E
-                uint32_t ep[PP][4];
-                split_a<PP>(e[0], e[1], ep);
+                uint32_t ep[3][4];
+                split_a<3>(e[0], e[1], ep);
                 Acc ya;
-                times<PP, PP, PP, false>(ya, true, true, ep, g.mats + 3 * kMat, kMat, off_m);
+                times<3, 3, 3, false>(ya, true, true, ep, g.mats + 3 * kMat, kMat, off_m);
                 float y[2][4];
                 ya.sum(y);
 #pragma unroll

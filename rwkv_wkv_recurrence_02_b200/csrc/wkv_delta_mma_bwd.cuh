@@ -17,8 +17,6 @@
 // dk of a segment need nothing from the others, and a third kernel forms them
 // for every segment at once.  It starts dw from the inner product <D, S> at the
 // segment's end.  The two walks run side by side in one kernel.
-// What only reaches dk takes the orders that its type keeps; dr takes them
-// all, as r.dr enters dw.
 //
 // Measured, bfloat16: 8 x 4096 tokens of 32 heads of 64 1540 us (reads and writes
 // alone: 150), the walks 820 to 880 of it, bound as the forward is, the segments
@@ -237,17 +235,17 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
 // wkv_delta_tc.cuh's kernel.
 template <typename IO, int N>
 struct SegmentShape {
-    static constexpr int KP = sizeof(IO) == 2 ? 1 : 3, PP = kOutOrders<IO>;
+    static constexpr int KP = sizeof(IO) == 2 ? 1 : 3;
     static constexpr int IC = 32, PARTS = N / IC;
     static constexpr int WARPS = 4 * PARTS, THREADS = 32 * WARPS;
     static constexpr int PIECE = kSegment * N;                // rows without padding (Swizzled)
     static constexpr int JB = 32;                             // value lines of S and D at a time
     static constexpr int SPIECE = JB * N;
-    static constexpr int BLOCKS = 10, MATS = 3 + PP;          // blocks of token pairs on and below the diagonal, pieces of each
+    static constexpr int BLOCKS = 10, MATS = 6;               // blocks of token pairs on and below the diagonal, pieces of each
     // u, dv, dy; S and D, later the blocks; K and R (float32's over the rows when
     // those are done with); the decays and the sums over channels
-    static constexpr int S_ROWS = (3 + PP + KP) * PIECE * 2;
-    static constexpr int A_ = (3 + PP) * SPIECE * 2, B_ = BLOCKS * MATS * kMat * 2, S_BUF = A_ > B_ ? A_ : B_;
+    static constexpr int S_ROWS = (6 + KP) * PIECE * 2;
+    static constexpr int A_ = 6 * SPIECE * 2, B_ = BLOCKS * MATS * kMat * 2, S_BUF = A_ > B_ ? A_ : B_;
     static constexpr int S_KEYS = KP == 1 ? 2 * PIECE * 2 : 0;
     static constexpr int S_SUM = kSegment * (8 + 4 + 4 * PARTS) + WARPS * 8;
     static constexpr int SMEM = S_ROWS + S_BUF + S_KEYS + S_SUM;
@@ -315,9 +313,9 @@ struct Segment {
     }
 };
 
-// A warp's RW rows of u = beta e (three pieces) and dv = beta du (PP pieces), at
-// their places in shared memory; dbeta, and dv . v of a token.
-template <typename IO, int N, int RW, int PP, typename AT>
+// A warp's RW rows of u = beta e and dv = beta du (three pieces each), at their
+// places in shared memory; dbeta, and dv . v of a token.
+template <typename IO, int N, int RW, typename AT>
 __device__ __forceinline__ void stage_values(const Args& a, const Segment& sg, __nv_bfloat16* ub, __nv_bfloat16* db, int piece, AT place,
                                              int row, float* dvv, int lane) {
     constexpr int KP = sizeof(IO) == 2 ? 1 : 3;
@@ -367,7 +365,7 @@ __device__ __forceinline__ void stage_values(const Args& a, const Segment& sg, _
                 dvv[row + t] = bt * z;
             }
             put4<3>(ub + place(row + t, c), piece, make_float4(bt * x[u].x, bt * x[u].y, bt * x[u].z, bt * x[u].w));
-            put4<PP>(db + place(row + t, c), piece, make_float4(bt * y[u].x, bt * y[u].y, bt * y[u].z, bt * y[u].w));
+            put4<3>(db + place(row + t, c), piece, make_float4(bt * y[u].x, bt * y[u].y, bt * y[u].z, bt * y[u].w));
         }
     }
 }
@@ -541,12 +539,12 @@ __device__ __forceinline__ void segment_rates(const Args& a, const Segment& sg, 
 template <typename IO, int N>
 __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO, N>::CTAS) delta_segment_kernel(const Args a) {
     using G = SegmentShape<IO, N>;
-    constexpr int KP = G::KP, PP = G::PP, NP = G::IC / 16;
+    constexpr int KP = G::KP, NP = G::IC / 16;
     constexpr Swizzled<N> place{};
     extern __shared__ __align__(16) char smem[];
     __nv_bfloat16* ub = reinterpret_cast<__nv_bfloat16*>(smem);   // u = beta e
     __nv_bfloat16* db = ub + 3 * G::PIECE;                        // dv = beta du
-    __nv_bfloat16* yb = db + PP * G::PIECE;
+    __nv_bfloat16* yb = db + 3 * G::PIECE;
     __nv_bfloat16* buf = reinterpret_cast<__nv_bfloat16*>(smem + G::S_ROWS);
     __nv_bfloat16* kb = KP == 1 ? reinterpret_cast<__nv_bfloat16*>(smem + G::S_ROWS + G::S_BUF) : ub;
     __nv_bfloat16* rb = kb + KP * G::PIECE;
@@ -595,7 +593,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         copy_rows<IO, RW, N>(reinterpret_cast<IO*>(rb), rows_at, rp + rr * sg.ks, sg.ks, left, a.vec, lane);
         cp_async_commit();
     }
-    stage_values<IO, N, RW, PP>(a, sg, ub, db, G::PIECE, place, row, dvv, lane);
+    stage_values<IO, N, RW>(a, sg, ub, db, G::PIECE, place, row, dvv, lane);
     if constexpr (KP == 3)
         split_rows<RW, N, 3>(yb, rows_at, G::PIECE, reinterpret_cast<const float*>(a.dy) + sg.rows + rr * sg.vs, sg.vs, left, a.vec, lane);
     const float2 rates = warp == 0 ? segment_sums(a, sg, sums, lane) : make_float2(0.f, 0.f);
@@ -613,7 +611,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     const uint32_t at_t = place((lane & 7) + ((lane >> 3) & 1) * 8, (lane >> 4) * 8) * 2;
     const uint32_t at_p = place((lane & 7) + (lane >> 4) * 8, ((lane >> 3) & 1) * 8) * 2;
     constexpr int PB = G::PIECE * 2, SB = G::SPIECE * 2, ROWS16 = 16 * N * 2;
-    const uint32_t ub_a = smem_u32(ub), db_a = ub_a + 3 * PB, yb_a = db_a + PP * PB, buf_a = ub_a + G::S_ROWS,
+    const uint32_t ub_a = smem_u32(ub), db_a = ub_a + 3 * PB, yb_a = db_a + 3 * PB, buf_a = ub_a + G::S_ROWS,
                    kb_a = KP == 1 ? buf_a + G::S_BUF : ub_a;
     const uint32_t own_a = ub_a + tb * ROWS16, at_i = at_t ^ (i0 * 2);   // the warp's tokens, its channels
     const int t_lo = tb * 16 + lane / 4;                  // this lane's rows: t_lo and t_lo + 8
@@ -625,7 +623,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         for (int u = 0; u < LU; ++u) {
             const int i = lane + u * 32, at = place(warp * LW + i / (N / 4), i % (N / 4) * 4);
             put4<3>(buf + at, G::SPIECE, ls[u]);
-            put4<PP>(buf + 3 * G::SPIECE + at, G::SPIECE, ld[u]);
+            put4<3>(buf + 3 * G::SPIECE + at, G::SPIECE, ld[u]);
             border[1] += fmaf(ld[u].x, le[u].x, ld[u].y * le[u].y) + fmaf(ld[u].z, le[u].z, ld[u].w * le[u].w);
         }
         if (KP == 1 && jb == 0) cp_async_wait();
@@ -637,9 +635,9 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
                 gq[q] = make_float2(decay_of(sums[t_lo + 8 * q], make_float2(0.f, 0.f)), decay_of(sums[kSegment - 1], sums[t_lo + 8 * q]));
         }
         const uint32_t col = at_t ^ (jb * 2);
-        add_lines<N, KP, 3, 3>(dr, gq[0].x, gq[1].x, own_a + (3 + PP) * PB, PB, col, buf_a, SB, at_i);
-        add_lines<N, PP, PP, PP>(dk, -gq[0].x, -gq[1].x, own_a + 3 * PB, PB, col, buf_a, SB, at_i);
-        add_lines<N, PP, PP, PP>(dk, gq[0].y, gq[1].y, own_a, PB, col, buf_a + 3 * SB, SB, at_i);
+        add_lines<N, KP, 3, 3>(dr, gq[0].x, gq[1].x, own_a + 6 * PB, PB, col, buf_a, SB, at_i);
+        add_lines<N, 3, 3, 3>(dk, -gq[0].x, -gq[1].x, own_a + 3 * PB, PB, col, buf_a, SB, at_i);
+        add_lines<N, 3, 3, 3>(dk, gq[0].y, gq[1].y, own_a, PB, col, buf_a + 3 * SB, SB, at_i);
     }
 
     // --- the blocks of token pairs s <= t, with the decays between the tokens: dy_t.u_s, and
@@ -653,7 +651,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         const uint32_t xt = bt * ROWS16 + at_t, ys = ub_a + bs * ROWS16 + at_p;
         const int far = (bt > bs ? kChunk : 0) - ofv;   // s <= t + far
         float x[2][4];
-        if (ofv) gram_at<N, PP, PP, PP, kChain<IO>, true>(x, db_a + xt, ys, PB);
+        if (ofv) gram_at<N, 3, 3, 3, kChain<IO>, true>(x, db_a + xt, ys, PB);
         else gram_at<N, KP, 3, 3, kChain<IO>, true>(x, yb_a + xt, ys, PB);
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -663,8 +661,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
                 const float2 wt = sums[bt * 16 + t], w0 = sums[bs * 16 + c], w1 = sums[bs * 16 + c + 1];
                 const float y0 = c <= t + far ? decay_of(wt, w0) * x[n][2 * q] : 0.f;
                 const float y1 = c + 1 <= t + far ? decay_of(wt, w1) * x[n][2 * q + 1] : 0.f;
-                if (ofv) put_pieces<PP>(m, t, c, -y0, -y1);
-                else put_pieces<3>(m, t, c, y0, y1);
+                put_pieces<3>(m, t, c, ofv ? -y0 : y0, ofv ? -y1 : y1);
             }
     }
     __syncthreads();
@@ -674,30 +671,26 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
         __syncthreads();
     }
     // dr takes K by the sg.rows of the blocks, dk K by sg.rows and columns and R by columns
-    const auto times_dk = [&](float (&d)[2][4], const uint32_t (&a)[PP][4], const uint32_t (&f)[KP][4]) {
-        if constexpr (KP == 1) {   // a bfloat16 output: into its sum at once
-            times_sum<PP, KP, PP>(d, false, a, f);
-        } else {
-            float x[2][4];
-            times_sum<PP, KP, PP>(x, true, a, f);
-            Acc::add(d, x, false);
-        }
+    const auto times_add = [&](float (&d)[2][4], const uint32_t (&a)[3][4], const uint32_t (&f)[KP][4]) {
+        float x[2][4];
+        times_sum<3, KP, 3>(x, true, a, f);
+        Acc::add(d, x, false);
     };
 #pragma unroll 1
     for (int sb = 0; sb < 4; ++sb) {
         const bool low = sb <= tb, up = sb >= tb;
-        uint32_t dq[3][4], kq[PP][4], rq[PP][4], kt[PP][4];
+        uint32_t dq[3][4], kq[3][4], rq[3][4], kt[3][4];
         if (low) {
             const uint32_t m = buf_a + ((tb * (tb + 1) / 2 + sb) * G::MATS * kMat + m_trans(lane)) * 2;
 #pragma unroll
             for (int c = 0; c < 3; ++c) ldsm4(dq[c], m + c * kMat * 2);
 #pragma unroll
-            for (int c = 0; c < PP; ++c) ldsm4(kq[c], m + (3 + c) * kMat * 2);
+            for (int c = 0; c < 3; ++c) ldsm4(kq[c], m + (3 + c) * kMat * 2);
         }
         if (up) {
             const uint32_t m = buf_a + ((sb * (sb + 1) / 2 + tb) * G::MATS * kMat + m_plain(lane)) * 2;
 #pragma unroll
-            for (int c = 0; c < PP; ++c) {
+            for (int c = 0; c < 3; ++c) {
                 ldsm4t(rq[c], m + c * kMat * 2);
                 ldsm4t(kt[c], m + (3 + c) * kMat * 2);
             }
@@ -708,18 +701,16 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
             uint32_t fk[KP][4];
 #pragma unroll
             for (int c = 0; c < KP; ++c) ldsm4t(fk[c], so + c * PB);
-            float x[2][4];
             if (low) {
-                times_sum<3, KP, 3>(x, true, dq, fk);
-                Acc::add(dr[p], x, false);
-                times_dk(dk[p], kq, fk);
+                times_add(dr[p], dq, fk);
+                times_add(dk[p], kq, fk);
             }
             if (up) {
                 uint32_t fr[KP][4];
 #pragma unroll
                 for (int c = 0; c < KP; ++c) ldsm4t(fr[c], so + (KP + c) * PB);
-                times_dk(dk[p], kt, fk);
-                times_dk(dk[p], rq, fr);
+                times_add(dk[p], kt, fk);
+                times_add(dk[p], rq, fr);
             }
         }
     }

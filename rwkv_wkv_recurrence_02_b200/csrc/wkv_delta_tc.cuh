@@ -10,9 +10,9 @@
 //   batch 3  A K (dr), B K + C R (dk): A, B, C the scores of tokens on their own
 //            sides of the diagonal, with the decays between them
 //
-// Operands are bfloat16 pieces (u and S three, dv and D two, dy, k and r exact),
-// products of pieces smallest first into one accumulator, as many as the mma.sync
-// form takes.  All tiles are K-major without swizzle: 16-byte slots of 8 values,
+// Operands are bfloat16 pieces (dy, k and r exact, all others three), products of
+// pieces smallest first into one accumulator, as many as the mma.sync form takes.
+// K and R, whose tiles lie where D was, come in under batch 2.  All tiles are K-major without swizzle: 16-byte slots of 8 values,
 // core matrices of 8 rows; a slot of padding behind each pair of core matrices and
 // two behind each k step keep the stores of a warp in different banks.
 //
@@ -37,19 +37,21 @@ namespace wkv {
 namespace delta {
 
 struct TcSegment {
-    static constexpr int N = 64, WARPS = 8, THREADS = 256, PARTS = 2;
+    static constexpr int N = 64, THREADS = 256, PARTS = 2;
     static constexpr uint32_t LBO = 9, SBO = 17, KS = 138;      // slots: core matrices of a k step, row groups, k steps
     static constexpr uint32_t TILE = (3 * KS + 8 * SBO) * 16;   // bytes of 64 x 64 values
-    // tiles: u (3), dv (2), dy; S (3), D (2).  Later C over u, B over dv, A over S,
-    // K^T and R^T over D
-    static constexpr int U = 0, V = 3, Y = 5, S = 6, D = 9, TILES = 11;
-    static constexpr int RAW = TILES * TILE, KEYS = 64 * 64 * 2;   // K and R as they come
-    static constexpr int SUMS = RAW + 2 * KEYS;
-    static constexpr int SMEM = SUMS + 64 * (8 + 4 + 8) + 64;
+    // tiles: u (3), dv (3), dy; S (3), D (3).  Later C over u, B over dv, A over S;
+    // over D first K, then R as they come (RAW), and K^T and R^T
+    static constexpr int U = 0, V = 3, Y = 6, S = 7, D = 10, RAW = 12, TILES = 13;
+    static constexpr int SUMS = TILES * TILE;
+    static constexpr int SMEM = SUMS + 64 * (8 + 4);
+    // in the end the outputs' rows over C, and the sums over channels behind them
+    static constexpr int ROWS = 8 * 2 * 16 * 40;                // elements
+    static_assert(ROWS * 2 + 64 * 8 + 64 <= 3 * int(TILE) && 64 * 64 * 2 <= int(TILE), "room in what is over");
     static constexpr uint32_t COLS = 256;                       // tensor memory: four accumulators
     // D fp32, A and B bfloat16, both K-major, N = 64, M = 64
     static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((64u >> 3) << 17) | ((64u >> 4) << 24);
-    static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs an SM");
+    static_assert(2 * (SMEM + 64 + 1024) <= 228 * 1024, "two CTAs an SM");
     // element offset of (row, k)
     __device__ __forceinline__ int operator()(int row, int k) const {
         return ((k >> 4) * KS + (row >> 3) * SBO + ((k >> 3) & 1) * LBO + (row & 7)) * 8 + (k & 7);
@@ -72,6 +74,15 @@ __device__ __forceinline__ void tile_product(uint32_t d, uint64_t a, uint64_t b,
 }
 __device__ __forceinline__ void tile_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// d = the products of two operands' three pieces, the first ones' descriptors
+// given, smallest orders first
+__device__ __forceinline__ void piece_products(uint32_t d, uint64_t a, uint64_t b) {
+    constexpr int TILE = TcSegment::TILE / 16;
+#pragma unroll
+    for (int o = 2; o >= 0; --o)
+#pragma unroll
+        for (int p = o; p >= 0; --p) tile_product(d, a + p * TILE, b + (o - p) * TILE, o == 2 && p == 2);
 }
 // what every thread wrote to shared memory or read of tensor memory, before the next batch
 __device__ __forceinline__ void before_batch() {
@@ -115,11 +126,10 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
     __shared__ __align__(8) uint64_t bar[3];
     __shared__ uint32_t slot;
     __nv_bfloat16* tiles = reinterpret_cast<__nv_bfloat16*>(smem);
-    __nv_bfloat16* kr = reinterpret_cast<__nv_bfloat16*>(smem + G::RAW);
-    __nv_bfloat16* rr = kr + N * kSegment;
+    __nv_bfloat16* raw = tiles + G::RAW * PC;
     float2* sums = reinterpret_cast<float2*>(smem + G::SUMS);
     float* dvv = reinterpret_cast<float*>(sums + kSegment);
-    float* rdr = dvv + kSegment;
+    float* rdr = reinterpret_cast<float*>(tiles + G::U * PC + G::ROWS);
     float* inner = rdr + kSegment * G::PARTS;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     // the warp's tokens and channels (and, of scores, columns)
@@ -156,11 +166,8 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
     const int64_t first = left > 0 ? row : 0;   // rows behind the last token: zeros, addressed at one that exists
     copy_rows<IO, 8, N>(tiles + G::Y * PC, [&](int r, int c) { return at(row + r, c); },
                         static_cast<const IO*>(a.dy) + sg.rows + first * sg.vs, sg.vs, left, a.vec, lane);
-    const auto raw_at = [&](int r, int c) { return place(row + r, c); };
-    copy_rows<IO, 8, N>(kr, raw_at, static_cast<const IO*>(a.k) + sg.keys + first * sg.ks, sg.ks, left, a.vec, lane);
-    copy_rows<IO, 8, N>(rr, raw_at, static_cast<const IO*>(a.r) + sg.keys + first * sg.ks, sg.ks, left, a.vec, lane);
     cp_async_commit();
-    stage_values<IO, N, 8, 2>(a, sg, tiles + G::U * PC, tiles + G::V * PC, PC, at, row, dvv, lane);
+    stage_values<IO, N, 8>(a, sg, tiles + G::U * PC, tiles + G::V * PC, PC, at, row, dvv, lane);
     const float2 rates = warp == 0 ? segment_sums(a, sg, sums, lane) : make_float2(0.f, 0.f);
     float border[2] = {0.f, 0.f};
 #pragma unroll
@@ -169,7 +176,7 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
         for (int u = 0; u < 2; ++u) {
             const int i = lane + u * 32, o = at(warp * 8 + half * 4 + i / 16, i % 16 * 4);
             put4<3>(tiles + G::S * PC + o, PC, ls[u]);
-            put4<2>(tiles + G::D * PC + o, PC, ld[u]);
+            put4<3>(tiles + G::D * PC + o, PC, ld[u]);
             border[1] += fmaf(ld[u].x, le[u].x, ld[u].y * le[u].y) + fmaf(ld[u].z, le[u].z, ld[u].w * le[u].w);
         }
         if (half == 0) load_lines_at(1);
@@ -183,12 +190,8 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
     if (tid == 0) {
 #pragma unroll
         for (int p = 2; p >= 0; --p) tile_product(acc, tile(G::Y), tile(G::S + p), p == 2);
-        tile_product(acc + 64, tile(G::V + 1), tile(G::S), true);
-        tile_product(acc + 64, tile(G::V), tile(G::S + 1), false);
-        tile_product(acc + 64, tile(G::V), tile(G::S), false);
-        tile_product(acc + 128, tile(G::U + 1), tile(G::D), true);
-        tile_product(acc + 128, tile(G::U), tile(G::D + 1), false);
-        tile_product(acc + 128, tile(G::U), tile(G::D), false);
+        piece_products(acc + 64, tile(G::V), tile(G::S));
+        piece_products(acc + 128, tile(G::U), tile(G::D));
 #pragma unroll
         for (int p = 2; p >= 0; --p) tile_product(acc + 192, tile(G::Y), tile(G::U + p), p == 2);
         tile_commit(&bar[0]);
@@ -215,6 +218,23 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
     }
     bool ok = mbar_wait(&bar[0], 0, kCopyWaitNs);
     after_batch();
+    // K, then R: a warp's 8 tokens as they come, later its 8 channels turned
+    const auto fetch_raw = [&](const void* from) {
+        copy_rows<IO, 8, N>(raw, [&](int r, int c) { return place(row + r, c); }, static_cast<const IO*>(from) + sg.keys + first * sg.ks,
+                            sg.ks, left, a.vec, lane);
+        cp_async_commit();
+    };
+    const auto turn_raw = [&](__nv_bfloat16* to) {   // 8 x 8 blocks turned on their way through registers
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            uint32_t f[4];   // tokens 32 b .. 32 b + 31
+            ldsm4t(f, smem_u32(raw + place(32 * b + lane, warp * 8)));
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+                *reinterpret_cast<uint32_t*>(to + at(warp * 8 + lane / 4, 32 * b + 8 * z + 2 * (lane % 4))) = f[z];
+        }
+    };
+    fetch_raw(a.k);
     float dr[2][2][4], dk[2][2][4], x[2][2][4];
     load_tile(mine, dr);
     load_tile(mine + 64, dk);
@@ -230,11 +250,11 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
             }
     // A: dy_t.u_s, s <= t
     load_tile(mine + 192, x);
-    const auto put_scores = [&](int t, int c, float y0, float y1, __nv_bfloat16* to, auto pieces) {
-        uint32_t w[decltype(pieces)::value];
-        split2<decltype(pieces)::value>(y0, y1, w);
+    const auto put_scores = [&](int t, int c, float y0, float y1, __nv_bfloat16* to) {
+        uint32_t w[3];
+        split2<3>(y0, y1, w);
 #pragma unroll
-        for (int z = 0; z < decltype(pieces)::value; ++z) *reinterpret_cast<uint32_t*>(to + z * PC + at(t, c)) = w[z];
+        for (int z = 0; z < 3; ++z) *reinterpret_cast<uint32_t*>(to + z * PC + at(t, c)) = w[z];
     };
 #pragma unroll
     for (int p = 0; p < 2; ++p)
@@ -245,33 +265,23 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
                 const int t = t_lo + 8 * h, c = i0 + 16 * p + 8 * n + 2 * (lane % 4);
                 const float y0 = c <= t ? decay_of(sums[t], sums[c]) * x[p][n][2 * h] : 0.f;
                 const float y1 = c + 1 <= t ? decay_of(sums[t], sums[c + 1]) * x[p][n][2 * h + 1] : 0.f;
-                put_scores(t, c, y0, y1, tiles + G::S * PC, std::integral_constant<int, 3>{});
+                put_scores(t, c, y0, y1, tiles + G::S * PC);
             }
+    cp_async_wait();
     before_batch();
     if (tid == 0) {
-        tile_product(acc, tile(G::V + 1), tile(G::U), true);
-        tile_product(acc, tile(G::V), tile(G::U + 1), false);
-        tile_product(acc, tile(G::V), tile(G::U), false);
-        tile_product(acc + 64, tile(G::U + 1), tile(G::V), true);
-        tile_product(acc + 64, tile(G::U), tile(G::V + 1), false);
-        tile_product(acc + 64, tile(G::U), tile(G::V), false);
-        tile_product(acc + 128, tile(G::U + 1), tile(G::Y), true);
-        tile_product(acc + 128, tile(G::U), tile(G::Y), false);
+        piece_products(acc, tile(G::V), tile(G::U));
+        piece_products(acc + 64, tile(G::U), tile(G::V));
+#pragma unroll
+        for (int p = 2; p >= 0; --p) tile_product(acc + 128, tile(G::U + p), tile(G::Y), p == 2);
         tile_commit(&bar[1]);
     }
-    // meanwhile K^T and R^T over D: 8 x 8 blocks turned on their way through registers
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            // the warp's 8 channels, tokens 32 b .. 32 b + 31
-            uint32_t f[4];
-            ldsm4t(f, smem_u32((m ? rr : kr) + place(32 * b + lane, warp * 8)));
-            __nv_bfloat16* to = tiles + (G::D + m) * PC;
-#pragma unroll
-            for (int z = 0; z < 4; ++z)
-                *reinterpret_cast<uint32_t*>(to + at(warp * 8 + lane / 4, 32 * b + 8 * z + 2 * (lane % 4))) = f[z];
-        }
+    turn_raw(tiles + G::D * PC);
+    __syncthreads();
+    fetch_raw(a.r);
+    cp_async_wait();
+    __syncthreads();
+    turn_raw(tiles + (G::D + 1) * PC);
     ok = mbar_wait(&bar[1], 0, kCopyWaitNs) && ok;
     after_batch();
     // B: -dv_t.u_s, s < t, and -u_t.dv_s, s > t; C: u_t.dy_s, s >= t
@@ -297,18 +307,19 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
                         b[e] = c + e == t ? 0.f : -d * (below ? x[p][n][2 * h + e] : y[p][n][2 * h + e]);
                         cc[e] = below ? 0.f : d * z[p][n][2 * h + e];
                     }
-                    put_scores(t, c, b[0], b[1], tiles + G::V * PC, std::integral_constant<int, 2>{});
-                    put_scores(t, c, cc[0], cc[1], tiles + G::U * PC, std::integral_constant<int, 2>{});
+                    put_scores(t, c, b[0], b[1], tiles + G::V * PC);
+                    put_scores(t, c, cc[0], cc[1], tiles + G::U * PC);
                 }
     }
     before_batch();
     if (tid == 0) {
 #pragma unroll
         for (int p = 2; p >= 0; --p) tile_product(acc, tile(G::S + p), tile(G::D), p == 2);
-        tile_product(acc + 64, tile(G::V + 1), tile(G::D), true);
-        tile_product(acc + 64, tile(G::U + 1), tile(G::D + 1), false);
-        tile_product(acc + 64, tile(G::V), tile(G::D), false);
-        tile_product(acc + 64, tile(G::U), tile(G::D + 1), false);
+#pragma unroll
+        for (int p = 2; p >= 0; --p) {
+            tile_product(acc + 64, tile(G::V + p), tile(G::D), p == 2);
+            tile_product(acc + 64, tile(G::U + p), tile(G::D + 1), false);
+        }
         tile_commit(&bar[2]);
     }
     ok = mbar_wait(&bar[2], 0, kCopyWaitNs) && ok;
@@ -330,8 +341,8 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
         dk[p][0][0] += bad;
     }
     float own[2];
-    row_products<N, 2, 1>(own, rr, 0, dr, t_lo, i0, lane);
-    store_rows<IO, N, 2>(a, sg, dr, dk, tiles + G::U * PC + warp * 2 * 16 * 40, tb, i0, lane);
+    row_products<N, 2, 1>(own, raw, 0, dr, t_lo, i0, lane);
+    store_rows<IO, N, 2>(a, sg, dr, dk, tiles + G::U * PC + warp * (G::ROWS / 8), tb, i0, lane);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     segment_rates<N, G::PARTS>(a, sg, own, border, rdr, dvv, inner, s_seg, d_seg, t_lo, rates, tid);
     if (warp == 0) {   // every warp's loads are done: the barrier in segment_rates
