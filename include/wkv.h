@@ -546,7 +546,10 @@ int wkv_delta_step(int64_t L, int64_t B, int64_t Hk, int64_t H, int64_t N, int d
  * dtype and dstate_out (B,H,N,N) float32, dL/d(returned state), or NULL:
  * dr, dk (B,T,Hk*N) and dv (B,T,H*N) in dtype, dr and dk summed over the
  * value heads that share a key head; dw, dbeta (B,T,H) float32; dstate_in
- * (B,H,N,N) float32 or NULL.  dw is 0 where e^{-w} is 0.  No output may
+ * (B,H,N,N) float32 or NULL.  dw is formed from sums of r.dr and dv.v of the
+ * tokens that follow, to the next multiple of 64 or the next reset, so its
+ * error is relative to those and not to dw itself, which strong finite decays
+ * make smaller; it is 0 where e^{-w} is 0.  No output may
  * overlap an input, another output or the workspace.  The workspace (256-byte
  * aligned, wkv_delta_backward_workspace_bytes() bytes) is as above; the walks
  * go in parts as the forward's do.  T == 0: dstate_in = dstate_out (zeros if

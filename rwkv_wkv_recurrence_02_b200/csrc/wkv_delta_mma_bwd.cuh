@@ -472,7 +472,9 @@ __device__ __forceinline__ void store_rows(const Args& a, const Segment& sg, con
 // end (border[1], a thread's share); rates: warp 0's, of two tokens a lane.  All
 // threads of the CTA.  <D, S> at its begin
 // follows from those, but in the first segment it is formed too: with an empty
-// state it is zero, and not what rounding leaves of the terms.
+// state it is zero, and not what rounding leaves of the terms.  At a token whose
+// decay is 0 the sum is 0 and begins anew, so that what rounding leaves of the
+// terms behind it does not reach the document ahead of it.
 template <int N, int PARTS>
 __device__ __forceinline__ void segment_rates(const Args& a, const Segment& sg, float (&own)[2], float (&border)[2], float* rdr,
                                               const float* dvv, float* inner, const float* s_seg, const float* d_seg, int t_lo, float2 rates,
@@ -516,22 +518,31 @@ __device__ __forceinline__ void segment_rates(const Args& a, const Segment& sg, 
             for (int p = 1; p < PARTS; ++p) x += rdr[p * kSegment + t];
             term[q] = t < nt ? x - dvv[t] : 0.f;
         }
-        float x = term[0] + term[1];   // suffix sums over the lanes
+        // suffix sums over the lanes, each to the first reset
+        const bool r0 = expf(-rates.x) == 0.f, r1 = expf(-rates.y) == 0.f;
+        float x = r0 ? 0.f : r1 ? term[0] : term[0] + term[1];
+        int cut = r0 || r1;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
             const float y = __shfl_down_sync(0xffffffffu, x, o);
-            if (lane + o < 32) x += y;
+            const int c = __shfl_down_sync(0xffffffffu, cut, o);
+            if (lane + o < 32) {
+                if (!cut) x += y;
+                cut |= c;
+            }
         }
         float after = __shfl_down_sync(0xffffffffu, x, 1);
+        const int far = __shfl_down_sync(0xffffffffu, cut, 1);
         if (lane == 31) after = 0.f;
-        const float s1 = end + (after + term[1]), s0 = end + (after + (term[1] + term[0]));
+        else if (far) end = 0.f;
+        const float s1 = r1 ? 0.f : end + (after + term[1]);
+        const float s0 = r0 ? 0.f : r1 ? term[0] : end + (after + (term[1] + term[0]));
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int t = ta + q;
             if (t >= nt) continue;
             const int64_t at = scalar + t * a.H;
-            // a state that nothing is left of has no gradient, whatever the sum's rounding left
-            a.dw[at] = expf(-(q ? rates.y : rates.x)) == 0.f ? 0.f : t == 0 && seg == 0 ? -first : -(q ? s1 : s0);
+            a.dw[at] = t == 0 && seg == 0 && !r0 ? -first : -(q ? s1 : s0);
         }
     }
 }
