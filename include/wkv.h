@@ -501,6 +501,10 @@ int wkv_token_shift(int64_t B, int64_t T, int64_t C, int dtype, int nmix,
  * A decay rate of +infinity forgets the state before the token (a document
  * border); beta = 0 with w = 0 leaves the state as it is (padding).  Keys
  * are taken as they are: with beta |k|^2 above 2 the recurrence grows.
+ * A value that is not finite reaches what the recurrence lets it reach and
+ * nothing else, in the forward and the reverse mode; what it reaches is NaN or
+ * infinite.  It stays in the state past a reset (e^{-inf} times it is NaN).  The
+ * heads that meet one are walked a second time, token by token.
  * All arithmetic is float32, the outputs rounded once to dtype; the order of
  * every sum is fixed, so equal calls give equal bits.
  *

@@ -24,6 +24,13 @@
 // once.  The state is updated by a float32 multiply-add of the chunk's sum, so
 // the accumulators' truncation does not add up along T.
 //
+// Values that are not finite: the zeros of these matrices, times a NaN, would carry
+// it to the tokens ahead of its own.  It always reaches the column's state, and
+// stays there.  So a walk that ends with a column not finite which began finite is
+// walked again, token by token (forward_again; 8 x 4096 tokens of 32 heads of 64 then
+// take 1765 us).  A test of every chunk's E in the first place, or only the code for it
+// in the loop, took 6% of the time of all calls.
+//
 // What bounds it: issue.  An mma.sync of 16 x 8 x 16 holds its scheduler for 8.3
 // cycles here and other instructions (1.1 each) do not issue meanwhile; 82 of
 // the ones and about 500 of the others a chunk and warp (bfloat16 heads of 64),
@@ -98,6 +105,14 @@ template <int THREADS>
 __device__ __forceinline__ void bar_sync(int id) { asm volatile("bar.sync %0, %1;" :: "r"(id), "n"(THREADS) : "memory"); }
 template <int THREADS>
 __device__ __forceinline__ void bar_arrive(int id) { asm volatile("bar.arrive %0, %1;" :: "r"(id), "n"(THREADS) : "memory"); }
+// all of them: does p hold for one?
+template <int THREADS>
+__device__ __forceinline__ bool bar_or(int id, bool p) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"(uint32_t(p)), "r"(id), "n"(THREADS) : "memory");
+    return r != 0;
+}
 // ids: one for each of four stages
 constexpr int kBarFull = 1, kBarFree = 5, kBarTask = 9;
 
@@ -630,6 +645,67 @@ __device__ __forceinline__ bool next_task(const Args& a, int64_t walks, int64_t 
     return t.part < a.parts;
 }
 
+// two neighbouring channels of a staged row, KP pieces `piece` elements apart
+template <int KP>
+__device__ __forceinline__ float2 staged_pair(const __nv_bfloat16* p, int piece) {
+    float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int c = KP - 1; c >= 0; --c) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(p + c * piece);
+        x.x += __uint_as_float(w << 16), x.y += __uint_as_float(w & 0xffff0000u);
+    }
+    return x;
+}
+__device__ __forceinline__ float quad_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+// Of each quad of lanes (two lines of a warp's tiles): does p hold in one of them?
+__device__ __forceinline__ uint32_t quad_any(bool p) {
+    uint32_t b = __ballot_sync(0xffffffffu, p);
+    b |= b >> 1;
+    return (b | b >> 2) & 0x11111111u;
+}
+// A walking warp's place: tokens [begin, end) of a head, columns from `column` on
+template <typename G, int N, bool PARTS, bool BACK>
+struct Reach {
+    int64_t head, row, begin, end, values;   // row, values: of token 0, in per-head scalars and in values
+    int column;
+    __device__ __forceinline__ Reach(const Args& a, const Task& t, int warp) {
+        head = t.walk / G::SLICES;
+        const int64_t b = head / a.H, h = head % a.H;
+        column = int(t.walk % G::SLICES) * G::CW + warp * 16;
+        begin = PARTS ? (BACK ? a.parts - 1 - t.part : t.part) * a.part_len : 0;
+        end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
+        row = b * a.T * a.H + h;
+        values = row * N + column;
+    }
+    // the state that the walk begins with: `given` (NULL: zeros), or what the part before left
+    __device__ __forceinline__ void start(float (&S)[N / 8][4], const Args& a, const Task& t, const float* given, int lane) const {
+        if (!PARTS || t.part == 0) load_state<N>(S, given == nullptr ? nullptr : given + head * N * N + column, lane);
+        else take_over<N>(S, hand(a), t.lost, lane);
+    }
+    __device__ __forceinline__ float* hand(const Args& a) const { return a.hand + head * N * N + int64_t(column) * N; }
+};
+// Which of a warp's lines are not finite?  Of a quad of lanes, its two lines in
+// neighbouring bits.  (0 times what is not finite is NaN.)
+template <int N>
+__device__ __forceinline__ uint32_t odd_lines(const float (&x)[N / 8][4]) {
+    float z[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < N / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i >> 1] = fmaf(x[n][i], 0.f, z[i >> 1]);
+    return quad_any(z[0] != 0.f) | quad_any(z[1] != 0.f) << 1;
+}
+// Was one of `lines` finite when the walk began?
+template <int N, typename PLACE>
+__device__ __noinline__ bool began_finite(const Args& a, const Task& t, const float* given, uint32_t lines) {
+    float s[N / 8][4];
+    PLACE(a, t, threadIdx.x / 32).start(s, a, t, given, threadIdx.x % 32);
+    return (lines & ~odd_lines<N>(s)) != 0;
+}
+
 // steps of 16 in a chain of the tensor cores' additions.  float32 heads of 128
 // with whole chains: y within 6.8e-7 of 64 bits, dw 2e-6; with chains of one
 // 1.3e-7 and 5e-7.  bfloat16 keeps chains of 4 (heads of 64 whole; heads of 128
@@ -661,6 +737,89 @@ __device__ __forceinline__ void walker_regs() {
 template <typename IO, int N, bool WANT_Y>
 using ForwardShape = Columns<IO, N, WANT_Y, WANT_Y ? 6 : 3, 2>;
 
+// A chunk's nt tokens of a warp's 16 columns one after another, from the staged rows:
+// outputs y or errors e at `out` (the lane's first line).  w, beta: of its first token.
+template <typename IO, int N, bool WANT_Y, typename OUT>
+__device__ __forceinline__ void forward_tokens(const ForwardShape<IO, N, WANT_Y>& g, float (&S)[N / 8][4], int j0, int nt, const float* w,
+                                               const float* beta, int64_t heads, OUT* out, int64_t vs, int lane) {
+    using G = ForwardShape<IO, N, WANT_Y>;
+#pragma unroll 1
+    for (int t = 0; t < nt; ++t) {
+        const __nv_bfloat16* kp = g.k + t * G::LD + 2 * (lane % 4);
+        const IO* vp = g.v + t * G::LDV + j0 + lane / 4;
+        const float a = expf(-w[t * heads]), be = beta[t * heads];
+        float p[2] = {0.f, 0.f}, u[2];
+#pragma unroll
+        for (int n = 0; n < N / 8; ++n) {
+            const float2 k = staged_pair<G::KP>(kp + 8 * n, G::PIECE);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                S[n][i] *= a;
+                p[i >> 1] = fmaf(S[n][i], (i & 1) ? k.y : k.x, p[i >> 1]);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            p[q] = to_f32(vp[8 * q]) - quad_sum(p[q]);
+            u[q] = be * p[q];
+        }
+        float y[2] = {0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < N / 8; ++n) {
+            const float2 k = staged_pair<G::KP>(kp + 8 * n, G::PIECE);
+            float2 r = make_float2(0.f, 0.f);
+            if constexpr (WANT_Y) r = staged_pair<G::KP>(kp + (g.r() - g.k) + 8 * n, G::PIECE);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                S[n][i] = fmaf((i & 1) ? k.y : k.x, u[i >> 1], S[n][i]);
+                if constexpr (WANT_Y) y[i >> 1] = fmaf(S[n][i], (i & 1) ? r.y : r.x, y[i >> 1]);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if constexpr (WANT_Y) p[q] = quad_sum(y[q]);
+            if (lane % 4 == 0) put(out + t * vs + 8 * q, p[q]);
+        }
+    }
+}
+
+// where the state behind the walk's last token goes
+template <typename IO, int N, bool WANT_Y, bool PARTS, typename PLACE>
+__device__ __forceinline__ void forward_end(const Args& a, const PLACE& p, const float (&S)[N / 8][4], int lane) {
+    const int64_t nseg = (a.T + kSegment - 1) / kSegment;
+    if (PARTS && p.end < a.T) {
+        hand_on<N>(p.hand(a), S, lane);
+    } else if constexpr (WANT_Y) {
+        if (a.s_out != nullptr) store_state<N>(a.s_out + p.head * N * N + p.column, S, lane);
+    } else {
+        keep_state<IO, N>(a.s_seg + (p.head * (nseg + 1) + nseg) * N * N, p.column, S, lane);
+    }
+}
+template <typename IO, int N, bool WANT_Y, bool PARTS>
+__device__ __noinline__ void forward_again(const Args& a, char* smem, const Task& task) {
+    using G = ForwardShape<IO, N, WANT_Y>;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t nseg = (a.T + kSegment - 1) / kSegment, vs = a.H * N;
+    const Reach<G, N, PARTS, false> p(a, task, warp);
+    float S[N / 8][4];
+    p.start(S, a, task, a.s_in, lane);
+    int st = 0;
+#pragma unroll 1
+    for (int64_t t0 = p.begin; t0 < p.end; t0 += kChunk, st = (st + 1) % G::NST) {
+        const int nt = p.end - t0 < kChunk ? int(p.end - t0) : kChunk;
+        const int64_t row = p.row + t0 * a.H, line = p.values + t0 * vs + lane / 4;
+        if (!WANT_Y && t0 % kSegment == 0)
+            keep_state<IO, N>(a.s_seg + (p.head * (nseg + 1) + t0 / kSegment) * N * N, p.column, S, lane);
+        bar_sync<G::BAR>(kBarFull + st);
+        if constexpr (WANT_Y)
+            forward_tokens<IO, N, true>(G(smem, st), S, warp * 16, nt, a.w + row, a.beta + row, a.H, static_cast<IO*>(a.y) + line, vs, lane);
+        else
+            forward_tokens<IO, N, false>(G(smem, st), S, warp * 16, nt, a.w + row, a.beta + row, a.H, a.e + line, vs, lane);
+        if (t0 + G::NST * kChunk < p.end) bar_arrive<G::BAR>(kBarFree + st);
+    }
+    forward_end<IO, N, WANT_Y, PARTS>(a, p, S, lane);
+}
+
 template <typename IO, int N, bool WANT_Y, bool PARTS>
 __device__ __forceinline__ void forward_walk(const Args& a, char* smem, int64_t block) {
     using G = ForwardShape<IO, N, WANT_Y>;
@@ -685,44 +844,47 @@ __device__ __forceinline__ void forward_walk(const Args& a, char* smem, int64_t 
             const IO* vp = static_cast<const IO*>(a.v) + (b * a.T * a.H + h) * N + task.walk % G::SLICES * G::CW;
             const float* wp = a.w + b * a.T * a.H + h;
             const float* bp = a.beta + b * a.T * a.H + h;
+            bool again = false;
+            do {
 #pragma unroll 1
-            for (int64_t t0 = begin + st * kChunk; t0 < end; t0 += G::NST * kChunk) {
-                const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
-                if (t0 >= begin + G::NST * kChunk) bar_sync<G::BAR>(kBarFree + st);
-                const float w = lane < nt ? wp[(t0 + lane) * a.H] : 0.f, be = lane < nt ? bp[(t0 + lane) * a.H] : 0.f;
-                g.fetch(kp + t0 * ks, rp + t0 * ks, ks, vp + t0 * vs, vs, nt, a.vec, lane);
-                // A, its inverse and P
-                const ChunkDecay d = chunk_decay<kChunk>(w, g.sums, lane);
-                if (lane < kChunk) {
-                    g.beta[lane] = be;
-                    g.sc[lane] = d.upto;
-                    g.sc[kChunk + lane] = d.after * be;
-                }
-                __syncwarp();
-                float kk[2][4], rk[2][4];
-                gram<N, KP, KP, KP, kChain<IO>>(kk, g.k, g.k, G::PIECE, lane);
-                if constexpr (WANT_Y) gram<N, KP, KP, KP, kChain<IO>>(rk, g.r(), g.k, G::PIECE, lane);
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float2 bs = pair_at(g.beta, n, lane);
-                    const int s = 8 * n + 2 * (lane % 4);
-                    const float2 s0 = g.sums[s], s1 = g.sums[s + 1];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int t = lane / 4 + 8 * q;
-                        const float2 tt = g.sums[t];
-                        const float g0 = decay_of(tt, s0) * bs.x, g1 = decay_of(tt, s1) * bs.y;
-                        g.diag[t * 20 + s] = s < t ? g0 * kk[n][2 * q] : 0.f;
-                        g.diag[t * 20 + s + 1] = s + 1 < t ? g1 * kk[n][2 * q + 1] : 0.f;
-                        if constexpr (WANT_Y)
-                            put_pieces<3>(g.mats + 3 * kMat, t, s, s <= t ? g0 * rk[n][2 * q] : 0.f,
-                                          s + 1 <= t ? g1 * rk[n][2 * q + 1] : 0.f);
+                for (int64_t t0 = begin + st * kChunk; t0 < end; t0 += G::NST * kChunk) {
+                    const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
+                    if (t0 >= begin + G::NST * kChunk) bar_sync<G::BAR>(kBarFree + st);
+                    const float w = lane < nt ? wp[(t0 + lane) * a.H] : 0.f, be = lane < nt ? bp[(t0 + lane) * a.H] : 0.f;
+                    g.fetch(kp + t0 * ks, rp + t0 * ks, ks, vp + t0 * vs, vs, nt, a.vec, lane);
+                    // A, its inverse and P
+                    const ChunkDecay d = chunk_decay<kChunk>(w, g.sums, lane);
+                    if (lane < kChunk) {
+                        g.beta[lane] = be;
+                        g.sc[lane] = d.upto;
+                        g.sc[kChunk + lane] = d.after * be;
                     }
+                    __syncwarp();
+                    float kk[2][4], rk[2][4];
+                    gram<N, KP, KP, KP, kChain<IO>>(kk, g.k, g.k, G::PIECE, lane);
+                    if constexpr (WANT_Y) gram<N, KP, KP, KP, kChain<IO>>(rk, g.r(), g.k, G::PIECE, lane);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const float2 bs = pair_at(g.beta, n, lane);
+                        const int s = 8 * n + 2 * (lane % 4);
+                        const float2 s0 = g.sums[s], s1 = g.sums[s + 1];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int t = lane / 4 + 8 * q;
+                            const float2 tt = g.sums[t];
+                            const float g0 = decay_of(tt, s0) * bs.x, g1 = decay_of(tt, s1) * bs.y;
+                            g.diag[t * 20 + s] = s < t ? g0 * kk[n][2 * q] : 0.f;
+                            g.diag[t * 20 + s + 1] = s + 1 < t ? g1 * kk[n][2 * q + 1] : 0.f;
+                            if constexpr (WANT_Y)
+                                put_pieces<3>(g.mats + 3 * kMat, t, s, s <= t ? g0 * rk[n][2 * q] : 0.f,
+                                              s + 1 <= t ? g1 * rk[n][2 * q + 1] : 0.f);
+                        }
+                    }
+                    __syncwarp();
+                    put_inverse(g.mats, g.diag, lane);
+                    bar_arrive<G::BAR>(kBarFull + st);
                 }
-                __syncwarp();
-                put_inverse(g.mats, g.diag, lane);
-                bar_arrive<G::BAR>(kBarFull + st);
-            }
+            } while (!again && (again = bar_or<G::THREADS>(kBarTask, false)));
         }
         return;
     }
@@ -731,23 +893,19 @@ __device__ __forceinline__ void forward_walk(const Args& a, char* smem, int64_t 
     const int j0 = warp * 16;
     const int64_t nseg = (a.T + kSegment - 1) / kSegment;
     const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = m_plain(lane);
+    using Place = Reach<G, N, PARTS, false>;
     for (; next_task<PARTS, G::THREADS>(a, walks, block, task, first); first = false) {
-        const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H;
-        const int slice = int(task.walk % G::SLICES) * G::CW;
-        const int64_t begin = PARTS ? task.part * a.part_len : 0;
-        const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
-        const int64_t vbase = (b * a.T * a.H + h) * N + slice;
-        float* keep = a.s_seg + head * (nseg + 1) * N * N;
-        float* hand = a.hand + head * N * N + int64_t(slice + j0) * N;
+        const Place here(a, task, warp);
+        const int64_t end = here.end;
+        float* keep = a.s_seg + here.head * (nseg + 1) * N * N;
         float S[N / 8][4];
-        if (!PARTS || task.part == 0) load_state<N>(S, a.s_in == nullptr ? nullptr : a.s_in + head * N * N + slice + j0, lane);
-        else take_over<N>(S, hand, task.lost, lane);
+        here.start(S, a, task, a.s_in, lane);
         int st = 0;
 #pragma unroll 1
-        for (int64_t t0 = begin; t0 < end; t0 += kChunk, st = (st + 1) % G::NST) {
+        for (int64_t t0 = here.begin; t0 < end; t0 += kChunk, st = (st + 1) % G::NST) {
             const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
             G g(smem, st);
-            if (!WANT_Y && t0 % kSegment == 0) keep_state<IO, N>(keep + t0 / kSegment * N * N, slice + j0, S, lane);
+            if (!WANT_Y && t0 % kSegment == 0) keep_state<IO, N>(keep + t0 / kSegment * N * N, here.column, S, lane);
             bar_sync<G::BAR>(kBarFull + st);
             // K S and R S, transposed
             float p[2][4], q[2][4], x[2][4];
@@ -800,7 +958,7 @@ __device__ __forceinline__ void forward_walk(const Args& a, char* smem, int64_t 
                     fade_add(S[2 * kk + 1], gl, d[1]);
                 }
             }
-            const int64_t at = vbase + t0 * vs + j0;
+            const int64_t at = here.values + t0 * vs;
             if constexpr (!WANT_Y) {
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
@@ -824,18 +982,17 @@ __device__ __forceinline__ void forward_walk(const Args& a, char* smem, int64_t 
             }
             if (t0 + G::NST * kChunk < end) bar_arrive<G::BAR>(kBarFree + st);
         }
-        if (PARTS && end < a.T) {
-            hand_on<N>(hand, S, lane);
-        } else if constexpr (WANT_Y) {
-            if (a.s_out != nullptr) store_state<N>(a.s_out + head * N * N + slice + j0, S, lane);
-        } else {
-            keep_state<IO, N>(keep + nseg * N * N, slice + j0, S, lane);
+        const uint32_t odd = odd_lines<N>(S);
+        if (bar_or<G::THREADS>(kBarTask, odd != 0 && began_finite<N, Place>(a, task, a.s_in, odd))) {
+            forward_again<IO, N, WANT_Y, PARTS>(a, smem, task);
+            continue;
         }
+        forward_end<IO, N, WANT_Y, PARTS>(a, here, S, lane);
     }
 }
 
 template <typename IO, int N, bool WANT_Y, bool PARTS>
-__global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO, N>) delta_forward_mma_kernel(const Args a) {
+__global__ void __launch_bounds__(ForwardShape<IO, N, WANT_Y>::THREADS, kCtas<IO, N>) delta_forward_mma_kernel(const __grid_constant__ Args a) {
     extern __shared__ __align__(16) char smem[];
     pdl_wait();
     forward_walk<IO, N, WANT_Y, PARTS>(a, smem, blockIdx.x);

@@ -38,6 +38,70 @@ namespace delta {
 template <typename IO, int N>
 using ReverseShape = Columns<IO, N, true, 6, 3>;
 
+// A chunk's nt tokens of a warp's 16 columns one after another, backwards, from the
+// staged rows (S: D^T); du and dv at the lane's first line.  w, beta: of its first token.
+template <typename IO, int N>
+__device__ __forceinline__ void reverse_tokens(const ReverseShape<IO, N>& g, float (&S)[N / 8][4], int j0, int nt, const float* w,
+                                               const float* beta, int64_t heads, float* du, IO* dv, int64_t vs, int lane) {
+    using G = ReverseShape<IO, N>;
+#pragma unroll 1
+    for (int t = nt - 1; t >= 0; --t) {
+        const __nv_bfloat16* kp = g.k + t * G::LD + 2 * (lane % 4);
+        const IO* yp = g.v + t * G::LDV + j0 + lane / 4;
+        const float a = expf(-w[t * heads]), be = beta[t * heads], dy[2] = {to_f32(yp[0]), to_f32(yp[8])};
+        float x[2] = {0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < N / 8; ++n) {
+            const float2 k = staged_pair<G::KP>(kp + 8 * n, G::PIECE), r = staged_pair<G::KP>(kp + (g.r() - g.k) + 8 * n, G::PIECE);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                S[n][i] = fmaf((i & 1) ? r.y : r.x, dy[i >> 1], S[n][i]);
+                x[i >> 1] = fmaf(S[n][i], (i & 1) ? k.y : k.x, x[i >> 1]);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            x[q] = quad_sum(x[q]);
+            if (lane % 4 == 0) du[t * vs + 8 * q] = x[q];
+            x[q] *= be;
+            if (lane % 4 == 0) put(dv + t * vs + 8 * q, x[q]);
+        }
+#pragma unroll
+        for (int n = 0; n < N / 8; ++n) {
+            const float2 k = staged_pair<G::KP>(kp + 8 * n, G::PIECE);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[n][i] = a * fmaf((i & 1) ? k.y : k.x, -x[i >> 1], S[n][i]);
+        }
+    }
+}
+
+// where the gradient of the state ahead of the walk's first token goes
+template <int N, bool PARTS, typename PLACE>
+__device__ __forceinline__ void reverse_end(const Args& a, const PLACE& p, const float (&S)[N / 8][4], int lane) {
+    if (PARTS && p.begin > 0) hand_on<N>(p.hand(a), S, lane);
+    else if (a.ds_in != nullptr) store_state<N>(a.ds_in + p.head * N * N + p.column, S, lane);
+}
+template <typename IO, int N, bool PARTS>
+__device__ __noinline__ void reverse_again(const Args& a, char* smem, const Task& task) {
+    using G = ReverseShape<IO, N>;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t nseg = (a.T + kSegment - 1) / kSegment, vs = a.H * N;
+    const Reach<G, N, PARTS, true> p(a, task, warp);
+    float S[N / 8][4];
+    p.start(S, a, task, a.ds_out, lane);
+    int st = 0;
+#pragma unroll 1
+    for (int64_t t0 = p.begin + (p.end - 1 - p.begin) / kChunk * kChunk; t0 >= p.begin; t0 -= kChunk, st = (st + 1) % G::NST) {
+        const int nt = p.end - t0 < kChunk ? int(p.end - t0) : kChunk;
+        const int64_t row = p.row + t0 * a.H, line = p.values + t0 * vs + lane / 4;
+        bar_sync<G::BAR>(kBarFull + st);
+        reverse_tokens<IO, N>(G(smem, st), S, warp * 16, nt, a.w + row, a.beta + row, a.H, a.du + line, static_cast<IO*>(a.dv) + line, vs, lane);
+        if (t0 >= p.begin + G::NST * kChunk) bar_arrive<G::BAR>(kBarFree + st);
+        if (t0 % kSegment == 0) keep_state<IO, N>(a.d_seg + (p.head * (nseg + 1) + t0 / kSegment) * N * N, p.column, S, lane);
+    }
+    reverse_end<N, PARTS>(a, p, S, lane);
+}
+
 template <typename IO, int N, bool PARTS>
 __device__ __forceinline__ void reverse_walk(const Args& a, char* smem, int64_t block) {
     using G = ReverseShape<IO, N>;
@@ -64,44 +128,47 @@ __device__ __forceinline__ void reverse_walk(const Args& a, char* smem, int64_t 
             const IO* yp = static_cast<const IO*>(a.dy) + vbase;
             const float* wp = a.w + b * a.T * a.H + h;
             const float* bp = a.beta + b * a.T * a.H + h;
+            bool again = false;
+            do {
 #pragma unroll 1
-            for (int64_t t0 = last - st * kChunk; t0 >= begin; t0 -= G::NST * kChunk) {
-                const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
-                if (last - t0 >= G::NST * kChunk) bar_sync<G::BAR>(kBarFree + st);
-                const float w = lane < nt ? wp[(t0 + lane) * a.H] : 0.f, be = lane < nt ? bp[(t0 + lane) * a.H] : 0.f;
-                g.fetch(kp + t0 * ks, rp + t0 * ks, ks, yp + t0 * vs, vs, nt, a.vec, lane);
-                // B, its inverse and P
-                const ChunkDecay d = chunk_decay<kChunk>(w, g.sums, lane);
-                if (lane < kChunk) {
-                    g.beta[lane] = be;
-                    g.sc[lane] = d.after;
-                    g.sc[kChunk + lane] = d.upto;
-                    g.sc[2 * kChunk + lane] = d.upto * be;
-                }
-                __syncwarp();
-                float kk[2][4], rk[2][4];
-                gram<N, KP, KP, KP, kChain<IO>>(kk, g.k, g.k, G::PIECE, lane);
-                gram<N, KP, KP, KP, kChain<IO>>(rk, g.r(), g.k, G::PIECE, lane);
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const int t = 8 * n + 2 * (lane % 4);
-                    const float2 t0s = g.sums[t], t1s = g.sums[t + 1];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int s = lane / 4 + 8 * q;
-                        const float bs = g.beta[s];
-                        const float2 ss = g.sums[s];
-                        const float g0 = decay_of(ss, t0s), g1 = decay_of(ss, t1s);
-                        g.diag[s * 20 + t] = t < s ? g0 * bs * kk[n][2 * q] : 0.f;
-                        g.diag[s * 20 + t + 1] = t + 1 < s ? g1 * bs * kk[n][2 * q + 1] : 0.f;
-                        put_pieces<3>(g.mats + 3 * kMat, s, t, t <= s ? g0 * rk[n][2 * q] : 0.f,
-                                      t + 1 <= s ? g1 * rk[n][2 * q + 1] : 0.f);
+                for (int64_t t0 = last - st * kChunk; t0 >= begin; t0 -= G::NST * kChunk) {
+                    const int nt = end - t0 < kChunk ? int(end - t0) : kChunk;
+                    if (last - t0 >= G::NST * kChunk) bar_sync<G::BAR>(kBarFree + st);
+                    const float w = lane < nt ? wp[(t0 + lane) * a.H] : 0.f, be = lane < nt ? bp[(t0 + lane) * a.H] : 0.f;
+                    g.fetch(kp + t0 * ks, rp + t0 * ks, ks, yp + t0 * vs, vs, nt, a.vec, lane);
+                    // B, its inverse and P
+                    const ChunkDecay d = chunk_decay<kChunk>(w, g.sums, lane);
+                    if (lane < kChunk) {
+                        g.beta[lane] = be;
+                        g.sc[lane] = d.after;
+                        g.sc[kChunk + lane] = d.upto;
+                        g.sc[2 * kChunk + lane] = d.upto * be;
                     }
+                    __syncwarp();
+                    float kk[2][4], rk[2][4];
+                    gram<N, KP, KP, KP, kChain<IO>>(kk, g.k, g.k, G::PIECE, lane);
+                    gram<N, KP, KP, KP, kChain<IO>>(rk, g.r(), g.k, G::PIECE, lane);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const int t = 8 * n + 2 * (lane % 4);
+                        const float2 t0s = g.sums[t], t1s = g.sums[t + 1];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int s = lane / 4 + 8 * q;
+                            const float bs = g.beta[s];
+                            const float2 ss = g.sums[s];
+                            const float g0 = decay_of(ss, t0s), g1 = decay_of(ss, t1s);
+                            g.diag[s * 20 + t] = t < s ? g0 * bs * kk[n][2 * q] : 0.f;
+                            g.diag[s * 20 + t + 1] = t + 1 < s ? g1 * bs * kk[n][2 * q + 1] : 0.f;
+                            put_pieces<3>(g.mats + 3 * kMat, s, t, t <= s ? g0 * rk[n][2 * q] : 0.f,
+                                          t + 1 <= s ? g1 * rk[n][2 * q + 1] : 0.f);
+                        }
+                    }
+                    __syncwarp();
+                    put_inverse(g.mats, g.diag, lane);
+                    bar_arrive<G::BAR>(kBarFull + st);
                 }
-                __syncwarp();
-                put_inverse(g.mats, g.diag, lane);
-                bar_arrive<G::BAR>(kBarFull + st);
-            }
+            } while (!again && (again = bar_or<G::THREADS>(kBarTask, false)));
         }
         return;
     }
@@ -110,20 +177,16 @@ __device__ __forceinline__ void reverse_walk(const Args& a, char* smem, int64_t 
     const int j0 = warp * 16;
     const int64_t nseg = (a.T + kSegment - 1) / kSegment;
     const int off_b = b_plain(lane, LD), off_t = b_trans(lane, LD), off_m = m_trans(lane);
+    using Place = Reach<G, N, PARTS, true>;
     for (; next_task<PARTS, G::THREADS>(a, walks, block, task, first); first = false) {
-        const int64_t head = task.walk / G::SLICES, b = head / a.H, h = head % a.H;
-        const int slice = int(task.walk % G::SLICES) * G::CW;
-        const int64_t begin = PARTS ? (a.parts - 1 - task.part) * a.part_len : 0;
-        const int64_t end = PARTS && begin + a.part_len < a.T ? begin + a.part_len : a.T;
+        const Place here(a, task, warp);
+        const int64_t begin = here.begin, end = here.end;
         const int64_t last = begin + (end - 1 - begin) / kChunk * kChunk;
-        const int64_t vbase = (b * a.T * a.H + h) * N + slice;
-        float* grads = a.d_seg + head * (nseg + 1) * N * N;
-        float* hand = a.hand + head * N * N + int64_t(slice + j0) * N;
+        float* grads = a.d_seg + here.head * (nseg + 1) * N * N;
         float S[N / 8][4];   // D^T
-        if (!PARTS || task.part == 0) load_state<N>(S, a.ds_out == nullptr ? nullptr : a.ds_out + head * N * N + slice + j0, lane);
-        else take_over<N>(S, hand, task.lost, lane);
+        here.start(S, a, task, a.ds_out, lane);
         // gradient states between segments, as S^T's
-        if (!PARTS || task.part == 0) keep_state<IO, N>(grads + nseg * N * N, slice + j0, S, lane);
+        if (!PARTS || task.part == 0) keep_state<IO, N>(grads + nseg * N * N, here.column, S, lane);
         int st = 0;
 #pragma unroll 1
         for (int64_t t0 = last; t0 >= begin; t0 -= kChunk, st = (st + 1) % G::NST) {
@@ -186,7 +249,7 @@ __device__ __forceinline__ void reverse_walk(const Args& a, char* smem, int64_t 
                     fade_add(S[2 * kk + 1], gl, d[1]);
                 }
             }
-            const int64_t at = vbase + t0 * vs + j0;
+            const int64_t at = here.values + t0 * vs;
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 store_half(a.du + at + 8 * n * vs, vs, nt - 8 * n, du[n], g.v, 0, false, lane);
@@ -197,15 +260,19 @@ __device__ __forceinline__ void reverse_walk(const Args& a, char* smem, int64_t 
                 store_half(static_cast<IO*>(a.dv) + at + 8 * n * vs, vs, nt - 8 * n, du[n], g.v + 8 * n * G::LDV + j0, G::LDV, a.vec, lane);
             }
             if (t0 >= begin + G::NST * kChunk) bar_arrive<G::BAR>(kBarFree + st);
-            if (t0 % kSegment == 0) keep_state<IO, N>(grads + t0 / kSegment * N * N, slice + j0, S, lane);
+            if (t0 % kSegment == 0) keep_state<IO, N>(grads + t0 / kSegment * N * N, here.column, S, lane);
         }
-        if (PARTS && begin > 0) hand_on<N>(hand, S, lane);
-        else if (a.ds_in != nullptr) store_state<N>(a.ds_in + head * N * N + slice + j0, S, lane);
+        const uint32_t odd = odd_lines<N>(S);
+        if (bar_or<G::THREADS>(kBarTask, odd != 0 && began_finite<N, Place>(a, task, a.ds_out, odd))) {   // as in the forward walk
+            reverse_again<IO, N, PARTS>(a, smem, task);
+            continue;
+        }
+        reverse_end<N, PARTS>(a, here, S, lane);
     }
 }
 
 template <typename IO, int N>
-__global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) delta_reverse_mma_kernel(const Args a) {
+__global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) delta_reverse_mma_kernel(const __grid_constant__ Args a) {
     extern __shared__ __align__(16) char smem[];
     pdl_wait();
     reverse_walk<IO, N, true>(a, smem, blockIdx.x);
@@ -216,7 +283,7 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
 // 1830 us, and 449 where 32 heads of one sequence take 379: both codes in one
 // instruction cache.
 template <typename IO, int N>
-__global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) delta_walks_kernel(const Args a) {
+__global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) delta_walks_kernel(const __grid_constant__ Args a) {
     extern __shared__ __align__(16) char smem[];
     const int64_t walks = a.B * a.H * ReverseShape<IO, N>::SLICES;
     pdl_wait();
@@ -401,13 +468,8 @@ __device__ __forceinline__ void row_products(float (&own)[2], const __nv_bfloat1
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const __nv_bfloat16* r2 = rb + place(t_lo + 8 * q, i0 + p * 16 + 8 * n + 2 * (lane % 4));
-                float x0 = 0.f, x1 = 0.f;
-#pragma unroll
-                for (int c = KP - 1; c >= 0; --c) {
-                    const uint32_t w2 = *reinterpret_cast<const uint32_t*>(r2 + c * piece);
-                    x0 += __uint_as_float(w2 << 16), x1 += __uint_as_float(w2 & 0xffff0000u);
-                }
-                own[q] = fmaf(x0, dr[p][n][2 * q], fmaf(x1, dr[p][n][2 * q + 1], own[q]));
+                const float2 x = staged_pair<KP>(r2, piece);
+                own[q] = fmaf(x.x, dr[p][n][2 * q], fmaf(x.y, dr[p][n][2 * q + 1], own[q]));
             }
 }
 
@@ -468,6 +530,142 @@ __device__ __forceinline__ void store_rows(const Args& a, const Segment& sg, con
     }
 }
 
+// A segment token by token, in which something is not finite: its products by
+// blocks met the zeros of tokens that it must not reach.  dr, dk and dw are written
+// again; e, du (the walks') and dvv are right.  A thread holds a quarter of a key's
+// row of the states.  smem: the segment's tiles, which are over.  False, and nothing
+// is done, where the products are right: a state that enters as not finite leaves
+// nothing finite, and a gradient of the last state that is not finite nothing of dk
+// and dw (odd_dr: something in this thread's dr is not finite).
+//   forward   S_t, dr_t = S_t dy_t, the part -a_t S_{t-1} dv_t of dk_t, and m, the
+//             last token that leaves a finite state
+//   backward  D_t, the part D_t u_t of dk_t, and <D, S> behind token m, where the
+//             sums that dw takes may begin: of tokens behind m + 1 there is none
+template <typename IO, int N>
+__device__ __forceinline__ bool segment_tokens(const Args& a, const Segment& sg, char* smem, const float* s_seg, const float* d_seg,
+                                               const float* dvv, bool odd_dr, int tid) {
+    constexpr int J = N / 4, WARPS = 4 * N / 32;
+    float* dkp = reinterpret_cast<float*>(smem);      // (tokens, N)
+    float* rdr = dkp + kSegment * N;                  // (tokens, warps)
+    float* sum = rdr + kSegment * WARPS;              // (2, warps)
+    int& bad = *reinterpret_cast<int*>(sum + 2 * WARPS);   // the first token whose state is not finite
+    const int i = tid / 4, j = tid % 4 * J, lane = tid % 32, warp = tid / 32, nt = sg.nt;
+    const bool whole = a.H == a.Hk;
+    const auto entry = [&](const float* s, int q) { return s[kTcSegments<IO, N> ? i * N + j + q : (j + q) * N + i]; };
+    const auto key = [&](const void* x, int t) { return to_f32(static_cast<const IO*>(x)[sg.keys + t * sg.ks + i]); };
+    const auto fade = [&](int t) { return expf(-a.w[sg.scalar + t * a.H]); };
+    const auto value = [&](const float* x, int t, int q) { return a.beta[sg.scalar + t * a.H] * x[sg.rows + t * sg.vs + j + q]; };
+    const auto dy = [&](int t, int q) { return to_f32(static_cast<const IO*>(a.dy)[sg.rows + t * sg.vs + j + q]); };
+    const auto out = [&](void* x, float* h, int t, float v) {
+        const int64_t at = sg.rows + t * sg.vs + i;
+        if (whole) put(static_cast<IO*>(x) + at, v);
+        else h[at] = v;
+    };
+    float S[J], D[J], z[2] = {0.f, 0.f};   // z: NaN where S, D are not finite
+#pragma unroll
+    for (int q = 0; q < J; ++q) {
+        S[q] = entry(s_seg, q);
+        z[0] = fmaf(S[q], 0.f, z[0]);
+        z[1] = fmaf(entry(d_seg, q), 0.f, z[1]);
+    }
+    const bool s_odd = __syncthreads_or(z[0] != 0.f), d_odd = __syncthreads_or(z[1] != 0.f);
+    if (s_odd || (d_odd && !__syncthreads_or(odd_dr))) return false;
+    if (tid == 0) bad = nt;
+    __syncthreads();
+#pragma unroll 1
+    for (int t = 0; t < nt; ++t) {
+        const float f = fade(t), k = key(a.k, t);
+        float x = 0.f, z = 0.f, odd = 0.f;
+#pragma unroll
+        for (int q = 0; q < J; ++q) {
+            S[q] *= f;
+            x = fmaf(S[q], value(a.du, t, q), x);
+            S[q] = fmaf(k, value(a.e, t, q), S[q]);
+            z = fmaf(S[q], dy(t, q), z);
+            odd = fmaf(S[q], 0.f, odd);
+        }
+        if (odd != 0.f) atomicMin(&bad, t);
+        x = quad_sum(x), z = quad_sum(z);
+        float p = lane % 4 == 0 ? key(a.r, t) * z : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) p += __shfl_xor_sync(0xffffffffu, p, o);
+        if (lane == 0) rdr[t * WARPS + warp] = p;
+        if (lane % 4 == 0) {
+            dkp[t * N + i] = -x;
+            out(a.dr, a.drh, t, z);
+        }
+    }
+    __syncthreads();
+    const int m = bad - 1;
+#pragma unroll
+    for (int q = 0; q < J; ++q) S[q] = entry(s_seg, q), D[q] = entry(d_seg, q);
+#pragma unroll 1
+    for (int t = 0; t <= m; ++t) {
+        const float f = fade(t), k = key(a.k, t);
+#pragma unroll
+        for (int q = 0; q < J; ++q) S[q] = fmaf(k, value(a.e, t, q), f * S[q]);
+    }
+    const auto inner = [&](int to) {   // of the state at hand and D
+        float x = 0.f;
+#pragma unroll
+        for (int q = 0; q < J; ++q) x = fmaf(S[q], D[q], x);
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane == 0) sum[to * WARPS + warp] = x;
+    };
+#pragma unroll 1
+    for (int t = nt - 1; t >= 0; --t) {
+        if (t == m) inner(0);
+        const float f = fade(t), k = key(a.k, t), r = key(a.r, t);
+        float x = 0.f;
+#pragma unroll
+        for (int q = 0; q < J; ++q) {
+            D[q] = fmaf(r, dy(t, q), D[q]);
+            x = fmaf(D[q], value(a.e, t, q), x);
+            D[q] = f * fmaf(k, -value(a.du, t, q), D[q]);
+        }
+        x = quad_sum(x);
+        if (lane % 4 == 0) out(a.dk, a.dkh, t, x + dkp[t * N + i]);
+    }
+    if (m < 0) inner(0);
+#pragma unroll
+    for (int q = 0; q < J; ++q) S[q] = entry(s_seg, q);
+    inner(1);
+    __syncthreads();
+    if (tid == 0) {
+        float phi = 0.f, begin = 0.f;   // <D, S> behind token t, ahead of the first
+        for (int w = 0; w < WARPS; ++w) phi += sum[w], begin += sum[WARPS + w];
+#pragma unroll 1
+        for (int t = nt - 1; t >= 0; --t) {
+            const bool reset = fade(t) == 0.f;
+            float g = t > m + 1 ? __int_as_float(0x7fffffff) : phi;
+            if (t <= m) {
+                float p = -dvv[t];
+                for (int w = 0; w < WARPS; ++w) p += rdr[t * WARPS + w];
+                g += p;
+            }
+            if (reset) g = 0.f;
+            if (t <= m) phi = g;
+            a.dw[sg.scalar + t * a.H] = -(t == 0 && !reset ? begin : g);
+        }
+    }
+    return true;
+}
+
+// Is one of these not finite, or their sum?  (A sum of finite values that is not
+// costs its segment time and nothing else.)
+template <int NP>
+__device__ __forceinline__ bool any_odd(const float (&x)[NP][2][4]) {
+    F2 s = f2s(0.f);
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) s = add2(s, f2(x[p][n][i], x[p][n][i + 1]));
+    return !(fabsf(f2lo(s) + f2hi(s)) <= 3.4e38f);
+}
+
 // dw of a segment from r . dr by the warps' rows (own), dv . v and <D, S> at its
 // end (border[1], a thread's share); rates: warp 0's, of two tokens a lane.  All
 // threads of the CTA.  <D, S> at its begin
@@ -475,10 +673,11 @@ __device__ __forceinline__ void store_rows(const Args& a, const Segment& sg, con
 // state it is zero, and not what rounding leaves of the terms.  At a token whose
 // decay is 0 the sum is 0 and begins anew, so that what rounding leaves of the
 // terms behind it does not reach the document ahead of it.
-template <int N, int PARTS>
+// odd_dr, odd_dk: something in this thread's is not finite; smem: the segment's tiles.
+template <typename IO, int N, int PARTS>
 __device__ __forceinline__ void segment_rates(const Args& a, const Segment& sg, float (&own)[2], float (&border)[2], float* rdr,
                                               const float* dvv, float* inner, const float* s_seg, const float* d_seg, int t_lo, float2 rates,
-                                              int tid) {
+                                              bool odd_dr, bool odd_dk, char* smem, int tid) {
     constexpr int WARPS = 4 * PARTS, THREADS = 32 * WARPS;
     const int lane = tid % 32, warp = tid / 32, nt = sg.nt;
     const int64_t scalar = sg.scalar, seg = sg.seg;
@@ -502,7 +701,7 @@ __device__ __forceinline__ void segment_rates(const Args& a, const Segment& sg, 
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) border[q] += __shfl_xor_sync(0xffffffffu, border[q], o);
     if (lane == 0) inner[2 * warp] = border[0], inner[2 * warp + 1] = border[1];
-    __syncthreads();
+    if (__syncthreads_or(odd_dr || odd_dk) && segment_tokens<IO, N>(a, sg, smem, s_seg, d_seg, dvv, odd_dr, tid)) return;
     // --- dw: the sum <Dn, S> from the segment's end backwards
     if (warp == 0) {
         float first = 0.f, end = 0.f;
@@ -552,7 +751,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     using G = SegmentShape<IO, N>;
     constexpr int KP = G::KP, NP = G::IC / 16;
     constexpr Swizzled<N> place{};
-    extern __shared__ __align__(16) char smem[];
+    extern __shared__ __align__(128) char smem[];                 // the swizzle is of addresses: no static array lies ahead of it
     __nv_bfloat16* ub = reinterpret_cast<__nv_bfloat16*>(smem);   // u = beta e
     __nv_bfloat16* db = ub + 3 * G::PIECE;                        // dv = beta du
     __nv_bfloat16* yb = db + 3 * G::PIECE;
@@ -728,7 +927,7 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     float own[2];
     row_products<N, NP, KP>(own, rb, G::PIECE, dr, t_lo, i0, lane);
     store_rows<IO, N, NP>(a, sg, dr, dk, ub + warp * 2 * 16 * (G::IC + 8), tb, i0, lane);
-    segment_rates<N, G::PARTS>(a, sg, own, border, rdr, dvv, inner, s_seg, d_seg, t_lo, rates, tid);
+    segment_rates<IO, N, G::PARTS>(a, sg, own, border, rdr, dvv, inner, s_seg, d_seg, t_lo, rates, any_odd(dr), any_odd(dk), smem, tid);
 }
 
 // dr and dk of a key head: the sums over the value heads that share it, in

@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
     row_products<N, 2, 1>(own, raw, 0, dr, t_lo, i0, lane);
     store_rows<IO, N, 2>(a, sg, dr, dk, tiles + G::U * PC + warp * (G::ROWS / 8), tb, i0, lane);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    segment_rates<N, G::PARTS>(a, sg, own, border, rdr, dvv, inner, s_seg, d_seg, t_lo, rates, tid);
+    segment_rates<IO, N, G::PARTS>(a, sg, own, border, rdr, dvv, inner, s_seg, d_seg, t_lo, rates, ok && any_odd(dr), ok && any_odd(dk), smem, tid);
     if (warp == 0) {   // every warp's loads are done: the barrier in segment_rates
         after_batch();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(acc), "r"(G::COLS) : "memory");
