@@ -182,32 +182,56 @@ class Workspace:
     GPU (the default: the current stream).  The delta rule's and the group
     norm's calls have a buffer of their own in it, whose contents mean nothing
     between calls.  A call that needs more than a buffer holds replaces it: a
-    CUDA graph captured with the old one has to be captured again."""
+    CUDA graph captured with the old one has to be captured again.
+
+    A Workspace is of one device, `device` or its first call's; calls on another
+    are refused.  Its memory is of the stream of the call that made it, and a
+    replaced buffer is reused only when every stream of its calls is done with it."""
 
     def __init__(self, device=None):
         self.device = device
         self.buf = None
         self.plain = None
+        self._owner = {}     # the raw stream that each buffer was allocated on
 
-    def get(self, nbytes: int, stream=None):
+    def get(self, nbytes: int, stream=None, device=None):
         if nbytes == 0:
             return None, 0
-        if self.buf is None or self.buf.numel() - 256 < nbytes:
-            self.buf = self._new(nbytes)
-            self._init(self.buf, self.buf.numel() - 256, stream)
-        return self._aligned_ptr(self.buf), self.buf.numel() - 256
+        return self._take("buf", nbytes, stream, device)
 
     def scratch(self, nbytes: int, stream=None, device=None):
         """The other buffer: only its header (the error word) is cleared."""
-        if self.plain is None or self.plain.numel() - 256 < nbytes:
-            self.plain = self._new(nbytes, device)
-            self._init(self.plain, 256, stream)
-        return self._aligned_ptr(self.plain), self.plain.numel() - 256
+        return self._take("plain", nbytes, stream, device)
 
-    def _new(self, nbytes, device=None):
+    def _take(self, name, nbytes, stream, device):
         torch = _torch()
-        dev = self.device or device or torch.device("cuda", torch.cuda.current_device())
-        return torch.empty(int(nbytes) + 256, dtype=torch.uint8, device=dev)
+        buf = getattr(self, name)
+        if device is None and buf is not None:
+            device = buf.device
+        if buf is None or buf.device != device or buf.numel() - 256 < nbytes:
+            buf = self._make(name, nbytes, stream, device)
+        elif _stream_ptr(stream, device) != self._owner[name]:
+            buf.record_stream(stream if stream is not None else torch.cuda.current_stream(device))
+        return self._aligned_ptr(buf), buf.numel() - 256
+
+    def _make(self, name, nbytes, stream, device):
+        torch = _torch()
+        for held in (self.device, self.buf, self.plain):
+            mine = getattr(held, "device", held)
+            if mine is None:
+                continue
+            mine = torch.device(mine)
+            if mine.index is not None and device is not None and mine != device:
+                raise ValueError(f"the workspace is on {mine}, the call on {device}: use one for each device")
+            device = device or mine
+        if device is None or device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        with torch.cuda.stream(stream):   # None: the current one
+            buf = torch.empty(int(nbytes) + 256, dtype=torch.uint8, device=device)
+        setattr(self, name, buf)
+        self._owner[name] = _stream_ptr(stream, device)
+        self._init(buf, buf.numel() - 256 if name == "buf" else 256, stream)
+        return buf
 
     def _init(self, buf, nbytes, stream):
         _launch(buf.device, "wkv_workspace_init", lib().wkv_workspace_init, self._aligned_ptr(buf), nbytes,
@@ -291,7 +315,7 @@ def wkv_forward(w, u, k, v, r=None, state_in=None, *, y=None, state_out=None, wa
         need = workspace_bytes(B, T, C, code)
         if chain is not None:
             need = max(need, 256 + 16 * B * C)   # the chain's words follow the header
-        ws_ptr, ws_bytes = ws.get(need, stream)
+        ws_ptr, ws_bytes = ws.get(need, stream, dev)
     else:
         ws_ptr, ws_bytes = None, 0
     flags = WKV_FLAG_INPUTS_READY if inputs_ready else 0
@@ -353,7 +377,7 @@ def wkv_state(w, k, v, state_in=None, *, state_out=None, workspace: Workspace = 
     sp = _stream_ptr(stream, dev)
     if use_workspace:
         ws = workspace if workspace is not None else default_workspace(dev)
-        ws_ptr, ws_bytes = ws.get(workspace_bytes(B, T, C, code), stream)
+        ws_ptr, ws_bytes = ws.get(workspace_bytes(B, T, C, code), stream, dev)
     else:
         ws_ptr, ws_bytes = None, 0
     _check(lib().wkv_state(B, T, C, code, _ptr(w), _ptr(k), _ptr(v), _ptr(state_in), _ptr(state_out), ws_ptr,
@@ -469,7 +493,7 @@ def wkv_backward(w, u, k, v, r=None, state_in=None, *, dy, dstate_out=None, dk=N
     _need(dstate_in, "dstate_in", (3, B, C), torch.float32, dev)
     ws = workspace if workspace is not None else default_workspace(dev)
     sp = _stream_ptr(stream, dev)
-    ws_ptr, ws_bytes = ws.get(backward_workspace_bytes(B, T, C, code), stream)
+    ws_ptr, ws_bytes = ws.get(backward_workspace_bytes(B, T, C, code), stream, dev)
     _check(lib().wkv_backward(B, T, C, code, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(r), _ptr(state_in),
                               _ptr(dy), _ptr(dstate_out), _ptr(dk), _ptr(dv), _ptr(dr), _ptr(dw), _ptr(du),
                               _ptr(dstate_in), ws_ptr, ws_bytes, sp), "wkv_backward")
