@@ -174,6 +174,22 @@ def _need(t, name, shape, dtype, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _empty(shape, dtype, dev, stream):
+    """A call's output: of `stream`, which writes it, and known to be used on the
+    current stream; without a stream of the call's own, an ordinary tensor."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
+def _empty_like(t, stream):
+    return _torch().empty_like(t) if stream is None else _empty(t.shape, t.dtype, t.device, stream)
+
+
 class Workspace:
     """Device scratch for wkv_forward's cross-block exchange, grown on demand.
 
@@ -304,10 +320,10 @@ def wkv_forward(w, u, k, v, r=None, state_in=None, *, y=None, state_out=None, wa
     _need(k, "k", (B, T, C), k.dtype, dev)
     _need(state_in, "state_in", (3, B, C), torch.float32, dev)
     if y is None:
-        y = torch.empty((B, T, C), dtype=k.dtype, device=dev)
+        y = _empty((B, T, C), k.dtype, dev, stream)
     _need(y, "y", (B, T, C), k.dtype, dev)
     if state_out is None and want_state:
-        state_out = torch.empty((3, B, C), dtype=torch.float32, device=dev)
+        state_out = _empty((3, B, C), torch.float32, dev, stream)
     _need(state_out, "state_out", (3, B, C), torch.float32, dev)
     sp = _stream_ptr(stream, dev)
     if use_workspace:
@@ -372,7 +388,7 @@ def wkv_state(w, k, v, state_in=None, *, state_out=None, workspace: Workspace = 
     _need(k, "k", (B, T, C), k.dtype, dev)
     _need(state_in, "state_in", (3, B, C), torch.float32, dev)
     if state_out is None:
-        state_out = torch.empty((3, B, C), dtype=torch.float32, device=dev)
+        state_out = _empty((3, B, C), torch.float32, dev, stream)
     _need(state_out, "state_out", (3, B, C), torch.float32, dev)
     sp = _stream_ptr(stream, dev)
     if use_workspace:
@@ -401,7 +417,7 @@ def wkv_state_combine(w, lens, states, state_in=None, *, state_out=None, stream=
     _need(w, "w", (C,), torch.float32, dev)
     _need(state_in, "state_in", (3, B, C), torch.float32, dev)
     if state_out is None:
-        state_out = torch.empty((3, B, C), dtype=torch.float32, device=dev)
+        state_out = _empty((3, B, C), torch.float32, dev, stream)
     _need(state_out, "state_out", (3, B, C), torch.float32, dev)
     arr = (ctypes.c_int64 * max(1, n))(*[int(x) for x in lens])
     _check(lib().wkv_state_combine(B, C, n, _ptr(w), arr, _ptr(states), _ptr(state_in), _ptr(state_out),
@@ -432,10 +448,10 @@ def wkv5_forward(w, u, r, k, v, H, state_in=None, *, y=None, state_out=None, wan
     _need(u, "u", (C,), torch.float32, dev)
     _need(state_in, "state_in", (B, H, N, N), torch.float32, dev)
     if y is None:
-        y = torch.empty((B, T, C), dtype=k.dtype, device=dev)
+        y = _empty((B, T, C), k.dtype, dev, stream)
     _need(y, "y", (B, T, C), k.dtype, dev)
     if state_out is None and want_state:
-        state_out = torch.empty((B, H, N, N), dtype=torch.float32, device=dev)
+        state_out = _empty((B, H, N, N), torch.float32, dev, stream)
     _need(state_out, "state_out", (B, H, N, N), torch.float32, dev)
     _check(lib().wkv5_forward(B, T, C, H, code, _ptr(w), int(per_token), _ptr(u), _ptr(r), _ptr(k), _ptr(v),
                               _ptr(state_in), _ptr(y), _ptr(state_out), _stream_ptr(stream, dev)), "wkv5_forward")
@@ -475,17 +491,17 @@ def wkv_backward(w, u, k, v, r=None, state_in=None, *, dy, dstate_out=None, dk=N
     _need(state_in, "state_in", (3, B, C), torch.float32, dev)
     _need(dstate_out, "dstate_out", (3, B, C), torch.float32, dev)
     if dk is None:
-        dk = torch.empty((B, T, C), dtype=k.dtype, device=dev)
+        dk = _empty((B, T, C), k.dtype, dev, stream)
     if dv is None:
-        dv = torch.empty((B, T, C), dtype=k.dtype, device=dev)
+        dv = _empty((B, T, C), k.dtype, dev, stream)
     if dr is None and r is not None:
-        dr = torch.empty((B, T, C), dtype=k.dtype, device=dev)
+        dr = _empty((B, T, C), k.dtype, dev, stream)
     if dw is None:
-        dw = torch.empty((C,), dtype=torch.float32, device=dev)
+        dw = _empty((C,), torch.float32, dev, stream)
     if du is None:
-        du = torch.empty((C,), dtype=torch.float32, device=dev)
+        du = _empty((C,), torch.float32, dev, stream)
     if dstate_in is None and want_dstate_in:
-        dstate_in = torch.empty((3, B, C), dtype=torch.float32, device=dev)
+        dstate_in = _empty((3, B, C), torch.float32, dev, stream)
     for t, name in ((dk, "dk"), (dv, "dv"), (dr, "dr")):
         _need(t, name, (B, T, C), k.dtype, dev)
     _need(dw, "dw", (C,), torch.float32, dev)
@@ -519,10 +535,10 @@ def wkv_token_shift(x, mu, x_prev=None, *, out=None, x_last=None, want_last=True
     _need(mu, "mu", (nmix, C), torch.float32, dev)
     _need(x_prev, "x_prev", (B, C), x.dtype, dev)
     if out is None:
-        out = torch.empty((nmix, B, T, C), dtype=x.dtype, device=dev)
+        out = _empty((nmix, B, T, C), x.dtype, dev, stream)
     _need(out, "out", (nmix, B, T, C), x.dtype, dev)
     if x_last is None and want_last:
-        x_last = torch.empty((B, C), dtype=x.dtype, device=dev)
+        x_last = _empty((B, C), x.dtype, dev, stream)
     _need(x_last, "x_last", (B, C), x.dtype, dev)
     _check(lib().wkv_token_shift(B, T, C, code, nmix, _ptr(x), _ptr(mu), _ptr(x_prev), _ptr(out), _ptr(x_last),
                                  _stream_ptr(stream, dev)), "wkv_token_shift")
@@ -546,7 +562,7 @@ def wkv_step(w, u, k, v, state, r=None, *, y=None, stream=None):
     _need(u, "u", (Lr, C), torch.float32, dev)
     _need(state, "state", (Lr, 3, B, C), torch.float32, dev)
     if y is None:
-        y = torch.empty((Lr, B, C), dtype=k.dtype, device=dev)
+        y = _empty((Lr, B, C), k.dtype, dev, stream)
     _need(y, "y", (Lr, B, C), k.dtype, dev)
     _check(lib().wkv_step(Lr, B, C, code, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(r), _ptr(state), _ptr(y),
                           _stream_ptr(stream, dev)), "wkv_step")
@@ -602,13 +618,13 @@ def wkv_delta_forward(w, beta, r, k, v, H, state_in=None, *, y=None, state_out=N
     _need(beta, "beta", scalars, f32, dev)
     _need(state_in, "state_in", states, f32, dev)
     if y is None:
-        y = torch.empty_like(v)
+        y = _empty_like(v, stream)
     else:
         _need(y, "y", values, dt, dev)
     if state_out is not None:
         _need(state_out, "state_out", states, f32, dev)
     elif want_state:
-        state_out = torch.empty(states, dtype=f32, device=dev) if state_in is None else torch.empty_like(state_in)
+        state_out = _empty(states, f32, dev, stream) if state_in is None else _empty_like(state_in, stream)
     ws_ptr, ws_bytes, owner = None, 0, None
     if use_workspace and B * H > 64:   # fewer heads never need one
         nbytes = int(lib().wkv_delta_forward_workspace_bytes(B, T, H, N))
@@ -637,7 +653,7 @@ def wkv_delta_step(w, beta, r, k, v, state, *, y=None, stream=None):
     _need(beta, "beta", scalars, f32, dev)
     _need(state, "state", (Lr, B, H, N, N), f32, dev)
     if y is None:
-        y = torch.empty_like(v)
+        y = _empty_like(v, stream)
     else:
         _need(y, "y", values, dt, dev)
     _launch(dev, "wkv_delta_step", lib().wkv_delta_step, Lr, B, Hk, H, N, code, _ptr(w), _ptr(beta), _ptr(r), _ptr(k), _ptr(v),
@@ -684,7 +700,7 @@ def wkv_delta_backward(w, beta, r, k, v, H, state_in=None, *, dy, dstate_out=Non
 
     def out(t, name, shape, dtype, like):
         if t is None:
-            return torch.empty_like(like)
+            return _empty_like(like, stream)
         _need(t, name, shape, dtype, dev)
         return t
 
@@ -693,7 +709,7 @@ def wkv_delta_backward(w, beta, r, k, v, H, state_in=None, *, dy, dstate_out=Non
     if dstate_in is not None:
         _need(dstate_in, "dstate_in", states, f32, dev)
     elif want_dstate_in:
-        dstate_in = torch.empty(states, dtype=f32, device=dev) if state_in is None else torch.empty_like(state_in)
+        dstate_in = _empty(states, f32, dev, stream) if state_in is None else _empty_like(state_in, stream)
     nbytes = int(lib().wkv_delta_backward_workspace_bytes(B, T, Hk, H, N))
     ws_ptr, ws_bytes, owner = _scratch(nbytes, workspace, dev, stream)
     _launch(dev, "wkv_delta_backward", lib().wkv_delta_backward, B, T, Hk, H, N, code, _ptr(w), _ptr(beta), _ptr(r), _ptr(k),
@@ -730,7 +746,7 @@ def wkv_group_norm(x, G, weight=None, bias=None, gate=None, *, act="none", eps=1
     "sigmoid".  Returns y."""
     rows, C, dev, code = _norm_args(x, G, weight, bias, gate, act, "wkv_group_norm")
     if y is None:
-        y = _torch().empty_like(x)
+        y = _empty_like(x, stream)
     else:
         _need(y, "y", x.shape, x.dtype, dev)
     _launch(dev, "wkv_group_norm", lib().wkv_group_norm, rows, C, G, code, _ACTS[act], eps, _ptr(x), _ptr(weight), _ptr(bias),
@@ -750,13 +766,13 @@ def wkv_group_norm_backward(x, G, weight=None, bias=None, gate=None, *, dy, act=
         if t is None and g is not None:
             raise ValueError(f"{name}: there is no {name[1:]}")
     if dx is None:
-        dx = torch.empty_like(x)
+        dx = _empty_like(x, stream)
     if gate is not None and dgate is None:
-        dgate = torch.empty_like(x)
+        dgate = _empty_like(x, stream)
     if weight is not None and dweight is None:
-        dweight = torch.empty((C,), dtype=torch.float32, device=dev)
+        dweight = _empty((C,), torch.float32, dev, stream)
     if bias is not None and dbias is None:
-        dbias = torch.empty((C,), dtype=torch.float32, device=dev)
+        dbias = _empty((C,), torch.float32, dev, stream)
     _need(dx, "dx", x.shape, x.dtype, dev)
     _need(dgate, "dgate", x.shape, x.dtype, dev)
     for t, name in ((dweight, "dweight"), (dbias, "dbias")):
