@@ -556,8 +556,11 @@ int wkv_delta_step(int64_t L, int64_t B, int64_t Hk, int64_t H, int64_t N, int d
  * make smaller; it is 0 where e^{-w} is 0.  No output may
  * overlap an input, another output or the workspace.  The workspace (256-byte
  * aligned, wkv_delta_backward_workspace_bytes() bytes) is as above; the walks
- * go in parts as the forward's do.  T == 0: dstate_in = dstate_out (zeros if
- * NULL), nothing else is written.  WKV_ERR_WORKSPACE: NULL or too small.
+ * go in parts as the forward's do.  dr, dk and dw of a segment of 64 tokens whose
+ * tensor-core products do not come within the wait limit are NaN, and
+ * wkv_workspace_status() returns WKV_ERR_TIMEOUT.  T == 0: dstate_in =
+ * dstate_out (zeros if NULL), nothing else is written.  WKV_ERR_WORKSPACE: NULL
+ * or too small.
  */
 size_t wkv_delta_backward_workspace_bytes(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N);
 int wkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, int dtype,

@@ -55,9 +55,9 @@ int launch_parts(Walk kern, int64_t slots, int threads, int smem, d::Args a, cha
     a.part_len = ((a.T + n - 1) / n + d::kSegment - 1) / d::kSegment * d::kSegment;
     a.parts = (a.T + a.part_len - 1) / a.part_len;
     a.control = reinterpret_cast<d::Control*>(ws);
+    a.wait_ns = wait_limit_ns();
     a.done = reinterpret_cast<uint32_t*>(ws + p.done);
     a.hand = reinterpret_cast<float*>(ws + p.hand);
-    a.wait_ns = wait_limit_ns();
     // the tickets and the parts that are done; the error word stays
     const size_t from = offsetof(d::Control, ticket);
     const int rc = record_cuda(cudaMemsetAsync(ws + from, 0, p.hand - from, st));
@@ -302,6 +302,7 @@ int wkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, i
     a.dr = dr, a.dk = dk, a.dw = dw, a.dbeta = dbeta;
     a.e = f(l.e), a.du = f(l.du), a.s_seg = f(l.s_seg), a.d_seg = f(l.d_seg);
     a.drh = f(l.drh), a.dkh = f(l.dkh);
+    a.control = reinterpret_cast<d::Control*>(ws), a.wait_ns = wait_limit_ns();
     a.vec = aligned(r, 16) && aligned(k, 16) && aligned(v, 16) && aligned(dy, 16) && aligned(dv, 16) &&
             aligned(dr, 16) && aligned(dk, 16);
     rc = with_type(dtype, N, [&](auto tag, auto size) {

@@ -67,12 +67,13 @@ struct Args {
     float* drh;          // (B, T, H, N): dr and dk of each value head, where heads share keys
     float* dkh;
     bool vec;            // 16-byte loads of every tensor in the I/O type
+    // the error word, and the limit of waits
+    Control* control;
+    uint64_t wait_ns;
     // a walk in parts of part_len tokens, taken by tickets (parts > 1)
     int64_t parts, part_len;
-    Control* control;
     uint32_t* done;      // (walks): parts that are done
     float* hand;         // (B, H, N, N): the state between a walk's parts, as its warps hold it
-    uint64_t wait_ns;
 };
 
 // ---------------------------------------------------------------------------

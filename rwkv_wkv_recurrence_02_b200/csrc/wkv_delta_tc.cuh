@@ -91,10 +91,38 @@ __device__ __forceinline__ void before_batch() {
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// a batch's accumulators, once its barrier was waited for
-__device__ __forceinline__ void after_batch() {
-    __syncwarp();
+// Did a batch come in time?  Every thread of the CTA; its accumulators may be read
+// then.  If not, the batch is waited for once more (it reads the tiles and writes
+// tensor memory), the error word is set, and the CTA ends.  A limit of 0 asks once.
+__device__ __forceinline__ bool batch_done(const Args& a, uint64_t* bar) {
+    const bool mine = a.wait_ns > 0 ? mbar_wait(bar, 0, a.wait_ns) : mbar_test(bar, 0);
+    const bool all = __syncthreads_and(mine);
+    if (!all) {
+        mbar_wait(bar, 0, kCopyWaitNs);
+        if (threadIdx.x == 0) a.control->error = 1u, a.control->err_unit = blockIdx.x;
+        __syncthreads();
+    }
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    return all;
+}
+__device__ __forceinline__ void free_columns(uint32_t acc, int warp) {   // after a barrier behind every warp's loads
+    if (warp == 0) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(acc), "r"(TcSegment::COLS) : "memory");
+    }
+}
+// NaN for dr, dk and dw of a segment whose products did not come
+__device__ __forceinline__ void lose_segment(const Args& a, const Segment& sg, uint32_t acc, int tid) {
+    const float bad = __int_as_float(0x7fffffff);
+    for (int i = tid; i < sg.nt * TcSegment::N; i += TcSegment::THREADS) {
+        const int64_t at = sg.rows + i / TcSegment::N * sg.vs + i % TcSegment::N;
+        if (a.H == a.Hk) put(static_cast<__nv_bfloat16*>(a.dr) + at, bad), put(static_cast<__nv_bfloat16*>(a.dk) + at, bad);
+        else a.drh[at] = a.dkh[at] = bad;
+        if (i < sg.nt) a.dw[sg.scalar + i * a.H] = bad;
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    free_columns(acc, tid / 32);
 }
 // 16 rows x 32 columns of an accumulator: x[p][n][i] is row lane / 4 + 8 (i / 2),
 // column 16 p + 8 n + 2 (lane % 4) + i % 2
@@ -216,8 +244,7 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
         g[h] = decay_of(sums[t_lo + 8 * h], make_float2(0.f, 0.f));
         q[h] = decay_of(sums[kSegment - 1], sums[t_lo + 8 * h]);
     }
-    bool ok = mbar_wait(&bar[0], 0, kCopyWaitNs);
-    after_batch();
+    if (!batch_done(a, &bar[0])) return lose_segment(a, sg, acc, tid);
     // K, then R: a warp's 8 tokens as they come, later its 8 channels turned
     const auto fetch_raw = [&](const void* from) {
         copy_rows<IO, 8, N>(raw, [&](int r, int c) { return place(row + r, c); }, static_cast<const IO*>(from) + sg.keys + first * sg.ks,
@@ -282,8 +309,7 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
     cp_async_wait();
     __syncthreads();
     turn_raw(tiles + (G::D + 1) * PC);
-    ok = mbar_wait(&bar[1], 0, kCopyWaitNs) && ok;
-    after_batch();
+    if (!batch_done(a, &bar[1])) return lose_segment(a, sg, acc, tid);
     // B: -dv_t.u_s, s < t, and -u_t.dv_s, s > t; C: u_t.dy_s, s >= t
     {
         float y[2][2][4], z[2][2][4];
@@ -322,33 +348,19 @@ __global__ void __launch_bounds__(TcSegment::THREADS, 2) delta_segment_tc_kernel
         }
         tile_commit(&bar[2]);
     }
-    ok = mbar_wait(&bar[2], 0, kCopyWaitNs) && ok;
-    after_batch();
-    const float bad = ok ? 0.f : __int_as_float(0x7fffffff);   // a wait that ran out
+    if (!batch_done(a, &bar[2])) return lose_segment(a, sg, acc, tid);
     load_tile(mine, x);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        Acc::add(dr[p], x[p], false);
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dr[p][n][i] += bad;
-    }
+    for (int p = 0; p < 2; ++p) Acc::add(dr[p], x[p], false);
     load_tile(mine + 64, x);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        Acc::add(dk[p], x[p], false);
-        dk[p][0][0] += bad;
-    }
+    for (int p = 0; p < 2; ++p) Acc::add(dk[p], x[p], false);
     float own[2];
     row_products<N, 2, 1>(own, raw, 0, dr, t_lo, i0, lane);
     store_rows<IO, N, 2>(a, sg, dr, dk, tiles + G::U * PC + warp * (G::ROWS / 8), tb, i0, lane);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    segment_rates<IO, N, G::PARTS>(a, sg, own, border, rdr, dvv, inner, s_seg, d_seg, t_lo, rates, ok && any_odd(dr), ok && any_odd(dk), smem, tid);
-    if (warp == 0) {   // every warp's loads are done: the barrier in segment_rates
-        after_batch();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(acc), "r"(G::COLS) : "memory");
-    }
+    segment_rates<IO, N, G::PARTS>(a, sg, own, border, rdr, dvv, inner, s_seg, d_seg, t_lo, rates, any_odd(dr), any_odd(dk), smem, tid);
+    free_columns(acc, warp);   // every warp's loads are done: the barrier in segment_rates
 }
 
 }  // namespace delta

@@ -50,7 +50,8 @@ inline bool mul_ok(int64_t a, int64_t b, int64_t c, int64_t* out) {
 
 inline size_t elem_bytes(int dtype) { return dtype == WKV_BF16 ? 2 : 4; }
 
-// Limit of every wait on another CTA's result: 1 s, or WKV_WAIT_LIMIT_NS (read
+// Limit of every wait on another CTA's result, and on the reverse delta rule's
+// batches of tensor-core products: 1 s, or WKV_WAIT_LIMIT_NS (read
 // once per process; used by the tests to make waits run out on purpose).
 // Waits for a CTA's own TMA copies have a fixed limit (kCopyWaitNs).
 inline uint64_t wait_limit_ns() {
