@@ -4,8 +4,6 @@
 #include "wkv_delta_tc.cuh"
 #include "wkv_host.cuh"
 
-#include <cstddef>
-
 namespace {
 
 using namespace wkv::host;
@@ -18,14 +16,15 @@ namespace d = wkv::delta;
 constexpr int64_t kPartMin = 256, kPartMax = 8, kSlotsMin = 148;
 
 struct Parts {
-    size_t done, hand, bytes;   // offsets behind the control words; 0 bytes: never in parts
+    size_t ticket, done, hand, bytes;   // offsets, behind the header; 0 bytes: never in parts
 };
 // walks: heads times slices of their columns
 Parts parts_layout(int64_t walks, int64_t states, int64_t T) {
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     Parts p{};
     if (walks <= kSlotsMin || T < 2 * kPartMin) return p;
-    p.done = kHeader;
+    p.ticket = kHeader;
+    p.done = p.ticket + 256;
     p.hand = p.done + up(size_t(walks) * 4);
     p.bytes = p.hand + up(size_t(states) * 4);
     return p;
@@ -54,13 +53,12 @@ int launch_parts(Walk kern, int64_t slots, int threads, int smem, d::Args a, cha
     const int64_t n = a.T / kPartMin < kPartMax ? a.T / kPartMin : kPartMax;
     a.part_len = ((a.T + n - 1) / n + d::kSegment - 1) / d::kSegment * d::kSegment;
     a.parts = (a.T + a.part_len - 1) / a.part_len;
-    a.control = reinterpret_cast<d::Control*>(ws);
-    a.wait_ns = wait_limit_ns();
+    a.control = reinterpret_cast<d::Control*>(ws), a.wait_ns = wait_limit_ns();
+    a.ticket = reinterpret_cast<uint32_t*>(ws + p.ticket);
     a.done = reinterpret_cast<uint32_t*>(ws + p.done);
     a.hand = reinterpret_cast<float*>(ws + p.hand);
-    // the tickets and the parts that are done; the error word stays
-    const size_t from = offsetof(d::Control, ticket);
-    const int rc = record_cuda(cudaMemsetAsync(ws + from, 0, p.hand - from, st));
+    // the tickets and the parts that are done; the header stays
+    const int rc = record_cuda(cudaMemsetAsync(ws + p.ticket, 0, p.hand - p.ticket, st));
     if (rc != WKV_OK) return rc;
     kern<<<dim3(unsigned(slots)), threads, smem, st>>>(a);
     return check_launch();

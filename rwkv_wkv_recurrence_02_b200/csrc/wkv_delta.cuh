@@ -33,9 +33,10 @@ __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// Words of a walk in parts; the error is where wkv_workspace_status() reads it.
+// A workspace's first words; the error is where wkv_workspace_status() reads it,
+// and these kernels write the last two only.
 struct Control {
-    uint32_t epoch, finished, error, err_unit, ticket;
+    uint32_t epoch, finished, error, err_unit;
 };
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -72,6 +73,7 @@ struct Args {
     uint64_t wait_ns;
     // a walk in parts of part_len tokens, taken by tickets (parts > 1)
     int64_t parts, part_len;
+    uint32_t* ticket;
     uint32_t* done;      // (walks): parts that are done
     float* hand;         // (B, H, N, N): the state between a walk's parts, as its warps hold it
 };

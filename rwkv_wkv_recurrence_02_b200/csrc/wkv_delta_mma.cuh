@@ -617,7 +617,7 @@ __device__ __forceinline__ bool next_task(const Args& a, int64_t walks, int64_t 
     if (threadIdx.x == 0) {
         if (!first)
             asm volatile("red.release.gpu.global.max.u32 [%0], %1;" ::"l"(a.done + t.walk), "r"(t.lost ? kLost : uint32_t(t.part + 1)) : "memory");
-        const int64_t id = atomicAdd(&a.control->ticket, 1u);
+        const int64_t id = atomicAdd(a.ticket, 1u);
         s_ticket = id;
         s_lost = 0;
         if (id < walks * a.parts) {
