@@ -569,6 +569,14 @@ int wkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, i
                        void* dr, void* dk, void* dv, float* dw, float* dbeta, float* dstate_in,
                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * wkv_delta_status -- synchronise `stream`, then WKV_OK, or WKV_ERR_TIMEOUT if a
+ * wait of any wkv_delta_* call on the current device has run out since the last
+ * call here with clear != 0.  Workspaces have their own record of it; this one
+ * outlives them.
+ */
+int wkv_delta_status(int clear, cudaStream_t stream);
+
 /* Activation of wkv_group_norm. */
 typedef enum { WKV_ACT_NONE = 0, WKV_ACT_SILU = 1, WKV_ACT_SIGMOID = 2 } wkv_act;
 

@@ -36,7 +36,7 @@ EXPORTS = ("wkv_forward", "wkv_forward_ex", "wkv_forward_workspace_bytes", "wkv_
            "wkv_backward", "wkv_state", "wkv_state_combine", "wkv5_forward",
            "wkv_backward_workspace_bytes", "wkv_token_shift", "wkv_delta_forward", "wkv_delta_forward_workspace_bytes",
            "wkv_delta_step",
-           "wkv_delta_backward", "wkv_delta_backward_workspace_bytes", "wkv_group_norm", "wkv_group_norm_backward",
+           "wkv_delta_backward", "wkv_delta_backward_workspace_bytes", "wkv_delta_status", "wkv_group_norm", "wkv_group_norm_backward",
            "wkv_group_norm_backward_workspace_bytes", "wkv_strerror", "wkv_last_cuda_error",
            "wkv_abi_version")
 
@@ -108,6 +108,8 @@ def lib():
         L.wkv_delta_backward.restype = i32
         L.wkv_delta_backward_workspace_bytes.argtypes = [i64] * 5
         L.wkv_delta_backward_workspace_bytes.restype = sz
+        L.wkv_delta_status.argtypes = [i32, vp]
+        L.wkv_delta_status.restype = i32
         L.wkv_group_norm.argtypes = [i64] * 3 + [i32, i32, ctypes.c_float] + [vp] * 6
         L.wkv_group_norm.restype = i32
         L.wkv_group_norm_backward.argtypes = [i64] * 3 + [i32, i32, ctypes.c_float] + [vp] * 10 + [sz, vp]
@@ -605,7 +607,9 @@ def wkv_delta_forward(w, beta, r, k, v, H, state_in=None, *, y=None, state_out=N
     float32 or None (zeros).  Per head
         e_t = v_t - exp(-w_t) S^T k_t,  S <- exp(-w_t) S + beta_t k_t e_t^T,  y_t = S^T r_t.
     Returns (y, state_out); state_out may be state_in.  use_workspace=False
-    passes no workspace (one CTA a head's slice, whatever the number of heads)."""
+    passes no workspace (one CTA a head's slice, whatever the number of heads).
+    A wait on the GPU that ran out leaves NaN; wkv_delta_status() tells, and
+    the workspace's status()."""
     torch = _torch()
     B, T, Hk, N = _delta_sizes(k, v, H, "wkv_delta_forward")
     dev, dt, f32 = k.device, k.dtype, torch.float32
@@ -716,6 +720,15 @@ def wkv_delta_backward(w, beta, r, k, v, H, state_in=None, *, dy, dstate_out=Non
             _ptr(v), _ptr(state_in), _ptr(dy), _ptr(dstate_out), _ptr(dr), _ptr(dk), _ptr(dv), _ptr(dw), _ptr(dbeta),
             _ptr(dstate_in), ws_ptr, ws_bytes, _stream_ptr(stream, dev))
     return dr, dk, dv, dw, dbeta, dstate_in
+
+
+def wkv_delta_status(*, clear=False, stream=None, device=None) -> int:
+    """Synchronise the stream (of `device`, the current one): 0, or
+    WKV_ERR_TIMEOUT (-7) if a wait of a delta rule call on the device has run
+    out since the last call with clear=True, with whatever workspace or none."""
+    torch = _torch()
+    with torch.cuda.device(device):   # None: the current one
+        return int(lib().wkv_delta_status(int(clear), _stream_ptr(stream, None)))
 
 
 _ACTS = {"none": 0, "silu": 1, "sigmoid": 2}

@@ -309,4 +309,15 @@ int wkv_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t H, int64_t N, i
     return rc != WKV_OK ? rc : check_launch();
 }
 
+int wkv_delta_status(int clear, cudaStream_t stream) {
+    uint32_t lost = 0;
+    int rc = record_cuda(cudaMemcpyFromSymbolAsync(&lost, d::g_lost, sizeof(lost), 0, cudaMemcpyDeviceToHost, stream));
+    if (rc == WKV_OK) rc = record_cuda(cudaStreamSynchronize(stream));
+    if (rc == WKV_OK && clear && lost) {
+        static const uint32_t none = 0;
+        rc = record_cuda(cudaMemcpyToSymbolAsync(d::g_lost, &none, sizeof(none), 0, cudaMemcpyHostToDevice, stream));
+    }
+    return rc != WKV_OK ? rc : lost ? WKV_ERR_TIMEOUT : WKV_OK;
+}
+
 }  // extern "C"

@@ -39,6 +39,15 @@ struct Control {
     uint32_t epoch, finished, error, err_unit;
 };
 
+// A wait ran out: in the call's workspace, and for the whole device (a call's
+// workspace may be gone when somebody asks).
+static __device__ uint32_t g_lost;
+__device__ __forceinline__ void record_lost(Control* c, uint32_t unit) {
+    c->error = 1u;
+    c->err_unit = unit;
+    g_lost = 1u;
+}
+
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 struct Args {

@@ -630,8 +630,7 @@ __device__ __forceinline__ bool next_task(const Args& a, int64_t walks, int64_t 
                 if (have >= want) break;
                 asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
                 if (now - begin > a.wait_ns) {
-                    a.control->error = 1u;
-                    a.control->err_unit = uint32_t(id);
+                    record_lost(a.control, uint32_t(id));
                     have = kLost;
                     break;
                 }

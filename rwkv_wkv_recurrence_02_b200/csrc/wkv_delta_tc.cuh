@@ -99,7 +99,7 @@ __device__ __forceinline__ bool batch_done(const Args& a, uint64_t* bar) {
     const bool all = __syncthreads_and(mine);
     if (!all) {
         mbar_wait(bar, 0, kCopyWaitNs);
-        if (threadIdx.x == 0) a.control->error = 1u, a.control->err_unit = blockIdx.x;
+        if (threadIdx.x == 0) record_lost(a.control, blockIdx.x);
         __syncthreads();
     }
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
