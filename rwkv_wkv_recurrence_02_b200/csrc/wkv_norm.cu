@@ -12,7 +12,6 @@ using namespace wkv::host;
 namespace nm = wkv::norm;
 
 constexpr int kMaxE = 16;           // channels of a lane in registers; larger groups take large_kernel
-constexpr int kChunks = 512;        // tokens are summed in at most about so many chunks
 constexpr int64_t kLargePer = 64;   // tokens a thread of large_params_kernel sums
 
 struct Plan {
