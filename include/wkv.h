@@ -510,7 +510,7 @@ int wkv_token_shift(int64_t B, int64_t T, int64_t C, int dtype, int nmix,
  *
  * wkv_delta_forward -- a chunk of T tokens.  state_in NULL: zeros; state_out
  * NULL: not wanted; it may equal state_in and must overlap nothing else.
- * Feeding it back chains chunks exactly like one pass.  T == 0: state_out =
+ * Feeding it back chains chunks like one pass, to rounding.  T == 0: state_out =
  * state_in.  16-byte aligned r, k, v are read in 16-byte pieces.  Errors as
  * wkv5_forward.  Asynchronous on `stream`.
  *   workspace    256-byte aligned scratch of wkv_delta_forward_workspace_bytes()

@@ -12,7 +12,7 @@ namespace d = wkv::delta;
 // Walks in parts (Task in wkv_delta_mma.cuh) need walks that are not few and
 // tokens for parts of kPartMin or more; kPartMax of them bound the work that
 // the last wave leaves undone to an eighth of a walk.  4 x 8192 tokens of 80 heads
-// of 64 (320 walks, 296 places): 1225 us whole, 902 to 928 in 8 parts, 954 in 32.
+// of 64 (320 walks, 296 places): 1303 us whole, 1015 in 8 parts, 1035 in 32.
 constexpr int64_t kPartMin = 256, kPartMax = 8, kSlotsMin = 148;
 
 struct Parts {
@@ -43,8 +43,8 @@ int walk_slots(Walk kern, int threads, int smem, int64_t* slots) {
 }
 // Do walks go in parts?  Where the share of the last wave's places that stay
 // empty, of all waves', is above a tenth (a part costs a pipeline's fill).  Not in
-// one wave that does not fill the GPU: 256 walks of 4096 tokens took 435 us in
-// parts, 402 whole.
+// one wave that does not fill the GPU: 256 walks of 4096 tokens take 479 us in
+// parts, 429 whole.
 bool in_parts(int64_t walks, int64_t slots) {
     const int64_t waves = slots > 0 ? (walks + slots - 1) / slots : 0;
     return waves > 1 && (waves * slots - walks) * 10 > waves * slots;

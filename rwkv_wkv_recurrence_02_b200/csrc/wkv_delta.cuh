@@ -90,7 +90,7 @@ struct Args {
 // ---------------------------------------------------------------------------
 // One token for L layers (B sequences, H heads each): the state is read once,
 // held in registers and written once, which is what bounds it: 24 layers of 256
-// sequences of 64 heads of 64 in 2220 us, 5.9 TB/s (91% of a copy's rate).  A warp
+// sequences of 64 heads of 64 in 2244 us, 5.8 TB/s (90% of a copy's rate).  A warp
 // takes CW value columns of a head; the sums over keys are shuffles.
 // ---------------------------------------------------------------------------
 template <typename IO, int N, int CL, int NW>

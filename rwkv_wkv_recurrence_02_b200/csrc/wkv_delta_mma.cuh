@@ -32,16 +32,17 @@
 // in the loop, took 6% of the time of all calls.
 //
 // What bounds it: issue.  An mma.sync of 16 x 8 x 16 holds its scheduler for 8.3
-// cycles here and other instructions (1.1 each) do not issue meanwhile; 82 of
-// the ones and about 500 of the others a chunk and warp (bfloat16 heads of 64),
-// with the staging warps' share, are 93% of the time.  Measured: 8 x 4096 tokens
-// of 32 heads of 64 in bfloat16 398 us (reads and writes alone: 85; the same
+// cycles here and other instructions do not issue meanwhile; bfloat16 heads of 64
+// have 96 of the ones and about 500 of the others a chunk and warp.  On an SM with
+// two walks the tensor pipe is active in 51% of the cycles and an instruction
+// issues in 44%.  Measured: 8 x 4096 tokens
+// of 32 heads of 64 in bfloat16 429 us (reads and writes alone: 85; the same
 // recurrence token by token in float32 multiply-adds: 1798).  With few heads a
-// chunk's chain of dependent products bounds it: 32 heads x 4096 tokens 228 us
-// (0.9 us a chunk), 32 heads of 128 363 us.  Chunks of 32 tokens were no faster
+// chunk's chain of dependent products bounds it: 32 heads x 4096 tokens 242 us
+// (0.95 us a chunk), 32 heads of 128 395 us.  Chunks of 32 tokens were no faster
 // (the code outgrows the instruction cache), 2 or 4 warps sharing a head's keys
-// slower (583 us, exchange in shared memory), fp16 pieces slower (428 us, the
-// scaling).
+// slower (583 us against 386, exchange in shared memory), fp16 pieces slower (428 us
+// against 402, the scaling).
 #pragma once
 
 #include "wkv_delta.cuh"
@@ -551,8 +552,8 @@ __device__ __forceinline__ void store_state(float* s, const float (&S)[N / 8][4]
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[(8 * n + 2 * (lane % 4) + (i & 1)) * N + lane / 4 + (i >> 1) * 8] = S[n][i];
 }
-// The segments' kernel of the reverse mode: tcgen05.mma (wkv_delta_tc.cuh; 1587 us
-// for 8 x 4096 tokens of 32 heads where mma.sync took 1656), or mma.sync, as heads of
+// The segments' kernel of the reverse mode: tcgen05.mma (wkv_delta_tc.cuh; 1735 us
+// for 8 x 4096 tokens of 32 heads where mma.sync takes 1837), or mma.sync, as heads of
 // other sizes and float32 take: heads of 128 and float32's pieces need more tiles
 // than two CTAs an SM have room for, heads of 32 would leave half of each unused.
 template <typename IO, int N>
@@ -713,8 +714,8 @@ template <typename IO>
 constexpr int kChain = sizeof(IO) == 2 ? 4 : 1;
 
 // CTAs an SM: two where the state's lines and the I/O type leave room (8 x 4096
-// tokens of 32 heads of 64: two walks an SM share its issue slots, 398 us for
-// 1.73 walks an SM where one walk alone takes 228)
+// tokens of 32 heads of 64: two walks an SM share its issue slots, 429 us for
+// 1.73 walks an SM where one walk alone takes 242)
 template <typename IO, int N>
 constexpr int kCtas = N <= 64 && sizeof(IO) == 2 ? 2 : 1;
 // Two walks of heads of 64 in bfloat16 fit an SM with 128 registers a thread on

@@ -18,12 +18,13 @@
 // for every segment at once.  It starts dw from the inner product <D, S> at the
 // segment's end.  The two walks run side by side in one kernel.
 //
-// Measured, bfloat16: 8 x 4096 tokens of 32 heads of 64 1540 us (reads and writes
-// alone: 150), the walks 820 to 880 of it, bound as the forward is, the segments
-// the rest (wkv_delta_tc.cuh).  2047 tokens of 16 heads of 128, 8 key heads: 312 us,
-// its segments bound by shared memory's wavefronts (67% of their peak) and latency.
+// Measured, bfloat16: 8 x 4096 tokens of 32 heads of 64 1735 us (reads and writes
+// alone: 150), the walks 870 of it, bound as the forward is, the segments
+// the rest (wkv_delta_tc.cuh).  2047 tokens of 16 heads of 128, 8 key heads: 343 us,
+// 220 of it the walks (64 CTAs, a chunk's chain), 120 the segments: one CTA an SM, the
+// tensor pipe active in 35% of the cycles, first among its stalls.
 // The two walks one after the other took 671 us on 4096 tokens of 32 heads of
-// 64; side by side all three kernels take 379.
+// 64 where side by side all kernels took 414 (406 now).
 #pragma once
 
 #include "wkv_delta_mma.cuh"
@@ -278,9 +279,9 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
     reverse_walk<IO, N, true>(a, smem, blockIdx.x);
 }
 // Whole walks of both kinds: they need nothing of each other.  The reverse
-// ones, which take longer, first: 4 x 4096 tokens of 24 heads of 64 663 us, 737 the
-// other way round (8 x 4096 of 32 heads 1548 and 1528).  In turn they took 858 and
-// 1830 us, and 449 where 32 heads of one sequence take 379: both codes in one
+// ones, which take longer, first: 4 x 4096 tokens of 24 heads of 64 737 us, 815 the
+// other way round (8 x 4096 of 32 heads 1741 and 1727).  In turn they take 938 and
+// 2032 us, and 481 where 32 heads of one sequence take 406: both codes in one
 // instruction cache.
 template <typename IO, int N>
 __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) delta_walks_kernel(const __grid_constant__ Args a) {
@@ -297,9 +298,9 @@ __global__ void __launch_bounds__(ReverseShape<IO, N>::THREADS, kCtas<IO, N>) de
 // segment's 16 x 16 blocks of (token, token) products.  A block is formed once,
 // by one warp, and read from shared memory as it lies and transposed.
 // ---------------------------------------------------------------------------
-// 16 x 32 of a warp's: 319 us for 2047 tokens of 16 heads of 128 (the whole call),
-// 330 with 16 x 64, whose warps are half as many.  Bfloat16 heads of 64 take
-// wkv_delta_tc.cuh's kernel.
+// 16 x 32 of a warp's: 343 us for 2047 tokens of 16 heads of 128 (the whole call), as
+// with 16 x 64, whose warps are half as many (segment_tokens wants four threads a
+// key).  Bfloat16 heads of 64 take wkv_delta_tc.cuh's kernel.
 template <typename IO, int N>
 struct SegmentShape {
     static constexpr int KP = sizeof(IO) == 2 ? 1 : 3;
@@ -505,7 +506,7 @@ __device__ __forceinline__ void store_rows(const Args& a, const Segment& sg, con
         }
     } else if constexpr (KP == 1) {   // through rows of the warp's own (where u was) to 16-byte stores
         constexpr int LD = 16 * NP + 8;
-                const uint32_t to = smem_u32(tile + ((lane & 7) + ((lane >> 3) & 1) * 8) * LD + (lane >> 4) * 8);
+        const uint32_t to = smem_u32(tile + ((lane & 7) + ((lane >> 3) & 1) * 8) * LD + (lane >> 4) * 8);
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             stsm_tile(to + p * 32, dr[p]);
@@ -544,7 +545,7 @@ __device__ __forceinline__ void store_rows(const Args& a, const Segment& sg, con
 template <typename IO, int N>
 __device__ __forceinline__ bool segment_tokens(const Args& a, const Segment& sg, char* smem, const float* s_seg, const float* d_seg,
                                                const float* dvv, bool odd_dr, int tid) {
-    constexpr int J = N / 4, WARPS = 4 * N / 32;
+    constexpr int J = N / 4, WARPS = 4 * N / 32;   // four threads a key
     float* dkp = reinterpret_cast<float*>(smem);      // (tokens, N)
     float* rdr = dkp + kSegment * N;                  // (tokens, warps)
     float* sum = rdr + kSegment * WARPS;              // (2, warps)
@@ -668,9 +669,9 @@ __device__ __forceinline__ bool any_odd(const float (&x)[NP][2][4]) {
 
 // dw of a segment from r . dr by the warps' rows (own), dv . v and <D, S> at its
 // end (border[1], a thread's share); rates: warp 0's, of two tokens a lane.  All
-// threads of the CTA.  <D, S> at its begin
-// follows from those, but in the first segment it is formed too: with an empty
-// state it is zero, and not what rounding leaves of the terms.  At a token whose
+// threads of the CTA.  <D, S> at its begin follows from those, but in the first
+// segment it is formed too: with an empty state it is zero, and not what rounding
+// leaves of the terms.  At a token whose
 // decay is 0 the sum is 0 and begins anew, so that what rounding leaves of the
 // terms behind it does not reach the document ahead of it.
 // odd_dr, odd_dk: something in this thread's is not finite; smem: the segment's tiles.
@@ -679,6 +680,7 @@ __device__ __forceinline__ void segment_rates(const Args& a, const Segment& sg, 
                                               const float* dvv, float* inner, const float* s_seg, const float* d_seg, int t_lo, float2 rates,
                                               bool odd_dr, bool odd_dk, char* smem, int tid) {
     constexpr int WARPS = 4 * PARTS, THREADS = 32 * WARPS;
+    static_assert(THREADS == 4 * N, "segment_tokens' threads");
     const int lane = tid % 32, warp = tid / 32, nt = sg.nt;
     const int64_t scalar = sg.scalar, seg = sg.seg;
 #pragma unroll
@@ -751,7 +753,8 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
     using G = SegmentShape<IO, N>;
     constexpr int KP = G::KP, NP = G::IC / 16;
     constexpr Swizzled<N> place{};
-    extern __shared__ __align__(128) char smem[];                 // the swizzle is of addresses: no static array lies ahead of it
+    extern __shared__ __align__(128) char swizzled_smem[];        // gram_at's exclusive or is of addresses
+    char* const smem = swizzled_smem;
     __nv_bfloat16* ub = reinterpret_cast<__nv_bfloat16*>(smem);   // u = beta e
     __nv_bfloat16* db = ub + 3 * G::PIECE;                        // dv = beta du
     __nv_bfloat16* yb = db + 3 * G::PIECE;
@@ -875,12 +878,12 @@ __global__ void __launch_bounds__(SegmentShape<IO, N>::THREADS, SegmentShape<IO,
             }
     }
     __syncthreads();
-    if constexpr (KP == 3) {   // K and R over the sg.rows
+    if constexpr (KP == 3) {   // K and R over the rows
         split_rows<RW, N, 3>(kb, rows_at, G::PIECE, reinterpret_cast<const float*>(kp) + rr * sg.ks, sg.ks, left, a.vec, lane);
         split_rows<RW, N, 3>(rb, rows_at, G::PIECE, reinterpret_cast<const float*>(rp) + rr * sg.ks, sg.ks, left, a.vec, lane);
         __syncthreads();
     }
-    // dr takes K by the sg.rows of the blocks, dk K by sg.rows and columns and R by columns
+    // dr takes K by the rows of the blocks, dk K by rows and columns and R by columns
     const auto times_add = [&](float (&d)[2][4], const uint32_t (&a)[3][4], const uint32_t (&f)[KP][4]) {
         float x[2][4];
         times_sum<3, KP, 3>(x, true, a, f);

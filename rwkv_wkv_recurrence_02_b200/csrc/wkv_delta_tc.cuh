@@ -16,12 +16,13 @@
 // core matrices of 8 rows; a slot of padding behind each pair of core matrices and
 // two behind each k step keep the stores of a warp in different banks.
 //
-// Measured for 8 x 2048 tokens of 32 heads (8192 segments): 395 us, as mma.sync 423;
-// the whole call on 8 x 4096 tokens 1587 us against 1656, and 1542 since.  What bounds it is a
-// CTA's chain at two CTAs an SM, about 22,000 cycles: loads and their conversion
-// 9,000, the three batches 6,500 (an M = 64 product of 16 columns reads 4 KB of shared
-// memory), scores 2,500, outputs 3,500; DRAM is at 28%, issue at 36%.  Steps, as
-// the whole call's time: heads before segments in the grid's order (neighbours in
+// Measured for 8 x 2048 tokens of 32 heads (8192 segments), the whole call: 885 us, with the
+// segments by mma.sync 929; on 8 x 4096 tokens 1735 us against 1837.  What bounds it is a
+// CTA's chain at two CTAs an SM, about 27,700 cycles: loads and their conversion
+// 6,700, the three batches 5,700, 5,500 and 2,600 (42 products; an M = 64 product of 16
+// columns reads 4 KB of shared memory, and the CTA beside it wants the same unit, which
+// is active in 48% of the cycles), scores 2,100 and 2,300, outputs 2,900; DRAM is at
+// 24%, issue at 37%.  Steps, as the whole call's time when dk took 27 products: heads before segments in the grid's order (neighbours in
 // memory at the same time) 1665 to 1637, descriptors by sums 1637 to 1617, dw's rates
 // kept from the decays' sums 1617 to 1600, the next CTA's data prefetched while
 // batch 1 runs 1600 to 1587 (with the CTA's own loads: no gain), 32-bit divisions

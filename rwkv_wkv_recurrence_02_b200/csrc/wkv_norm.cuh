@@ -11,9 +11,9 @@
 // the reverse mode sums dweight and dbias there.  Mean and variance are two
 // passes over registers: x is read once.  Bound by memory, and near it by the
 // instructions, so the arithmetic is in packed pairs.  8 x 4096 tokens of 2048
-// bfloat16 channels in 32 groups with a gate: forward 82 us (4.9 TB/s, 76% of a
+// bfloat16 channels in 32 groups with a gate: forward 80 us (5.0 TB/s, 78% of a
 // copy's rate; 103 with loads into registers a token ahead instead of the ring),
-// reverse 147 us (4.6 TB/s; 214).
+// reverse 146 us (4.6 TB/s; 214).
 #pragma once
 
 #include "wkv_common.cuh"
