@@ -259,6 +259,8 @@ class Workspace:
         return ((self.buf if buf is None else buf).data_ptr() + 255) & ~255
 
     def status(self, stream=None) -> int:
+        """The error word, once `stream` (that of the calls; None: the current
+        one) is done with what was queued on it."""
         for buf in (self.buf, self.plain):
             if buf is not None:
                 rc = lib().wkv_workspace_status(self._aligned_ptr(buf), _stream_ptr(stream, buf.device))

@@ -104,3 +104,50 @@ def test_a_state_that_overflows(N, dtype):
     r0 = np.abs(f64(d["r"])[:, :44, :1])
     scale = r0 * np.maximum.accumulate(np.abs(ref) / r0, axis=1)
     assert np.all(np.abs(f64(y)[:, :44] - ref) <= 2e-5 * scale + (2.0 ** -8 * np.abs(ref) if dtype == BF16 else 0))
+
+
+@pytest.mark.parametrize("B,T,Hk,H,N,dtype", [(3, 700, 50, 100, 64, BF16), (5, 600, 20, 20, 128, BF16), (3, 600, 60, 60, 32, F32)])
+@pytest.mark.parametrize("name,at", [("v", 300), ("k", 520), ("dy", 300), ("state_in", 0), ("ds", 0)])
+def test_walks_in_parts(name, at, B, T, Hk, H, N, dtype):
+    """More walks than the GPU holds: the one with the value is as in a call of its
+    own, where it is walked whole, and all others keep their bits."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    k = n(B, T, Hk, N)
+    d = {"w": torch.exp(n(B, T, H) - 2), "beta": torch.sigmoid(n(B, T, H)), "r": (n(B, T, Hk * N) * N ** -0.5).to(dtype),
+         "k": (k / k.norm(dim=-1, keepdim=True)).flatten(2).to(dtype), "v": n(B, T, H * N).to(dtype), "state_in": 0.3 * n(B, H, N, N),
+         "dy": n(B, T, H * N).to(dtype), "ds": 0.3 * n(B, H, N, N)}
+    clean = [*forward(d, H), *backward(d, H)]
+    b, hk, share = B - 2, Hk - 3, H // Hk
+    h = hk * share
+    if name in ("state_in", "ds"):
+        d[name][b, h, 4, 9] = NAN
+    else:
+        d[name][b, at, (h if name in ("v", "dy") else hk) * N + 9] = NAN
+    got = [*forward(d, H), *backward(d, H)]
+    heads = lambda x, m: x.unflatten(-1, (m, -1)) if x.dim() == 3 else x.transpose(1, 2)  # noqa: E731
+    sizes = (H, H, Hk, Hk, H, H, H, H)
+    # the heads of that key head by themselves
+    pick = lambda x, m: x[b:b + 1].unflatten(-1, (m, -1))[..., m // Hk * hk:m // Hk * (hk + 1), :].flatten(2).contiguous()  # noqa: E731
+    one = {x: pick(d[x], Hk if x in ("r", "k") else H) for x in ("w", "beta", "r", "k", "v", "dy")}
+    one.update({x: d[x][b:b + 1, h:h + share].contiguous() for x in ("state_in", "ds")})
+    alone = [*forward(one, share), *backward(one, share)]
+    assert any(not torch.isfinite(x).all() for x in alone)
+    for i, (x, y, z, m) in enumerate(zip(got, clean, alone, sizes)):
+        if x.dim() == 4:      # states
+            x, y, z = x.clone(), y.clone(), z[0]
+            mine, x[b, h:h + share], y[b, h:h + share] = x[b, h:h + share].clone(), 0, 0
+        else:
+            per = m // Hk
+            x, y = x.unflatten(-1, (m, -1)).clone(), y.unflatten(-1, (m, -1)).clone()
+            mine = x[b, :, per * hk:per * (hk + 1)].flatten(1).clone()
+            x[b, :, per * hk:per * (hk + 1)], y[b, :, per * hk:per * (hk + 1)] = 0, 0
+            z = z[0]
+        assert torch.equal(x, y), f"another head of output {i}"
+        ok = torch.isfinite(z)
+        assert torch.equal(torch.isfinite(mine), ok), f"output {i}"
+        if ok.any():
+            scale = z[ok].abs().max().double()
+            err = (mine[ok].double() - z[ok].double()).abs()
+            # both within 2e-5 of the largest (dw: of the sums it comes from, up to ten times as large), rounded once each
+            assert (err <= (4e-4 if i == 5 else 4e-5) * scale + (2 * 2.0 ** -8 * z[ok].double().abs() if z.dtype == BF16 else 0)).all(), f"output {i}"
